@@ -67,7 +67,10 @@ typedef enum {
   ZL_ECUDA = -5,         /* a CUDA runtime/driver call failed                   */
   ZL_ETIMEOUT = -6,      /* a kernel gave up a bounded wait (reported by
                             zl_sync_check)                                      */
-  ZL_ENODEVICE = -7      /* no usable sm_103 device                             */
+  ZL_ENODEVICE = -7,     /* no usable sm_103 device                             */
+  ZL_EPAGE = -8          /* a kernel met a page number, slot or length outside
+                            the cache and left it out (reported by
+                            zl_sync_check)                                      */
 } zl_status;
 
 typedef enum {
@@ -117,7 +120,8 @@ const char* zl_status_string(int32_t status);
 
 /* ABI version of this header: (major << 16) | minor.  2.0: head-sharded
  * tiles; 2.1 adds ZL_FWD_BF16_PARTIALS, zl_lse_merge_ex and the schedule
- * queries (no existing entry changed). */
+ * queries; 2.2 adds rotary positions (zl_rope_*) and the paged key/value cache
+ * (zl_paged_*, zl_pages_*) (no existing entry changed). */
 int32_t zl_version(void);
 
 /*
@@ -367,11 +371,234 @@ zl_status zl_varlen_attn_bwd_static(
     int32_t num_heads, int32_t head_dim, float softmax_scale,
     void* dq, void* dk, void* dv, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions.
+ *
+ * Each head's first rot_dim columns form rot_dim / 2 pairs (a, b), and every
+ * pair i of a token turns by its own angle:
+ *
+ *     angle = position[axis_i] * f_i
+ *     (a, b) -> magnitude * (a cos - b sin, a sin + b cos)
+ *
+ * Pair i is columns (i, i + rot_dim/2), or (2i, 2i+1) when interleaved; the
+ * columns from rot_dim on stay as they are.  The pairs are dealt out to
+ * n_axes position axes in order (one axis for a text or packed token order;
+ * frame, row and column for video latents); pair j of an axis that has d
+ * columns has f = base^(-2j/d), scaled for long contexts by `factor`:
+ *
+ *     without a ramp   f / factor
+ *     with a ramp      f * (w + (1 - w) / factor),
+ *                      w = clamp((length * f / 2pi - low) / (high - low), 0, 1)
+ *
+ * so that with a ramp the pairs that turn more than `high` times over
+ * `length` positions keep their frequency and those that turn less than `low`
+ * times take the scaled one.  Angles are exact to 2^-31 of a turn at every
+ * int32 position (fixed-point fractions of a turn), positions may be negative.
+ */
+#define ZL_ROPE_MAX_PAIRS 64
+#define ZL_ROPE_MAX_AXES 4
+
+/* A prepared plan: filled by zl_rope_init, then passed to any number of
+ * calls.  Plain data; the caller owns it and may copy it. */
+typedef struct {
+  int32_t head_dim;                       /* 64 or 128                            */
+  int32_t rot_dim;                        /* rotated columns, even, <= head_dim   */
+  int32_t interleaved;                    /* 0: halves, 1: neighbours             */
+  int32_t n_axes;                         /* 1 .. ZL_ROPE_MAX_AXES                */
+  int32_t pair_end[ZL_ROPE_MAX_AXES];     /* pairs of axes 0 .. a, cumulative     */
+  float magnitude;
+  int32_t reserved;
+  uint64_t step[ZL_ROPE_MAX_PAIRS];       /* f_i / 2pi turns, mod 1, times 2^64   */
+} zl_rope_t;
+
+/*
+ * Fills *plan.  axis_dims (host, n_axes entries): the rotated columns of each
+ * axis, even and >= 2, their sum rot_dim <= head_dim.  base > 1, factor > 0,
+ * magnitude finite and not 0.  ramp: NULL, or {low, high, length} with
+ * 0 <= low < high and length > 0.  Host only.
+ */
+zl_status zl_rope_init(zl_rope_t* plan, int32_t head_dim, int32_t interleaved, int32_t n_axes,
+                       const int32_t* axis_dims, double base, double factor, const double* ramp,
+                       double magnitude);
+
+/*
+ * Turns packed queries and keys: q [T, Hq, d] and k [T, Hk, d] in `dtype`
+ * (ZL_BF16 or ZL_FP32; float32 arithmetic, one rounding), with *_stride
+ * elements between tokens (>= heads * d, a multiple of 16 bytes; heads and
+ * columns contiguous, so that q and k may be parts of one projection's rows).
+ * num_kv_heads = 0 leaves k out.  positions: device int32, axis a of token t
+ * at [a * pos_stride + t].  An output may be its own input (same pointer and
+ * stride); otherwise no output may overlap an input.  One launch.
+ */
+zl_status zl_rope_fwd(const zl_rope_t* plan, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                      const int32_t* positions, int64_t pos_stride, int64_t tokens, int32_t num_heads,
+                      int32_t num_kv_heads, int32_t dtype, void* q_out, int64_t q_out_stride, void* k_out,
+                      int64_t k_out_stride, void* stream);
+
+/*
+ * Gradient of zl_rope_fwd: the transposed (negative) turn, applied to the
+ * gradients of its outputs.  Same arguments: q = the gradient of q_out, and so on.
+ */
+zl_status zl_rope_bwd(const zl_rope_t* plan, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                      const int32_t* positions, int64_t pos_stride, int64_t tokens, int32_t num_heads,
+                      int32_t num_kv_heads, int32_t dtype, void* q_out, int64_t q_out_stride, void* k_out,
+                      int64_t k_out_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key/value cache.
+ *
+ * One layer's cache is two pools of pages, k_pages and v_pages, each bf16
+ * [num_pages][Hk][page_size][d]: a page holds page_size consecutive tokens of
+ * one sequence, head by head.  Sequence s (a row of the tables, in the order
+ * of the batch) owns the pages page_table[s][0 .. ceil(kv_lens[s]/page_size)),
+ * and token j of it lies in page_table[s][j / page_size] at j % page_size.
+ * Entries past a sequence's pages, and pool rows past its length, are never
+ * used, whatever they hold.  page_refs[p] counts the sequences that hold page
+ * p (0: free); a shared page is always a full one.  All tables are DEVICE
+ * arrays: a captured graph replays with the lengths and pages of the moment.
+ *
+ * Kernels check every page number, slot and length that they read from the
+ * device: one out of range is left out (its token is not written, its keys
+ * are not attended), and the next zl_sync_check reports ZL_EPAGE.
+ */
+typedef struct {
+  void* k_pages;               /* [num_pages][num_kv_heads][page_size][head_dim] bf16 */
+  void* v_pages;
+  const int32_t* page_table;   /* [num_seqs][table_cols]                              */
+  const int32_t* kv_lens;      /* [num_seqs]: tokens, the call's new ones included    */
+  int32_t table_cols;          /* >= 1                                                */
+  int32_t num_pages;           /* >= 1                                                */
+  int32_t page_size;           /* 16, 32, 64, 128 or 256                              */
+  int32_t num_kv_heads;
+  int32_t head_dim;            /* 64 or 128                                           */
+  int32_t reserved;            /* 0                                                   */
+} zl_paged_cache_t;
+
+/*
+ * Writes a batch's new tokens into the cache: sequence s's tokens
+ * [cu_seqlens[s], cu_seqlens[s+1]) become its positions kv_lens[s] - n_s ..
+ * kv_lens[s] - 1.  k and v: bf16 [T, Hk, d] with k_stride / v_stride elements
+ * between tokens.  With a rope plan (NULL: none) the keys, and the queries
+ * q [T, Hq, d] -> q_out (q may be NULL, then num_heads is 0), are turned on
+ * the way, at the tokens' cache positions, or at `positions` (device, as for
+ * zl_rope_fwd) when given; a plan of more than one axis needs them.  The
+ * pages that the tokens go to must not be shared.  One launch per 640
+ * sequences.
+ */
+zl_status zl_paged_append(const zl_paged_cache_t* cache, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs, const zl_rope_t* plan,
+                          const int32_t* positions, int64_t pos_stride, const void* q, int64_t q_stride,
+                          int32_t num_heads, void* q_out, int64_t q_out_stride, void* stream);
+
+/*
+ * Workspace needed by zl_paged_attn for this batch, in bytes (0 when no
+ * sequence's keys are split).  Same argument rules as zl_paged_attn.
+ */
+zl_status zl_paged_attn_workspace_size(const int32_t* cu_seqlens_q, int32_t num_seqs, int32_t max_kv_len,
+                                       int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, size_t* bytes);
+
+/*
+ * Attention of a chunk of new tokens over the paged cache.  Sequence s has
+ * n_s = cu_seqlens_q[s+1] - cu_seqlens_q[s] queries (any number from 0 on;
+ * 1: a single new token) at positions p = kv_lens[s] - n_s + i.  Query p sees
+ * the keys j with
+ *
+ *     j < kv_lens[s],   j <= p if causal,   j > p - window if window > 0
+ *
+ * A query that sees none gets o = 0 and lse = -inf.  Query head h reads key
+ * head h / (num_heads / num_kv_heads).
+ *
+ * q [Tq, H, d] bf16, q_stride elements between tokens; o [Tq, H, d] bf16,
+ * lse [H, Tq] float32 (natural log, as zl_varlen_attn_fwd's, so that results
+ * over other keys can be joined with zl_lse_merge).  max_kv_len: an upper
+ * bound of kv_lens (a longer sequence is cut there and reported as ZL_EPAGE);
+ * the work split is chosen from it.  num_heads is a multiple of num_kv_heads
+ * and at most 128 times as many.  Scores, the running maximum and sum, and the
+ * output accumulate in float32; the probabilities are rounded to bf16 once for
+ * the tensor cores.  A value row that some query of its 128-key block sees
+ * must be finite for the block's other queries too (0 * inf).  Long caches
+ * with few query rows are split over the keys and joined in a second launch.
+ */
+zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_stride, const int32_t* cu_seqlens_q,
+                        int32_t num_seqs, int32_t max_kv_len, int32_t num_heads, float softmax_scale, int32_t causal,
+                        int32_t window, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The tables of a cache as the page operations change them. */
+typedef struct {
+  int32_t* page_table;         /* [slots][table_cols]                                 */
+  int32_t* kv_lens;            /* [slots]                                             */
+  int32_t* page_refs;          /* [num_pages]                                         */
+  int32_t slots;               /* 1 .. 8192                                           */
+  int32_t table_cols;          /* >= 1                                                */
+  int32_t num_pages;           /* >= 1                                                */
+  int32_t page_size;           /* 16, 32, 64, 128 or 256                              */
+} zl_page_tables_t;
+
+/*
+ * The pools whose pages are moved: group g's page p is the page_bytes (a
+ * multiple of 16) at base + g * group_stride + p * page_bytes.  The layers'
+ * key and value pools of one allocation are its groups.
+ */
+typedef struct {
+  void* base;
+  int64_t page_bytes;
+  int64_t group_stride;        /* bytes, >= num_pages * page_bytes                    */
+  int32_t groups;              /* >= 1                                                */
+  int32_t num_pages;           /* >= 1                                                */
+} zl_page_pool_t;
+
+/* Scratch of zl_pages_fork and zl_pages_compact, in bytes. */
+zl_status zl_pages_workspace_size(int32_t num_pages, size_t* bytes);
+
+/*
+ * Makes room for counts[s] (device, >= 0) new tokens in every slot: kv_lens
+ * grows by counts, and the pages that the new lengths need are taken from the
+ * free ones, lowest number first, in the order of slots and positions.
+ * *status (device): 0; or the number of pages that were lacking, or -1 for a
+ * negative count or a length that does not fit a table row; unless it is 0
+ * nothing was changed.
+ */
+zl_status zl_pages_extend(const zl_page_tables_t* tables, const int32_t* counts, int32_t* status, void* stream);
+
+/*
+ * Makes slot children[i] a copy of slot parents[i] (device, n of each): the
+ * child shares the parent's full pages, and a last page that is not full is
+ * copied into a free page of its own (lowest number first, in the order of i),
+ * in every group of the pool.  A parent may be forked any number of times; the
+ * children are distinct empty slots.  *status as for zl_pages_extend (-1: a
+ * slot out of range, a child that is not empty or named twice).
+ */
+zl_status zl_pages_fork(const zl_page_pool_t* pool, const zl_page_tables_t* tables, const int32_t* parents,
+                        const int32_t* children, int32_t n, int32_t* status, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * Empties the slots (device, n of them; one that is named twice or is empty
+ * already counts once): their pages lose a reference, their table entries
+ * become -1 and their lengths 0.  A page that no slot holds any more is free.
+ */
+zl_status zl_pages_free(const zl_page_tables_t* tables, const int32_t* slots, int32_t n, void* stream);
+
+/*
+ * Packs the pool: with L pages in use, those numbered L and up move to the
+ * free pages below L (both in ascending order), in every group of the pool,
+ * and the tables and counts follow.  *live (device) = L.
+ */
+zl_status zl_pages_compact(const zl_page_pool_t* pool, const zl_page_tables_t* tables, int32_t* live, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Copies page src[i] over page dst[i] (device, n pairs) in every group.  No
+ * page may be both a source and a target, nor a target twice.
+ */
+zl_status zl_pages_copy(const zl_page_pool_t* pool, const int32_t* src, const int32_t* dst, int32_t n, void* stream);
+
 /*
  * Synchronizes `stream`, then reports (and clears) any error a kernel of this
  * library flagged on the current device: ZL_ETIMEOUT when a bounded wait
  * inside a kernel ran out (the kernel stopped early and its outputs are
- * undefined), ZL_ECUDA for a CUDA error.  ZL_OK otherwise.
+ * undefined), ZL_EPAGE when a kernel of the paged cache left something out
+ * that its tables misplaced, ZL_ECUDA for a CUDA error.  ZL_OK otherwise.
  */
 zl_status zl_sync_check(void* stream);
 

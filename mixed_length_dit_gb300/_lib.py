@@ -20,6 +20,7 @@ ZL_EWORKSPACE = -4
 ZL_ECUDA = -5
 ZL_ETIMEOUT = -6
 ZL_ENODEVICE = -7
+ZL_EPAGE = -8
 
 ZL_BF16 = 0
 ZL_FP32 = 1
@@ -30,7 +31,9 @@ EXPORTS = (
     "zl_lse_merge", "zl_varlen_attn_bwd_workspace_size", "zl_varlen_attn_bwd", "zl_sync_check",
     "zl_launch_count", "zl_profile_begin", "zl_profile_end", "zl_varlen_attn_bwd_static",
     "zl_varlen_attn_fwd_ex", "zl_lse_merge_ex", "zl_varlen_attn_fwd_schedule", "zl_varlen_attn_bwd_schedule",
-    "zl_selftest_wait_timeout",
+    "zl_selftest_wait_timeout", "zl_rope_init", "zl_rope_fwd", "zl_rope_bwd", "zl_paged_append",
+    "zl_paged_attn_workspace_size", "zl_paged_attn", "zl_pages_workspace_size", "zl_pages_extend", "zl_pages_fork",
+    "zl_pages_free", "zl_pages_compact", "zl_pages_copy",
 )
 
 ZL_FWD_FUSED_MERGE = 1
@@ -58,6 +61,31 @@ class Tile(ctypes.Structure):
 class ProfileEntry(ctypes.Structure):
     """zl_profile_entry_t"""
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double)]
+
+
+class Rope(ctypes.Structure):
+    """zl_rope_t"""
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("pair_end", ctypes.c_int32 * 4), ("magnitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("step", ctypes.c_uint64 * 64)]
+
+
+class PagedCache(ctypes.Structure):
+    """zl_paged_cache_t"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "page_table", "kv_lens")] + \
+        [(n, ctypes.c_int32) for n in ("table_cols", "num_pages", "page_size", "num_kv_heads", "head_dim", "reserved")]
+
+
+class PageTables(ctypes.Structure):
+    """zl_page_tables_t"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("page_table", "kv_lens", "page_refs")] + \
+        [(n, ctypes.c_int32) for n in ("slots", "table_cols", "num_pages", "page_size")]
+
+
+class PagePool(ctypes.Structure):
+    """zl_page_pool_t"""
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("group_stride", ctypes.c_int64),
+                ("groups", ctypes.c_int32), ("num_pages", ctypes.c_int32)]
 
 
 class ZlError(RuntimeError):
@@ -122,6 +150,26 @@ def load() -> ctypes.CDLL:
     lib.zl_varlen_attn_bwd_static.restype = c_i32
     lib.zl_varlen_attn_bwd_static.argtypes = [vp, vp, vp, vp, vp, vp, i32p, i32p, c_i32, c_i32, c_i32,
                                               c_f32, vp, vp, vp, vp]
+    c_f64, f64p = ctypes.c_double, ctypes.POINTER(ctypes.c_double)
+    ropep, cachep = ctypes.POINTER(Rope), ctypes.POINTER(PagedCache)
+    tabp, poolp = ctypes.POINTER(PageTables), ctypes.POINTER(PagePool)
+    lib.zl_rope_init.argtypes = [ropep, c_i32, c_i32, c_i32, i32p, c_f64, c_f64, f64p, c_f64]
+    rope_args = [ropep, vp, c_i64, vp, c_i64, vp, c_i64, c_i64, c_i32, c_i32, c_i32, vp, c_i64, vp, c_i64, vp]
+    lib.zl_rope_fwd.argtypes = rope_args
+    lib.zl_rope_bwd.argtypes = rope_args
+    lib.zl_paged_append.argtypes = [cachep, vp, c_i64, vp, c_i64, i32p, c_i32, ropep, vp, c_i64, vp, c_i64, c_i32,
+                                    vp, c_i64, vp]
+    lib.zl_paged_attn_workspace_size.argtypes = [i32p, c_i32, c_i32, c_i32, c_i32, c_i32, szp]
+    lib.zl_paged_attn.argtypes = [cachep, vp, c_i64, i32p, c_i32, c_i32, c_i32, c_f32, c_i32, c_i32, vp, vp, vp, c_sz,
+                                  vp]
+    lib.zl_pages_workspace_size.argtypes = [c_i32, szp]
+    lib.zl_pages_extend.argtypes = [tabp, vp, vp, vp]
+    lib.zl_pages_fork.argtypes = [poolp, tabp, vp, vp, c_i32, vp, vp, c_sz, vp]
+    lib.zl_pages_free.argtypes = [tabp, vp, c_i32, vp]
+    lib.zl_pages_compact.argtypes = [poolp, tabp, vp, vp, c_sz, vp]
+    lib.zl_pages_copy.argtypes = [poolp, vp, vp, c_i32, vp]
+    for name in EXPORTS[-12:]:
+        getattr(lib, name).restype = c_i32
     _lib = lib
     return lib
 
@@ -135,8 +183,27 @@ def check(status: int, where: str) -> None:
         raise ZlError(status, where)
 
 
+class HostInt32:
+    """A host int32 array made once and passed to many calls (the cu_seqlens
+    of a batch that every layer shares)."""
+    __slots__ = ("array", "_n", "last")
+
+    def __init__(self, values):
+        self.array, self._n = int32_array(values)
+        self.last = int(self.array[self._n - 1]) if self._n else None
+
+    def __len__(self):
+        return self._n
+
+    def __iter__(self):
+        return iter(self.array[:self._n])
+
+
 def int32_array(values):
-    """Host int32 array for cu_seqlens (list, tuple, numpy or CPU tensor)."""
+    """Host int32 array for cu_seqlens (list, tuple, numpy or CPU tensor; an
+    array made by an earlier call is taken as it is)."""
+    if isinstance(values, HostInt32):
+        return values.array, len(values)
     vals = [int(x) for x in (values.tolist() if hasattr(values, "tolist") else values)]
     return (ctypes.c_int32 * max(1, len(vals)))(*vals), len(vals)
 

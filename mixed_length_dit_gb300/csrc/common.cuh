@@ -24,6 +24,7 @@ enum : uint32_t {
   ERR_TIMEOUT_SOFTMAX = 4u,
   ERR_TIMEOUT_OTHER = 8u,
   ERR_BAD_WORK = 16u,
+  ERR_BAD_PAGE = 32u,      // a page number, slot or length outside the cache (kErrBadPage)
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -37,6 +37,13 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int nh, int hd, 
 // adds into with TMA.
 bool make_map_acc(CUtensorMap* map, const float* base, int64_t rows, int nh, int hd, int box_rows);
 
+// The current device's SM count, once it has been found to be an sm_103 one
+// (asked once per device).
+zl_status device_sms(int* sms);
+
+// ZL_OK, or ZL_ECUDA with the runtime's error cleared.
+zl_status cuda_status(cudaError_t e);
+
 // One launch, counted and (while zl_profile_begin is active) bracketed by two
 // CUDA events on `stream`: prof_before creates and records the first event,
 // prof_after records the second and files the pair under `name`.

@@ -1,0 +1,140 @@
+// Internal interface between the host entries of the paged cache
+// (zl_paged.cpp) and its kernels.  Not part of the public C ABI.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "launch.h"
+#include "zl_attn.h"
+
+namespace zl {
+
+// Sequences whose token ranges one append launch carries in its parameters.
+constexpr int kAppendSeqs = kMaxSegs;
+
+// One launch of rotary positions.  As rope_fwd / rope_bwd it turns `q` and
+// `k` into `q_out` and `k_out` at given positions; as paged_append (`append`
+// set) the keys go into the cache's pages, the values beside them, and the
+// positions follow from the cache's lengths unless they are given.
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  const void* v;                // append only
+  void* q_out;
+  void* k_out;                  // append: the key pages
+  void* v_out;                  // append: the value pages
+  const int32_t* positions;     // [n_axes][pos_stride], or null (append)
+  int64_t pos_stride;
+  int64_t q_stride, k_stride, v_stride;          // elements between tokens
+  int64_t q_out_stride, k_out_stride;
+  int64_t token0;               // first token of this launch
+  int64_t tokens;               // tokens of this launch
+  int32_t nq, nk;               // query heads, key heads
+  int32_t head_dim;
+  int32_t inverse;              // turn by the negative angle (the transpose)
+  int32_t elem_bytes;           // 2: bf16, 4: float32
+  int32_t append;
+  int32_t skip_kept;            // q and k are turned in place: unrotated columns stay
+  // append: the cache
+  const int32_t* page_table;    // [seqs][table_cols]
+  const int32_t* kv_lens;       // [seqs]
+  int32_t table_cols;
+  int32_t num_pages;
+  int32_t page_shift;
+  int32_t n_seqs;               // sequences of this launch
+  int32_t seq0;                 // table row of the launch's first sequence
+  zl_rope_t rope;
+  int32_t cu[kAppendSeqs + 1];  // append: first token of each sequence of the launch
+};
+static_assert(sizeof(RopeArgs) <= 32764, "rotary arguments exceed the kernel parameter space");
+
+// One sequence's queries in a paged attention launch.
+struct PagedSeg {
+  int32_t seq;       // row of the page table and of the lengths
+  int32_t q_row0;    // packed row of its first query
+  int32_t q_len;     // queries, >= 1
+};
+
+struct PagedAttnArgs {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* page_table;
+  const int32_t* kv_lens;
+  void* o;                      // [Tq][H][d] bf16
+  float* lse;                   // [H][lse_stride]
+  int64_t q_stride;
+  int64_t lse_stride;           // Tq
+  int64_t token0;               // first query row of this launch
+  int32_t tokens;               // query rows of this launch
+  int32_t num_heads;
+  int32_t num_kv_heads;
+  int32_t group;                // query heads of a key head
+  int32_t table_cols;
+  int32_t num_pages;
+  int32_t page_shift;
+  int32_t max_kv_len;
+  int32_t causal;
+  int32_t window;
+  float scale_log2;             // softmax scale * log2(e)
+  int32_t n_segs;
+  PagedSeg segs[kMaxSegs];
+};
+static_assert(sizeof(PagedAttnArgs) <= 32764, "paged attention arguments exceed the kernel parameter space");
+
+// A pool of pages seen by the kernels that move whole pages.
+struct PagePool {
+  uint8_t* base;                // groups x num_pages x page_bytes
+  int64_t page_bytes;           // multiple of 16
+  int64_t group_stride;         // bytes between groups
+  int32_t groups;
+  int32_t num_pages;
+};
+
+struct PageTable {
+  int32_t* table;               // [slots][cols]
+  int32_t* kv_lens;             // [slots]
+  int32_t* refs;                // [num_pages]
+  int32_t slots;
+  int32_t cols;
+  int32_t num_pages;
+  int32_t page_shift;
+};
+
+// Most slots a page operation handles (their page counts are scanned in one
+// CTA's shared memory).
+constexpr int kMaxSlots = 8192;
+
+// Scratch of fork and compact, in int32 words: a header, per-fork lengths,
+// the list of page moves and, for compact, the page renumbering.
+constexpr int kPageHeader = 64;
+inline size_t pages_workspace_words(int64_t num_pages) {
+  return kPageHeader + kMaxSlots + 3 * static_cast<size_t>(num_pages);
+}
+
+cudaError_t launch_rope(const RopeArgs& args, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_attn(int head_dim, const PagedAttnArgs& args, cudaStream_t stream);
+cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const int32_t* dst, int32_t n, int num_sms,
+                              cudaStream_t stream);
+cudaError_t launch_pages_extend(const PageTable& t, const int32_t* counts, int32_t* status, cudaStream_t stream);
+cudaError_t launch_pages_free(const PageTable& t, const int32_t* slots, int32_t n, cudaStream_t stream);
+cudaError_t launch_pages_fork_plan(const PageTable& t, const int32_t* parents, const int32_t* children, int32_t n,
+                                   int32_t* ws, int32_t* status, cudaStream_t stream);
+cudaError_t launch_pages_fork_move(const PagePool& pool, const PageTable& t, const int32_t* parents,
+                                   const int32_t* children, int32_t n, const int32_t* ws, int num_sms,
+                                   cudaStream_t stream);
+cudaError_t launch_pages_compact_plan(const PageTable& t, int32_t* ws, int32_t* live, cudaStream_t stream);
+cudaError_t launch_pages_compact_move(const PagePool& pool, const PageTable& t, const int32_t* ws, int num_sms,
+                                      cudaStream_t stream);
+
+// Error words of these kernels (read and cleared; synchronous), and all of
+// them in one (0xFFFFFFFF: a CUDA call failed).  kErrBadPage is the bit of
+// page numbers, slots and lengths outside the cache.
+constexpr uint32_t kErrBadPage = 32u;
+uint32_t rope_take_error();
+uint32_t pages_take_error();
+uint32_t paged_attn_take_error();
+uint32_t paged_take_error();
+
+}  // namespace zl

@@ -1,0 +1,256 @@
+// Rotary positions of packed queries and keys, and the append of new tokens
+// to a paged cache, which turns them on the way.
+//
+//     angle = pos * f,   (a, b) -> m (a cos - b sin, a sin + b cos)
+//
+// Memory-bound: every element is read and written once, with three float32
+// operations in between.  What would cost more than the traffic is the angle,
+// so a block computes the cosines and sines of its tokens once, into shared
+// memory, and all of their heads use them.  The angle itself is a 64-bit
+// fixed-point fraction of a turn, pos * step mod 2^64: exact in integers at
+// any position, where a float32 product loses the fraction after 2^24 turns'
+// worth of bits and a float64 one would run on a unit that this GPU has few
+// of.  The top 32 bits go to sincospi.
+//
+// A thread turns one unit at a time: 16 columns for bf16, 8 for float32, as
+// two 16-byte loads and stores (the two halves' pieces, or two neighbours), so
+// a head's units are consecutive threads and a token's heads are one run.
+// Plans whose pairs do not fill such units take units of one pair.
+#include "common.cuh"
+#include "paged.h"
+
+namespace zl {
+namespace {
+
+__device__ uint32_t g_rope_err;
+
+constexpr int kRopeThreads = 256;
+constexpr int kTokensMax = 4;                  // tokens of a block
+
+template <typename T>
+struct Vec16;
+template <>
+struct Vec16<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = bf16x2_to_float2(w[i]);
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  }
+};
+template <>
+struct Vec16<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void load(const float* p, float (&x)[4]) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&x)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+};
+
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// One unit of a head: pairs [pair0, pair0 + N/...) turned, or columns kept.
+// VECTOR: units of 16 columns (bf16) / 8 columns (float32); else one pair.
+template <typename T, bool VECTOR, bool INTERLEAVED>
+__device__ __forceinline__ void turn_unit(const T* src, T* dst, int unit, int half,
+                                          const float2* cs, bool skip_kept) {
+  if constexpr (VECTOR) {
+    constexpr int N = Vec16<T>::N;             // pairs of a unit
+    float a[N], b[N];
+    if (unit * N >= half) {                    // columns past rot_dim
+      if (skip_kept) return;
+      const uint4 x = *reinterpret_cast<const uint4*>(src + 2 * N * unit);
+      const uint4 y = *reinterpret_cast<const uint4*>(src + 2 * N * unit + N);
+      *reinterpret_cast<uint4*>(dst + 2 * N * unit) = x;
+      *reinterpret_cast<uint4*>(dst + 2 * N * unit + N) = y;
+      return;
+    }
+    const int c0 = INTERLEAVED ? 2 * N * unit : N * unit;
+    const int c1 = INTERLEAVED ? c0 + N : c0 + half;
+    Vec16<T>::load(src + c0, a);
+    Vec16<T>::load(src + c1, b);
+    const float4* w4 = reinterpret_cast<const float4*>(cs + N * unit);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float4 w = w4[i / 2];              // cos, sin of two pairs
+      if constexpr (INTERLEAVED) {
+        // pairs i, i+1 of the unit: columns 2i .. 2i+3 of the 2N loaded ones
+        float* x = 2 * i < N ? a + 2 * i : b + 2 * i - N;
+        const float x0 = x[0], x1 = x[1], x2 = x[2], x3 = x[3];
+        x[0] = x0 * w.x - x1 * w.y;
+        x[1] = x0 * w.y + x1 * w.x;
+        x[2] = x2 * w.z - x3 * w.w;
+        x[3] = x2 * w.w + x3 * w.z;
+      } else {
+        const float a0 = a[i], b0 = b[i], a1 = a[i + 1], b1 = b[i + 1];
+        a[i] = a0 * w.x - b0 * w.y;
+        b[i] = a0 * w.y + b0 * w.x;
+        a[i + 1] = a1 * w.z - b1 * w.w;
+        b[i + 1] = a1 * w.w + b1 * w.z;
+      }
+    }
+    Vec16<T>::store(dst + c0, a);
+    Vec16<T>::store(dst + c1, b);
+  } else {
+    const bool kept = unit >= half;
+    if (kept && skip_kept) return;
+    const int c0 = kept || INTERLEAVED ? 2 * unit : unit;
+    const int c1 = kept || INTERLEAVED ? c0 + 1 : c0 + half;
+    const float a = as_float(src[c0]), b = as_float(src[c1]);
+    const float2 w = kept ? make_float2(1.f, 0.f) : cs[unit];
+    put(dst + c0, kept ? a : a * w.x - b * w.y);
+    put(dst + c1, kept ? b : a * w.y + b * w.x);
+  }
+}
+
+template <typename T, bool VECTOR, bool INTERLEAVED, bool APPEND>
+__global__ void __launch_bounds__(kRopeThreads)
+rope_kernel(const __grid_constant__ RopeArgs a, int tokens_per_block, int heads_per_block) {
+  __shared__ __align__(16) float2 cs[kTokensMax][ZL_ROPE_MAX_PAIRS];
+  __shared__ int32_t pos_of[kTokensMax];       // append: position in the sequence
+  __shared__ int64_t page_row[kTokensMax];     // append: first row of the token's page, + its row; -1: left out
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(tokens_per_block), a.tokens - t0));
+  const int half = a.rope.rot_dim / 2;
+
+  if constexpr (APPEND) {
+    if (threadIdx.x < nt) {
+      const int64_t t = a.token0 + t0 + threadIdx.x;
+      int lo = 0, hi = a.n_seqs - 1;           // the last sequence that starts at or before t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      const int64_t seq = a.seq0 + lo;
+      const int n = a.cu[lo + 1] - a.cu[lo];
+      const int len = a.kv_lens[seq];
+      const int64_t p = static_cast<int64_t>(len) - n + (t - a.cu[lo]);
+      int64_t row = -1;
+      if (p >= 0 && (p >> a.page_shift) < a.table_cols) {
+        const int page = a.page_table[seq * a.table_cols + (p >> a.page_shift)];
+        if (page >= 0 && page < a.num_pages)
+          row = ((static_cast<int64_t>(page) * a.nk) << a.page_shift) + (p & ((1 << a.page_shift) - 1));
+      }
+      if (row < 0) atomicOr(&g_rope_err, ERR_BAD_PAGE);
+      page_row[threadIdx.x] = row;
+      pos_of[threadIdx.x] = static_cast<int32_t>(p);
+    }
+    __syncthreads();
+  }
+  for (int x = threadIdx.x; x < nt * half; x += kRopeThreads) {
+    const int tl = x / half, i = x - tl * half;
+    int axis = 0;
+    while (axis < a.rope.n_axes - 1 && i >= a.rope.pair_end[axis]) ++axis;
+    int64_t p;
+    if (APPEND && !a.positions)
+      p = pos_of[tl];
+    else
+      p = a.positions[axis * a.pos_stride + a.token0 + t0 + tl];
+    const uint64_t phase = static_cast<uint64_t>(p) * a.rope.step[i];
+    // signed fraction of a turn in the top 32 bits; in half turns for sincospi
+    const float x2 = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;
+    float s, c;
+    sincospif(x2, &s, &c);
+    const float m = a.rope.magnitude;
+    cs[tl][i] = make_float2(c * m, (a.inverse ? -s : s) * m);
+  }
+  __syncthreads();
+
+  constexpr int kUnitCols = VECTOR ? 2 * Vec16<T>::N : 2;
+  const int units = a.head_dim / kUnitCols;    // of a head; a power of two
+  const int ushift = 31 - __clz(units);
+  const int heads = a.nq + (APPEND ? 2 : 1) * a.nk;
+  const int h0 = blockIdx.y * heads_per_block;
+  const int h1 = min(heads, h0 + heads_per_block);
+  for (int tl = 0; tl < nt; ++tl) {
+    const int64_t t = a.token0 + t0 + tl;
+    const T* q = static_cast<const T*>(a.q) + t * a.q_stride;
+    const T* k = static_cast<const T*>(a.k) + t * a.k_stride;
+    T* qo = static_cast<T*>(a.q_out) + t * a.q_out_stride;
+    for (int x = (h0 << ushift) + threadIdx.x; x < (h1 << ushift); x += kRopeThreads) {
+      const int h = x >> ushift, u = x & (units - 1);
+      if (h < a.nq) {
+        turn_unit<T, VECTOR, INTERLEAVED>(q + h * a.head_dim, qo + h * a.head_dim, u, half, cs[tl], a.skip_kept);
+      } else if constexpr (!APPEND) {
+        const int hk = h - a.nq;
+        turn_unit<T, VECTOR, INTERLEAVED>(k + hk * a.head_dim,
+                                          static_cast<T*>(a.k_out) + t * a.k_out_stride + hk * a.head_dim, u, half,
+                                          cs[tl], a.skip_kept);
+      } else {
+        const int64_t row = page_row[tl];
+        if (row < 0) continue;
+        const bool is_v = h >= a.nq + a.nk;
+        const int hk = h - a.nq - (is_v ? a.nk : 0);
+        const int64_t off = (row + (static_cast<int64_t>(hk) << a.page_shift)) * a.head_dim;
+        if (is_v)
+          turn_unit<T, VECTOR, INTERLEAVED>(static_cast<const T*>(a.v) + t * a.v_stride + hk * a.head_dim,
+                                            static_cast<T*>(a.v_out) + off, u, 0, cs[tl], false);
+        else
+          turn_unit<T, VECTOR, INTERLEAVED>(k + hk * a.head_dim, static_cast<T*>(a.k_out) + off, u, half, cs[tl],
+                                            false);
+      }
+    }
+  }
+}
+
+template <typename T, bool VECTOR, bool APPEND>
+void launch_il(const RopeArgs& a, dim3 grid, int tpb, int hpb, cudaStream_t stream) {
+  if (a.rope.interleaved)
+    rope_kernel<T, VECTOR, true, APPEND><<<grid, kRopeThreads, 0, stream>>>(a, tpb, hpb);
+  else
+    rope_kernel<T, VECTOR, false, APPEND><<<grid, kRopeThreads, 0, stream>>>(a, tpb, hpb);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
+  const int heads = a.nq + (a.append ? 2 : 1) * a.nk;
+  if (a.tokens == 0 || heads == 0) return cudaSuccess;
+  const int per_unit = a.elem_bytes == 2 ? 8 : 4;
+  const bool vec = (a.rope.rot_dim / 2) % per_unit == 0;
+  const int units = a.head_dim / (vec ? 2 * per_unit : 2);
+  // Few tokens: one a block, and its heads dealt out to more blocks (each
+  // block makes the token's cosines again) until the SMs have a block or two.
+  const int tpb = a.tokens >= int64_t(num_sms) * 4 * kTokensMax ? kTokensMax : 1;
+  const int64_t blocks = (a.tokens + tpb - 1) / tpb;
+  const int fill = (kRopeThreads + units - 1) / units;       // heads that fill a block's threads once
+  int hpb = heads;
+  while (hpb > fill && blocks * ((heads + hpb - 1) / hpb) < 2 * num_sms) hpb = (hpb + 1) / 2;
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + hpb - 1) / hpb));
+  if (a.elem_bytes == 2) {
+    if (a.append)
+      vec ? launch_il<__nv_bfloat16, true, true>(a, grid, tpb, hpb, stream)
+          : launch_il<__nv_bfloat16, false, true>(a, grid, tpb, hpb, stream);
+    else
+      vec ? launch_il<__nv_bfloat16, true, false>(a, grid, tpb, hpb, stream)
+          : launch_il<__nv_bfloat16, false, false>(a, grid, tpb, hpb, stream);
+  } else {
+    vec ? launch_il<float, true, false>(a, grid, tpb, hpb, stream)
+        : launch_il<float, false, false>(a, grid, tpb, hpb, stream);
+  }
+  return cudaGetLastError();
+}
+
+uint32_t rope_take_error() {
+  uint32_t v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_rope_err, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
+  if (v != 0) cudaMemcpyToSymbol(g_rope_err, &zero, sizeof(zero));
+  return v;
+}
+
+}  // namespace zl

@@ -25,6 +25,7 @@
 
 #include "host.h"
 #include "launch.h"
+#include "paged.h"
 #include "zl_attn.h"
 
 namespace {
@@ -35,6 +36,8 @@ using zl::kBlockM;
 using zl::kBlockN;
 using zl::kMaxSegs;
 using zl::aligned16;
+using zl::cuda_status;
+using zl::device_sms;
 using zl::launch_counted;
 using zl::make_map;
 using zl::make_map_acc;
@@ -58,33 +61,6 @@ struct DevInfo {
 };
 std::mutex g_dev_mu;
 DevInfo g_dev[128];
-
-zl_status device_sms(int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return ZL_ENODEVICE;
-  }
-  if (dev < 0 || dev >= 128) return ZL_ENODEVICE;
-  std::lock_guard<std::mutex> lock(g_dev_mu);
-  DevInfo& d = g_dev[dev];
-  if (d.status == 1) {
-    int major = 0, minor = 0, n = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-      cudaGetLastError();
-      d.status = ZL_ECUDA;
-    } else if (major != 10 || minor != 3) {
-      d.status = ZL_ENODEVICE;   // the kernels are built for sm_103a only
-    } else {
-      d.sms = n;
-      d.status = ZL_OK;
-    }
-  }
-  *sms = d.sms;
-  return static_cast<zl_status>(d.status);
-}
 
 // ------------------------------------------------------------------ validation
 struct SplitSeq {
@@ -341,17 +317,44 @@ bool fill_args(FwdArgs* args, const std::vector<Segment>& segs, size_t first, si
   return true;
 }
 
-zl_status cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return ZL_OK;
-  cudaGetLastError();
-  return ZL_ECUDA;
-}
-
 }  // namespace
 
 namespace zl {
 
 void note_launch() { g_launches.fetch_add(1); }
+
+zl_status device_sms(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return ZL_ENODEVICE;
+  }
+  if (dev < 0 || dev >= 128) return ZL_ENODEVICE;
+  std::lock_guard<std::mutex> lock(g_dev_mu);
+  DevInfo& d = g_dev[dev];
+  if (d.status == 1) {
+    int major = 0, minor = 0, n = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      d.status = ZL_ECUDA;
+    } else if (major != 10 || minor != 3) {
+      d.status = ZL_ENODEVICE;   // the kernels are built for sm_103a only
+    } else {
+      d.sms = n;
+      d.status = ZL_OK;
+    }
+  }
+  *sms = d.sms;
+  return static_cast<zl_status>(d.status);
+}
+
+zl_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return ZL_OK;
+  cudaGetLastError();
+  return ZL_ECUDA;
+}
 
 zl_status check_batch(const int32_t* cu_q, const int32_t* cu_k, int32_t num_seqs, int32_t num_heads,
                       int32_t head_dim, int64_t* tq, int64_t* tk) {
@@ -467,11 +470,12 @@ const char* zl_status_string(int32_t status) {
     case ZL_ECUDA: return "CUDA error";
     case ZL_ETIMEOUT: return "a kernel gave up a bounded wait";
     case ZL_ENODEVICE: return "no sm_103 CUDA device";
+    case ZL_EPAGE: return "a page number, slot or length lies outside the paged cache";
     default: return "unknown status";
   }
 }
 
-int32_t zl_version(void) { return (2 << 16) | 1; }
+int32_t zl_version(void) { return (2 << 16) | 2; }
 
 int64_t zl_launch_count(void) { return g_launches.load(); }
 
@@ -853,8 +857,10 @@ zl_status zl_sync_check(void* stream) {
   const uint32_t ef = zl::fwd_take_error();
   const uint32_t eb = zl::bwd_take_error();
   const uint32_t es = zl::selftest_take_error();
-  if (ef == 0xFFFFFFFFu || eb == 0xFFFFFFFFu || es == 0xFFFFFFFFu) return ZL_ECUDA;
-  if (ef != 0 || eb != 0 || es != 0) return ZL_ETIMEOUT;
+  const uint32_t ec = zl::paged_take_error();
+  if (ef == 0xFFFFFFFFu || eb == 0xFFFFFFFFu || es == 0xFFFFFFFFu || ec == 0xFFFFFFFFu) return ZL_ECUDA;
+  if (ef != 0 || eb != 0 || es != 0 || (ec & ~static_cast<uint32_t>(zl::kErrBadPage)) != 0) return ZL_ETIMEOUT;
+  if (ec != 0) return ZL_EPAGE;
   return ZL_OK;
 }
 

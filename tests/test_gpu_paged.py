@@ -1,0 +1,406 @@
+"""The paged cache's append and attention on the GPU against the float64
+definition.
+
+Tolerance of an output element o with reach r = sum_j p_j |v_j| (derived, per
+element): each probability is rounded to bf16 once (2^-8 of it at most), so the
+sum is off by 2^-8 r; the result is rounded once, 2^-8 |o|; the scores' float32
+sums (at most 128 terms of products exact in float32, truncated at worst:
+128 * 2^-23 * sum|q_i k_i| * scale, under 2e-4 for the inputs here) and the
+exponential (2^-22) move every probability by under 2^-11 of it, numerator and
+denominator both.  LSE: the scores' 2e-4, and 2^-20 of its value.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mixed_length_dit_gb300 as zl
+from oracle import paged_f64 as ref
+from _helpers import f64
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+class Batch:
+    """New tokens and a cache in use: pages in any order, pool rows and table
+    entries that belong to nobody filled with what must not matter."""
+
+    def __init__(self, new, lens, heads, kv_heads, hd, page, seed=0, spare_cols=2, fill=float("nan")):
+        rng = np.random.default_rng(seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.new, self.lens, self.hd, self.page = list(new), list(lens), hd, page
+        self.cu = [0]
+        for n in new:
+            self.cu.append(self.cu[-1] + n)
+        used = [-(-n // page) for n in lens]
+        self.num_pages = sum(used) + 3
+        numbers = rng.permutation(self.num_pages)
+        cols = max(used) + spare_cols
+        self.table = np.full((len(lens), cols), -1, dtype=np.int32)
+        at = 0
+        for s, n in enumerate(used):
+            self.table[s, :n] = numbers[at:at + n]
+            self.table[s, n:] = rng.integers(-5, self.num_pages + 5, cols - n)      # past the sequence: anything
+            at += n
+        shape = (self.num_pages, kv_heads, page, hd)
+        self.k_pages, self.v_pages = (torch.randn(shape, generator=g, device="cuda").to(BF16) for _ in range(2))
+        for s, n in enumerate(lens):
+            if n % page:
+                for p in (self.k_pages, self.v_pages):
+                    p[int(self.table[s, n // page]), :, n % page:] = fill
+        for p in numbers[at:]:
+            self.k_pages[int(p)] = fill
+            self.v_pages[int(p)] = fill
+        self.q = torch.randn((self.cu[-1], heads, hd), generator=g, device="cuda").to(BF16)
+        self.dtable = torch.tensor(self.table, device="cuda")
+        self.dlens = torch.tensor(self.lens, dtype=torch.int32, device="cuda")
+
+    def run(self, q=None, most=None, **kw):
+        q = self.q if q is None else q
+        return zl.paged_attn(q, self.k_pages, self.v_pages, self.dtable, self.dlens, self.cu,
+                             max(self.lens) if most is None else most, **kw)
+
+    def check(self, o, lse, **kw):
+        want, want_lse, reach = ref.paged_attn(f64(self.q), f64(self.k_pages), f64(self.v_pages), self.table, self.lens,
+                                               self.cu, **kw)
+        tol = (2.0 ** -8 + 2.0 ** -11) * reach + 2.0 ** -8 * np.abs(want)
+        err = np.abs(f64(o) - want)
+        assert np.all(err <= tol), float((err - tol).max())
+        none = np.isneginf(want_lse)
+        assert np.array_equal(np.isneginf(f64(lse)), none)
+        fin = ~none
+        err = np.abs(f64(lse)[fin] - want_lse[fin])
+        assert np.all(err <= 2e-4 + 2.0 ** -20 * np.abs(want_lse[fin])), float(err.max())
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (4, 4), (8, 1), (10, 2), (6, 2), (40, 8)])
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_single_tokens(heads, kv_heads, hd, page):
+    b = Batch([1] * 6, [1, 2, 127, 128, 129, 700], heads, kv_heads, hd, page)
+    o, lse = b.run()
+    zl.sync_check()
+    b.check(o, lse)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads,kv_heads,hd,page", [(2, 2, 64, 16), (6, 2, 128, 32), (10, 2, 128, 128), (7, 1, 64, 64)])
+def test_chunks(heads, kv_heads, hd, page, causal):
+    new = [130, 1, 300, 0, 37, 128, 2, 257]
+    lens = [130, 500, 431, 90, 300, 1000, 64, 258]
+    b = Batch(new, lens, heads, kv_heads, hd, page, seed=1)
+    o, lse = b.run(causal=causal)
+    zl.sync_check()
+    b.check(o, lse, causal=causal)
+
+
+@pytest.mark.parametrize("causal,window", [(True, 1), (True, 7), (True, 128), (True, 200), (False, 33), (False, 129),
+                                           (True, 10 ** 6)])
+def test_windows(causal, window):
+    b = Batch([1, 260, 33, 5], [900, 500, 33, 389], 6, 2, 64, 32, seed=2)
+    o, lse = b.run(causal=causal, window=window)
+    zl.sync_check()
+    b.check(o, lse, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("group", [3, 5, 7, 12, 48, 100, 128])
+def test_many_heads_of_one_key_head(group):
+    b = Batch([1, 9, 40], [300, 140, 44], group, 1, 64, 16, seed=3)
+    o, lse = b.run()
+    zl.sync_check()
+    b.check(o, lse)
+
+
+def test_long_cache_is_split_and_joined():
+    b = Batch([1, 3, 1], [20011, 513, 6000], 8, 2, 128, 64, seed=4)
+    for kw in ({}, {"window": 4097}, {"causal": False}):
+        o, lse = b.run(**kw)
+        zl.sync_check()
+        b.check(o, lse, **kw)
+    # a larger bound of the lengths changes the split, not the result
+    o, lse = b.run(most=b.dtable.shape[1] * b.page)
+    b.check(o, lse)
+
+
+def test_few_chunk_rows_over_a_long_cache():
+    b = Batch([140, 5], [9000, 333], 2, 1, 64, 16, seed=5)
+    for kw in ({}, {"causal": False}, {"window": 2500}):
+        o, lse = b.run(**kw)
+        zl.sync_check()
+        b.check(o, lse, **kw)
+
+
+def test_rows_that_see_nothing():
+    """Lengths shorter than the chunk (positions below zero) and empty ones."""
+    b = Batch([5, 3, 1, 200], [2, 0, 0, 150], 4, 2, 64, 16, seed=6)
+    for kw in ({}, {"causal": False}, {"window": 2}):
+        o, lse = b.run(**kw)
+        zl.sync_check()
+        b.check(o, lse, **kw)
+        assert torch.isfinite(o.float()).all()
+    assert torch.all(o[5:9] == 0)
+
+
+@pytest.mark.parametrize("fill", [float("inf"), float("-inf"), 3e38])
+def test_what_belongs_to_nobody_does_not_matter(fill):
+    b = Batch([1, 40], [77, 100], 4, 2, 128, 64, seed=7, fill=fill)
+    o, lse = b.run()
+    zl.sync_check()
+    b.check(o, lse)
+
+
+def test_non_finite_keys_past_the_mask():
+    """A key that a query does not see may hold anything."""
+    b = Batch([60], [300], 4, 2, 64, 16, seed=8)
+    last = f64(b.k_pages)
+    o1, l1 = b.run()
+    b.k_pages[int(b.table[0, 299 // 16]), :, 299 % 16] = float("nan")    # the newest token's key
+    o2, l2 = b.run()
+    zl.sync_check()
+    assert torch.equal(o1[:59], o2[:59]) and torch.equal(l1[:, :59], l2[:, :59])
+    assert np.isfinite(last[int(b.table[0, 0])]).all()
+
+
+def test_large_scores():
+    """Scores of thousands, whose running maximum jumps block by block."""
+    b = Batch([1, 50], [700, 700], 4, 2, 64, 16, seed=9)
+    b.q *= 64
+    o, lse = b.run(softmax_scale=1.0)
+    zl.sync_check()
+    want, want_lse, _ = ref.paged_attn(f64(b.q), f64(b.k_pages), f64(b.v_pages), b.table, b.lens, b.cu, scale=1.0)
+    # scores reach 64 * 64 * 4: their sums' 64 * 2^-23 * sum|q k| (about 3,300) is 0.03 of a logit
+    assert np.abs(f64(lse) - want_lse).max() <= 0.03 + 2.0 ** -20 * np.abs(want_lse).max()
+    assert np.abs(f64(o) - want).max() <= 0.07 * np.abs(f64(b.v_pages)[b.table[0, :43]]).max() + 2.0 ** -7 * np.abs(want).max()
+
+
+def test_queries_inside_wider_rows_and_given_buffers():
+    b = Batch([1, 200, 7], [50, 260, 130], 6, 2, 128, 32, seed=10)
+    o1, l1 = b.run()
+    rows = torch.randn((b.cu[-1], 10, 128), device="cuda").to(BF16)
+    rows[:, 2:8] = b.q
+    out = torch.full_like(o1, 9.0)
+    lse = torch.full_like(l1, 9.0)
+    ws = zl.alloc_workspace(zl.paged_attn_workspace_bytes(b.cu, max(b.lens), 6, 2, 128), "cuda")
+    o2, l2 = b.run(q=rows[:, 2:8], out=out, lse=lse, workspace=ws)
+    assert o2 is out and l2 is lse and torch.equal(o1, out) and torch.equal(l1, lse)
+
+
+def test_small_workspace_is_refused():
+    b = Batch([1], [20000], 2, 1, 64, 64, seed=11)
+    need = zl.paged_attn_workspace_bytes(b.cu, 20000, 2, 1, 64)
+    if need == 0:
+        pytest.skip("nothing is split here")
+    with pytest.raises(zl.ZlError) as e:
+        b.run(workspace=torch.empty(need - 256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == -4
+
+
+def test_more_sequences_than_one_launch_holds():
+    rng = np.random.default_rng(12)
+    lens = [int(x) for x in rng.integers(1, 90, 700)]
+    b = Batch([1] * 700, lens, 2, 1, 64, 16, seed=12)
+    o, lse = b.run()
+    zl.sync_check()
+    b.check(o, lse)
+
+
+def test_same_bits_every_time():
+    b = Batch([1, 300, 2], [5000, 900, 2500], 8, 2, 128, 16, seed=13)
+    o, lse = b.run()
+    for _ in range(3):
+        o2, l2 = b.run()
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
+def test_pages_and_lengths_out_of_range_are_left_out_and_reported():
+    b = Batch([1, 1, 4], [100, 90, 60], 4, 2, 64, 16, seed=14)
+    b.dtable[1, 2] = b.num_pages
+    b.run()
+    with pytest.raises(zl.ZlError) as e:
+        zl.sync_check()
+    assert e.value.status == -8
+    b.dtable[1, 2] = -7
+    o, lse = b.run()
+    with pytest.raises(zl.ZlError):
+        zl.sync_check()
+    b.dtable[1, 2] = int(b.table[1, 2])
+    b.dlens[1] = 5000                     # past the bound that was given
+    o, lse = b.run()
+    with pytest.raises(zl.ZlError):
+        zl.sync_check()
+    b.dlens[1] = -3
+    o, lse = b.run()
+    with pytest.raises(zl.ZlError):
+        zl.sync_check()
+    b.dlens[1] = 90
+    o, lse = b.run()
+    zl.sync_check()
+    b.check(o, lse)
+
+
+def test_graph_replays_with_the_lengths_and_pages_of_the_moment():
+    b = Batch([1, 1, 1], [40, 2500, 333], 8, 2, 128, 16, seed=15, spare_cols=6)
+    most = b.dtable.shape[1] * 16
+    out, lse = torch.zeros_like(b.q), torch.zeros((8, 3), device="cuda")
+    ws = zl.alloc_workspace(zl.paged_attn_workspace_bytes(b.cu, most, 8, 2, 128), "cuda")
+    b.run(most=most, out=out, lse=lse, workspace=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.run(most=most, out=out, lse=lse, workspace=ws)
+    for lens in ([40, 2500, 333], [33, 17, 330], [1, 1290, 16]):
+        b.lens = lens
+        b.dlens.copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        zl.sync_check()
+        b.check(out, lse)
+
+
+def test_two_streams_at_once():
+    bs = [Batch([1, 90], [3000 + 500 * i, 300], 8, 2, 128, 16, seed=20 + i) for i in range(2)]
+    want = [b.run() for b in bs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in bs]
+    got = []
+    for _ in range(5):
+        for b, s in zip(bs, streams):
+            got.append(b.run(stream=s))
+    torch.cuda.synchronize()
+    for i, (o, lse) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("hd,heads,kv_heads,page,axes,il", [
+    (64, 4, 2, 16, (64,), False), (128, 10, 2, 64, (128,), True), (128, 3, 3, 256, (64,), False), (64, 2, 1, 32, (6,), True),
+])
+def test_append_turns_and_writes(hd, heads, kv_heads, page, axes, il):
+    new, lens = [1, 40, 0, 200, 3], [90, 40, 5, 333, 259]
+    b = Batch(new, lens, heads, kv_heads, hd, page, seed=30, fill=5.0)
+    g = torch.Generator(device="cuda").manual_seed(31)
+    rows = torch.randn((b.cu[-1], kv_heads * 2, hd), generator=g, device="cuda").to(BF16)
+    k, v = rows[:, :kv_heads], rows[:, kv_heads:]
+    plan = zl.RopePlan(hd, axes=axes, interleaved=il)
+    k0, v0 = f64(b.k_pages), f64(b.v_pages)
+    q = zl.paged_append(k, v, b.k_pages, b.v_pages, b.dtable, b.dlens, b.cu, q=b.q, rope=plan)
+    zl.sync_check()
+    pos = np.concatenate([np.arange(n - m, n) for m, n in zip(new, lens)])[None]
+    turned = ref.rope(f64(k), pos, axes, interleaved=il)
+    want_v = ref.append(v0, b.table, lens, b.cu, f64(v))
+    assert np.array_equal(f64(b.v_pages), want_v)
+    want_k = ref.append(k0, b.table, lens, b.cu, turned)
+    tol = 2.0 ** -8 * np.abs(want_k) + 2.0 ** -21 * ref.append(0 * k0, b.table, lens, b.cu, ref.rope_reach(f64(k), axes, il))
+    tol[want_k == k0] = 0
+    assert np.all(np.abs(f64(b.k_pages) - want_k) <= tol)
+    want_q = ref.rope(f64(b.q), pos, axes, interleaved=il)
+    tol = 2.0 ** -8 * np.abs(want_q) + 2.0 ** -21 * ref.rope_reach(f64(b.q), axes, il)
+    assert np.all(np.abs(f64(q) - want_q) <= tol)
+
+
+def test_append_without_rope_and_with_positions():
+    b = Batch([5, 1], [20, 300], 2, 2, 64, 16, seed=32, fill=1.0)
+    k, v = torch.randn((6, 2, 64), device="cuda").to(BF16), torch.randn((6, 2, 64), device="cuda").to(BF16)
+    k0, v0 = f64(b.k_pages), f64(b.v_pages)
+    assert zl.paged_append(k, v, b.k_pages, b.v_pages, b.dtable, b.dlens, b.cu) is None
+    assert np.array_equal(f64(b.k_pages), ref.append(k0, b.table, b.lens, b.cu, f64(k)))
+    assert np.array_equal(f64(b.v_pages), ref.append(v0, b.table, b.lens, b.cu, f64(v)))
+    plan = zl.RopePlan(64, axes=(32, 32))
+    pos = torch.tensor([[1, 2, 3, 4, 5, 6], [9, 9, 9, 9, 9, -9]], dtype=torch.int32, device="cuda")
+    q = zl.paged_append(k, v, b.k_pages, b.v_pages, b.dtable, b.dlens, b.cu, q=b.q, rope=plan, positions=pos)
+    want, _ = zl.rope_fwd(b.q, None, pos, plan)
+    assert torch.equal(q, want)
+    want, _ = zl.rope_fwd(k, None, pos, plan)
+    assert np.array_equal(f64(b.k_pages), ref.append(k0, b.table, b.lens, b.cu, f64(want)))
+
+
+def test_append_past_the_cache_is_left_out_and_reported():
+    b = Batch([3, 2], [30, 20], 2, 1, 64, 16, seed=33, fill=1.0)
+    k = torch.randn((5, 1, 64), device="cuda").to(BF16)
+    k0 = f64(b.k_pages)
+    b.dlens[0] = 10 ** 6                   # far past the table row
+    b.dtable[1, 1] = -1
+    zl.paged_append(k, k, b.k_pages, b.v_pages, b.dtable, b.dlens, b.cu)
+    with pytest.raises(zl.ZlError) as e:
+        zl.sync_check()
+    assert e.value.status == -8
+    assert np.array_equal(f64(b.k_pages), k0)
+    b.dlens[0] = 1                         # shorter than the new tokens: the last of them is its only one
+    b.dtable[1, 1] = int(b.table[1, 1])
+    zl.paged_append(k, k, b.k_pages, b.v_pages, b.dtable, b.dlens, b.cu)
+    with pytest.raises(zl.ZlError):
+        zl.sync_check()
+    assert np.array_equal(f64(b.k_pages)[b.table[0, 0], 0, 0], f64(k)[2, 0])
+
+
+def test_append_many_sequences():
+    rng = np.random.default_rng(34)
+    lens = [int(x) for x in rng.integers(1, 60, 1300)]
+    new = [min(n, int(x)) for n, x in zip(lens, rng.integers(0, 4, 1300))]
+    b = Batch(new, lens, 1, 1, 64, 16, seed=34, fill=1.0)
+    k = torch.randn((b.cu[-1], 1, 64), device="cuda").to(BF16)
+    k0 = f64(b.k_pages)
+    zl.paged_append(k, k, b.k_pages, b.v_pages, b.dtable, b.dlens, b.cu)
+    zl.sync_check()
+    assert np.array_equal(f64(b.k_pages), ref.append(k0, b.table, b.lens, b.cu, f64(k)))
+
+
+# ------------------------------------------------------------------ a run of them together
+def test_generation_loop():
+    """Prompts, single tokens, a fork, more tokens, a sequence freed and the
+    pool compacted, on one cache of two layers; every step's attention equals
+    the packed attention over the sequences' whole histories."""
+    layers, page, hd, heads, kv, slots, pages = 2, 16, 64, 4, 2, 6, 60
+    g = torch.Generator(device="cuda").manual_seed(40)
+    cache = torch.full((layers, 2, pages, kv, page, hd), float("nan"), dtype=BF16, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table = torch.full((slots, 12), -1, dtype=torch.int32, device="cuda")
+    lens, refs = i32([0] * slots), i32([0] * pages)
+    plan = zl.RopePlan(hd)
+    past = [[] for _ in range(slots)]          # per slot and layer: (k, v) rows as appended, unturned
+    past = [[[] for _ in range(layers)] for _ in range(slots)]
+    host = ref.Pages(table.tolist(), [0] * slots, [0] * pages, page)
+
+    def step(counts):
+        cu = [0]
+        for c in counts:
+            cu.append(cu[-1] + c)
+        status = zl.pages_extend(table, lens, refs, i32(counts), page)
+        assert host.extend(counts) == int(status) == 0
+        for layer in range(layers):
+            q = torch.randn((cu[-1], heads, hd), generator=g, device="cuda").to(BF16)
+            k, v = (torch.randn((cu[-1], kv, hd), generator=g, device="cuda").to(BF16) for _ in range(2))
+            kp, vp = cache[layer]
+            qr = zl.paged_append(k, v, kp, vp, table, lens, cu, q=q, rope=plan)
+            o, lse = zl.paged_attn(qr, kp, vp, table, lens, cu, 12 * page)
+            zl.sync_check()
+            for s in range(slots):
+                if counts[s] == 0:
+                    continue
+                past[s][layer].append((k[cu[s]:cu[s + 1]], v[cu[s]:cu[s + 1]]))
+                kk, vv = (torch.cat([x[i] for x in past[s][layer]]) for i in range(2))
+                assert kk.shape[0] == host.lens[s]
+                pos = torch.arange(kk.shape[0], dtype=torch.int32, device="cuda")
+                kr, _ = zl.rope_fwd(kk, None, pos, plan)
+                p0 = kk.shape[0] - counts[s]
+                for h in range(heads):
+                    want, wl, reach = ref.attn_rows(f64(qr)[cu[s]:cu[s + 1], h], f64(kr)[:, h // 2], f64(vv)[:, h // 2],
+                                                    p0 + np.arange(counts[s]), True, 0, hd ** -0.5)
+                    err = np.abs(f64(o)[cu[s]:cu[s + 1], h] - want)
+                    assert np.all(err <= (2.0 ** -8 + 2.0 ** -11) * reach + 2.0 ** -8 * np.abs(want))
+                    assert np.all(np.abs(f64(lse)[h, cu[s]:cu[s + 1]] - wl) <= 2e-4 + 2.0 ** -20 * np.abs(wl))
+
+    step([35, 100, 16, 0, 0, 0])
+    step([1, 1, 1, 0, 0, 0])
+    assert int(zl.pages_fork(cache, table, lens, refs, i32([1, 1, 2]), i32([3, 5, 4]))) == host.fork([1, 1, 2], [3, 5, 4]) == 0
+    for p, c in ((1, 3), (1, 5), (2, 4)):
+        past[c] = [list(x) for x in past[p]]
+    step([1, 1, 1, 1, 1, 1])
+    step([0, 20, 0, 3, 0, 1])
+    zl.pages_free(table, lens, refs, i32([0, 5]), page)
+    host.release([0, 5])
+    past[0], past[5] = ([[] for _ in range(layers)] for _ in range(2))
+    assert int(zl.pages_compact(cache, table, lens, refs)) == host.compact()
+    assert refs.tolist() == host.refs and lens.tolist() == host.lens
+    for s in range(slots):
+        assert table[s, :host.used(host.lens[s])].tolist() == host.table[s][:host.used(host.lens[s])]
+    step([17, 1, 1, 1, 1, 40])
