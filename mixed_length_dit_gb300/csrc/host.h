@@ -37,6 +37,12 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int nh, int hd, 
 // adds into with TMA.
 bool make_map_acc(CUtensorMap* map, const float* base, int64_t rows, int nh, int hd, int box_rows);
 
+// 3-D view [tokens][heads][hd] of packed bf16 rows `stride` elements apart:
+// boxes of 64 columns x box_heads x box_tokens with the 128-byte swizzle;
+// tokens past the end read as zero and are not stored.
+bool make_map_heads(CUtensorMap* map, const void* base, int64_t tokens, int heads, int hd, int64_t stride,
+                    int box_heads, int box_tokens);
+
 // The current device's SM count, once it has been found to be an sm_103 one
 // (asked once per device).
 zl_status device_sms(int* sms);

@@ -49,28 +49,34 @@ struct RopeArgs {
 };
 static_assert(sizeof(RopeArgs) <= 32764, "rotary arguments exceed the kernel parameter space");
 
+// Most splits of one sequence's keys.
+constexpr int kMaxSplits = 128;
+
 // One sequence's queries in a paged attention launch.
 struct PagedSeg {
   int32_t seq;       // row of the page table and of the lengths
   int32_t q_row0;    // packed row of its first query
   int32_t q_len;     // queries, >= 1
+  int32_t item0;     // first work item
+  int32_t splits;    // splits of its keys, 1 .. kMaxSplits
+  int32_t tok0;      // queries of the launch's earlier segments
+  int64_t part0;     // splits > 1: its first row in o_part / lse_part
 };
 
 struct PagedAttnArgs {
-  const void* q;
-  const void* k_pages;
-  const void* v_pages;
   const int32_t* page_table;
   const int32_t* kv_lens;
   void* o;                      // [Tq][H][d] bf16
   float* lse;                   // [H][lse_stride]
-  int64_t q_stride;
+  float* o_part;                // [rows][H][d]: row part0 + split * q_len + query
+  float* lse_part;              // [rows][H]
   int64_t lse_stride;           // Tq
-  int64_t token0;               // first query row of this launch
-  int32_t tokens;               // query rows of this launch
+  int32_t tokens;               // queries of this launch
   int32_t num_heads;
   int32_t num_kv_heads;
   int32_t group;                // query heads of a key head
+  int32_t tile_tokens;          // tokens of a query tile: 128 / group
+  int32_t split_blocks;         // 128-key blocks of a split
   int32_t table_cols;
   int32_t num_pages;
   int32_t page_shift;
@@ -78,10 +84,20 @@ struct PagedAttnArgs {
   int32_t causal;
   int32_t window;
   float scale_log2;             // softmax scale * log2(e)
+  int32_t n_items;
   int32_t n_segs;
   PagedSeg segs[kMaxSegs];
 };
-static_assert(sizeof(PagedAttnArgs) <= 32764, "paged attention arguments exceed the kernel parameter space");
+
+// Tensor maps: q[i] takes the tokens of a tile that holds 1, 2 or 4 copies of
+// its rows (boxes of 64 columns x group heads x 128 / copies / group tokens),
+// o stores a tile like q[0]; k and v see a pool as rows of one head of one
+// token (boxes of 64 columns x min(page, 128) rows).
+struct PagedMaps {
+  CUtensorMap q[3];
+  CUtensorMap k, v, o;
+};
+static_assert(sizeof(PagedAttnArgs) + sizeof(PagedMaps) <= 32764, "paged attention arguments exceed the kernel parameter space");
 
 // A pool of pages seen by the kernels that move whole pages.
 struct PagePool {
@@ -114,7 +130,11 @@ inline size_t pages_workspace_words(int64_t num_pages) {
 }
 
 cudaError_t launch_rope(const RopeArgs& args, int num_sms, cudaStream_t stream);
-cudaError_t launch_paged_attn(int head_dim, const PagedAttnArgs& args, cudaStream_t stream);
+// pair: sequences of more than one query tile each; else of one.
+cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, const PagedAttnArgs& args,
+                              cudaStream_t stream);
+// Joins the split rows of a launch_paged_attn with the same arguments.
+cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnArgs& args, cudaStream_t stream);
 cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const int32_t* dst, int32_t n, int num_sms,
                               cudaStream_t stream);
 cudaError_t launch_pages_extend(const PageTable& t, const int32_t* counts, int32_t* status, cudaStream_t stream);

@@ -1,8 +1,41 @@
-// Attention of a chunk of new tokens over a paged key/value cache.
+// Attention of a chunk of new tokens over a paged key/value cache, on tensor
+// cores.
 //
-// One warp per (query token, head) row: the row's keys are walked once with a
-// running maximum and sum (base 2), each lane owning d/32 columns of q, k, v
-// and the output.
+//     S = q K^T scale,  o = softmax(S) V  over the keys that each query sees,
+//
+// in one pass over the keys with a running maximum m and sum l (base 2).  The
+// query heads that share a key head are rows of one tile: row r of a tile is
+// token r / group, head r % group, so a page that is read serves all of them,
+// and single tokens fill a tile as far as they can.
+//
+// A work item is (sequence, key head, unit of query tiles, split of the keys).
+// Two kernels, by what bounds them:
+//
+//   PAIR   chunks of more than one tile: tensor-bound.  An item is two 128-row
+//          tiles that share every K/V block, softmax group t and issuer t for
+//          tile t, as in the packed forward.
+//   SPLIT  a sequence whose new rows fit one tile (single tokens, drafts):
+//          bound by HBM.  The two groups take alternate key blocks of the one
+//          tile.  With 32 rows or fewer (64) the tile holds them four times
+//          (twice) over, 32 (64) rows apart: each warp of a group then takes
+//          its own quarter (half) of a block's keys for the same rows, so the
+//          exponentials of few rows are spread over all four schedulers
+//          instead of one.  What the groups and warps have summed, up to
+//          eight parts of a row, is joined in shared memory at the end.
+//
+// Roles of a CTA (384 threads, 1 per SM):
+//   warps 0-7   softmax: warpgroup t's thread owns TMEM lane (row) threadIdx
+//               % 128 of tile t; P = 2^(S scale log2e - m) goes back over S as
+//               bf16 (the one rounding of the probabilities: the tensor cores
+//               take P in V's type), O is rescaled when m grows by more than
+//               2^8
+//   warp 8      producer: all lanes fetch page numbers, each lane issues the
+//               TMA box of its page; items by cluster launch control
+//   warps 9,10  MMA issuers (S = Q K^T, O += P V) of group t
+//   warp 11     clears what a sequence's last V block holds past its length
+//               (unwritten rows may be NaN, and 0 * NaN is not 0)
+// The lengths are read on the device, so a captured launch follows them.
+#define ZL_TRY_WAIT_HINT_NS 10000
 #include "common.cuh"
 #include "paged.h"
 
@@ -11,78 +44,1020 @@ namespace {
 
 __device__ uint32_t g_paged_err;
 
-constexpr int kSimpleThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp0 = 9;
+constexpr int kTailWarp = 11;
+constexpr int kReaders = 11;                   // 2 issuer threads, 8 softmax warps, the tail warp
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleThreshold = 8.0f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-template <int HD>
-__global__ void __launch_bounds__(kSimpleThreads) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
-  constexpr int C = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kSimpleThreads / 32) + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(a.tokens) * a.num_heads) return;
-  const int64_t t = a.token0 + row / a.num_heads;
-  const int h = static_cast<int>(row % a.num_heads);
+// K/V blocks of 128 keys in shared memory.  PAIR holds two query tiles and
+// needs depth only to cover the latency; SPLIT lives from bytes in flight.
+// PAIR's issuers both pass every stage of one ring.  In SPLIT each issuer has
+// half of the stages as a ring of its own: a wait on an mbarrier's parity is
+// only right for a thread that sees every phase, and an issuer that skipped
+// the other's blocks in a shared ring would take a phase two before the one
+// it waits for (a block that lands late) for its own.
+template <int HD, bool PAIR>
+__host__ __device__ constexpr int stages() { return HD == 128 ? (PAIR ? 4 : 6) : (PAIR ? 8 : 12); }
+
+template <int HD, bool PAIR>
+struct Stages {
+  static constexpr int kRing = PAIR ? stages<HD, PAIR>() : stages<HD, PAIR>() / 2;
+  // Stage and parity of the u-th block half (K or V) of ring t.
+  static __device__ __forceinline__ uint32_t stage(int t, uint32_t u) { return (PAIR ? 0u : t * kRing) + u % kRing; }
+  static __device__ __forceinline__ uint32_t parity(uint32_t u) { return (u / kRing) & 1u; }
+};
+
+template <int HD, bool PAIR>
+struct PagedSmem {
+  static constexpr int kStages = stages<HD, PAIR>();
+  uint8_t q[PAIR ? 2 : 1][kBlockM * HD * 2];   // HD/64 boxes of [128 rows][128 B], 128-byte swizzle
+  uint8_t kv[kStages][kBlockN * HD * 2];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[kStages], kv_empty[kStages], tail[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t turn[2], grp_sync[2], all_sync;
+  ItemRing ring;
+  int item_len[2];                             // the length of the ring slot's sequence
+  uint32_t tmem_base;
+  int abort_flag;
+  float2 ml[2 * kBlockM];                      // SPLIT: m and l of every group's rows
+};
+
+// Block ranges [b0, b1) of 128 keys.
+struct Range {
+  int b0, b1;
+};
+
+// Keys [lo, hi) that the query at position p of a sequence of `len` sees.
+__device__ __forceinline__ void keys_of(const PagedAttnArgs& a, int len, int p, int* lo, int* hi) {
+  *hi = a.causal ? max(0, min(len, p + 1)) : len;
+  *lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+}
+
+// Blocks that queries [t0, t1) of the sequence see.
+__device__ __forceinline__ Range blocks_of(const PagedAttnArgs& a, int len, int q_len, int t0, int t1) {
+  int lo, hi, x;
+  keys_of(a, len, len - q_len + t0, &lo, &x);
+  keys_of(a, len, len - q_len + t1 - 1, &x, &hi);
+  if (hi <= lo) return {0, 0};
+  return {lo / kBlockN, (hi + kBlockN - 1) / kBlockN};
+}
+
+// One work item, as every role sees it.
+struct Work {
+  int seq, q_row0, q_len, len;
+  int hk;
+  int tile0;        // first query tile
+  int split;
+  int active;       // splits of this unit that have keys
+  int s0, s1;       // this split's blocks
+  int64_t part0;    // first partial row of the sequence
+  Range tile[2];    // each tile's blocks within [s0, s1)
+  bool has[2];      // the tile exists
+};
+
+__device__ __forceinline__ int find_seg(const PagedAttnArgs& a, int it) {
   int lo = 0, hi = a.n_segs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (a.segs[mid].q_row0 <= t) lo = mid; else hi = mid - 1;
+    if (a.segs[mid].item0 <= it) lo = mid; else hi = mid - 1;
   }
-  const PagedSeg sg = a.segs[lo];
-  const int hk = h / a.group;
-  int len = a.kv_lens[sg.seq];
-  if (len < 0 || len > a.max_kv_len) {
-    if (lane == 0) atomicOr(&g_paged_err, ERR_BAD_PAGE);
-    len = len < 0 ? 0 : a.max_kv_len;
+  return lo;
+}
+
+__device__ __forceinline__ Range cut(Range r, int s0, int s1) {
+  const int b0 = max(r.b0, s0), b1 = min(r.b1, s1);
+  return b1 > b0 ? Range{b0, b1} : Range{s0, s0};
+}
+
+// The blocks that the splits of a unit (first tile `tile0`) divide: the union
+// of its tiles'.
+template <bool PAIR>
+__device__ __forceinline__ Range unit_blocks(const PagedAttnArgs& a, int len, int q_len, int tile0) {
+  const int t0 = tile0 * a.tile_tokens;
+  Range r = blocks_of(a, len, q_len, t0, min(q_len, t0 + a.tile_tokens));
+  if (PAIR && t0 + a.tile_tokens < q_len) {
+    const Range s = blocks_of(a, len, q_len, t0 + a.tile_tokens, min(q_len, t0 + 2 * a.tile_tokens));
+    if (r.b1 <= r.b0) return s;
+    if (s.b1 > s.b0) r = {min(r.b0, s.b0), max(r.b1, s.b1)};
   }
-  const int p = len - sg.q_len + static_cast<int>(t - sg.q_row0);
-  const int k_end = a.causal ? min(len, p + 1) : len;
-  const int k_begin = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + t * a.q_stride + static_cast<int64_t>(h) * HD;
-  float x[C], acc[C];
+  return r;
+}
+
+// Items of a segment: key head outermost, then the unit, last tokens first
+// (under a causal mask they see the most), then the split.
+template <bool PAIR>
+__device__ __forceinline__ Work decode(const PagedAttnArgs& a, int it, int len) {
+  const PagedSeg& s = a.segs[find_seg(a, it)];
+  Work w;
+  w.seq = s.seq;
+  w.q_row0 = s.q_row0;
+  w.q_len = s.q_len;
+  w.len = len;
+  w.part0 = s.part0;
+  const int tiles = (s.q_len + a.tile_tokens - 1) / a.tile_tokens;
+  const int units = PAIR ? (tiles + 1) / 2 : 1;
+  int x = it - s.item0;
+  w.split = x % s.splits;
+  x /= s.splits;
+  const int u = units - 1 - x % units;
+  w.hk = x / units;
+  w.tile0 = PAIR ? 2 * u : 0;
+  const Range r = unit_blocks<PAIR>(a, len, s.q_len, w.tile0);
+  w.active = (r.b1 - r.b0 + a.split_blocks - 1) / a.split_blocks;
+  w.s0 = min(r.b1, r.b0 + w.split * a.split_blocks);
+  w.s1 = min(r.b1, w.s0 + a.split_blocks);
+  w.has[0] = true;
+  w.has[1] = PAIR && w.tile0 + 1 < tiles;
+  const int t0 = w.tile0 * a.tile_tokens;
+  w.tile[0] = cut(blocks_of(a, len, s.q_len, t0, min(s.q_len, t0 + a.tile_tokens)), w.s0, w.s1);
+  w.tile[1] = w.tile[0];
+  if (w.has[1])
+    w.tile[1] = cut(blocks_of(a, len, s.q_len, t0 + a.tile_tokens, min(s.q_len, t0 + 2 * a.tile_tokens)), w.s0, w.s1);
+  return w;
+}
+
+// Copies of a SPLIT tile's rows: 4, 2 or 1, 128 / copies rows apart.
+__device__ __forceinline__ int row_copies(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
+
+__device__ __forceinline__ void drain_delay(uint64_t ns) {
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < ns) {
+  }
+}
+
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
+                                            int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];"
+      :: "r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int32_t x, int32_t y,
+                                             int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+      :: "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// A ring reader's next item and its sequence's length.
+template <typename SM>
+__device__ __forceinline__ int take(SM* sm, uint32_t n, uint32_t code, bool warp_wide, int* len) {
+  ItemRing* r = &sm->ring;
+  const uint32_t s = n & 1u;
+  bool ok = mbar_wait(&r->full[s], (n >> 1) & 1u, &sm->abort_flag, &g_paged_err, code);
+  if (warp_wide) ok = __all_sync(0xffffffffu, ok);
+  if (!ok) return -2;
+  const int it = *reinterpret_cast<volatile int*>(&r->item[s]);
+  *len = *reinterpret_cast<volatile int*>(&sm->item_len[s]);
+  if (warp_wide) __syncwarp();
+  if (!warp_wide || (threadIdx.x & 31) == 0) mbar_arrive(&r->empty[s]);
+  return it;
+}
+
+// ------------------------------------------------------------------ producer
+template <int HD, bool PAIR>
+__device__ void produce(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs& a, const PagedMaps& maps) {
+  using Ring = Stages<HD, PAIR>;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sm->abort_flag;
+  const uint32_t code = ERR_TIMEOUT_PRODUCER;
+  const int page = 1 << a.page_shift;
+  const int box_rows = min(page, kBlockN);
+  uint32_t kv_it0 = 0, kv_it1 = 0, q_it[2] = {0u, 0u}, steal_ph = 0;   // uses of ring 0 and 1
+  int it = static_cast<int>(blockIdx.x);
+  for (uint32_t n = 0;; ++n) {
+    int len = 0;
+    if (it >= 0) {
+      const PagedSeg& s = a.segs[find_seg(a, it)];
+      len = __ldg(a.kv_lens + s.seq);
+      if (len < 0 || len > a.max_kv_len) {
+        if (lane == 0) atomicOr(&g_paged_err, ERR_BAD_PAGE);
+        len = len < 0 ? 0 : a.max_kv_len;
+      }
+    }
+    // publish once every reader has taken the slot's previous item
+    bool ok = true;
+    if (lane == 0) {
+      const uint32_t s = n & 1u;
+      ok = mbar_wait(&sm->ring.empty[s], ((n >> 1) & 1u) ^ 1u, abort_flag, &g_paged_err, code);
+      if (ok) {
+        sm->ring.item[s] = it;
+        sm->item_len[s] = len;
+        mbar_arrive(&sm->ring.full[s]);
+      }
+    }
+    if (!__shfl_sync(0xffffffffu, ok, 0) || it < 0) return;
+    const Work w = decode<PAIR>(a, it, len);
+    bool asked = false;
+    if (w.s1 > w.s0) {
+      const int32_t* row = a.page_table + static_cast<int64_t>(w.seq) * a.table_cols;
+      // page numbers of the split's blocks, 32 at a time, the next 32 on their way
+      const int e0 = (w.s0 * kBlockN) >> a.page_shift;
+      const int e1 = min((min(w.len, w.s1 * kBlockN) + page - 1) >> a.page_shift, a.table_cols);
+      int chunk = 0;
+      int cur = e0 + lane < e1 ? __ldg(row + e0 + lane) : 0;
+      int nxt = e0 + 32 + lane < e1 ? __ldg(row + e0 + 32 + lane) : 0;
+      for (int j = w.s0; j < w.s1; ++j) {
+        if (j == w.s1 - 1) {
+          if (lane == 0) ring_ask(&sm->ring);
+          asked = true;
+        }
+        const int rel = ((j * kBlockN) >> a.page_shift) - e0;
+        if ((rel >> 5) != chunk) {
+          ++chunk;
+          cur = nxt;
+          nxt = e0 + 32 * (chunk + 1) + lane < e1 ? __ldg(row + e0 + 32 * (chunk + 1) + lane) : 0;
+        }
+        const int valid = min(kBlockN, w.len - j * kBlockN);
+        const int boxes = (valid + box_rows - 1) / box_rows;
+        int pg = __shfl_sync(0xffffffffu, cur, ((rel & 31) + lane) & 31);
+        if (lane < boxes && (pg < 0 || pg >= a.num_pages)) {
+          atomicOr(&g_paged_err, ERR_BAD_PAGE);        // reads page 0 in its place
+          pg = 0;
+        }
+        const int y = ((pg * a.num_kv_heads + w.hk) << a.page_shift) + ((j * kBlockN) & (page - 1));
+        const int ring = PAIR ? 0 : (j - w.s0) & 1;
+        uint32_t& kv_it = ring ? kv_it1 : kv_it0;
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    x[c] = __bfloat162float(q[lane * C + c]) * a.scale_log2;
-    acc[c] = 0.f;
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t st = Ring::stage(ring, kv_it);
+          if (!__all_sync(0xffffffffu, mbar_wait(&sm->kv_empty[st], Ring::parity(kv_it) ^ 1u, abort_flag,
+                                                 &g_paged_err, code)))
+            return;
+          // a V block that the sequence ends in goes by way of the tail warp
+          uint64_t* bar = kv == 1 && valid < kBlockN ? &sm->tail[st] : &sm->kv_full[st];
+          if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * box_rows * HD * 2));
+          __syncwarp();
+          if (lane < boxes) {
+            const CUtensorMap* map = kv ? &maps.v : &maps.k;
+#pragma unroll
+            for (int c = 0; c < HD / 64; ++c)
+              tma_load_2d(sm->kv[st] + c * kBlockN * 128 + lane * box_rows * 128, map, bar, c * 64, y);
+          }
+          ++kv_it;
+          if (j == w.s0 && kv == 0) {
+            // the item's queries, once the previous item has released them
+            if (lane == 0) {
+#pragma unroll
+              for (int t = 0; t < (PAIR ? 2 : 1); ++t) {
+                if (!w.has[t]) continue;
+                if (!mbar_wait(&sm->q_empty[t], (q_it[t] & 1u) ^ 1u, abort_flag, &g_paged_err, code)) {
+                  ok = false;
+                  break;
+                }
+                ++q_it[t];
+                const int copies = PAIR ? 1 : row_copies(w.q_len * a.group);
+                const CUtensorMap* map = &maps.q[PAIR ? 0 : copies >> 1];
+                const int rows = (kBlockM / copies) / a.group * a.group;
+                mbar_arrive_expect_tx(&sm->q_full[t], static_cast<uint32_t>(copies * rows * HD * 2));
+                for (int r = 0; r < copies; ++r)
+#pragma unroll
+                  for (int c = 0; c < HD / 64; ++c)
+                    tma_load_3d(sm->q[t] + c * kBlockM * 128 + r * (kBlockM / copies) * 128, map, &sm->q_full[t],
+                                c * 64, w.hk * a.group, w.q_row0 + (w.tile0 + t) * a.tile_tokens);
+              }
+            }
+            if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+          }
+        }
+      }
+    }
+    int next = -2;
+    if (lane == 0) {
+      if (!asked) ring_ask(&sm->ring);
+      next = ring_answer(&sm->ring, steal_ph, a.n_items, abort_flag, &g_paged_err, code);
+    }
+    next = __shfl_sync(0xffffffffu, next, 0);
+    if (next == -2) return;
+    it = next;
   }
-  float m = -INFINITY, l = 0.f;
-  for (int j = k_begin; j < k_end; ++j) {
-    const int page = a.page_table[static_cast<int64_t>(sg.seq) * a.table_cols + (j >> a.page_shift)];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) atomicOr(&g_paged_err, ERR_BAD_PAGE);
+}
+
+// ------------------------------------------------------------------ MMA issuer t
+template <int HD, bool PAIR>
+__device__ void issue(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs& a, uint32_t tmem, int t) {
+  using Ring = Stages<HD, PAIR>;
+  constexpr uint32_t idesc_qk = idesc_bf16(kBlockM, kBlockN, false, false);
+  constexpr uint32_t idesc_pv = idesc_bf16(kBlockM, HD, false, true);
+  volatile int* abort_flag = &sm->abort_flag;
+  const uint32_t code = ERR_TIMEOUT_MMA;
+  const int qt = PAIR ? t : 0;
+  const uint64_t q_desc = sdesc_sw128(smem_u32(sm->q[qt]), 16, 1024);
+  const uint32_t tS = tmem + 256u * t;
+  const uint32_t tO = tS + 128u;
+  uint32_t kv_it = 0, q_it = 0, blk_it = 0;
+  for (uint32_t n = 0;; ++n) {
+    int len;
+    const int it = take(sm, n, code, false, &len);
+    if (it < 0) return;
+    const Work w = decode<PAIR>(a, it, len);
+    if (w.s1 <= w.s0) continue;
+    const bool has = PAIR ? w.has[t] : true;
+    if (has && !mbar_wait(&sm->q_full[qt], q_it & 1u, abort_flag, &g_paged_err, code)) return;
+    bool first = true;
+    // PAIR: both issuers pass every stage, and each uses the blocks that its
+    // tile sees; SPLIT: issuer t's blocks alternate with the other's, in its
+    // own ring
+    const int last_mine = PAIR ? w.tile[t].b1 - 1 : w.s1 - 1 - ((w.s1 - 1 - w.s0 - t) & 1);
+    for (int j = PAIR ? w.s0 : w.s0 + t; j < w.s1; j += PAIR ? 1 : 2) {
+      const bool mine = has && (!PAIR || (j >= w.tile[t].b0 && j < w.tile[t].b1));
+      uint32_t st = Ring::stage(t, kv_it);
+      if (!mbar_wait(&sm->kv_full[st], Ring::parity(kv_it), abort_flag, &g_paged_err, code)) return;
+      if (mine) {
+        tc_fence_after();
+        const uint64_t k_desc = sdesc_sw128(smem_u32(sm->kv[st]), 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          const uint64_t off16 = ((ks >> 2) * (kBlockM * 128) + (ks & 3) * 32) >> 4;
+          umma_ss(tS, q_desc + off16, k_desc + off16, idesc_qk, ks > 0 ? 1u : 0u);
+        }
+        umma_commit(&sm->s_full[t]);
+        if (j == last_mine) umma_commit(&sm->q_empty[qt]);
+        umma_commit(&sm->kv_empty[st]);
+      } else {
+        mbar_arrive(&sm->kv_empty[st]);
+      }
+      ++kv_it;
+      st = Ring::stage(t, kv_it);
+      if (!mbar_wait(&sm->kv_full[st], Ring::parity(kv_it), abort_flag, &g_paged_err, code)) return;
+      if (mine) {
+        if (!mbar_wait(&sm->p_full[t], blk_it & 1u, abort_flag, &g_paged_err, code)) return;
+        tc_fence_after();
+        const uint64_t v_desc = sdesc_sw128(smem_u32(sm->kv[st]), kBlockN * 128, 1024);
+#pragma unroll
+        for (int ks = 0; ks < kBlockN / 16; ++ks)
+          umma_ts(tO, tS + ks * 8, v_desc + static_cast<uint64_t>(ks * (2048 >> 4)), idesc_pv,
+                  (!first || ks > 0) ? 1u : 0u);
+        first = false;
+        ++blk_it;
+        umma_commit(&sm->kv_empty[st]);
+      } else {
+        mbar_arrive(&sm->kv_empty[st]);
+      }
+      ++kv_it;
+    }
+    if (has) {
+      if (first) umma_commit(&sm->q_empty[qt]);          // no block of this item was this issuer's
+      umma_commit(&sm->o_full[t]);
+      ++q_it;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ tail warp
+template <int HD, bool PAIR>
+__device__ void clear_tails(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs& a) {
+  using Ring = Stages<HD, PAIR>;
+  const int lane = threadIdx.x & 31;
+  uint32_t base0 = 0, base1 = 0, phases = 0;     // uses of ring 0 and 1 by earlier items; parity of each tail barrier
+  for (uint32_t n = 0;; ++n) {
+    int len;
+    const int it = take(sm, n, ERR_TIMEOUT_OTHER, true, &len);
+    if (it < 0) return;
+    const Work w = decode<PAIR>(a, it, len);
+    if (w.s1 <= w.s0) continue;
+    const int jt = w.len / kBlockN, valid = w.len % kBlockN;
+    if (valid > 0 && jt >= w.s0 && jt < w.s1) {
+      const int ring = PAIR ? 0 : (jt - w.s0) & 1;
+      const uint32_t blk = static_cast<uint32_t>(PAIR ? jt - w.s0 : (jt - w.s0) >> 1);
+      const uint32_t st = Ring::stage(ring, (ring ? base1 : base0) + 2u * blk + 1u);
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm->tail[st], (phases >> st) & 1u, &sm->abort_flag, &g_paged_err,
+                                             ERR_TIMEOUT_OTHER)))
+        return;
+      phases ^= 1u << st;
+      // rows [valid, 128) of every 64-column box: whole 128-byte rows
+      for (int x = lane; x < (kBlockN - valid) * 8; x += 32)
+#pragma unroll
+        for (int c = 0; c < HD / 64; ++c)
+          *reinterpret_cast<uint4*>(sm->kv[st] + c * kBlockN * 128 + valid * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->kv_full[st]);
+    }
+    const uint32_t blocks = static_cast<uint32_t>(w.s1 - w.s0);
+    base0 += 2u * (PAIR ? blocks : (blocks + 1) / 2);
+    base1 += 2u * (PAIR ? 0u : blocks / 2);
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+// P of 32 scores as 16 packed columns; adds their sum to acc.
+__device__ __forceinline__ void exp_pack(const uint32_t (&s)[32], float sl2, float neg_m, uint64_t (&acc)[2],
+                                         uint32_t (&p)[16]) {
+  const uint64_t sl2x2 = f2_pack(sl2, sl2);
+  const uint64_t negm2 = f2_pack(neg_m, neg_m);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sl2x2, negm2);
+    float x0, x1;
+    f2_unpack(x, x0, x1);
+    const float e0 = fast_exp2(x0);
+    const float e1 = fast_exp2(x1);
+    acc[i & 1] = f2_add(acc[i & 1], f2_pack(e0, e1));
+    p[i] = pack_bf16x2(e0, e1);
+  }
+}
+
+// Scores of columns [col0, col0 + 32) outside [lo, hi) become -inf.
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], int col0, int lo, int hi) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (col0 + i < lo || col0 + i >= hi) s[i] = __float_as_uint(-INFINITY);
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    m0 = fmax3(m0, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+    m1 = fmax3(m1, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+  }
+  return fmaxf(m0, m1);
+}
+
+// The running maximum after a block whose own is m_blk; *alpha: the factor of
+// what was summed before.  A row that has seen nothing keeps -inf.
+__device__ __forceinline__ bool raise_max(float m_blk, float* m_run, float* alpha) {
+  const float m_new = fmaxf(*m_run, m_blk);
+  const bool need = m_new > *m_run + kRescaleThreshold;
+  *alpha = 1.f;
+  if (need) {
+    *alpha = fast_exp2(*m_run - m_new);
+    *m_run = m_new;
+  }
+  return need;
+}
+
+template <int HD>
+__device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < HD / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld32(tO + c * 32, o);
+    tmem_wait_ld();
+    reg_fence(o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+    tmem_st32(tO + c * 32, o);
+  }
+}
+
+__device__ __forceinline__ float neg_or_zero(float m) { return m == -INFINITY ? 0.f : -m; }
+
+// PAIR: group t runs tile t.
+template <int HD>
+__device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs& a, const PagedMaps& maps, uint32_t tmem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = warp >> 2;
+  const int row = (warp & 3) * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t tS = tmem + 256u * t + lane_off;
+  const uint32_t tO = tS + 128u;
+  const float sl2 = a.scale_log2;
+  volatile int* abort_flag = &sm->abort_flag;
+  const uint32_t code = ERR_TIMEOUT_SOFTMAX;
+  const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+  uint32_t blk_it = 0, q_it = 0, turn_it = 0, sync_uses = 0;
+  if (t == 1) mbar_arrive(&sm->turn[0]);         // the first turn is group 0's
+  for (uint32_t n = 0;; ++n) {
+    int len;
+    const int it = take(sm, n, code, true, &len);
+    if (it < 0) break;
+    const Work w = decode<true>(a, it, len);
+    const bool has = w.has[t];
+    const int tok0 = (w.tile0 + t) * a.tile_tokens;
+    const int tokens = min(a.tile_tokens, w.q_len - tok0);
+    const int tok = tok0 + row_tok;
+    const bool row_ok = has && row_tok < tokens;
+    float m_run = -INFINITY, l_run = 0.f;
+    bool first = true;
+    if (w.s1 > w.s0) {
+      // this row's keys, and the keys that every row of the tile sees
+      int lo, hi, lo_all, hi_all, x;
+      const int p0 = w.len - w.q_len;
+      keys_of(a, w.len, p0 + tok, &lo, &hi);
+      keys_of(a, w.len, p0 + tok0, &x, &hi_all);
+      keys_of(a, w.len, p0 + tok0 + max(0, tokens - 1), &lo_all, &x);
+      bool ok = true;
+      for (int j = w.s0; j < w.s1; ++j, ++turn_it) {
+        const bool mine = has && j >= w.tile[t].b0 && j < w.tile[t].b1;
+        if (!__all_sync(0xffffffffu,
+                        (!mine || mbar_wait(&sm->s_full[t], blk_it & 1u, abort_flag, &g_paged_err, code)) &&
+                            mbar_wait(&sm->turn[t], turn_it & 1u, abort_flag, &g_paged_err, code))) {
+          ok = false;
+          break;
+        }
+        if (!mine) {
+          mbar_arrive(&sm->turn[t ^ 1]);
+          continue;
+        }
+        tc_fence_after();
+        uint32_t s[4][32];
+        float m_raw;
+        const int k0 = j * kBlockN;
+        if (k0 >= lo_all && k0 + kBlockN <= hi_all) {
+          float r[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) r[c] = tmem_ld32_max(tS + c * 32, s[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            reg_fence(s[c]);
+            reg_fence_f(r[c]);
+          }
+          m_raw = fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+          tmem_wait_ld();
+          m_raw = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            reg_fence(s[c]);
+            mask32(s[c], k0 + c * 32, lo, hi);
+            m_raw = fmaxf(m_raw, max32(s[c]));
+          }
+        }
+        float alpha;
+        const bool need = raise_max(m_raw * sl2, &m_run, &alpha);
+        l_run *= alpha;
+        const float neg_m = neg_or_zero(m_run);
+        uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
+          exp_pack(s[c], sl2, neg_m, acc, p);
+          tmem_st16(tS + 16 * c, p);
+        }
+        mbar_arrive(&sm->turn[t ^ 1]);
+        if (!first && __any_sync(0xffffffffu, need)) rescale_o<HD>(tO, alpha);
+        first = false;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sm->p_full[t]);
+        ++blk_it;
+        float ls0, ls1;
+        f2_unpack(f2_add(acc[0], acc[1]), ls0, ls1);
+        l_run += ls0 + ls1;
+      }
+      if (!ok) break;
+      if (has) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm->o_full[t], q_it & 1u, abort_flag, &g_paged_err, code))) break;
+        ++q_it;
+        tc_fence_after();
+      }
+    } else if (w.split > 0) {
       continue;
     }
-    const int64_t off = (((static_cast<int64_t>(page) * a.num_kv_heads + hk) << a.page_shift) +
-                         (j & ((1 << a.page_shift) - 1))) * HD + lane * C;
-    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k_pages) + off;
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_pages) + off;
-    float s = 0.f;
+    if (!has) continue;
+    // ---------------------------------------------------------- epilogue
+    const bool seen = l_run > 0.f;
+    const float inv_l = seen ? 1.f / l_run : 0.f;
+    const float lse = seen ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+    const int h = w.hk * a.group + row_head;
+    const bool loaded = w.s1 > w.s0;            // this item's Q went through q[t]
+    const bool final_rows = w.active <= 1;
+    // a full tile of final rows leaves by TMA through the tile's own Q
+    // buffer; rows without keys would read O as it was: per thread
+    const bool by_tma = final_rows && loaded && !first && tokens == a.tile_tokens;
+    if (loaded && !by_tma && row == 0) mbar_arrive(&sm->q_empty[t]);
+    if (by_tma) {
+      const uint32_t r7 = static_cast<uint32_t>(row & 7);
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + c * 32, o);
+        tmem_wait_ld();
+        reg_fence(o);
+        uint8_t* box_row = sm->q[t] + (c >> 1) * (kBlockM * 128) + row * 128;
 #pragma unroll
-    for (int c = 0; c < C; ++c) s = fmaf(x[c], __bfloat162float(k[c]), s);
+        for (int k = 0; k < 4; ++k) {
+          uint4 pk;
+          uint32_t* v = &pk.x;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float m_new = fmaxf(m, s);
-    const float alpha = m_new == -INFINITY ? 1.f : exp2f(m - m_new);
-    const float w = m_new == -INFINITY ? 0.f : exp2f(s - m_new);
-    l = l * alpha + w;
+          for (int e = 0; e < 4; ++e) {
+            const float x0 = seen ? __uint_as_float(o[8 * k + 2 * e]) * inv_l : 0.f;
+            const float x1 = seen ? __uint_as_float(o[8 * k + 2 * e + 1]) * inv_l : 0.f;
+            v[e] = pack_bf16x2(x0, x1);
+          }
+          const uint32_t ch = static_cast<uint32_t>((c & 1) * 4 + k);
+          *reinterpret_cast<uint4*>(box_row + ((ch ^ r7) << 4)) = pk;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sm->grp_sync[t]);
+      const uint32_t phase = sync_uses++;
+      if (row == 0) {
+        if (!mbar_wait(&sm->grp_sync[t], phase & 1u, abort_flag, &g_paged_err, code)) break;
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = fmaf(w, __bfloat162float(v[c]), acc[c] * alpha);
-    m = m_new;
+        for (int c = 0; c < HD / 64; ++c)
+          tma_store_3d(&maps.o, sm->q[t] + c * (kBlockM * 128), c * 64, w.hk * a.group, w.q_row0 + tok0);
+        bulk_commit_group();
+        bulk_wait_group_read0();
+        mbar_arrive(&sm->q_empty[t]);
+      }
+      if (row_ok) a.lse[static_cast<int64_t>(h) * a.lse_stride + w.q_row0 + tok] = lse;
+    } else {
+      const int64_t out = final_rows
+          ? (static_cast<int64_t>(w.q_row0 + tok) * a.num_heads + h)
+          : ((w.part0 + static_cast<int64_t>(w.split) * w.q_len + tok) * a.num_heads + h);
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t o[32];
+        if (loaded && !first) {
+          tmem_ld32(tO + c * 32, o);
+          tmem_wait_ld();
+          reg_fence(o);
+        }
+        __syncwarp();
+        if (row_ok) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = seen ? __float_as_uint(__uint_as_float(o[i]) * inv_l) : 0u;
+          if (final_rows) {
+            uint4* d4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + out * HD + c * 32);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              uint4 pk;
+              uint32_t* u = &pk.x;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                u[e] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * e]), __uint_as_float(o[8 * v + 2 * e + 1]));
+              d4[v] = pk;
+            }
+          } else {
+            uint4* d4 = reinterpret_cast<uint4*>(a.o_part + out * HD + c * 32);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) d4[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (row_ok) {
+        if (final_rows)
+          a.lse[static_cast<int64_t>(h) * a.lse_stride + w.q_row0 + tok] = lse;
+        else
+          a.lse_part[out] = lse;
+      }
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (t * a.num_heads + h) * HD;
+  if (row == 0) bulk_wait_group0();              // the group's stores, before the CTA leaves
+}
+
+// SPLIT: group t takes every other block; with copies of the rows, a warp
+// takes its own part of a block's columns.
+template <int HD>
+__device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs& a, uint32_t tmem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = warp >> 2, quad = warp & 3;
+  const int row = quad * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t tS = tmem + 256u * t + lane_off;
+  const uint32_t tO = tS + 128u;
+  const float sl2 = a.scale_log2;
+  volatile int* abort_flag = &sm->abort_flag;
+  const uint32_t code = ERR_TIMEOUT_SOFTMAX;
+  uint32_t blk_it = 0, q_it = 0, sync_uses = 0;
+  for (uint32_t n = 0;; ++n) {
+    int len;
+    const int it = take(sm, n, code, true, &len);
+    if (it < 0) return;
+    const Work w = decode<false>(a, it, len);
+    if (w.s1 <= w.s0 && w.split > 0) continue;
+    const int rows = w.q_len * a.group;
+    const int copies = row_copies(rows);
+    const int span = kBlockM / copies;           // rows of a copy
+    const int r = row & (span - 1);              // the row it stands for
+    const int nch = 4 / copies;                  // 32-column pieces of a block that are this warp's,
+    const int ch0 = (quad / nch) * nch;          // from this one on
+    const bool warp_rows = (r & ~31) < rows;     // the warp has a row at all
+    const int tok = r / a.group;
+    int lo, hi, lo_all, hi_all, x;
+    const int p0 = w.len - w.q_len;
+    keys_of(a, w.len, p0 + tok, &lo, &hi);
+    keys_of(a, w.len, p0, &x, &hi_all);
+    keys_of(a, w.len, p0 + w.q_len - 1, &lo_all, &x);
+    float m_run = -INFINITY, l_run = 0.f;
+    bool first = true;
+    for (int j = w.s0 + t; j < w.s1; j += 2) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm->s_full[t], blk_it & 1u, abort_flag, &g_paged_err, code))) return;
+      ++blk_it;
+      if (warp_rows) {
+        tc_fence_after();
+        const int k0 = j * kBlockN;
+        const bool whole = k0 >= lo_all && k0 + kBlockN <= hi_all;
+        uint32_t s[4][32];
 #pragma unroll
-  for (int c = 0; c < C; ++c) o[lane * C + c] = __float2bfloat16_rn(acc[c] * inv);
-  if (lane == 0) a.lse[static_cast<int64_t>(h) * a.lse_stride + t] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        for (int c = 0; c < 4; ++c)
+          if (c < nch) tmem_ld32(tS + (ch0 + c) * 32, s[c]);
+        tmem_wait_ld();
+        float m_raw = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < nch) {
+            reg_fence(s[c]);
+            if (!whole) mask32(s[c], k0 + (ch0 + c) * 32, lo, hi);
+            m_raw = fmaxf(m_raw, max32(s[c]));
+          }
+        float alpha;
+        const bool need = raise_max(m_raw * sl2, &m_run, &alpha);
+        l_run *= alpha;
+        const float neg_m = neg_or_zero(m_run);
+        uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < nch) {
+            uint32_t p[16];
+            exp_pack(s[c], sl2, neg_m, acc, p);
+            tmem_st16(tS + (ch0 + c) * 16, p);
+          }
+        if (nch < 4) {                           // the other warps' columns do not count for this copy
+          uint32_t z[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = 0u;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c < ch0 || c >= ch0 + nch) tmem_st16(tS + c * 16, z);
+        }
+        if (!first && __any_sync(0xffffffffu, need)) rescale_o<HD>(tO, alpha);
+        first = false;
+        tmem_wait_st();
+        tc_fence_before();
+        float ls0, ls1;
+        f2_unpack(f2_add(acc[0], acc[1]), ls0, ls1);
+        l_run += ls0 + ls1;
+      }
+      mbar_arrive(&sm->p_full[t]);
+    }
+    const bool loaded = w.s1 > w.s0;
+    if (!loaded) {                               // nothing is seen; the Q buffer may be the next item's already
+      const int F8 = HD / 8;
+      for (int y = threadIdx.x; y < rows * F8; y += 2 * kBlockM) {
+        const int rr = y / F8, tk = rr / a.group, h = w.hk * a.group + rr - tk * a.group;
+        const int64_t orow = static_cast<int64_t>(w.q_row0 + tk) * a.num_heads + h;
+        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + orow * HD)[y % F8] = make_uint4(0, 0, 0, 0);
+        if (y % F8 == 0) a.lse[static_cast<int64_t>(h) * a.lse_stride + w.q_row0 + tk] = -INFINITY;
+      }
+      continue;
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(&sm->o_full[t], q_it & 1u, abort_flag, &g_paged_err, code))) return;
+    ++q_it;
+    tc_fence_after();
+    // ---------------------------------------------------------- join the parts of each row
+    sm->ml[t * kBlockM + row] = make_float2(m_run, l_run);
+    if (!__all_sync(0xffffffffu, mbar_sync(&sm->all_sync, sync_uses, abort_flag, &g_paged_err, code))) return;
+    float m_all = -INFINITY;
+    for (int i = 0; i < 2 * copies; ++i) m_all = fmaxf(m_all, sm->ml[i * span + r].x);
+    float l_all = 0.f;
+    for (int i = 0; i < 2 * copies; ++i) {
+      const float2 v = sm->ml[i * span + r];
+      if (v.x != -INFINITY) l_all += v.y * fast_exp2(v.x - m_all);
+    }
+    const float scale = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_all) / l_all;
+    const bool final_rows = w.active <= 1;
+    const int64_t row0 = final_rows ? w.q_row0 : w.part0 + static_cast<int64_t>(w.split) * w.q_len;
+    if (t == 0 && quad * 32 < span && r < rows) {   // the first copy's threads know the row's LSE
+      const int h = w.hk * a.group + r - tok * a.group;
+      const float lse = l_all > 0.f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
+      if (final_rows)
+        a.lse[static_cast<int64_t>(h) * a.lse_stride + w.q_row0 + tok] = lse;
+      else
+        a.lse_part[(row0 + tok) * a.num_heads + h] = lse;
+    }
+    // a quarter of the columns at a time through the Q buffer, which is dead
+    // now: [t * 128 + row][HD / 4] floats, 16-byte pieces swizzled by the row
+    constexpr int F4 = HD / 16;                  // 16-byte pieces of a quarter row
+    float4* stage = reinterpret_cast<float4*>(sm->q[0]);
+    const int swz = HD == 128 ? row & 7 : (row >> 1) & 3;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      __syncwarp();
+      if (warp_rows) {
+        float4* dst = stage + (t * kBlockM + row) * F4;
+        if constexpr (HD == 128) {
+          uint32_t o[32];
+          tmem_ld32(tO + c * 32, o);
+          tmem_wait_ld();
+          reg_fence(o);
+#pragma unroll
+          for (int i = 0; i < F4; ++i) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (scale != 0.f)
+              v = make_float4(__uint_as_float(o[4 * i]) * scale, __uint_as_float(o[4 * i + 1]) * scale,
+                              __uint_as_float(o[4 * i + 2]) * scale, __uint_as_float(o[4 * i + 3]) * scale);
+            dst[i ^ swz] = v;
+          }
+        } else {
+          uint32_t o[16];
+          tmem_ld16(tO + c * 16, o);
+          tmem_wait_ld();
+          reg_fence(o);
+#pragma unroll
+          for (int i = 0; i < F4; ++i) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (scale != 0.f)
+              v = make_float4(__uint_as_float(o[4 * i]) * scale, __uint_as_float(o[4 * i + 1]) * scale,
+                              __uint_as_float(o[4 * i + 2]) * scale, __uint_as_float(o[4 * i + 3]) * scale);
+            dst[i ^ swz] = v;
+          }
+        }
+      }
+      if (!__all_sync(0xffffffffu, mbar_sync(&sm->all_sync, sync_uses, abort_flag, &g_paged_err, code))) return;
+      for (int y = threadIdx.x; y < rows * F4; y += 2 * kBlockM) {
+        const int rr = y / F4, f = y % F4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < 2 * copies; ++i) {
+          const int rw = i * span + rr;          // group (i / copies), copy (i % copies): 128 rows apart
+          const int sw = HD == 128 ? rw & 7 : (rw >> 1) & 3;
+          const float4 u = stage[rw * F4 + (f ^ sw)];
+          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+        const int tk = rr / a.group, h = w.hk * a.group + rr - tk * a.group;
+        const int64_t off = ((row0 + tk) * a.num_heads + h) * HD + c * (HD / 4) + 4 * f;
+        if (final_rows)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + off) =
+              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        else
+          *reinterpret_cast<float4*>(a.o_part + off) = v;
+      }
+      if (c == 3) fence_proxy_async_smem();      // the next item's Q may land there after this
+      if (!__all_sync(0xffffffffu, mbar_sync(&sm->all_sync, sync_uses, abort_flag, &g_paged_err, code))) return;
+    }
+    if (threadIdx.x == 0) mbar_arrive(&sm->q_empty[0]);
+  }
+}
+
+template <int HD, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttnArgs args) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  auto* sm = reinterpret_cast<PagedSmem<HD, PAIR>*>(smem_raw);
+  if ((smem_u32(smem_raw) & 1023u) != 0) {       // the declared alignment; the swizzle needs it
+    if (threadIdx.x == 0) atomicOr(&g_paged_err, ERR_BAD_WORK);
+    return;
+  }
+  constexpr int kStages = stages<HD, PAIR>();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sm->q_full[t], 1);
+      mbar_init(&sm->q_empty[t], PAIR ? 2 : 3);  // its issuers' last S, and the epilogue
+      mbar_init(&sm->s_full[t], 1);
+      mbar_init(&sm->p_full[t], 128);
+      mbar_init(&sm->o_full[t], 1);
+      mbar_init(&sm->turn[t], 128);
+      mbar_init(&sm->grp_sync[t], 128);
+    }
+    mbar_init(&sm->all_sync, 256);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm->kv_full[s], 1);
+      mbar_init(&sm->kv_empty[s], PAIR ? 2 : 1); // PAIR: both issuers pass every stage
+      mbar_init(&sm->tail[s], 1);
+    }
+    ring_init(&sm->ring, kReaders);
+    sm->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp0) {
+    tmem_alloc(&sm->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem_base;
+
+  if (warp == kProducerWarp) {
+    produce<HD, PAIR>(sm, args, maps);
+  } else if (warp == kMmaWarp0 || warp == kMmaWarp0 + 1) {
+    if (lane == 0) issue<HD, PAIR>(sm, args, tmem, warp - kMmaWarp0);
+  } else if (warp == kTailWarp) {
+    clear_tails<HD, PAIR>(sm, args);
+  } else if constexpr (PAIR) {
+    softmax_pair<HD>(sm, args, maps, tmem);
+  } else {
+    softmax_split<HD>(sm, args, tmem);
+  }
+
+  __syncwarp();
+  if (*reinterpret_cast<volatile int*>(&sm->abort_flag)) drain_delay(2000000ull);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp0) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------ joining the splits
+// One block per (query, head) row whose keys were split:
+//     lse = log sum_s exp(lse_s),  o = sum_s exp(lse_s - lse) o_s.
+// The warps take the splits in turn, so that few rows with many splits still
+// have their loads in flight together.  Rows of one split were written in
+// place.
+constexpr int kJoinThreads = 128;
+
+template <int HD, bool PAIR>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
+  constexpr int C = HD / 32;
+  constexpr int kWarps = kJoinThreads / 32;
+  __shared__ float part[kWarps][HD];
+  __shared__ float lse_s[kMaxSplits];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t tok_all = blockIdx.x / a.num_heads;
+  const int h = static_cast<int>(blockIdx.x - tok_all * a.num_heads);
+  int lo = 0, hi = a.n_segs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.segs[mid].tok0 <= tok_all) lo = mid; else hi = mid - 1;
+  }
+  const PagedSeg& s = a.segs[lo];
+  if (s.splits <= 1) return;
+  const int tok = static_cast<int>(tok_all) - s.tok0;
+  int len = __ldg(a.kv_lens + s.seq);
+  len = max(0, min(len, a.max_kv_len));
+  const int tile = tok / a.tile_tokens;
+  const Range r = unit_blocks<PAIR>(a, len, s.q_len, PAIR ? tile & ~1 : 0);
+  const int n = (r.b1 - r.b0 + a.split_blocks - 1) / a.split_blocks;
+  if (n <= 1) return;
+  const int64_t row0 = (s.part0 + tok) * a.num_heads + h;
+  const int64_t step = static_cast<int64_t>(s.q_len) * a.num_heads;
+  for (int i = threadIdx.x; i < n; i += kJoinThreads) lse_s[i] = a.lse_part[row0 + i * step];
+  __syncthreads();
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, lse_s[i]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const bool seen = m != -INFINITY;
+  float sum = 0.f;
+  for (int i = lane; i < n; i += 32) sum += seen ? expf(lse_s[i] - m) : 0.f;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  const float inv = seen ? 1.f / sum : 0.f;
+  float acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += kWarps) {
+    const float wgt = seen ? expf(lse_s[i] - m) * inv : 0.f;
+    const float* src = a.o_part + (row0 + i * step) * HD + lane * C;
+    if constexpr (C == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      acc[0] = fmaf(wgt, v.x, acc[0]); acc[1] = fmaf(wgt, v.y, acc[1]);
+      acc[2] = fmaf(wgt, v.z, acc[2]); acc[3] = fmaf(wgt, v.w, acc[3]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      acc[0] = fmaf(wgt, v.x, acc[0]); acc[1] = fmaf(wgt, v.y, acc[1]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) part[warp][lane * C + c] = acc[c];
+  __syncthreads();
+  for (int c = threadIdx.x; c < HD; c += kJoinThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) v += part[q][c];
+    static_cast<__nv_bfloat16*>(a.o)[(static_cast<int64_t>(s.q_row0 + tok) * a.num_heads + h) * HD + c] =
+        __float2bfloat16_rn(v);
+  }
+  if (threadIdx.x == 0)
+    a.lse[static_cast<int64_t>(h) * a.lse_stride + s.q_row0 + tok] = seen ? m + logf(sum) : -INFINITY;
+}
+
+template <int HD, bool PAIR>
+cudaError_t launch_one(const PagedMaps& maps, const PagedAttnArgs& a, cudaStream_t stream) {
+  constexpr size_t smem = sizeof(PagedSmem<HD, PAIR>);
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<HD, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  paged_attn_kernel<HD, PAIR><<<a.n_items, kThreads, smem, stream>>>(maps, a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attn(int head_dim, const PagedAttnArgs& a, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(a.tokens) * a.num_heads;
-  const int64_t blocks = (rows + kSimpleThreads / 32 - 1) / (kSimpleThreads / 32);
-  if (head_dim == 64)
-    paged_attn_kernel<64><<<static_cast<unsigned>(blocks), kSimpleThreads, 0, stream>>>(a);
-  else
-    paged_attn_kernel<128><<<static_cast<unsigned>(blocks), kSimpleThreads, 0, stream>>>(a);
+cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, const PagedAttnArgs& a,
+                              cudaStream_t stream) {
+  if (head_dim == 64) return pair ? launch_one<64, true>(maps, a, stream) : launch_one<64, false>(maps, a, stream);
+  return pair ? launch_one<128, true>(maps, a, stream) : launch_one<128, false>(maps, a, stream);
+}
+
+cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnArgs& a, cudaStream_t stream) {
+  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.tokens) * a.num_heads);
+  if (head_dim == 64) {
+    if (pair) paged_join_kernel<64, true><<<blocks, kJoinThreads, 0, stream>>>(a);
+    else paged_join_kernel<64, false><<<blocks, kJoinThreads, 0, stream>>>(a);
+  } else {
+    if (pair) paged_join_kernel<128, true><<<blocks, kJoinThreads, 0, stream>>>(a);
+    else paged_join_kernel<128, false><<<blocks, kJoinThreads, 0, stream>>>(a);
+  }
   return cudaGetLastError();
 }
 

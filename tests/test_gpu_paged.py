@@ -123,6 +123,27 @@ def test_long_cache_is_split_and_joined():
     b.check(o, lse)
 
 
+def test_a_serving_batch_of_long_ragged_sequences():
+    """More work items than SMs, each of many key blocks, taken over and over:
+    sampled rows against the definition in 64 bits, and the same bits again."""
+    lens = [1501 + i * 12701 % 14885 for i in range(48)]
+    b = Batch([1] * 48, lens, 40, 8, 128, 16, seed=16, fill=1.0)
+    o, lse = b.run()
+    for _ in range(20):
+        o2, l2 = b.run()
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+    zl.sync_check()
+    for s in range(0, 48, 5):
+        rows = b.dtable[s, :-(-lens[s] // 16)].long()
+        k, v = (x[rows].transpose(1, 2).flatten(0, 1)[:lens[s]].double() for x in (b.k_pages, b.v_pages))
+        for h in range(0, 40, 3):
+            p = (k[:, h // 5] @ b.q[s, h].double()) * 128 ** -0.5
+            w = torch.softmax(p, 0)
+            want, reach = w @ v[:, h // 5], w @ v[:, h // 5].abs()
+            assert torch.all((o[s, h].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * reach + 2.0 ** -8 * want.abs())
+            assert abs(float(lse[h, s].double() - torch.logsumexp(p, 0))) <= 2e-4 + 2.0 ** -20 * 15
+
+
 def test_few_chunk_rows_over_a_long_cache():
     b = Batch([140, 5], [9000, 333], 2, 1, 64, 16, seed=5)
     for kw in ({}, {"causal": False}, {"window": 2500}):
