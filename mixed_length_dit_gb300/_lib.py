@@ -151,8 +151,8 @@ def load() -> ctypes.CDLL:
     lib.zl_varlen_attn_bwd_static.argtypes = [vp, vp, vp, vp, vp, vp, i32p, i32p, c_i32, c_i32, c_i32,
                                               c_f32, vp, vp, vp, vp]
     c_f64, f64p = ctypes.c_double, ctypes.POINTER(ctypes.c_double)
-    ropep, cachep = ctypes.POINTER(Rope), ctypes.POINTER(PagedCache)
-    tabp, poolp = ctypes.POINTER(PageTables), ctypes.POINTER(PagePool)
+    ropep = ctypes.POINTER(Rope)
+    cachep = tabp = poolp = vp          # zl_paged_cache_t, zl_page_tables_t, zl_page_pool_t, by any pointer
     lib.zl_rope_init.argtypes = [ropep, c_i32, c_i32, c_i32, i32p, c_f64, c_f64, f64p, c_f64]
     rope_args = [ropep, vp, c_i64, vp, c_i64, vp, c_i64, c_i64, c_i32, c_i32, c_i32, vp, c_i64, vp, c_i64, vp]
     lib.zl_rope_fwd.argtypes = rope_args
@@ -186,24 +186,24 @@ def check(status: int, where: str) -> None:
 class HostInt32:
     """A host int32 array made once and passed to many calls (the cu_seqlens
     of a batch that every layer shares)."""
-    __slots__ = ("array", "_n", "last")
+    __slots__ = ("array", "n", "last")
 
     def __init__(self, values):
-        self.array, self._n = int32_array(values)
-        self.last = int(self.array[self._n - 1]) if self._n else None
+        self.array, self.n = int32_array(values)
+        self.last = int(self.array[self.n - 1]) if self.n else None
 
     def __len__(self):
-        return self._n
+        return self.n
 
     def __iter__(self):
-        return iter(self.array[:self._n])
+        return iter(self.array[:self.n])
 
 
 def int32_array(values):
     """Host int32 array for cu_seqlens (list, tuple, numpy or CPU tensor; an
     array made by an earlier call is taken as it is)."""
     if isinstance(values, HostInt32):
-        return values.array, len(values)
+        return values.array, values.n
     vals = [int(x) for x in (values.tolist() if hasattr(values, "tolist") else values)]
     return (ctypes.c_int32 * max(1, len(vals)))(*vals), len(vals)
 

@@ -10,14 +10,16 @@
 
 namespace zl {
 
-// Sequences whose token ranges one append launch carries in its parameters.
-constexpr int kAppendSeqs = kMaxSegs;
+// A launch carries its sequences by value.  Most calls have few, and a launch
+// pays for every byte of its parameters, so each kernel exists for kFewSegs
+// sequences and for kMaxSegs.
+constexpr int kFewSegs = 64;
 
 // One launch of rotary positions.  As rope_fwd / rope_bwd it turns `q` and
 // `k` into `q_out` and `k_out` at given positions; as paged_append (`append`
 // set) the keys go into the cache's pages, the values beside them, and the
 // positions follow from the cache's lengths unless they are given.
-struct RopeArgs {
+struct RopeHead {
   const void* q;
   const void* k;
   const void* v;                // append only
@@ -45,9 +47,14 @@ struct RopeArgs {
   int32_t n_seqs;               // sequences of this launch
   int32_t seq0;                 // table row of the launch's first sequence
   zl_rope_t rope;
-  int32_t cu[kAppendSeqs + 1];  // append: first token of each sequence of the launch
 };
-static_assert(sizeof(RopeArgs) <= 32764, "rotary arguments exceed the kernel parameter space");
+
+// N sequences; N = 0: no append.
+template <int N>
+struct RopeArgs : RopeHead {
+  int32_t cu[N + 1];            // append: first token of each sequence of the launch
+};
+static_assert(sizeof(RopeArgs<kMaxSegs>) <= 32764, "rotary arguments exceed the kernel parameter space");
 
 // Most splits of one sequence's keys.
 constexpr int kMaxSplits = 128;
@@ -63,7 +70,7 @@ struct PagedSeg {
   int64_t part0;     // splits > 1: its first row in o_part / lse_part
 };
 
-struct PagedAttnArgs {
+struct PagedAttnHead {
   const int32_t* page_table;
   const int32_t* kv_lens;
   void* o;                      // [Tq][H][d] bf16
@@ -86,7 +93,11 @@ struct PagedAttnArgs {
   float scale_log2;             // softmax scale * log2(e)
   int32_t n_items;
   int32_t n_segs;
-  PagedSeg segs[kMaxSegs];
+};
+
+template <int N>
+struct PagedAttnArgs : PagedAttnHead {
+  PagedSeg segs[N];
 };
 
 // Tensor maps: q[i] takes the tokens of a tile that holds 1, 2 or 4 copies of
@@ -97,7 +108,7 @@ struct PagedMaps {
   CUtensorMap q[3];
   CUtensorMap k, v, o;
 };
-static_assert(sizeof(PagedAttnArgs) + sizeof(PagedMaps) <= 32764, "paged attention arguments exceed the kernel parameter space");
+static_assert(sizeof(PagedAttnArgs<kMaxSegs>) + sizeof(PagedMaps) <= 32764, "paged attention arguments exceed the kernel parameter space");
 
 // A pool of pages seen by the kernels that move whole pages.
 struct PagePool {
@@ -129,12 +140,13 @@ inline size_t pages_workspace_words(int64_t num_pages) {
   return kPageHeader + kMaxSlots + 3 * static_cast<size_t>(num_pages);
 }
 
-cudaError_t launch_rope(const RopeArgs& args, int num_sms, cudaStream_t stream);
+// Takes the head's sequences from args.cu when args.append is set.
+cudaError_t launch_rope(const RopeArgs<kMaxSegs>& args, int num_sms, cudaStream_t stream);
 // pair: sequences of more than one query tile each; else of one.
-cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, const PagedAttnArgs& args,
+cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, const PagedAttnArgs<kMaxSegs>& args,
                               cudaStream_t stream);
 // Joins the split rows of a launch_paged_attn with the same arguments.
-cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnArgs& args, cudaStream_t stream);
+cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnArgs<kMaxSegs>& args, cudaStream_t stream);
 cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const int32_t* dst, int32_t n, int num_sms,
                               cudaStream_t stream);
 cudaError_t launch_pages_extend(const PageTable& t, const int32_t* counts, int32_t* status, cudaStream_t stream);

@@ -36,6 +36,8 @@
 //               (unwritten rows may be NaN, and 0 * NaN is not 0)
 // The lengths are read on the device, so a captured launch follows them.
 #define ZL_TRY_WAIT_HINT_NS 10000
+#include <atomic>
+
 #include "common.cuh"
 #include "paged.h"
 
@@ -93,13 +95,13 @@ struct Range {
 };
 
 // Keys [lo, hi) that the query at position p of a sequence of `len` sees.
-__device__ __forceinline__ void keys_of(const PagedAttnArgs& a, int len, int p, int* lo, int* hi) {
+__device__ __forceinline__ void keys_of(const PagedAttnHead& a, int len, int p, int* lo, int* hi) {
   *hi = a.causal ? max(0, min(len, p + 1)) : len;
   *lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
 }
 
 // Blocks that queries [t0, t1) of the sequence see.
-__device__ __forceinline__ Range blocks_of(const PagedAttnArgs& a, int len, int q_len, int t0, int t1) {
+__device__ __forceinline__ Range blocks_of(const PagedAttnHead& a, int len, int q_len, int t0, int t1) {
   int lo, hi, x;
   keys_of(a, len, len - q_len + t0, &lo, &x);
   keys_of(a, len, len - q_len + t1 - 1, &x, &hi);
@@ -120,7 +122,8 @@ struct Work {
   bool has[2];      // the tile exists
 };
 
-__device__ __forceinline__ int find_seg(const PagedAttnArgs& a, int it) {
+template <int N>
+__device__ __forceinline__ int find_seg(const PagedAttnArgs<N>& a, int it) {
   int lo = 0, hi = a.n_segs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -137,7 +140,7 @@ __device__ __forceinline__ Range cut(Range r, int s0, int s1) {
 // The blocks that the splits of a unit (first tile `tile0`) divide: the union
 // of its tiles'.
 template <bool PAIR>
-__device__ __forceinline__ Range unit_blocks(const PagedAttnArgs& a, int len, int q_len, int tile0) {
+__device__ __forceinline__ Range unit_blocks(const PagedAttnHead& a, int len, int q_len, int tile0) {
   const int t0 = tile0 * a.tile_tokens;
   Range r = blocks_of(a, len, q_len, t0, min(q_len, t0 + a.tile_tokens));
   if (PAIR && t0 + a.tile_tokens < q_len) {
@@ -150,8 +153,8 @@ __device__ __forceinline__ Range unit_blocks(const PagedAttnArgs& a, int len, in
 
 // Items of a segment: key head outermost, then the unit, last tokens first
 // (under a causal mask they see the most), then the split.
-template <bool PAIR>
-__device__ __forceinline__ Work decode(const PagedAttnArgs& a, int it, int len) {
+template <bool PAIR, int N>
+__device__ __forceinline__ Work decode(const PagedAttnArgs<N>& a, int it, int len) {
   const PagedSeg& s = a.segs[find_seg(a, it)];
   Work w;
   w.seq = s.seq;
@@ -223,8 +226,8 @@ __device__ __forceinline__ int take(SM* sm, uint32_t n, uint32_t code, bool warp
 }
 
 // ------------------------------------------------------------------ producer
-template <int HD, bool PAIR>
-__device__ void produce(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs& a, const PagedMaps& maps) {
+template <int HD, bool PAIR, int N>
+__device__ void produce(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps) {
   using Ring = Stages<HD, PAIR>;
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm->abort_flag;
@@ -342,8 +345,8 @@ __device__ void produce(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs& a, const P
 }
 
 // ------------------------------------------------------------------ MMA issuer t
-template <int HD, bool PAIR>
-__device__ void issue(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs& a, uint32_t tmem, int t) {
+template <int HD, bool PAIR, int N>
+__device__ void issue(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, uint32_t tmem, int t) {
   using Ring = Stages<HD, PAIR>;
   constexpr uint32_t idesc_qk = idesc_bf16(kBlockM, kBlockN, false, false);
   constexpr uint32_t idesc_pv = idesc_bf16(kBlockM, HD, false, true);
@@ -413,8 +416,8 @@ __device__ void issue(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs& a, uint32_t 
 }
 
 // ------------------------------------------------------------------ tail warp
-template <int HD, bool PAIR>
-__device__ void clear_tails(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs& a) {
+template <int HD, bool PAIR, int N>
+__device__ void clear_tails(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a) {
   using Ring = Stages<HD, PAIR>;
   const int lane = threadIdx.x & 31;
   uint32_t base0 = 0, base1 = 0, phases = 0;     // uses of ring 0 and 1 by earlier items; parity of each tail barrier
@@ -513,8 +516,8 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
 __device__ __forceinline__ float neg_or_zero(float m) { return m == -INFINITY ? 0.f : -m; }
 
 // PAIR: group t runs tile t.
-template <int HD>
-__device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs& a, const PagedMaps& maps, uint32_t tmem) {
+template <int HD, int N>
+__device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = warp >> 2;
   const int row = (warp & 3) * 32 + lane;
@@ -713,8 +716,8 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs& a, co
 
 // SPLIT: group t takes every other block; with copies of the rows, a warp
 // takes its own part of a block's columns.
-template <int HD>
-__device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs& a, uint32_t tmem) {
+template <int HD, int N>
+__device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& a, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = warp >> 2, quad = warp & 3;
   const int row = quad * 32 + lane;
@@ -894,9 +897,9 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs& a, 
   }
 }
 
-template <int HD, bool PAIR>
+template <int HD, bool PAIR, int N>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttnArgs args) {
+paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttnArgs<N> args) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   auto* sm = reinterpret_cast<PagedSmem<HD, PAIR>*>(smem_raw);
   if ((smem_u32(smem_raw) & 1023u) != 0) {       // the declared alignment; the swizzle needs it
@@ -936,15 +939,15 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
   const uint32_t tmem = sm->tmem_base;
 
   if (warp == kProducerWarp) {
-    produce<HD, PAIR>(sm, args, maps);
+    produce<HD, PAIR, N>(sm, args, maps);
   } else if (warp == kMmaWarp0 || warp == kMmaWarp0 + 1) {
-    if (lane == 0) issue<HD, PAIR>(sm, args, tmem, warp - kMmaWarp0);
+    if (lane == 0) issue<HD, PAIR, N>(sm, args, tmem, warp - kMmaWarp0);
   } else if (warp == kTailWarp) {
-    clear_tails<HD, PAIR>(sm, args);
+    clear_tails<HD, PAIR, N>(sm, args);
   } else if constexpr (PAIR) {
-    softmax_pair<HD>(sm, args, maps, tmem);
+    softmax_pair<HD, N>(sm, args, maps, tmem);
   } else {
-    softmax_split<HD>(sm, args, tmem);
+    softmax_split<HD, N>(sm, args, tmem);
   }
 
   __syncwarp();
@@ -963,8 +966,8 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
 // place.
 constexpr int kJoinThreads = 128;
 
-template <int HD, bool PAIR>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
+template <int HD, bool PAIR, int N>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs<N> a) {
   constexpr int C = HD / 32;
   constexpr int kWarps = kJoinThreads / 32;
   __shared__ float part[kWarps][HD];
@@ -1030,35 +1033,65 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     a.lse[static_cast<int64_t>(h) * a.lse_stride + s.q_row0 + tok] = seen ? m + logf(sum) : -INFINITY;
 }
 
-template <int HD, bool PAIR>
-cudaError_t launch_one(const PagedMaps& maps, const PagedAttnArgs& a, cudaStream_t stream) {
+// The first n_segs of N.
+template <int N>
+PagedAttnArgs<N> cut(const PagedAttnArgs<kMaxSegs>& a) {
+  PagedAttnArgs<N> r;
+  static_cast<PagedAttnHead&>(r) = a;
+  for (int i = 0; i < a.n_segs; ++i) r.segs[i] = a.segs[i];
+  return r;
+}
+
+template <int HD, bool PAIR, int N>
+cudaError_t launch_attn(const PagedMaps& maps, const PagedAttnArgs<N>& a, cudaStream_t stream) {
   constexpr size_t smem = sizeof(PagedSmem<HD, PAIR>);
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<HD, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  // once per device
+  static std::atomic<uint64_t> done[2];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  paged_attn_kernel<HD, PAIR><<<a.n_items, kThreads, smem, stream>>>(maps, a);
+  std::atomic<uint64_t>& word = done[(dev >> 6) & 1];
+  if (!(word.load() >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(paged_attn_kernel<HD, PAIR, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    word.fetch_or(uint64_t(1) << (dev & 63));
+  }
+  paged_attn_kernel<HD, PAIR, N><<<a.n_items, kThreads, smem, stream>>>(maps, a);
   return cudaGetLastError();
+}
+
+template <int HD, bool PAIR, int N>
+cudaError_t launch_join(const PagedAttnArgs<N>& a, cudaStream_t stream) {
+  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.tokens) * a.num_heads);
+  paged_join_kernel<HD, PAIR, N><<<blocks, kJoinThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int HD, bool PAIR>
+cudaError_t attn_kind(const PagedMaps& maps, const PagedAttnArgs<kMaxSegs>& a, cudaStream_t stream) {
+  return a.n_segs <= kFewSegs ? launch_attn<HD, PAIR, kFewSegs>(maps, cut<kFewSegs>(a), stream)
+                              : launch_attn<HD, PAIR, kMaxSegs>(maps, a, stream);
+}
+
+template <int HD, bool PAIR>
+cudaError_t join_kind(const PagedAttnArgs<kMaxSegs>& a, cudaStream_t stream) {
+  return a.n_segs <= kFewSegs ? launch_join<HD, PAIR, kFewSegs>(cut<kFewSegs>(a), stream)
+                              : launch_join<HD, PAIR, kMaxSegs>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, const PagedAttnArgs& a,
+cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, const PagedAttnArgs<kMaxSegs>& a,
                               cudaStream_t stream) {
-  if (head_dim == 64) return pair ? launch_one<64, true>(maps, a, stream) : launch_one<64, false>(maps, a, stream);
-  return pair ? launch_one<128, true>(maps, a, stream) : launch_one<128, false>(maps, a, stream);
+  if (head_dim == 64) return pair ? attn_kind<64, true>(maps, a, stream) : attn_kind<64, false>(maps, a, stream);
+  return pair ? attn_kind<128, true>(maps, a, stream) : attn_kind<128, false>(maps, a, stream);
 }
 
-cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnArgs& a, cudaStream_t stream) {
-  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.tokens) * a.num_heads);
-  if (head_dim == 64) {
-    if (pair) paged_join_kernel<64, true><<<blocks, kJoinThreads, 0, stream>>>(a);
-    else paged_join_kernel<64, false><<<blocks, kJoinThreads, 0, stream>>>(a);
-  } else {
-    if (pair) paged_join_kernel<128, true><<<blocks, kJoinThreads, 0, stream>>>(a);
-    else paged_join_kernel<128, false><<<blocks, kJoinThreads, 0, stream>>>(a);
-  }
-  return cudaGetLastError();
+cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnArgs<kMaxSegs>& a, cudaStream_t stream) {
+  if (head_dim == 64) return pair ? join_kind<64, true>(a, stream) : join_kind<64, false>(a, stream);
+  return pair ? join_kind<128, true>(a, stream) : join_kind<128, false>(a, stream);
 }
 
 uint32_t paged_attn_take_error() {

@@ -118,12 +118,14 @@ __device__ __forceinline__ void turn_unit(const T* src, T* dst, int unit, int ha
   }
 }
 
-template <typename T, bool VECTOR, bool INTERLEAVED, bool APPEND>
+// SEQS: sequences of an append's parameters; 0: no append.
+template <typename T, bool VECTOR, bool INTERLEAVED, int SEQS>
 __global__ void __launch_bounds__(kRopeThreads)
-rope_kernel(const __grid_constant__ RopeArgs a, int tokens_per_block, int heads_per_block) {
+rope_kernel(const __grid_constant__ RopeArgs<SEQS> a, int tokens_per_block, int heads_per_block) {
   __shared__ __align__(16) float2 cs[kTokensMax][ZL_ROPE_MAX_PAIRS];
   __shared__ int32_t pos_of[kTokensMax];       // append: position in the sequence
   __shared__ int64_t page_row[kTokensMax];     // append: first row of the token's page, + its row; -1: left out
+  constexpr bool APPEND = SEQS > 0;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tokens_per_block), a.tokens - t0));
   const int half = a.rope.rot_dim / 2;
@@ -208,17 +210,37 @@ rope_kernel(const __grid_constant__ RopeArgs a, int tokens_per_block, int heads_
   }
 }
 
-template <typename T, bool VECTOR, bool APPEND>
-void launch_il(const RopeArgs& a, dim3 grid, int tpb, int hpb, cudaStream_t stream) {
-  if (a.rope.interleaved)
-    rope_kernel<T, VECTOR, true, APPEND><<<grid, kRopeThreads, 0, stream>>>(a, tpb, hpb);
-  else
-    rope_kernel<T, VECTOR, false, APPEND><<<grid, kRopeThreads, 0, stream>>>(a, tpb, hpb);
+template <int SEQS>
+RopeArgs<SEQS> cut(const RopeArgs<kMaxSegs>& a) {
+  RopeArgs<SEQS> r;
+  static_cast<RopeHead&>(r) = a;
+  for (int i = 0; i <= SEQS && i <= a.n_seqs; ++i) r.cu[i] = a.cu[i];
+  return r;
+}
+
+template <typename T, bool VECTOR, bool INTERLEAVED>
+void launch_kind(const RopeArgs<kMaxSegs>& a, dim3 grid, int tpb, int hpb, cudaStream_t stream) {
+  if (!a.append) {
+    rope_kernel<T, VECTOR, INTERLEAVED, 0><<<grid, kRopeThreads, 0, stream>>>(cut<0>(a), tpb, hpb);
+  } else if constexpr (sizeof(T) == 2) {
+    if (a.n_seqs <= kFewSegs)
+      rope_kernel<T, VECTOR, INTERLEAVED, kFewSegs><<<grid, kRopeThreads, 0, stream>>>(cut<kFewSegs>(a), tpb, hpb);
+    else
+      rope_kernel<T, VECTOR, INTERLEAVED, kMaxSegs><<<grid, kRopeThreads, 0, stream>>>(a, tpb, hpb);
+  }
+}
+
+template <typename T>
+void launch_type(const RopeArgs<kMaxSegs>& a, bool vec, dim3 grid, int tpb, int hpb, cudaStream_t stream) {
+  if (vec && a.rope.interleaved) launch_kind<T, true, true>(a, grid, tpb, hpb, stream);
+  else if (vec) launch_kind<T, true, false>(a, grid, tpb, hpb, stream);
+  else if (a.rope.interleaved) launch_kind<T, false, true>(a, grid, tpb, hpb, stream);
+  else launch_kind<T, false, false>(a, grid, tpb, hpb, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rope(const RopeArgs<kMaxSegs>& a, int num_sms, cudaStream_t stream) {
   const int heads = a.nq + (a.append ? 2 : 1) * a.nk;
   if (a.tokens == 0 || heads == 0) return cudaSuccess;
   const int per_unit = a.elem_bytes == 2 ? 8 : 4;
@@ -232,17 +254,8 @@ cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   int hpb = heads;
   while (hpb > fill && blocks * ((heads + hpb - 1) / hpb) < 2 * num_sms) hpb = (hpb + 1) / 2;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + hpb - 1) / hpb));
-  if (a.elem_bytes == 2) {
-    if (a.append)
-      vec ? launch_il<__nv_bfloat16, true, true>(a, grid, tpb, hpb, stream)
-          : launch_il<__nv_bfloat16, false, true>(a, grid, tpb, hpb, stream);
-    else
-      vec ? launch_il<__nv_bfloat16, true, false>(a, grid, tpb, hpb, stream)
-          : launch_il<__nv_bfloat16, false, false>(a, grid, tpb, hpb, stream);
-  } else {
-    vec ? launch_il<float, true, false>(a, grid, tpb, hpb, stream)
-        : launch_il<float, false, false>(a, grid, tpb, hpb, stream);
-  }
+  if (a.elem_bytes == 2) launch_type<__nv_bfloat16>(a, vec, grid, tpb, hpb, stream);
+  else launch_type<float>(a, vec, grid, tpb, hpb, stream);
   return cudaGetLastError();
 }
 

@@ -3,7 +3,6 @@
 // of include/zl_attn.h.
 #include <algorithm>
 #include <cmath>
-#include <cstddef>
 #include <cstring>
 
 #include <cuda.h>
@@ -18,7 +17,7 @@ namespace {
 using zl::aligned16;
 using zl::device_sms;
 using zl::launch_counted;
-using zl::RopeArgs;
+using RopeArgs = zl::RopeArgs<zl::kMaxSegs>;
 
 bool page_size_ok(int32_t p) { return p >= 16 && p <= 256 && (p & (p - 1)) == 0; }
 
@@ -72,7 +71,7 @@ zl_status rope(const zl_rope_t* plan, const void* q, int64_t q_stride, const voi
   st = device_sms(&sms);
   if (st != ZL_OK) return st;
   static thread_local RopeArgs a;
-  std::memset(&a, 0, sizeof(a));
+  static_cast<zl::RopeHead&>(a) = zl::RopeHead();
   a.q = q;
   a.k = k;
   a.q_out = q_out;
@@ -364,7 +363,7 @@ zl_status zl_paged_append(const zl_paged_cache_t* cache, const void* k, int64_t 
   st = device_sms(&sms);
   if (st != ZL_OK) return st;
   static thread_local RopeArgs a;
-  std::memset(&a, 0, sizeof(a));
+  static_cast<zl::RopeHead&>(a) = zl::RopeHead();
   a.q = q;
   a.k = k;
   a.v = v;
@@ -390,9 +389,9 @@ zl_status zl_paged_append(const zl_paged_cache_t* cache, const void* k, int64_t 
   a.page_shift = shift_of(cache->page_size);
   if (plan) a.rope = *plan;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  for (int32_t s0 = 0; s0 < num_seqs; s0 += zl::kAppendSeqs) {
+  for (int32_t s0 = 0; s0 < num_seqs; s0 += zl::kMaxSegs) {
     a.seq0 = s0;
-    a.n_seqs = std::min(num_seqs - s0, zl::kAppendSeqs);
+    a.n_seqs = std::min(num_seqs - s0, zl::kMaxSegs);
     for (int32_t i = 0; i <= a.n_seqs; ++i) a.cu[i] = cu_seqlens[s0 + i];
     a.token0 = a.cu[0];
     a.tokens = a.cu[a.n_seqs] - a.cu[0];
@@ -450,8 +449,8 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
   if (st != ZL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
-  static thread_local zl::PagedAttnArgs a;      // ~21 KB: kept off the stack
-  std::memset(&a, 0, offsetof(zl::PagedAttnArgs, segs));
+  static thread_local zl::PagedAttnArgs<zl::kMaxSegs> a;      // ~21 KB: kept off the stack
+  static_cast<zl::PagedAttnHead&>(a) = zl::PagedAttnHead();
   a.page_table = cache->page_table;
   a.kv_lens = cache->kv_lens;
   a.o = o;
@@ -471,17 +470,25 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
   a.window = window;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
 
+  // the maps that the call's kinds of sequences use
+  bool copies[3] = {false, false, false}, pairs = false;
+  for (int32_t i = 0; i < num_seqs; ++i) {
+    const int64_t n = cu_seqlens_q[i + 1] - cu_seqlens_q[i];
+    if (n == 0) continue;
+    pairs = pairs || n > a.tile_tokens;
+    const int64_t tile_rows = n * a.group;
+    copies[n > a.tile_tokens || tile_rows > 64 ? 0 : tile_rows > 32 ? 1 : 2] = true;
+  }
   zl::PagedMaps maps;
   const int64_t pool_rows = int64_t(cache->num_pages) * cache->num_kv_heads * cache->page_size;
   const int box_rows = std::min(cache->page_size, zl::kBlockN);
   bool ok = zl::make_map(&maps.k, cache->k_pages, pool_rows, 1, hd, box_rows) &&
-            zl::make_map(&maps.v, cache->v_pages, pool_rows, 1, hd, box_rows) &&
-            zl::make_map_heads(&maps.o, o, tq, num_heads, hd, int64_t(num_heads) * hd, a.group, a.tile_tokens);
-  for (int i = 0; i < 3; ++i) {
-    // a group of more than 64 (32) heads never has 2 (4) copies in a tile
-    const int tokens = std::max(1, zl::kBlockM / (1 << i) / a.group);
-    ok = ok && zl::make_map_heads(&maps.q[i], q, tq, num_heads, hd, q_stride, a.group, tokens);
-  }
+            zl::make_map(&maps.v, cache->v_pages, pool_rows, 1, hd, box_rows);
+  if (pairs)
+    ok = ok && zl::make_map_heads(&maps.o, o, tq, num_heads, hd, int64_t(num_heads) * hd, a.group, a.tile_tokens);
+  for (int i = 0; i < 3; ++i)
+    if (copies[i])
+      ok = ok && zl::make_map_heads(&maps.q[i], q, tq, num_heads, hd, q_stride, a.group, zl::kBlockM / (1 << i) / a.group);
   if (!ok) return ZL_ECUDA;
 
   int64_t part0 = 0;

@@ -10,16 +10,24 @@ cu_seqlens are host sequences of ints, or host_int32 of one.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
-import functools
 import math
+import struct
 
 import torch
 
 from . import _lib
-from .attention import _check_like, _check_tensor, _workspace_bytes, alloc_workspace
+from .attention import _check_like, alloc_workspace
 
 _BF16, _I32 = torch.bfloat16, torch.int32
+
+
+# The structs of the C ABI that a call fills, packed in one step (a call on a
+# single token is bound by the host).
+_CACHE = struct.Struct("@4P6i")          # zl_paged_cache_t
+_TABLES = struct.Struct("@3P4i")         # zl_page_tables_t
+_POOL = struct.Struct("@P2q2i")          # zl_page_pool_t
 
 
 def host_int32(values) -> _lib.HostInt32:
@@ -30,66 +38,61 @@ def host_int32(values) -> _lib.HostInt32:
 def _cu(values):
     if not isinstance(values, _lib.HostInt32):
         values = _lib.HostInt32(values)
-    if values.last is None:
+    if values.n == 0:
         raise ValueError("cu_seqlens must have at least one entry")
     return values
 
 
-def _on_stream(fn):
-    """Runs fn under the stream it is given, so that what it allocates belongs
-    to that stream too."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, stream=stream, **kw)
-    return call
+def _call(name, index, stream, *args):
+    """Calls the library with the device `index` of the call's tensors as the
+    current one (its launches go there) and that device's current stream."""
+    if index < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    fn = getattr(_lib.load(), name)
+    if stream is not None:
+        if stream.device_index != index:
+            raise ValueError(f"the stream belongs to device {stream.device_index}, the tensors to {index}")
+    elif torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        if st:
+            _lib.check(st, name)
+        return
+    with torch.cuda.device(index):
+        _lib.check(fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream), name)
 
 
-class _On:
-    """Makes the tensors' device the current one while the library is called
-    (its launches go there) and gives that device's current stream."""
-    __slots__ = ("index", "guard")
-
-    def __init__(self, tensor, stream):
-        self.index = tensor.device.index
-        if stream is not None and stream.device_index != self.index:
-            raise ValueError(f"the stream belongs to device {stream.device_index}, the tensors to {self.index}")
-        self.guard = None if self.index == torch.cuda.current_device() else torch.cuda.device(self.index)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _given(stream):
+    """What a call allocates belongs to the stream it is given."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _check_rows(t, name, tokens, heads, dim, dtype, device):
-    """[tokens, heads, dim] with contiguous heads and columns."""
-    if t.shape != (tokens, heads, dim) or t.dtype != dtype or t.device != device:
+def _rows(t, name, tokens, heads, dim, dtype, device):
+    """Checks for [tokens, heads, dim] with contiguous heads and columns;
+    returns the elements between tokens (for one token, any do)."""
+    if t.shape != (tokens, heads, dim) or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name} must be {(tokens, heads, dim)} {dtype} on {device}, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-    if tokens and heads and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+    s0, s1, s2 = t.stride()
+    if tokens and heads and (s2 != 1 or (heads > 1 and s1 != dim)):
         raise ValueError(f"{name}: a token's heads and columns must be contiguous")
+    return s0 if tokens > 1 else heads * dim
 
 
-def _row_stride(t):
-    """Elements between tokens (one token may have any)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _exact(t, name, shape, dtype, device):
+    """Checks for this shape, dtype and device, contiguous."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        _check_like(t, name, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _check_int32(t, name, shape, device):
-    _check_like(t, name, shape, _I32, device)
-
-
-def _require_cuda(*tensors):
-    for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
+def _scratch(workspace, device):
+    """Pointer and size of a workspace (or None)."""
+    if workspace is None:
+        return 0, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 # ------------------------------------------------------------------ rotary positions
@@ -116,11 +119,12 @@ class RopePlan:
         ramp_arr = None if ramp is None else (ctypes.c_double * 3)(*(float(x) for x in ramp))
         _lib.check(_lib.load().zl_rope_init(ctypes.byref(self.struct), self.head_dim, int(bool(interleaved)), n, arr,
                                             float(base), float(factor), ramp_arr, float(magnitude)), "zl_rope_init")
+        self.ref = ctypes.byref(self.struct)
 
 
 def _positions(positions, plan, tokens, device):
     """Pointer and distance between axes of positions [T] or [n_axes, T]."""
-    if positions.dtype != _I32 or positions.device != device:
+    if positions.dtype is not _I32 or positions.device != device:
         raise ValueError(f"positions must be int32 on {device}")
     if positions.shape != (plan.n_axes, tokens) and not (plan.n_axes == 1 and positions.shape == (tokens,)):
         raise ValueError(f"positions must be [{plan.n_axes}, {tokens}], got {tuple(positions.shape)}")
@@ -130,73 +134,76 @@ def _positions(positions, plan, tokens, device):
 
 
 def _overlap(a, b):
-    """Whether two row tensors share memory without being the same rows."""
-    if a.numel() == 0 or b.numel() == 0 or (a.data_ptr() == b.data_ptr() and a.stride() == b.stride()
-                                            and a.shape == b.shape):
+    """Whether two [T, heads, d] tensors share memory."""
+    if a.numel() == 0 or b.numel() == 0 or a.untyped_storage().data_ptr() != b.untyped_storage().data_ptr():
         return False
-    if a.untyped_storage().data_ptr() != b.untyped_storage().data_ptr():
-        return False
-    ends = []
+    spans = []
     for t in (a, b):
-        first = t.data_ptr()
-        row = t.shape[1] * t.shape[2] * t.element_size()
-        ends.append((first, first + (t.shape[0] - 1) * _row_stride(t) * t.element_size() + row, row,
-                     _row_stride(t) * t.element_size()))
-    (a0, a1, ra, sa), (b0, b1, rb, sb) = ends
+        size = t.element_size()
+        row, step = t.shape[1] * t.shape[2] * size, (t.stride(0) if t.shape[0] > 1 else 0) * size
+        spans.append((t.data_ptr(), t.data_ptr() + (t.shape[0] - 1) * step + row, row, step))
+    (a0, a1, ra, sa), (b0, b1, rb, sb) = spans
     if a1 <= b0 or b1 <= a0:
         return False
-    if sa == sb:        # columns of the same rows: apart when their offsets within a row are
+    if sa == sb and sa > 0:     # columns of the same rows: apart when their offsets within a row are
         d = (b0 - a0) % sa
-        return not (d >= ra and d + rb <= sa)
+        return d < ra or d + rb > sa
     return True
 
 
+def _same(a, b):
+    return a.data_ptr() == b.data_ptr() and a.shape == b.shape and a.stride() == b.stride()
+
+
+def _check_outputs(outs, inputs):
+    """An output may be the input beside it, and shares no memory otherwise."""
+    if len(outs) > 1 and outs[0] is not None and outs[1] is not None and _overlap(*outs):
+        raise ValueError("q_out and k_out overlap")
+    for i, o in enumerate(outs):
+        for j, t in enumerate(inputs):
+            if o is not None and t is not None and not (i == j and _same(o, t)) and _overlap(o, t):
+                raise ValueError("an output overlaps an input without being it")
+
+
 def _rope(name, q, k, positions, plan, q_out, k_out, stream):
-    lib = _lib.load()
     if q.dim() != 3 or (k is not None and k.dim() != 3):
         raise ValueError("q and k must be [T, heads, d]")
-    if q.dtype not in (_BF16, torch.float32):
-        raise TypeError(f"unsupported dtype {q.dtype}")
+    dtype, dev = q.dtype, q.device
+    if dtype is not _BF16 and dtype is not torch.float32:
+        raise TypeError(f"unsupported dtype {dtype}")
     tokens, nq, hd = q.shape
     if hd != plan.head_dim:
         raise ValueError(f"the plan is for head_dim {plan.head_dim}, q has {hd}")
-    _check_rows(q, "q", tokens, nq, hd, q.dtype, q.device)
-    nk = 0
+    qs = _rows(q, "q", tokens, nq, hd, dtype, dev)
+    nk = kp = ks = kop = kos = 0
     if k is not None:
         nk = k.shape[1]
-        _check_rows(k, "k", tokens, nk, hd, q.dtype, q.device)
+        ks = _rows(k, "k", tokens, nk, hd, dtype, dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    pos, pos_stride = _positions(positions, plan, tokens, q.device)
-    if q_out is None:
-        q_out = torch.empty((tokens, nq, hd), dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty((tokens, nk, hd), dtype=q.dtype, device=q.device)
-    _check_rows(q_out, "q_out", tokens, nq, hd, q.dtype, q.device)
-    outs = [q_out]
-    if k is not None:
-        _check_rows(k_out, "k_out", tokens, nk, hd, q.dtype, q.device)
-        outs.append(k_out)
-    for i, o in enumerate(outs):
-        for t in (q,) if k is None else (q, k):
-            if _overlap(o, t):
-                raise ValueError("an output overlaps an input without being it")
-        if i and (_overlap(o, outs[0]) or (o.numel() and o.data_ptr() == outs[0].data_ptr())):
-            raise ValueError("q_out and k_out overlap")
+    pos, pos_stride = _positions(positions, plan, tokens, dev)
+    if q_out is not None or k_out is not None:
+        if q_out is not None:
+            _rows(q_out, "q_out", tokens, nq, hd, dtype, dev)
+        if k_out is not None:
+            _rows(k_out, "k_out", tokens, nk, hd, dtype, dev)
+        _check_outputs((q_out, k_out), (q, k))
+    index = q.get_device()
+    with _given(stream):
+        if q_out is None:
+            q_out = torch.empty((tokens, nq, hd), dtype=dtype, device=dev)
+        if k is not None and k_out is None:
+            k_out = torch.empty((tokens, nk, hd), dtype=dtype, device=dev)
     if tokens == 0:
         return q_out, k_out
-    _require_cuda(q)
-    code = _lib.ZL_BF16 if q.dtype == _BF16 else _lib.ZL_FP32
-    with _On(q, stream) as s:
-        st = getattr(lib, name)(ctypes.byref(plan.struct), q.data_ptr(), _row_stride(q),
-                                0 if k is None else k.data_ptr(), 0 if k is None else _row_stride(k), pos, pos_stride,
-                                tokens, nq, nk, code, q_out.data_ptr(), _row_stride(q_out),
-                                0 if k is None else k_out.data_ptr(), 0 if k is None else _row_stride(k_out), s)
-    _lib.check(st, name)
+    if k is not None:
+        kp, kop, kos = k.data_ptr(), k_out.data_ptr(), k_out.stride(0) if tokens > 1 else nk * hd
+    _call(name, index, stream, plan.ref, q.data_ptr(), qs, kp, ks, pos, pos_stride, tokens, nq, nk,
+          _lib.ZL_BF16 if dtype is _BF16 else _lib.ZL_FP32, q_out.data_ptr(),
+          q_out.stride(0) if tokens > 1 else nq * hd, kop, kos)
     return q_out, k_out
 
 
-@_on_stream
 def rope_fwd(q, k, positions, plan, q_out=None, k_out=None, stream=None):
     """Turns q [T, Hq, d] and k [T, Hk, d] (or None) by their tokens' positions
     (int32 [T], or [n_axes, T]).  Returns (q_out, k_out); an output may be its
@@ -204,7 +211,6 @@ def rope_fwd(q, k, positions, plan, q_out=None, k_out=None, stream=None):
     return _rope("zl_rope_fwd", q, k, positions, plan, q_out, k_out, stream)
 
 
-@_on_stream
 def rope_bwd(dq, dk, positions, plan, dq_out=None, dk_out=None, stream=None):
     """Gradient of rope_fwd: from the gradients of its outputs to those of its
     inputs.  Returns (dq_out, dk_out)."""
@@ -213,65 +219,61 @@ def rope_bwd(dq, dk, positions, plan, dq_out=None, dk_out=None, stream=None):
 
 # ------------------------------------------------------------------ the cache
 def _cache(k_pages, v_pages, page_table, kv_lens, seqs):
+    """The checked zl_paged_cache_t, its key heads and head_dim."""
     if k_pages.dim() != 4 or page_table.dim() != 2:
         raise ValueError("k_pages must be [P, Hk, page, d] and page_table [S, cols]")
-    dev = k_pages.device
-    _check_like(v_pages, "v_pages", k_pages.shape, k_pages.dtype, dev)
-    if k_pages.dtype != _BF16:
+    dev, shape = k_pages.device, k_pages.shape
+    if k_pages.dtype is not _BF16:
         raise TypeError("the pages must be bf16")
+    cols = page_table.shape[1]
     if page_table.shape[0] != seqs:
         raise ValueError(f"page_table has {page_table.shape[0]} rows, the batch {seqs} sequences")
-    _check_int32(page_table, "page_table", page_table.shape, dev)
-    _check_int32(kv_lens, "kv_lens", (seqs,), dev)
-    if not (k_pages.is_contiguous() and v_pages.is_contiguous() and page_table.is_contiguous()
-            and kv_lens.is_contiguous()):
-        raise ValueError("pages, page_table and kv_lens must be contiguous")
-    p, nk, page, hd = k_pages.shape
-    return _lib.PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(),
-                           page_table.shape[1], p, page, nk, hd, 0)
+    if not k_pages.is_contiguous():
+        raise ValueError("k_pages must be contiguous")
+    _exact(v_pages, "v_pages", shape, _BF16, dev)
+    _exact(page_table, "page_table", (seqs, cols), _I32, dev)
+    _exact(kv_lens, "kv_lens", (seqs,), _I32, dev)
+    p, nk, page, hd = shape
+    return _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cols, p,
+                       page, nk, hd, 0), nk, hd
 
 
-@_on_stream
 def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None, q_out=None, rope=None,
                  positions=None, stream=None):
     """Writes a batch's new tokens k, v [T, Hk, d] into the pages: sequence s's
     rows of cu_seqlens become its last positions below kv_lens[s].  With a
     RopePlan the keys (and q [T, H, d], if given) are turned at their cache
     positions, or at `positions`.  Returns the turned q (or None)."""
-    lib = _lib.load()
     cu = _cu(cu_seqlens)
-    cache = _cache(k_pages, v_pages, page_table, kv_lens, len(cu) - 1)
+    cache, nk, hd = _cache(k_pages, v_pages, page_table, kv_lens, cu.n - 1)
     tokens, dev = cu.last, k_pages.device
-    _check_rows(k, "k", tokens, cache.num_kv_heads, cache.head_dim, _BF16, dev)
-    _check_rows(v, "v", tokens, cache.num_kv_heads, cache.head_dim, _BF16, dev)
-    nq = 0
+    ks = _rows(k, "k", tokens, nk, hd, _BF16, dev)
+    vs = _rows(v, "v", tokens, nk, hd, _BF16, dev)
+    nq = qp = qs = qop = qos = pos = pos_stride = 0
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [T, H, d]")
         nq = q.shape[1]
-        _check_rows(q, "q", tokens, nq, cache.head_dim, _BF16, dev)
+        qs = _rows(q, "q", tokens, nq, hd, _BF16, dev)
         if q_out is None:
-            q_out = torch.empty((tokens, nq, cache.head_dim), dtype=_BF16, device=dev)
-        _check_rows(q_out, "q_out", tokens, nq, cache.head_dim, _BF16, dev)
-        for t in (q, k, v):
-            if _overlap(q_out, t) or (t is not q and q_out.numel() and q_out.data_ptr() == t.data_ptr()):
-                raise ValueError("q_out overlaps an input without being q")
+            with _given(stream):
+                q_out = torch.empty((tokens, nq, hd), dtype=_BF16, device=dev)
+            qos = nq * hd
+        else:
+            qos = _rows(q_out, "q_out", tokens, nq, hd, _BF16, dev)
+            _check_outputs((q_out,), (q, k, v))
+        qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    pos, pos_stride = 0, 0
     if positions is not None:
         if rope is None:
             raise ValueError("positions without a rope plan")
         pos, pos_stride = _positions(positions, rope, tokens, dev)
-    _require_cuda(k_pages)
-    if tokens == 0:
+    index = k_pages.get_device()
+    if tokens == 0 and index >= 0:
         return q_out
-    with _On(k_pages, stream) as s:
-        st = lib.zl_paged_append(ctypes.byref(cache), k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v),
-                                 cu.array, len(cu) - 1, None if rope is None else ctypes.byref(rope.struct), pos,
-                                 pos_stride, 0 if not nq else q.data_ptr(), 0 if not nq else _row_stride(q), nq,
-                                 0 if not nq else q_out.data_ptr(), 0 if not nq else _row_stride(q_out), s)
-    _lib.check(st, "zl_paged_append")
+    _call("zl_paged_append", index, stream, cache, k.data_ptr(), ks, v.data_ptr(), vs, cu.array, cu.n - 1,
+          None if rope is None else rope.ref, pos, pos_stride, qp, qs, nq, qop, qos)
     return q_out
 
 
@@ -279,95 +281,101 @@ def paged_attn_workspace_bytes(cu_seqlens_q, max_kv_len, num_heads, num_kv_heads
     lib = _lib.load()
     cu = _cu(cu_seqlens_q)
     out = ctypes.c_size_t(0)
-    _lib.check(lib.zl_paged_attn_workspace_size(cu.array, len(cu) - 1, max_kv_len, num_heads, num_kv_heads, head_dim,
+    _lib.check(lib.zl_paged_attn_workspace_size(cu.array, cu.n - 1, max_kv_len, num_heads, num_kv_heads, head_dim,
                                                 ctypes.byref(out)), "zl_paged_attn_workspace_size")
     return int(out.value)
 
 
-@_on_stream
 def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, max_kv_len, causal=True, window=0,
                softmax_scale=None, out=None, lse=None, workspace=None, stream=None):
     """Attention of each sequence's new queries q [Tq, H, d] over its cached
     keys and values.  The queries stand at the last positions below kv_lens;
     max_kv_len (host) bounds kv_lens.  Returns (o [Tq, H, d], lse [H, Tq])."""
-    lib = _lib.load()
     cu = _cu(cu_seqlens_q)
-    cache = _cache(k_pages, v_pages, page_table, kv_lens, len(cu) - 1)
+    cache, nk, hd = _cache(k_pages, v_pages, page_table, kv_lens, cu.n - 1)
     if q.dim() != 3:
         raise ValueError("q must be [Tq, H, d]")
-    tq, nh, hd = q.shape
+    tq, nh, _ = q.shape
     if tq != cu.last:
         raise ValueError(f"q has {tq} rows, cu_seqlens_q ends at {cu.last}")
-    dev = q.device
-    _check_rows(q, "q", tq, nh, cache.head_dim, _BF16, k_pages.device)
-    if out is None:
-        out = torch.empty((tq, nh, hd), dtype=_BF16, device=dev)
-    else:
-        _check_like(out, "out", (tq, nh, hd), _BF16, dev)
-    if lse is None:
-        lse = torch.empty((nh, tq), dtype=torch.float32, device=dev)
-    else:
-        _check_like(lse, "lse", (nh, tq), torch.float32, dev)
-    if not (out.is_contiguous() and lse.is_contiguous()):
-        raise ValueError("out and lse must be contiguous")
-    _require_cuda(q)
-    if workspace is None:
-        workspace = alloc_workspace(paged_attn_workspace_bytes(cu, max_kv_len, nh, cache.num_kv_heads, hd), dev)
-    scale = 1.0 / math.sqrt(hd) if softmax_scale is None else float(softmax_scale)
-    with _On(q, stream) as s:
-        st = lib.zl_paged_attn(ctypes.byref(cache), q.data_ptr(), _row_stride(q), cu.array, len(cu) - 1, max_kv_len,
-                               nh, scale, int(bool(causal)), int(window), out.data_ptr(), lse.data_ptr(),
-                               0 if workspace is None else workspace.data_ptr(), _workspace_bytes(workspace), s)
-    _lib.check(st, "zl_paged_attn")
+    dev = k_pages.device
+    qs = _rows(q, "q", tq, nh, hd, _BF16, dev)
+    if out is not None:
+        _exact(out, "out", (tq, nh, hd), _BF16, dev)
+    if lse is not None:
+        _exact(lse, "lse", (nh, tq), torch.float32, dev)
+    index = q.get_device()
+    if index < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if out is None or lse is None or workspace is None:
+        with _given(stream):
+            if out is None:
+                out = torch.empty((tq, nh, hd), dtype=_BF16, device=dev)
+            if lse is None:
+                lse = torch.empty((nh, tq), dtype=torch.float32, device=dev)
+            if workspace is None:
+                workspace = alloc_workspace(paged_attn_workspace_bytes(cu, max_kv_len, nh, nk, hd), dev)
+    ws, ws_bytes = _scratch(workspace, dev)
+    _call("zl_paged_attn", index, stream, cache, q.data_ptr(), qs, cu.array, cu.n - 1, max_kv_len, nh,
+          1.0 / math.sqrt(hd) if softmax_scale is None else softmax_scale, 1 if causal else 0, window, out.data_ptr(),
+          lse.data_ptr(), ws, ws_bytes)
     return out, lse
 
 
 # ------------------------------------------------------------------ whole pages
 def _tables(page_table, kv_lens, page_refs, page_size):
+    """The checked zl_page_tables_t, and the device."""
     if page_table.dim() != 2 or page_refs.dim() != 1:
         raise ValueError("page_table must be [S, cols] and page_refs [P]")
     dev = page_table.device
-    _check_int32(page_table, "page_table", page_table.shape, dev)
-    _check_int32(kv_lens, "kv_lens", (page_table.shape[0],), dev)
-    _check_int32(page_refs, "page_refs", page_refs.shape, dev)
-    if not (page_table.is_contiguous() and kv_lens.is_contiguous() and page_refs.is_contiguous()):
-        raise ValueError("page_table, kv_lens and page_refs must be contiguous")
-    _require_cuda(page_table)
-    return _lib.PageTables(page_table.data_ptr(), kv_lens.data_ptr(), page_refs.data_ptr(), page_table.shape[0],
-                           page_table.shape[1], page_refs.shape[0], page_size)
+    slots, cols = page_table.shape
+    pages = page_refs.shape[0]
+    _exact(page_table, "page_table", (slots, cols), _I32, dev)
+    _exact(kv_lens, "kv_lens", (slots,), _I32, dev)
+    _exact(page_refs, "page_refs", (pages,), _I32, dev)
+    return _TABLES.pack(page_table.data_ptr(), kv_lens.data_ptr(), page_refs.data_ptr(), slots, cols, pages,
+                        page_size), dev
 
 
 def _pool(cache, num_pages=None, device=None):
-    """cache [..., P, Hk, page, d] with contiguous pages; the dimensions before
-    P (layers, keys and values) are the groups."""
-    if cache.dim() < 4:
+    """The checked zl_page_pool_t of cache [..., P, Hk, page, d]; the dimensions
+    before P (layers, keys and values) are the groups."""
+    shape = cache.shape
+    if len(shape) < 4:
         raise ValueError("the cache must be [..., P, Hk, page, d]")
-    p, nk, page, hd = cache.shape[-4:]
+    p = shape[-4]
     if num_pages is not None and p != num_pages:
         raise ValueError(f"the cache has {p} pages, page_refs {num_pages}")
     if device is not None and cache.device != device:
         raise ValueError(f"the cache must be on {device}")
     if not cache.is_contiguous():
         raise ValueError("the cache must be contiguous")
-    _require_cuda(cache)
-    size = nk * page * hd * cache.element_size()
-    groups = cache.numel() // max(1, p * nk * page * hd)
-    return _lib.PagePool(cache.data_ptr(), size, p * size, groups, p)
+    page = shape[-3] * shape[-2] * shape[-1]
+    size = page * cache.element_size()
+    return _POOL.pack(cache.data_ptr(), size, p * size, cache.numel() // max(1, p * page), p)
 
 
 def _list(t, name, device):
     if t.dim() != 1:
         raise ValueError(f"{name} must be a vector")
-    _check_int32(t, name, t.shape, device)
-    _check_tensor(t, name)
+    _exact(t, name, t.shape, _I32, device)
     return t.shape[0]
 
 
-def _status(status, device):
+def _status(status, device, stream):
     if status is None:
-        return torch.empty(1, dtype=_I32, device=device)
-    _check_int32(status, "status", (1,), device)
+        with _given(stream):
+            return torch.empty(1, dtype=_I32, device=device)
+    _exact(status, "status", (1,), _I32, device)
     return status
+
+
+def _pages_scratch(workspace, num_pages, device, stream):
+    if workspace is None:
+        with _given(stream):
+            workspace = alloc_workspace(pages_workspace_bytes(num_pages), device)
+    ws, size = _scratch(workspace, device)
+    return workspace, ws, size
 
 
 def pages_workspace_bytes(num_pages) -> int:
@@ -376,70 +384,53 @@ def pages_workspace_bytes(num_pages) -> int:
     return int(out.value)
 
 
-@_on_stream
 def pages_extend(page_table, kv_lens, page_refs, counts, page_size, status=None, stream=None):
     """Makes room for counts[s] (int32, device) new tokens in every slot, in
     place: kv_lens grows, free pages (lowest first) enter the rows.  Returns a
     device int32 [1]: 0, or the pages lacking, or -1 for counts that are
     negative or do not fit a row; unless it is 0 nothing was changed."""
-    t = _tables(page_table, kv_lens, page_refs, page_size)
-    _check_int32(counts, "counts", kv_lens.shape, kv_lens.device)
-    _check_tensor(counts, "counts")
-    status = _status(status, kv_lens.device)
-    with _On(kv_lens, stream) as s:
-        st = _lib.load().zl_pages_extend(ctypes.byref(t), counts.data_ptr(), status.data_ptr(), s)
-    _lib.check(st, "zl_pages_extend")
+    t, dev = _tables(page_table, kv_lens, page_refs, page_size)
+    _exact(counts, "counts", kv_lens.shape, _I32, dev)
+    status = _status(status, dev, stream)
+    _call("zl_pages_extend", kv_lens.get_device(), stream, t, counts.data_ptr(), status.data_ptr())
     return status
 
 
-@_on_stream
 def pages_fork(cache, page_table, kv_lens, page_refs, parents, children, status=None, workspace=None, stream=None):
     """Makes each empty slot children[i] a copy of slot parents[i] (int32,
     device), in place: full pages are shared, a part-filled last page is copied
     in every group of cache [..., P, Hk, page, d].  Returns a device int32 [1]
     as pages_extend does."""
-    t = _tables(page_table, kv_lens, page_refs, cache.shape[-2] if cache.dim() >= 2 else 0)
-    p = _pool(cache, page_refs.shape[0], page_table.device)
-    n = _list(parents, "parents", kv_lens.device)
-    if _list(children, "children", kv_lens.device) != n:
+    t, dev = _tables(page_table, kv_lens, page_refs, cache.shape[-2] if cache.dim() >= 2 else 0)
+    p = _pool(cache, page_refs.shape[0], dev)
+    n = _list(parents, "parents", dev)
+    if _list(children, "children", dev) != n:
         raise ValueError("parents and children differ in length")
-    status = _status(status, kv_lens.device)
-    if workspace is None:
-        workspace = alloc_workspace(pages_workspace_bytes(page_refs.shape[0]), kv_lens.device)
-    with _On(kv_lens, stream) as s:
-        st = _lib.load().zl_pages_fork(ctypes.byref(p), ctypes.byref(t), parents.data_ptr(), children.data_ptr(), n,
-                                       status.data_ptr(), workspace.data_ptr(), _workspace_bytes(workspace), s)
-    _lib.check(st, "zl_pages_fork")
+    status = _status(status, dev, stream)
+    workspace, ws, size = _pages_scratch(workspace, page_refs.shape[0], dev, stream)
+    _call("zl_pages_fork", kv_lens.get_device(), stream, p, t, parents.data_ptr(), children.data_ptr(), n,
+          status.data_ptr(), ws, size)
     return status
 
 
-@_on_stream
 def pages_free(page_table, kv_lens, page_refs, slots, page_size, stream=None):
     """Empties the slots (int32, device), in place."""
-    t = _tables(page_table, kv_lens, page_refs, page_size)
-    n = _list(slots, "slots", kv_lens.device)
-    with _On(kv_lens, stream) as s:
-        st = _lib.load().zl_pages_free(ctypes.byref(t), slots.data_ptr(), n, s)
-    _lib.check(st, "zl_pages_free")
+    t, dev = _tables(page_table, kv_lens, page_refs, page_size)
+    n = _list(slots, "slots", dev)
+    _call("zl_pages_free", kv_lens.get_device(), stream, t, slots.data_ptr(), n)
 
 
-@_on_stream
 def pages_compact(cache, page_table, kv_lens, page_refs, live=None, workspace=None, stream=None):
     """Moves the used pages to the front of the pool, in place, in every group
     of cache [..., P, Hk, page, d].  Returns their number, a device int32 [1]."""
-    t = _tables(page_table, kv_lens, page_refs, cache.shape[-2] if cache.dim() >= 2 else 0)
-    p = _pool(cache, page_refs.shape[0], page_table.device)
-    live = _status(live, kv_lens.device)
-    if workspace is None:
-        workspace = alloc_workspace(pages_workspace_bytes(page_refs.shape[0]), kv_lens.device)
-    with _On(kv_lens, stream) as s:
-        st = _lib.load().zl_pages_compact(ctypes.byref(p), ctypes.byref(t), live.data_ptr(), workspace.data_ptr(),
-                                          _workspace_bytes(workspace), s)
-    _lib.check(st, "zl_pages_compact")
+    t, dev = _tables(page_table, kv_lens, page_refs, cache.shape[-2] if cache.dim() >= 2 else 0)
+    p = _pool(cache, page_refs.shape[0], dev)
+    live = _status(live, dev, stream)
+    workspace, ws, size = _pages_scratch(workspace, page_refs.shape[0], dev, stream)
+    _call("zl_pages_compact", kv_lens.get_device(), stream, p, t, live.data_ptr(), ws, size)
     return live
 
 
-@_on_stream
 def pages_copy(cache, src, dst, stream=None):
     """Copies page src[i] over page dst[i] (int32, device) in every group of
     cache [..., P, Hk, page, d]; no page may be both, nor a target twice."""
@@ -447,6 +438,4 @@ def pages_copy(cache, src, dst, stream=None):
     n = _list(src, "src", cache.device)
     if _list(dst, "dst", cache.device) != n:
         raise ValueError("src and dst differ in length")
-    with _On(cache, stream) as s:
-        st = _lib.load().zl_pages_copy(ctypes.byref(p), src.data_ptr(), dst.data_ptr(), n, s)
-    _lib.check(st, "zl_pages_copy")
+    _call("zl_pages_copy", cache.get_device(), stream, p, src.data_ptr(), dst.data_ptr(), n)
