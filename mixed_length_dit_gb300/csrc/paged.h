@@ -56,18 +56,30 @@ struct RopeArgs : RopeHead {
 };
 static_assert(sizeof(RopeArgs<kMaxSegs>) <= 32764, "rotary arguments exceed the kernel parameter space");
 
-// Most splits of one sequence's keys.
-constexpr int kMaxSplits = 128;
+// Most splits of a PAIR sequence's keys, CTAs of a SPLIT launch (one for each
+// of this GPU's SMs), and parts of one row that a join takes.
+constexpr int kMaxSplits = 8;
+constexpr int kSplitCtas = 152;
+constexpr int kMaxParts = kSplitCtas;
 
 // One sequence's queries in a paged attention launch.
 struct PagedSeg {
   int32_t seq;       // row of the page table and of the lengths
   int32_t q_row0;    // packed row of its first query
   int32_t q_len;     // queries, >= 1
-  int32_t item0;     // first work item
-  int32_t splits;    // splits of its keys, 1 .. kMaxSplits
-  int32_t tok0;      // queries of the launch's earlier segments
-  int64_t part0;     // splits > 1: its first row in o_part / lse_part
+  int32_t item0;     // PAIR: first work item
+  int32_t splits;    // PAIR: splits of its keys, 1 .. kMaxSplits
+  int32_t tok0;      // PAIR: queries of the launch's earlier segments
+  int64_t part0;     // PAIR, splits > 1: its first row in o_part / lse_part
+};
+
+// SPLIT: the unit that begins in a CTA and goes on in the CTAs up to `last`
+// (-1: none).
+struct PagedJoin {
+  int32_t q_row0;
+  int32_t q_len;
+  int32_t hk;
+  int32_t last;
 };
 
 struct PagedAttnHead {
@@ -75,15 +87,19 @@ struct PagedAttnHead {
   const int32_t* kv_lens;
   void* o;                      // [Tq][H][d] bf16
   float* lse;                   // [H][lse_stride]
-  float* o_part;                // [rows][H][d]: row part0 + split * q_len + query
-  float* lse_part;              // [rows][H]
+  // parts of rows whose keys were split.  PAIR: rows [part0 + split * q_len +
+  // query][H]; SPLIT: [2 * CTAs slots][slot_rows], row token * group + head.
+  float* o_part;                // [rows][d]
+  float* lse_part;              // [rows]
+  PagedJoin* joins;             // SPLIT: [CTAs]
   int64_t lse_stride;           // Tq
   int32_t tokens;               // queries of this launch
   int32_t num_heads;
   int32_t num_kv_heads;
   int32_t group;                // query heads of a key head
   int32_t tile_tokens;          // tokens of a query tile: 128 / group
-  int32_t split_blocks;         // 128-key blocks of a split
+  int32_t split_blocks;         // PAIR: 128-key blocks of a split
+  int32_t slot_rows;            // SPLIT: most rows of a unit
   int32_t table_cols;
   int32_t num_pages;
   int32_t page_shift;
@@ -91,7 +107,7 @@ struct PagedAttnHead {
   int32_t causal;
   int32_t window;
   float scale_log2;             // softmax scale * log2(e)
-  int32_t n_items;
+  int32_t n_items;              // CTAs to launch: PAIR's work items, SPLIT's kSplitCtas
   int32_t n_segs;
 };
 

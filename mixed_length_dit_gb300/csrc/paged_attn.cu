@@ -8,7 +8,7 @@
 // token r / group, head r % group, so a page that is read serves all of them,
 // and single tokens fill a tile as far as they can.
 //
-// A work item is (sequence, key head, unit of query tiles, split of the keys).
+// A work item is (sequence, key head, unit of query tiles, range of key blocks).
 // Two kernels, by what bounds them:
 //
 //   PAIR   chunks of more than one tile: tensor-bound.  An item is two 128-row
@@ -30,12 +30,15 @@
 //               take P in V's type), O is rescaled when m grows by more than
 //               2^8
 //   warp 8      producer: all lanes fetch page numbers, each lane issues the
-//               TMA box of its page; items by cluster launch control
+//               TMA box of its page.  PAIR takes items by cluster launch
+//               control; SPLIT's are the CTA's equal share of all key blocks
 //   warps 9,10  MMA issuers (S = Q K^T, O += P V) of group t
-//   warp 11     clears what a sequence's last V block holds past its length
-//               (unwritten rows may be NaN, and 0 * NaN is not 0)
+//   warp 11     brings the queries, and clears what a sequence's last V block
+//               holds past its length (unwritten rows may be NaN, and 0 * NaN
+//               is not 0)
 // The lengths are read on the device, so a captured launch follows them.
 #define ZL_TRY_WAIT_HINT_NS 10000
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -49,10 +52,11 @@ __device__ uint32_t g_paged_err;
 constexpr int kThreads = 384;
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp0 = 9;
-constexpr int kTailWarp = 11;
-constexpr int kReaders = 11;                   // 2 issuer threads, 8 softmax warps, the tail warp
+constexpr int kAuxWarp = 11;
+constexpr int kReaders = 11;                   // 2 issuer threads, 8 softmax warps, the aux warp
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;
+constexpr int kMinBlocks = 2;                  // SPLIT: key blocks of a CTA at least, one for each group
 constexpr float kLn2 = 0.6931471805599453f;
 
 // K/V blocks of 128 keys in shared memory.  PAIR holds two query tiles and
@@ -64,6 +68,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 // it waits for (a block that lands late) for its own.
 template <int HD, bool PAIR>
 __host__ __device__ constexpr int stages() { return HD == 128 ? (PAIR ? 4 : 6) : (PAIR ? 8 : 12); }
+
+// A work item as the producer hands it out.
+struct Item {
+  int id;             // PAIR: the item's number, SPLIT: its segment; -1: no item left
+  int len;            // keys of the sequence
+  int hk, s0, s1;     // SPLIT: key head and key blocks
+  int slot;           // SPLIT: partial slot, or -1: the rows are final
+};
 
 template <int HD, bool PAIR>
 struct Stages {
@@ -83,7 +95,7 @@ struct PagedSmem {
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t turn[2], grp_sync[2], all_sync;
   ItemRing ring;
-  int item_len[2];                             // the length of the ring slot's sequence
+  Item item[2];                                // what the ring's slots hold
   uint32_t tmem_base;
   int abort_flag;
   float2 ml[2 * kBlockM];                      // SPLIT: m and l of every group's rows
@@ -114,12 +126,12 @@ struct Work {
   int seq, q_row0, q_len, len;
   int hk;
   int tile0;        // first query tile
-  int split;
-  int active;       // splits of this unit that have keys
-  int s0, s1;       // this split's blocks
-  int64_t part0;    // first partial row of the sequence
+  int s0, s1;       // the item's key blocks
+  bool final;       // its rows are final: they go to o and lse
+  int64_t part;     // else: PAIR: the first partial row of the split, SPLIT: of the slot
   Range tile[2];    // each tile's blocks within [s0, s1)
   bool has[2];      // the tile exists
+  bool idle;        // PAIR: a split without keys that is not the first
 };
 
 template <int N>
@@ -137,13 +149,12 @@ __device__ __forceinline__ Range cut(Range r, int s0, int s1) {
   return b1 > b0 ? Range{b0, b1} : Range{s0, s0};
 }
 
-// The blocks that the splits of a unit (first tile `tile0`) divide: the union
-// of its tiles'.
-template <bool PAIR>
-__device__ __forceinline__ Range unit_blocks(const PagedAttnHead& a, int len, int q_len, int tile0) {
+// The blocks that the splits of a PAIR unit (first tile `tile0`) divide: the
+// union of its tiles'.
+__device__ __forceinline__ Range pair_blocks(const PagedAttnHead& a, int len, int q_len, int tile0) {
   const int t0 = tile0 * a.tile_tokens;
   Range r = blocks_of(a, len, q_len, t0, min(q_len, t0 + a.tile_tokens));
-  if (PAIR && t0 + a.tile_tokens < q_len) {
+  if (t0 + a.tile_tokens < q_len) {
     const Range s = blocks_of(a, len, q_len, t0 + a.tile_tokens, min(q_len, t0 + 2 * a.tile_tokens));
     if (r.b1 <= r.b0) return s;
     if (s.b1 > s.b0) r = {min(r.b0, s.b0), max(r.b1, s.b1)};
@@ -153,35 +164,63 @@ __device__ __forceinline__ Range unit_blocks(const PagedAttnHead& a, int len, in
 
 // Items of a segment: key head outermost, then the unit, last tokens first
 // (under a causal mask they see the most), then the split.
-template <bool PAIR, int N>
-__device__ __forceinline__ Work decode(const PagedAttnArgs<N>& a, int it, int len) {
-  const PagedSeg& s = a.segs[find_seg(a, it)];
+template <int N>
+__device__ __forceinline__ Work decode_pair(const PagedAttnArgs<N>& a, const Item& item) {
+  const PagedSeg& s = a.segs[find_seg(a, item.id)];
   Work w;
   w.seq = s.seq;
   w.q_row0 = s.q_row0;
   w.q_len = s.q_len;
-  w.len = len;
-  w.part0 = s.part0;
+  w.len = item.len;
   const int tiles = (s.q_len + a.tile_tokens - 1) / a.tile_tokens;
-  const int units = PAIR ? (tiles + 1) / 2 : 1;
-  int x = it - s.item0;
-  w.split = x % s.splits;
+  const int units = (tiles + 1) / 2;
+  int x = item.id - s.item0;
+  const int split = x % s.splits;
   x /= s.splits;
   const int u = units - 1 - x % units;
   w.hk = x / units;
-  w.tile0 = PAIR ? 2 * u : 0;
-  const Range r = unit_blocks<PAIR>(a, len, s.q_len, w.tile0);
-  w.active = (r.b1 - r.b0 + a.split_blocks - 1) / a.split_blocks;
-  w.s0 = min(r.b1, r.b0 + w.split * a.split_blocks);
+  w.tile0 = 2 * u;
+  const Range r = pair_blocks(a, item.len, s.q_len, w.tile0);
+  w.s0 = min(r.b1, r.b0 + split * a.split_blocks);
   w.s1 = min(r.b1, w.s0 + a.split_blocks);
+  w.final = r.b1 - r.b0 <= a.split_blocks;
+  w.part = s.part0 + static_cast<int64_t>(split) * s.q_len;
+  w.idle = w.s1 <= w.s0 && split > 0;
   w.has[0] = true;
-  w.has[1] = PAIR && w.tile0 + 1 < tiles;
+  w.has[1] = w.tile0 + 1 < tiles;
   const int t0 = w.tile0 * a.tile_tokens;
-  w.tile[0] = cut(blocks_of(a, len, s.q_len, t0, min(s.q_len, t0 + a.tile_tokens)), w.s0, w.s1);
+  w.tile[0] = cut(blocks_of(a, w.len, s.q_len, t0, min(s.q_len, t0 + a.tile_tokens)), w.s0, w.s1);
   w.tile[1] = w.tile[0];
   if (w.has[1])
-    w.tile[1] = cut(blocks_of(a, len, s.q_len, t0 + a.tile_tokens, min(s.q_len, t0 + 2 * a.tile_tokens)), w.s0, w.s1);
+    w.tile[1] = cut(blocks_of(a, w.len, s.q_len, t0 + a.tile_tokens, min(s.q_len, t0 + 2 * a.tile_tokens)), w.s0, w.s1);
   return w;
+}
+
+template <int N>
+__device__ __forceinline__ Work decode_split(const PagedAttnArgs<N>& a, const Item& item) {
+  const PagedSeg& s = a.segs[item.id];
+  Work w;
+  w.seq = s.seq;
+  w.q_row0 = s.q_row0;
+  w.q_len = s.q_len;
+  w.len = item.len;
+  w.hk = item.hk;
+  w.tile0 = 0;
+  w.s0 = item.s0;
+  w.s1 = item.s1;
+  w.final = item.slot < 0;
+  w.part = static_cast<int64_t>(item.slot) * a.slot_rows;
+  w.idle = false;
+  w.has[0] = true;
+  w.has[1] = false;
+  w.tile[0] = w.tile[1] = {item.s0, item.s1};
+  return w;
+}
+
+template <bool PAIR, int N>
+__device__ __forceinline__ Work decode(const PagedAttnArgs<N>& a, const Item& item) {
+  if constexpr (PAIR) return decode_pair(a, item);
+  else return decode_split(a, item);
 }
 
 // Copies of a SPLIT tile's rows: 4, 2 or 1, 128 / copies rows apart.
@@ -210,138 +249,210 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       : "memory");
 }
 
-// A ring reader's next item and its sequence's length.
+// A ring reader's next item; false: none left, or a wait ran out.
 template <typename SM>
-__device__ __forceinline__ int take(SM* sm, uint32_t n, uint32_t code, bool warp_wide, int* len) {
-  ItemRing* r = &sm->ring;
+__device__ __forceinline__ bool take(SM* sm, uint32_t n, uint32_t code, bool warp_wide, Item* item) {
   const uint32_t s = n & 1u;
-  bool ok = mbar_wait(&r->full[s], (n >> 1) & 1u, &sm->abort_flag, &g_paged_err, code);
+  bool ok = mbar_wait(&sm->ring.full[s], (n >> 1) & 1u, &sm->abort_flag, &g_paged_err, code);
   if (warp_wide) ok = __all_sync(0xffffffffu, ok);
-  if (!ok) return -2;
-  const int it = *reinterpret_cast<volatile int*>(&r->item[s]);
-  *len = *reinterpret_cast<volatile int*>(&sm->item_len[s]);
+  if (!ok) return false;
+  const volatile Item* i = &sm->item[s];
+  item->id = i->id;
+  item->len = i->len;
+  item->hk = i->hk;
+  item->s0 = i->s0;
+  item->s1 = i->s1;
+  item->slot = i->slot;
   if (warp_wide) __syncwarp();
-  if (!warp_wide || (threadIdx.x & 31) == 0) mbar_arrive(&r->empty[s]);
-  return it;
+  if (!warp_wide || (threadIdx.x & 31) == 0) mbar_arrive(&sm->ring.empty[s]);
+  return item->id >= 0;
 }
 
 // ------------------------------------------------------------------ producer
+// Hands out the n-th item once every reader has taken the slot's previous one.
+template <typename SM>
+__device__ __forceinline__ bool publish(SM* sm, uint32_t n, const Item& item) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    const uint32_t s = n & 1u;
+    ok = mbar_wait(&sm->ring.empty[s], ((n >> 1) & 1u) ^ 1u, &sm->abort_flag, &g_paged_err, ERR_TIMEOUT_PRODUCER);
+    if (ok) {
+      sm->item[s] = item;
+      mbar_arrive(&sm->ring.full[s]);
+    }
+  }
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+// The length of a segment's sequence, within the call's bound.
+template <int N>
+__device__ __forceinline__ int length_of(const PagedAttnArgs<N>& a, int seg) {
+  const int len = __ldg(a.kv_lens + a.segs[seg].seq);
+  if (len >= 0 && len <= a.max_kv_len) return len;
+  atomicOr(&g_paged_err, ERR_BAD_PAGE);
+  return len < 0 ? 0 : a.max_kv_len;
+}
+
+// Brings an item's K/V blocks into the rings; `ask` requests the next PAIR
+// item when the last block is next.  uses0 / uses1: the rings' counts.
 template <int HD, bool PAIR, int N>
-__device__ void produce(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps) {
+__device__ __forceinline__ bool load_blocks(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps,
+                                            const Work& w, uint32_t& uses0, uint32_t& uses1, bool ask) {
   using Ring = Stages<HD, PAIR>;
   const int lane = threadIdx.x & 31;
-  volatile int* abort_flag = &sm->abort_flag;
-  const uint32_t code = ERR_TIMEOUT_PRODUCER;
   const int page = 1 << a.page_shift;
   const int box_rows = min(page, kBlockN);
-  uint32_t kv_it0 = 0, kv_it1 = 0, q_it[2] = {0u, 0u}, steal_ph = 0;   // uses of ring 0 and 1
-  int it = static_cast<int>(blockIdx.x);
+  const int32_t* row = a.page_table + static_cast<int64_t>(w.seq) * a.table_cols;
+  // page numbers of the item's blocks, 32 at a time, the next 32 on their way
+  const int e0 = (w.s0 * kBlockN) >> a.page_shift;
+  const int e1 = min((min(w.len, w.s1 * kBlockN) + page - 1) >> a.page_shift, a.table_cols);
+  int chunk = 0;
+  int cur = e0 + lane < e1 ? __ldg(row + e0 + lane) : 0;
+  int nxt = e0 + 32 + lane < e1 ? __ldg(row + e0 + 32 + lane) : 0;
+  for (int j = w.s0; j < w.s1; ++j) {
+    if (ask && j == w.s1 - 1 && lane == 0) ring_ask(&sm->ring);
+    const int rel = ((j * kBlockN) >> a.page_shift) - e0;
+    if ((rel >> 5) != chunk) {
+      ++chunk;
+      cur = nxt;
+      nxt = e0 + 32 * (chunk + 1) + lane < e1 ? __ldg(row + e0 + 32 * (chunk + 1) + lane) : 0;
+    }
+    const int valid = min(kBlockN, w.len - j * kBlockN);
+    const int boxes = (valid + box_rows - 1) / box_rows;
+    int pg = __shfl_sync(0xffffffffu, cur, ((rel & 31) + lane) & 31);
+    if (lane < boxes && (pg < 0 || pg >= a.num_pages)) {
+      atomicOr(&g_paged_err, ERR_BAD_PAGE);            // reads page 0 in its place
+      pg = 0;
+    }
+    const int y = ((pg * a.num_kv_heads + w.hk) << a.page_shift) + ((j * kBlockN) & (page - 1));
+    const int ring = PAIR ? 0 : (j - w.s0) & 1;
+    uint32_t& uses = ring ? uses1 : uses0;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const uint32_t st = Ring::stage(ring, uses);
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm->kv_empty[st], Ring::parity(uses) ^ 1u, &sm->abort_flag,
+                                             &g_paged_err, ERR_TIMEOUT_PRODUCER)))
+        return false;
+      // a V block that the sequence ends in goes by way of the aux warp
+      uint64_t* bar = kv == 1 && valid < kBlockN ? &sm->tail[st] : &sm->kv_full[st];
+      if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * box_rows * HD * 2));
+      __syncwarp();
+      if (lane < boxes) {
+        const CUtensorMap* map = kv ? &maps.v : &maps.k;
+#pragma unroll
+        for (int c = 0; c < HD / 64; ++c)
+          tma_load_2d(sm->kv[st] + c * kBlockN * 128 + lane * box_rows * 128, map, bar, c * 64, y);
+      }
+      ++uses;
+    }
+  }
+  return true;
+}
+
+// PAIR: the CTA's own item first, then stolen ones, in launch order.
+template <int HD, int N>
+__device__ void produce_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps) {
+  const int lane = threadIdx.x & 31;
+  uint32_t uses0 = 0, uses1 = 0, steal_ph = 0;
+  Item item = {static_cast<int>(blockIdx.x), 0, 0, 0, 0, 0};
   for (uint32_t n = 0;; ++n) {
-    int len = 0;
-    if (it >= 0) {
-      const PagedSeg& s = a.segs[find_seg(a, it)];
-      len = __ldg(a.kv_lens + s.seq);
-      if (len < 0 || len > a.max_kv_len) {
-        if (lane == 0) atomicOr(&g_paged_err, ERR_BAD_PAGE);
-        len = len < 0 ? 0 : a.max_kv_len;
-      }
-    }
-    // publish once every reader has taken the slot's previous item
-    bool ok = true;
-    if (lane == 0) {
-      const uint32_t s = n & 1u;
-      ok = mbar_wait(&sm->ring.empty[s], ((n >> 1) & 1u) ^ 1u, abort_flag, &g_paged_err, code);
-      if (ok) {
-        sm->ring.item[s] = it;
-        sm->item_len[s] = len;
-        mbar_arrive(&sm->ring.full[s]);
-      }
-    }
-    if (!__shfl_sync(0xffffffffu, ok, 0) || it < 0) return;
-    const Work w = decode<PAIR>(a, it, len);
-    bool asked = false;
-    if (w.s1 > w.s0) {
-      const int32_t* row = a.page_table + static_cast<int64_t>(w.seq) * a.table_cols;
-      // page numbers of the split's blocks, 32 at a time, the next 32 on their way
-      const int e0 = (w.s0 * kBlockN) >> a.page_shift;
-      const int e1 = min((min(w.len, w.s1 * kBlockN) + page - 1) >> a.page_shift, a.table_cols);
-      int chunk = 0;
-      int cur = e0 + lane < e1 ? __ldg(row + e0 + lane) : 0;
-      int nxt = e0 + 32 + lane < e1 ? __ldg(row + e0 + 32 + lane) : 0;
-      for (int j = w.s0; j < w.s1; ++j) {
-        if (j == w.s1 - 1) {
-          if (lane == 0) ring_ask(&sm->ring);
-          asked = true;
-        }
-        const int rel = ((j * kBlockN) >> a.page_shift) - e0;
-        if ((rel >> 5) != chunk) {
-          ++chunk;
-          cur = nxt;
-          nxt = e0 + 32 * (chunk + 1) + lane < e1 ? __ldg(row + e0 + 32 * (chunk + 1) + lane) : 0;
-        }
-        const int valid = min(kBlockN, w.len - j * kBlockN);
-        const int boxes = (valid + box_rows - 1) / box_rows;
-        int pg = __shfl_sync(0xffffffffu, cur, ((rel & 31) + lane) & 31);
-        if (lane < boxes && (pg < 0 || pg >= a.num_pages)) {
-          atomicOr(&g_paged_err, ERR_BAD_PAGE);        // reads page 0 in its place
-          pg = 0;
-        }
-        const int y = ((pg * a.num_kv_heads + w.hk) << a.page_shift) + ((j * kBlockN) & (page - 1));
-        const int ring = PAIR ? 0 : (j - w.s0) & 1;
-        uint32_t& kv_it = ring ? kv_it1 : kv_it0;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t st = Ring::stage(ring, kv_it);
-          if (!__all_sync(0xffffffffu, mbar_wait(&sm->kv_empty[st], Ring::parity(kv_it) ^ 1u, abort_flag,
-                                                 &g_paged_err, code)))
-            return;
-          // a V block that the sequence ends in goes by way of the tail warp
-          uint64_t* bar = kv == 1 && valid < kBlockN ? &sm->tail[st] : &sm->kv_full[st];
-          if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * box_rows * HD * 2));
-          __syncwarp();
-          if (lane < boxes) {
-            const CUtensorMap* map = kv ? &maps.v : &maps.k;
-#pragma unroll
-            for (int c = 0; c < HD / 64; ++c)
-              tma_load_2d(sm->kv[st] + c * kBlockN * 128 + lane * box_rows * 128, map, bar, c * 64, y);
-          }
-          ++kv_it;
-          if (j == w.s0 && kv == 0) {
-            // the item's queries, once the previous item has released them
-            if (lane == 0) {
-#pragma unroll
-              for (int t = 0; t < (PAIR ? 2 : 1); ++t) {
-                if (!w.has[t]) continue;
-                if (!mbar_wait(&sm->q_empty[t], (q_it[t] & 1u) ^ 1u, abort_flag, &g_paged_err, code)) {
-                  ok = false;
-                  break;
-                }
-                ++q_it[t];
-                const int copies = PAIR ? 1 : row_copies(w.q_len * a.group);
-                const CUtensorMap* map = &maps.q[PAIR ? 0 : copies >> 1];
-                const int rows = (kBlockM / copies) / a.group * a.group;
-                mbar_arrive_expect_tx(&sm->q_full[t], static_cast<uint32_t>(copies * rows * HD * 2));
-                for (int r = 0; r < copies; ++r)
-#pragma unroll
-                  for (int c = 0; c < HD / 64; ++c)
-                    tma_load_3d(sm->q[t] + c * kBlockM * 128 + r * (kBlockM / copies) * 128, map, &sm->q_full[t],
-                                c * 64, w.hk * a.group, w.q_row0 + (w.tile0 + t) * a.tile_tokens);
-              }
-            }
-            if (!__shfl_sync(0xffffffffu, ok, 0)) return;
-          }
-        }
-      }
-    }
+    if (item.id >= 0) item.len = length_of(a, find_seg(a, item.id));
+    if (!publish(sm, n, item) || item.id < 0) return;
+    const Work w = decode_pair(a, item);
+    if (!load_blocks<HD, true, N>(sm, a, maps, w, uses0, uses1, true)) return;
     int next = -2;
     if (lane == 0) {
-      if (!asked) ring_ask(&sm->ring);
-      next = ring_answer(&sm->ring, steal_ph, a.n_items, abort_flag, &g_paged_err, code);
+      if (w.s1 <= w.s0) ring_ask(&sm->ring);
+      next = ring_answer(&sm->ring, steal_ph, a.n_items, &sm->abort_flag, &g_paged_err, ERR_TIMEOUT_PRODUCER);
     }
     next = __shfl_sync(0xffffffffu, next, 0);
     if (next == -2) return;
-    it = next;
+    item.id = next;
   }
+}
+
+// Key blocks that one key head of a SPLIT segment counts for (a sequence
+// without keys still has rows to write).
+template <int N>
+__device__ __forceinline__ int weight_of(const PagedAttnArgs<N>& a, int seg, int len, int* b0) {
+  const Range r = blocks_of(a, len, a.segs[seg].q_len, 0, a.segs[seg].q_len);
+  *b0 = r.b0;
+  return max(1, r.b1 - r.b0);
+}
+
+// SPLIT: the blocks of all (sequence, key head) units stand in one line, which
+// is cut into equal pieces, one per CTA: every SM has the same number of
+// blocks whatever the lengths, and only units that a cut goes through are
+// joined afterwards.  A CTA's piece of the unit that its range starts inside
+// goes to slot 2c, of the unit that goes on behind its range to 2c + 1, and
+// joins[c] tells the join what begins in slot 2c + 1.
+template <int HD, int N>
+__device__ void produce_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps) {
+  const int lane = threadIdx.x & 31;
+  const int c = blockIdx.x;
+  uint32_t uses0 = 0, uses1 = 0, n = 0;
+  int64_t total = 0;
+  for (int s = lane; s < a.n_segs; s += 32) {
+    int b0;
+    total += weight_of(a, s, length_of(a, s), &b0);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+  total *= a.num_kv_heads;
+  const int64_t per = max(static_cast<int64_t>(kMinBlocks), (total + gridDim.x - 1) / gridDim.x);
+  int64_t g = c * per;
+  const int64_t end = min(total, g + per);
+  PagedJoin join = {0, 0, 0, -1};
+  // the segment that block g lies in: 32 segments at a time
+  int64_t base = 0;            // blocks before the chunk of segments
+  int chunk = 0;
+  int len = 0, w_seg = 0, b0 = 0;
+  int64_t incl = 0;
+  for (; g < end; chunk += 32) {
+    const int s = chunk + lane;
+    len = 0;
+    w_seg = 0;
+    b0 = 0;
+    if (s < a.n_segs) {
+      len = length_of(a, s);
+      w_seg = weight_of(a, s, len, &b0);
+    }
+    incl = static_cast<int64_t>(w_seg) * a.num_kv_heads;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += y;
+    }
+    incl += base;
+    base = __shfl_sync(0xffffffffu, incl, 31);
+    // all units of this chunk that the range meets
+    while (g < end && g < base) {
+      const int k = __ffs(__ballot_sync(0xffffffffu, incl > g)) - 1;      // g's segment in the chunk
+      const int weight = __shfl_sync(0xffffffffu, w_seg, k);
+      const int64_t seg_end = __shfl_sync(0xffffffffu, incl, k);
+      const int64_t off = g - (seg_end - static_cast<int64_t>(weight) * a.num_kv_heads);
+      const int hk = static_cast<int>(off / weight);
+      const int blk = static_cast<int>(off - static_cast<int64_t>(hk) * weight);
+      const int cnt = static_cast<int>(min(static_cast<int64_t>(weight - blk), end - g));
+      const int first = __shfl_sync(0xffffffffu, b0, k);
+      Item item;
+      item.id = chunk + k;
+      item.len = __shfl_sync(0xffffffffu, len, k);
+      item.hk = hk;
+      const Range r = blocks_of(a, item.len, a.segs[item.id].q_len, 0, a.segs[item.id].q_len);
+      item.s0 = r.b1 > r.b0 ? first + blk : 0;
+      item.s1 = r.b1 > r.b0 ? first + blk + cnt : 0;
+      item.slot = blk > 0 ? 2 * c : blk + cnt < weight ? 2 * c + 1 : -1;
+      if (blk == 0 && cnt < weight)
+        join = {a.segs[item.id].q_row0, a.segs[item.id].q_len, hk, static_cast<int>((g + weight - 1) / per)};
+      if (!publish(sm, n++, item)) return;
+      const Work w = decode_split(a, item);
+      if (!load_blocks<HD, false, N>(sm, a, maps, w, uses0, uses1, false)) return;
+      g += cnt;
+    }
+  }
+  if (lane == 0) a.joins[c] = join;
+  publish(sm, n, Item{-1, 0, 0, 0, 0, 0});
 }
 
 // ------------------------------------------------------------------ MMA issuer t
@@ -358,10 +469,9 @@ __device__ void issue(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, uint32
   const uint32_t tO = tS + 128u;
   uint32_t kv_it = 0, q_it = 0, blk_it = 0;
   for (uint32_t n = 0;; ++n) {
-    int len;
-    const int it = take(sm, n, code, false, &len);
-    if (it < 0) return;
-    const Work w = decode<PAIR>(a, it, len);
+    Item item;
+    if (!take(sm, n, code, false, &item)) return;
+    const Work w = decode<PAIR>(a, item);
     if (w.s1 <= w.s0) continue;
     const bool has = PAIR ? w.has[t] : true;
     if (has && !mbar_wait(&sm->q_full[qt], q_it & 1u, abort_flag, &g_paged_err, code)) return;
@@ -415,25 +525,51 @@ __device__ void issue(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, uint32
   }
 }
 
-// ------------------------------------------------------------------ tail warp
+// ------------------------------------------------------------------ aux warp
+// Brings each item's queries once the previous item has released them (a warp
+// of its own, so that the producer runs ahead with keys meanwhile), and clears
+// the end of a sequence's last V block.
 template <int HD, bool PAIR, int N>
-__device__ void clear_tails(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a) {
+__device__ void assist(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps) {
   using Ring = Stages<HD, PAIR>;
   const int lane = threadIdx.x & 31;
+  const uint32_t code = ERR_TIMEOUT_OTHER;
   uint32_t base0 = 0, base1 = 0, phases = 0;     // uses of ring 0 and 1 by earlier items; parity of each tail barrier
+  uint32_t q_it0 = 0, q_it1 = 0;
   for (uint32_t n = 0;; ++n) {
-    int len;
-    const int it = take(sm, n, ERR_TIMEOUT_OTHER, true, &len);
-    if (it < 0) return;
-    const Work w = decode<PAIR>(a, it, len);
+    Item item;
+    if (!take(sm, n, code, true, &item)) return;
+    const Work w = decode<PAIR>(a, item);
     if (w.s1 <= w.s0) continue;
+    bool ok = true;
+    if (lane == 0) {
+#pragma unroll
+      for (int t = 0; t < (PAIR ? 2 : 1); ++t) {
+        if (!w.has[t]) continue;
+        uint32_t& q_it = t ? q_it1 : q_it0;
+        if (!mbar_wait(&sm->q_empty[t], (q_it & 1u) ^ 1u, &sm->abort_flag, &g_paged_err, code)) {
+          ok = false;
+          break;
+        }
+        ++q_it;
+        const int copies = PAIR ? 1 : row_copies(w.q_len * a.group);
+        const CUtensorMap* map = &maps.q[PAIR ? 0 : copies >> 1];
+        const int rows = (kBlockM / copies) / a.group * a.group;
+        mbar_arrive_expect_tx(&sm->q_full[t], static_cast<uint32_t>(copies * rows * HD * 2));
+        for (int r = 0; r < copies; ++r)
+#pragma unroll
+          for (int c = 0; c < HD / 64; ++c)
+            tma_load_3d(sm->q[t] + c * kBlockM * 128 + r * (kBlockM / copies) * 128, map, &sm->q_full[t], c * 64,
+                        w.hk * a.group, w.q_row0 + (w.tile0 + t) * a.tile_tokens);
+      }
+    }
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
     const int jt = w.len / kBlockN, valid = w.len % kBlockN;
     if (valid > 0 && jt >= w.s0 && jt < w.s1) {
       const int ring = PAIR ? 0 : (jt - w.s0) & 1;
       const uint32_t blk = static_cast<uint32_t>(PAIR ? jt - w.s0 : (jt - w.s0) >> 1);
       const uint32_t st = Ring::stage(ring, (ring ? base1 : base0) + 2u * blk + 1u);
-      if (!__all_sync(0xffffffffu, mbar_wait(&sm->tail[st], (phases >> st) & 1u, &sm->abort_flag, &g_paged_err,
-                                             ERR_TIMEOUT_OTHER)))
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm->tail[st], (phases >> st) & 1u, &sm->abort_flag, &g_paged_err, code)))
         return;
       phases ^= 1u << st;
       // rows [valid, 128) of every 64-column box: whole 128-byte rows
@@ -531,10 +667,10 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
   uint32_t blk_it = 0, q_it = 0, turn_it = 0, sync_uses = 0;
   if (t == 1) mbar_arrive(&sm->turn[0]);         // the first turn is group 0's
   for (uint32_t n = 0;; ++n) {
-    int len;
-    const int it = take(sm, n, code, true, &len);
-    if (it < 0) break;
-    const Work w = decode<true>(a, it, len);
+    Item item;
+    if (!take(sm, n, code, true, &item)) break;
+    const Work w = decode_pair(a, item);
+    if (w.idle) continue;
     const bool has = w.has[t];
     const int tok0 = (w.tile0 + t) * a.tile_tokens;
     const int tokens = min(a.tile_tokens, w.q_len - tok0);
@@ -617,8 +753,6 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
         ++q_it;
         tc_fence_after();
       }
-    } else if (w.split > 0) {
-      continue;
     }
     if (!has) continue;
     // ---------------------------------------------------------- epilogue
@@ -627,7 +761,7 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
     const float lse = seen ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
     const int h = w.hk * a.group + row_head;
     const bool loaded = w.s1 > w.s0;            // this item's Q went through q[t]
-    const bool final_rows = w.active <= 1;
+    const bool final_rows = w.final;
     // a full tile of final rows leaves by TMA through the tile's own Q
     // buffer; rows without keys would read O as it was: per thread
     const bool by_tma = final_rows && loaded && !first && tokens == a.tile_tokens;
@@ -671,7 +805,7 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
     } else {
       const int64_t out = final_rows
           ? (static_cast<int64_t>(w.q_row0 + tok) * a.num_heads + h)
-          : ((w.part0 + static_cast<int64_t>(w.split) * w.q_len + tok) * a.num_heads + h);
+          : ((w.part + tok) * a.num_heads + h);
 #pragma unroll 1
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t o[32];
@@ -729,11 +863,9 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
   const uint32_t code = ERR_TIMEOUT_SOFTMAX;
   uint32_t blk_it = 0, q_it = 0, sync_uses = 0;
   for (uint32_t n = 0;; ++n) {
-    int len;
-    const int it = take(sm, n, code, true, &len);
-    if (it < 0) return;
-    const Work w = decode<false>(a, it, len);
-    if (w.s1 <= w.s0 && w.split > 0) continue;
+    Item item;
+    if (!take(sm, n, code, true, &item)) return;
+    const Work w = decode_split(a, item);
     const int rows = w.q_len * a.group;
     const int copies = row_copies(rows);
     const int span = kBlockM / copies;           // rows of a copy
@@ -824,15 +956,14 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
       if (v.x != -INFINITY) l_all += v.y * fast_exp2(v.x - m_all);
     }
     const float scale = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_all) / l_all;
-    const bool final_rows = w.active <= 1;
-    const int64_t row0 = final_rows ? w.q_row0 : w.part0 + static_cast<int64_t>(w.split) * w.q_len;
+    const bool final_rows = w.final;
     if (t == 0 && quad * 32 < span && r < rows) {   // the first copy's threads know the row's LSE
       const int h = w.hk * a.group + r - tok * a.group;
       const float lse = l_all > 0.f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
       if (final_rows)
         a.lse[static_cast<int64_t>(h) * a.lse_stride + w.q_row0 + tok] = lse;
       else
-        a.lse_part[(row0 + tok) * a.num_heads + h] = lse;
+        a.lse_part[w.part + r] = lse;
     }
     // a quarter of the columns at a time through the Q buffer, which is dead
     // now: [t * 128 + row][HD / 4] floats, 16-byte pieces swizzled by the row
@@ -882,13 +1013,15 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
           const float4 u = stage[rw * F4 + (f ^ sw)];
           v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
         }
-        const int tk = rr / a.group, h = w.hk * a.group + rr - tk * a.group;
-        const int64_t off = ((row0 + tk) * a.num_heads + h) * HD + c * (HD / 4) + 4 * f;
-        if (final_rows)
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + off) =
+        const int col = c * (HD / 4) + 4 * f;
+        if (final_rows) {
+          const int tk = rr / a.group, h = w.hk * a.group + rr - tk * a.group;
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) +
+                                    (static_cast<int64_t>(w.q_row0 + tk) * a.num_heads + h) * HD + col) =
               make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        else
-          *reinterpret_cast<float4*>(a.o_part + off) = v;
+        } else {
+          *reinterpret_cast<float4*>(a.o_part + (w.part + rr) * HD + col) = v;
+        }
       }
       if (c == 3) fence_proxy_async_smem();      // the next item's Q may land there after this
       if (!__all_sync(0xffffffffu, mbar_sync(&sm->all_sync, sync_uses, abort_flag, &g_paged_err, code))) return;
@@ -902,6 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttnArgs<N> args) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   auto* sm = reinterpret_cast<PagedSmem<HD, PAIR>*>(smem_raw);
+  if (!PAIR && threadIdx.x == 0) args.joins[blockIdx.x].last = -1;   // also when this CTA gives up a wait
   if ((smem_u32(smem_raw) & 1023u) != 0) {       // the declared alignment; the swizzle needs it
     if (threadIdx.x == 0) atomicOr(&g_paged_err, ERR_BAD_WORK);
     return;
@@ -939,11 +1073,12 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
   const uint32_t tmem = sm->tmem_base;
 
   if (warp == kProducerWarp) {
-    produce<HD, PAIR, N>(sm, args, maps);
+    if constexpr (PAIR) produce_pair<HD, N>(sm, args, maps);
+    else produce_split<HD, N>(sm, args, maps);
   } else if (warp == kMmaWarp0 || warp == kMmaWarp0 + 1) {
     if (lane == 0) issue<HD, PAIR, N>(sm, args, tmem, warp - kMmaWarp0);
-  } else if (warp == kTailWarp) {
-    clear_tails<HD, PAIR, N>(sm, args);
+  } else if (warp == kAuxWarp) {
+    assist<HD, PAIR, N>(sm, args, maps);
   } else if constexpr (PAIR) {
     softmax_pair<HD, N>(sm, args, maps, tmem);
   } else {
@@ -959,39 +1094,22 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
 }
 
 // ------------------------------------------------------------------ joining the splits
-// One block per (query, head) row whose keys were split:
-//     lse = log sum_s exp(lse_s),  o = sum_s exp(lse_s - lse) o_s.
-// The warps take the splits in turn, so that few rows with many splits still
-// have their loads in flight together.  Rows of one split were written in
-// place.
-constexpr int kJoinThreads = 128;
+//     lse = log sum_i exp(lse_i),  o = sum_i exp(lse_i - lse) o_i
+// over the n parts of one row, part i at row part(i) of o_part and lse_part.
+// The warps of the block take the parts in turn, so that few rows with many
+// parts still have their loads in flight together.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 16;                  // SPLIT: blocks that share a unit's rows
 
-template <int HD, bool PAIR, int N>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs<N> a) {
+template <int HD, typename F>
+__device__ __forceinline__ void join_row(const PagedAttnHead& a, int n, F part, int64_t o_row, float* lse_out) {
   constexpr int C = HD / 32;
   constexpr int kWarps = kJoinThreads / 32;
-  __shared__ float part[kWarps][HD];
-  __shared__ float lse_s[kMaxSplits];
+  __shared__ float sum_o[kWarps][HD];
+  __shared__ float lse_s[kMaxParts];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t tok_all = blockIdx.x / a.num_heads;
-  const int h = static_cast<int>(blockIdx.x - tok_all * a.num_heads);
-  int lo = 0, hi = a.n_segs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.segs[mid].tok0 <= tok_all) lo = mid; else hi = mid - 1;
-  }
-  const PagedSeg& s = a.segs[lo];
-  if (s.splits <= 1) return;
-  const int tok = static_cast<int>(tok_all) - s.tok0;
-  int len = __ldg(a.kv_lens + s.seq);
-  len = max(0, min(len, a.max_kv_len));
-  const int tile = tok / a.tile_tokens;
-  const Range r = unit_blocks<PAIR>(a, len, s.q_len, PAIR ? tile & ~1 : 0);
-  const int n = (r.b1 - r.b0 + a.split_blocks - 1) / a.split_blocks;
-  if (n <= 1) return;
-  const int64_t row0 = (s.part0 + tok) * a.num_heads + h;
-  const int64_t step = static_cast<int64_t>(s.q_len) * a.num_heads;
-  for (int i = threadIdx.x; i < n; i += kJoinThreads) lse_s[i] = a.lse_part[row0 + i * step];
+  __syncthreads();                             // the row before has read its sums
+  for (int i = threadIdx.x; i < n; i += kJoinThreads) lse_s[i] = a.lse_part[part(i)];
   __syncthreads();
   float m = -INFINITY;
   for (int i = lane; i < n; i += 32) m = fmaxf(m, lse_s[i]);
@@ -1009,7 +1127,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 #pragma unroll 4
   for (int i = warp; i < n; i += kWarps) {
     const float wgt = seen ? expf(lse_s[i] - m) * inv : 0.f;
-    const float* src = a.o_part + (row0 + i * step) * HD + lane * C;
+    const float* src = a.o_part + part(i) * HD + lane * C;
     if constexpr (C == 4) {
       const float4 v = *reinterpret_cast<const float4*>(src);
       acc[0] = fmaf(wgt, v.x, acc[0]); acc[1] = fmaf(wgt, v.y, acc[1]);
@@ -1020,17 +1138,55 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     }
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c) part[warp][lane * C + c] = acc[c];
+  for (int c = 0; c < C; ++c) sum_o[warp][lane * C + c] = acc[c];
   __syncthreads();
   for (int c = threadIdx.x; c < HD; c += kJoinThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int q = 0; q < kWarps; ++q) v += part[q][c];
-    static_cast<__nv_bfloat16*>(a.o)[(static_cast<int64_t>(s.q_row0 + tok) * a.num_heads + h) * HD + c] =
-        __float2bfloat16_rn(v);
+    for (int q = 0; q < kWarps; ++q) v += sum_o[q][c];
+    static_cast<__nv_bfloat16*>(a.o)[o_row * HD + c] = __float2bfloat16_rn(v);
   }
-  if (threadIdx.x == 0)
-    a.lse[static_cast<int64_t>(h) * a.lse_stride + s.q_row0 + tok] = seen ? m + logf(sum) : -INFINITY;
+  if (threadIdx.x == 0) *lse_out = seen ? m + logf(sum) : -INFINITY;
+}
+
+// PAIR: one block per (query, head) row; rows of one split were written in place.
+template <int HD, int N>
+__global__ void __launch_bounds__(kJoinThreads) join_pair_kernel(const __grid_constant__ PagedAttnArgs<N> a) {
+  const int64_t tok_all = blockIdx.x / a.num_heads;
+  const int h = static_cast<int>(blockIdx.x - tok_all * a.num_heads);
+  int lo = 0, hi = a.n_segs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.segs[mid].tok0 <= tok_all) lo = mid; else hi = mid - 1;
+  }
+  const PagedSeg& s = a.segs[lo];
+  if (s.splits <= 1) return;
+  const int tok = static_cast<int>(tok_all) - s.tok0;
+  const int len = max(0, min(__ldg(a.kv_lens + s.seq), a.max_kv_len));
+  const Range r = pair_blocks(a, len, s.q_len, tok / a.tile_tokens & ~1);
+  const int n = (r.b1 - r.b0 + a.split_blocks - 1) / a.split_blocks;
+  if (n <= 1) return;
+  const int64_t row0 = (s.part0 + tok) * a.num_heads + h;
+  const int64_t step = static_cast<int64_t>(s.q_len) * a.num_heads;
+  join_row<HD>(a, n, [&](int i) { return row0 + i * step; },
+               static_cast<int64_t>(s.q_row0 + tok) * a.num_heads + h,
+               a.lse + static_cast<int64_t>(h) * a.lse_stride + s.q_row0 + tok);
+}
+
+// SPLIT: block x looks after the unit that begins in CTA x and goes on in the
+// CTAs behind it; kJoinRows blocks share its rows.
+template <int HD>
+__global__ void __launch_bounds__(kJoinThreads) join_split_kernel(const __grid_constant__ PagedAttnHead a) {
+  const int c = blockIdx.x;
+  const PagedJoin j = a.joins[c];
+  if (j.last < 0) return;
+  for (int r = blockIdx.y; r < j.q_len * a.group; r += kJoinRows) {
+    const int tok = r / a.group, h = j.hk * a.group + r - tok * a.group;
+    join_row<HD>(a, j.last - c + 1,
+                 [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.slot_rows + r; },
+                 static_cast<int64_t>(j.q_row0 + tok) * a.num_heads + h,
+                 a.lse + static_cast<int64_t>(h) * a.lse_stride + j.q_row0 + tok);
+  }
 }
 
 // The first n_segs of N.
@@ -1062,23 +1218,22 @@ cudaError_t launch_attn(const PagedMaps& maps, const PagedAttnArgs<N>& a, cudaSt
   return cudaGetLastError();
 }
 
-template <int HD, bool PAIR, int N>
-cudaError_t launch_join(const PagedAttnArgs<N>& a, cudaStream_t stream) {
-  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.tokens) * a.num_heads);
-  paged_join_kernel<HD, PAIR, N><<<blocks, kJoinThreads, 0, stream>>>(a);
-  return cudaGetLastError();
-}
-
 template <int HD, bool PAIR>
 cudaError_t attn_kind(const PagedMaps& maps, const PagedAttnArgs<kMaxSegs>& a, cudaStream_t stream) {
   return a.n_segs <= kFewSegs ? launch_attn<HD, PAIR, kFewSegs>(maps, cut<kFewSegs>(a), stream)
                               : launch_attn<HD, PAIR, kMaxSegs>(maps, a, stream);
 }
 
-template <int HD, bool PAIR>
-cudaError_t join_kind(const PagedAttnArgs<kMaxSegs>& a, cudaStream_t stream) {
-  return a.n_segs <= kFewSegs ? launch_join<HD, PAIR, kFewSegs>(cut<kFewSegs>(a), stream)
-                              : launch_join<HD, PAIR, kMaxSegs>(a, stream);
+template <int HD>
+cudaError_t join_kind(bool pair, const PagedAttnArgs<kMaxSegs>& a, cudaStream_t stream) {
+  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.tokens) * a.num_heads);
+  if (!pair)
+    join_split_kernel<HD><<<dim3(a.n_items, std::min(a.slot_rows, kJoinRows)), kJoinThreads, 0, stream>>>(a);
+  else if (a.n_segs <= kFewSegs)
+    join_pair_kernel<HD, kFewSegs><<<blocks, kJoinThreads, 0, stream>>>(cut<kFewSegs>(a));
+  else
+    join_pair_kernel<HD, kMaxSegs><<<blocks, kJoinThreads, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -1090,8 +1245,7 @@ cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, co
 }
 
 cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnArgs<kMaxSegs>& a, cudaStream_t stream) {
-  if (head_dim == 64) return pair ? join_kind<64, true>(a, stream) : join_kind<64, false>(a, stream);
-  return pair ? join_kind<128, true>(a, stream) : join_kind<128, false>(a, stream);
+  return head_dim == 64 ? join_kind<64>(pair, a, stream) : join_kind<128>(pair, a, stream);
 }
 
 uint32_t paged_attn_take_error() {

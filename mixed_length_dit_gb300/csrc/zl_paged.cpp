@@ -134,12 +134,12 @@ zl_status check_attn(const int32_t* cu_q, int32_t num_seqs, int32_t max_kv_len, 
 }
 
 // ------------------------------------------------------------------ the attention's work split
-// What the split depends on.
+// What the split depends on.  It does not look at a window: a workspace serves
+// every window.
 struct Shape {
   int32_t group;         // query heads of a key head: rows of one token in a tile
   int32_t kv_heads;
   int32_t max_kv_len;
-  int32_t window;
 
   int32_t tile_tokens() const { return zl::kBlockM / group; }
   bool pair(int32_t n) const { return n > tile_tokens(); }
@@ -147,81 +147,62 @@ struct Shape {
     const int64_t tiles = (n + tile_tokens() - 1) / tile_tokens();
     return pair(n) ? (tiles + 1) / 2 : 1;
   }
-  // Most 128-key blocks that a unit of a sequence with n queries is split
-  // over: the whole length, or for one tile what a window reaches back from
-  // the first query to the end.
-  int32_t blocks(int32_t n) const {
-    int64_t keys = max_kv_len;
-    if (window > 0 && !pair(n)) keys = std::min<int64_t>(keys, int64_t(window) + n + zl::kBlockN);
-    return static_cast<int32_t>((keys + zl::kBlockN - 1) / zl::kBlockN);
-  }
+  int32_t blocks() const { return std::max(1, max_kv_len / zl::kBlockN + (max_kv_len % zl::kBlockN != 0)); }
 };
 
+// One launch of a kind: up to kMaxSegs sequences.
 struct Launch {
-  int64_t items = 0;
-  int64_t part_rows = 0;
-  int64_t most_rows = 0;      // part_rows of any window
-  int32_t split_blocks = 1;
-
-  int32_t splits(const Shape& sh, int32_t n) const {
-    return std::max(1, (sh.blocks(n) + split_blocks - 1) / split_blocks);
-  }
+  int32_t segs = 0;
+  int64_t items = 0;          // PAIR
+  int32_t split_blocks = 1;   // PAIR
+  int32_t splits = 1;         // PAIR
+  int64_t part_rows = 0;      // rows of o_part and lse_part
+  int32_t slot_rows = 0;      // SPLIT
 };
 
-constexpr int64_t kPlanSms = 152;
-
-// The next launch of one kind: as many sequences from *i on as it holds, and
-// the key blocks of a split.  A call's workspace is planned on hosts without a
-// GPU too, so the split counts on this GPU's 152 SMs.
+// The next launch of a kind: as many sequences from *i on as it holds.
 Launch plan_launch(const Shape& sh, const int32_t* cu, int32_t num_seqs, int32_t* i, bool pair) {
   Launch l;
-  const int32_t first = *i;
-  int32_t segs = 0, most = 1;
-  int64_t units = 0, work = 0;
-  for (; *i < num_seqs && segs < zl::kMaxSegs; ++*i) {
+  int64_t units = 0, tokens = 0;
+  int32_t most = 0;
+  for (; *i < num_seqs && l.segs < zl::kMaxSegs; ++*i) {
     const int32_t n = cu[*i + 1] - cu[*i];
     if (n == 0 || sh.pair(n) != pair) continue;
-    ++segs;
+    ++l.segs;
     units += sh.units(n) * sh.kv_heads;
-    work += sh.units(n) * sh.kv_heads * sh.blocks(n);
-    most = std::max(most, sh.blocks(n));
+    tokens += n;
+    most = std::max(most, n);
   }
-  if (pair) {
-    // Long items are fine as long as the last wave of them is full: split
-    // only where it would leave more than 15% of the SMs' time empty.
-    int32_t s = 1;
-    while (s < 8 && most / (s + 1) >= 16) {
-      const int64_t waves = (units * s + kPlanSms - 1) / kPlanSms;
-      if (units * s * 100 >= waves * kPlanSms * 85) break;
-      ++s;
-    }
-    l.split_blocks = (most + s - 1) / s;
-  } else {
-    // Eight items for every SM even out lengths that the host does not know,
-    // of at most 32 blocks and at least 2 (one for each softmax group).
-    const int64_t b = (work + 8 * kPlanSms - 1) / (8 * kPlanSms);
-    l.split_blocks = static_cast<int32_t>(std::min<int64_t>(32, std::max<int64_t>(2, b)));
+  if (l.segs == 0) return l;
+  if (!pair) {
+    l.slot_rows = most * sh.group;
+    l.part_rows = int64_t(2) * zl::kSplitCtas * l.slot_rows;
+    return l;
   }
-  l.split_blocks = std::max(1, std::max(l.split_blocks, (most + zl::kMaxSplits - 1) / zl::kMaxSplits));
-  for (int32_t x = first; x < *i; ++x) {
-    const int32_t n = cu[x + 1] - cu[x];
-    if (n == 0 || sh.pair(n) != pair) continue;
-    const int32_t splits = l.splits(sh, n);
-    l.items += sh.units(n) * sh.kv_heads * splits;
-    if (splits > 1) l.part_rows += int64_t(splits) * n;
-    // With a window, b blocks instead of B are split by a b-th of the same
-    // rule: at most twice the items it aims for and one more (sequences differ
-    // by one block at most), B / 32 of full size, or B / 2 of the smallest.
-    const int32_t all = Shape{sh.group, sh.kv_heads, sh.max_kv_len, 0}.blocks(n);
-    const int64_t bound = std::max<int64_t>(16 * kPlanSms / units + 2, (all + 31) / 32);
-    const int64_t widest = pair ? splits : std::min<int64_t>({zl::kMaxSplits, (all + 1) / 2, bound});
-    if (widest > 1) l.most_rows += widest * n;
+  // Long items are fine as long as the last wave of them is full: split only
+  // where it would leave more than 15% of the SMs' time empty.
+  while (l.splits < zl::kMaxSplits && sh.blocks() / (l.splits + 1) >= 16) {
+    const int64_t items = units * l.splits, waves = (items + zl::kSplitCtas - 1) / zl::kSplitCtas;
+    if (items * 100 >= waves * zl::kSplitCtas * 85) break;
+    ++l.splits;
   }
+  l.split_blocks = (sh.blocks() + l.splits - 1) / l.splits;
+  l.items = units * l.splits;
+  if (l.splits > 1) l.part_rows = l.splits * tokens * sh.group * sh.kv_heads;
   return l;
 }
 
-size_t part_bytes(int64_t rows, int64_t heads, int64_t hd) {
-  return static_cast<size_t>(rows) * heads * (hd + 1) * sizeof(float);
+// The launches of a call run one after another and share their parts' memory.
+size_t attn_workspace(const Shape& sh, const int32_t* cu, int32_t num_seqs, int32_t hd) {
+  size_t need = 0;
+  for (const bool pair : {false, true})
+    for (int32_t i = 0; i < num_seqs;) {
+      const Launch l = plan_launch(sh, cu, num_seqs, &i, pair);
+      size_t bytes = static_cast<size_t>(l.part_rows) * (hd + 1) * sizeof(float);
+      if (l.slot_rows > 0) bytes += zl::kSplitCtas * sizeof(zl::PagedJoin);
+      need = std::max(need, bytes);
+    }
+  return need;
 }
 
 zl_status check_tables(const zl_page_tables_t* t, zl::PageTable* out) {
@@ -409,11 +390,7 @@ zl_status zl_paged_attn_workspace_size(const int32_t* cu_seqlens_q, int32_t num_
   int64_t tq = 0;
   const zl_status st = check_attn(cu_seqlens_q, num_seqs, max_kv_len, num_heads, num_kv_heads, head_dim, &tq);
   if (st != ZL_OK) return st;
-  int64_t rows = 0;
-  const Shape sh{num_heads / num_kv_heads, num_kv_heads, max_kv_len, 0};
-  for (const bool pair : {false, true})
-    for (int32_t i = 0; i < num_seqs;) rows += plan_launch(sh, cu_seqlens_q, num_seqs, &i, pair).most_rows;
-  *bytes = part_bytes(rows, num_heads, head_dim);
+  *bytes = attn_workspace(Shape{num_heads / num_kv_heads, num_kv_heads, max_kv_len}, cu_seqlens_q, num_seqs, head_dim);
   return ZL_OK;
 }
 
@@ -437,11 +414,8 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
   st = check_rows(q, q_stride, num_heads, hd, tq, 2);
   if (st != ZL_OK) return st;
 
-  const Shape sh{num_heads / cache->num_kv_heads, cache->num_kv_heads, max_kv_len, window};
-  int64_t rows = 0;
-  for (const bool pair : {false, true})
-    for (int32_t i = 0; i < num_seqs;) rows += plan_launch(sh, cu_seqlens_q, num_seqs, &i, pair).part_rows;
-  const size_t need = part_bytes(rows, num_heads, hd);
+  const Shape sh{num_heads / cache->num_kv_heads, cache->num_kv_heads, max_kv_len};
+  const size_t need = attn_workspace(sh, cu_seqlens_q, num_seqs, hd);
   if (need > 0 && (!workspace || workspace_bytes < need)) return ZL_EWORKSPACE;
   if (need > 0 && !aligned16(workspace)) return ZL_EALIGN;
   int sms = 0;
@@ -455,8 +429,6 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
   a.kv_lens = cache->kv_lens;
   a.o = o;
   a.lse = lse;
-  a.o_part = static_cast<float*>(workspace);
-  a.lse_part = a.o_part + rows * num_heads * hd;
   a.lse_stride = tq;
   a.num_heads = num_heads;
   a.num_kv_heads = cache->num_kv_heads;
@@ -491,26 +463,32 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
       ok = ok && zl::make_map_heads(&maps.q[i], q, tq, num_heads, hd, q_stride, a.group, zl::kBlockM / (1 << i) / a.group);
   if (!ok) return ZL_ECUDA;
 
-  int64_t part0 = 0;
   for (const bool pair : {false, true}) {
     for (int32_t i = 0; i < num_seqs;) {
       const int32_t first = i;
       const Launch l = plan_launch(sh, cu_seqlens_q, num_seqs, &i, pair);
-      if (l.items == 0) continue;
+      if (l.segs == 0) continue;
       if (l.items > INT32_MAX) return ZL_EINVAL;
+      char* ws = static_cast<char*>(workspace);
+      a.joins = reinterpret_cast<zl::PagedJoin*>(ws);
+      if (!pair) ws += zl::kSplitCtas * sizeof(zl::PagedJoin);
+      a.o_part = reinterpret_cast<float*>(ws);
+      a.lse_part = a.o_part + l.part_rows * hd;
       a.split_blocks = l.split_blocks;
+      a.slot_rows = l.slot_rows;
       a.n_segs = 0;
       a.n_items = 0;
       a.tokens = 0;
+      int64_t part0 = 0;
       for (int32_t x = first; x < i; ++x) {
         const int32_t n = cu_seqlens_q[x + 1] - cu_seqlens_q[x];
         if (n == 0 || sh.pair(n) != pair) continue;
-        const int32_t splits = l.splits(sh, n);
-        a.segs[a.n_segs++] = zl::PagedSeg{x, cu_seqlens_q[x], n, a.n_items, splits, a.tokens, part0};
-        a.n_items += static_cast<int32_t>(sh.units(n) * sh.kv_heads * splits);
+        a.segs[a.n_segs++] = zl::PagedSeg{x, cu_seqlens_q[x], n, a.n_items, l.splits, a.tokens, part0};
+        a.n_items += static_cast<int32_t>(sh.units(n) * sh.kv_heads * l.splits);
         a.tokens += n;
-        if (splits > 1) part0 += int64_t(splits) * n;
+        part0 += int64_t(l.splits) * n;
       }
+      if (!pair) a.n_items = zl::kSplitCtas;
       st = launch_counted("paged_attn", s, [&] { return zl::launch_paged_attn(hd, pair, maps, a, s); });
       if (st != ZL_OK) return st;
       if (l.part_rows == 0) continue;
