@@ -511,15 +511,18 @@ __device__ void issue(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, uint32
                   (!first || ks > 0) ? 1u : 0u);
         first = false;
         ++blk_it;
-        umma_commit(&sm->kv_empty[st]);
+        if (PAIR || j < w.s1 - 1) umma_commit(&sm->kv_empty[st]);   // SPLIT's epilogue joins parts in the last V stage
       } else {
         mbar_arrive(&sm->kv_empty[st]);
       }
       ++kv_it;
     }
     if (has) {
-      if (first) umma_commit(&sm->q_empty[qt]);          // no block of this item was this issuer's
-      umma_commit(&sm->o_full[t]);
+      // An issuer without a block in this item does not wait for the softmax
+      // group's work on the one before: it must not complete o_full, or could
+      // complete it a second time before the group has seen the first.
+      if (first) umma_commit(&sm->q_empty[qt]);
+      else umma_commit(&sm->o_full[t]);
       ++q_it;
     }
   }
@@ -588,6 +591,22 @@ __device__ void assist(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const
 }
 
 // ------------------------------------------------------------------ softmax
+// One arrival for a warp: what its lanes did before is ordered before it (the
+// lanes of an arrival on one barrier go one after another, so 128 of them cost
+// more than the block's TMEM traffic).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// A barrier among warps that each count as one; `uses` counts the calls.
+__device__ __forceinline__ bool warps_sync(uint64_t* bar, uint32_t& uses, volatile int* abort_flag, uint32_t code) {
+  warp_arrive(bar);
+  const bool ok = mbar_wait(bar, uses & 1u, abort_flag, &g_paged_err, code);
+  ++uses;
+  return __all_sync(0xffffffffu, ok);
+}
+
 // P of 32 scores as 16 packed columns; adds their sum to acc.
 __device__ __forceinline__ void exp_pack(const uint32_t (&s)[32], float sl2, float neg_m, uint64_t (&acc)[2],
                                          uint32_t (&p)[16]) {
@@ -665,7 +684,7 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
   const uint32_t code = ERR_TIMEOUT_SOFTMAX;
   const int row_tok = row / a.group, row_head = row - row_tok * a.group;
   uint32_t blk_it = 0, q_it = 0, turn_it = 0, sync_uses = 0;
-  if (t == 1) mbar_arrive(&sm->turn[0]);         // the first turn is group 0's
+  if (t == 1) warp_arrive(&sm->turn[0]);         // the first turn is group 0's
   for (uint32_t n = 0;; ++n) {
     Item item;
     if (!take(sm, n, code, true, &item)) break;
@@ -695,7 +714,7 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
           break;
         }
         if (!mine) {
-          mbar_arrive(&sm->turn[t ^ 1]);
+          warp_arrive(&sm->turn[t ^ 1]);
           continue;
         }
         tc_fence_after();
@@ -736,19 +755,19 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
           exp_pack(s[c], sl2, neg_m, acc, p);
           tmem_st16(tS + 16 * c, p);
         }
-        mbar_arrive(&sm->turn[t ^ 1]);
+        warp_arrive(&sm->turn[t ^ 1]);
         if (!first && __any_sync(0xffffffffu, need)) rescale_o<HD>(tO, alpha);
         first = false;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&sm->p_full[t]);
+        warp_arrive(&sm->p_full[t]);
         ++blk_it;
         float ls0, ls1;
         f2_unpack(f2_add(acc[0], acc[1]), ls0, ls1);
         l_run += ls0 + ls1;
       }
       if (!ok) break;
-      if (has) {
+      if (!first) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sm->o_full[t], q_it & 1u, abort_flag, &g_paged_err, code))) break;
         ++q_it;
         tc_fence_after();
@@ -790,7 +809,7 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sm->grp_sync[t]);
+      warp_arrive(&sm->grp_sync[t]);
       const uint32_t phase = sync_uses++;
       if (row == 0) {
         if (!mbar_wait(&sm->grp_sync[t], phase & 1u, abort_flag, &g_paged_err, code)) break;
@@ -852,6 +871,7 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
 // takes its own part of a block's columns.
 template <int HD, int N>
 __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& a, uint32_t tmem) {
+  using Ring = Stages<HD, false>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = warp >> 2, quad = warp & 3;
   const int row = quad * 32 + lane;
@@ -861,7 +881,7 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
   const float sl2 = a.scale_log2;
   volatile int* abort_flag = &sm->abort_flag;
   const uint32_t code = ERR_TIMEOUT_SOFTMAX;
-  uint32_t blk_it = 0, q_it = 0, sync_uses = 0;
+  uint32_t blk_it = 0, q_it = 0, sync_uses = 0, base0 = 0, base1 = 0;
   for (uint32_t n = 0;; ++n) {
     Item item;
     if (!take(sm, n, code, true, &item)) return;
@@ -929,10 +949,10 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
         f2_unpack(f2_add(acc[0], acc[1]), ls0, ls1);
         l_run += ls0 + ls1;
       }
-      mbar_arrive(&sm->p_full[t]);
+      warp_arrive(&sm->p_full[t]);
     }
     const bool loaded = w.s1 > w.s0;
-    if (!loaded) {                               // nothing is seen; the Q buffer may be the next item's already
+    if (!loaded) {                               // nothing is seen
       const int F8 = HD / 8;
       for (int y = threadIdx.x; y < rows * F8; y += 2 * kBlockM) {
         const int rr = y / F8, tk = rr / a.group, h = w.hk * a.group + rr - tk * a.group;
@@ -942,79 +962,80 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
       }
       continue;
     }
-    if (!__all_sync(0xffffffffu, mbar_wait(&sm->o_full[t], q_it & 1u, abort_flag, &g_paged_err, code))) return;
-    ++q_it;
-    tc_fence_after();
+    if (w.s1 - w.s0 > t) {                       // the group had a block
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm->o_full[t], q_it & 1u, abort_flag, &g_paged_err, code))) return;
+      ++q_it;
+      tc_fence_after();
+    }
     // ---------------------------------------------------------- join the parts of each row
+    // part i: group i / copies, copy i % copies
     sm->ml[t * kBlockM + row] = make_float2(m_run, l_run);
-    if (!__all_sync(0xffffffffu, mbar_sync(&sm->all_sync, sync_uses, abort_flag, &g_paged_err, code))) return;
+    if (!warps_sync(&sm->all_sync, sync_uses, abort_flag, code)) return;
+    const int parts = 2 * copies;
     float m_all = -INFINITY;
-    for (int i = 0; i < 2 * copies; ++i) m_all = fmaxf(m_all, sm->ml[i * span + r].x);
+    for (int i = 0; i < parts; ++i) m_all = fmaxf(m_all, sm->ml[i * span + r].x);
     float l_all = 0.f;
-    for (int i = 0; i < 2 * copies; ++i) {
+    for (int i = 0; i < parts; ++i) {
       const float2 v = sm->ml[i * span + r];
       if (v.x != -INFINITY) l_all += v.y * fast_exp2(v.x - m_all);
     }
     const float scale = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_all) / l_all;
-    const bool final_rows = w.final;
     if (t == 0 && quad * 32 < span && r < rows) {   // the first copy's threads know the row's LSE
       const int h = w.hk * a.group + r - tok * a.group;
       const float lse = l_all > 0.f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
-      if (final_rows)
+      if (w.final)
         a.lse[static_cast<int64_t>(h) * a.lse_stride + w.q_row0 + tok] = lse;
       else
         a.lse_part[w.part + r] = lse;
     }
-    // a quarter of the columns at a time through the Q buffer, which is dead
-    // now: [t * 128 + row][HD / 4] floats, 16-byte pieces swizzled by the row
-    constexpr int F4 = HD / 16;                  // 16-byte pieces of a quarter row
-    float4* stage = reinterpret_cast<float4*>(sm->q[0]);
-    const int swz = HD == 128 ? row & 7 : (row >> 1) & 3;
+    // Through the item's last V stage, which its issuer leaves to this
+    // epilogue: [part][row][width] floats, 16-byte pieces swizzled by the
+    // row, in as few passes over the columns as the stage allows (one for
+    // eight rows or fewer).
+    const int blocks = w.s1 - w.s0;
+    const int ring = (blocks - 1) & 1;
+    const uint32_t st = Ring::stage(ring, (ring ? base1 : base0) + 2u * static_cast<uint32_t>((blocks - 1) >> 1) + 1u);
+    base0 += 2u * static_cast<uint32_t>((blocks + 1) / 2);
+    base1 += 2u * static_cast<uint32_t>(blocks / 2);
+    float4* stage = reinterpret_cast<float4*>(sm->kv[st]);
+    const int passes = copies * rows <= 32 ? 1 : copies * rows <= 64 ? 2 : 4;
+    const int width = HD / passes;               // columns of a pass
+    const int f4 = width / 4;                    // 16-byte pieces of a row, 4 at least
+    const int swz_mask = min(7, f4 - 1);
+    const int part = t * copies + row / span;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      __syncwarp();
+    for (int c = 0; c < passes; ++c) {
       if (warp_rows) {
-        float4* dst = stage + (t * kBlockM + row) * F4;
-        if constexpr (HD == 128) {
-          uint32_t o[32];
-          tmem_ld32(tO + c * 32, o);
-          tmem_wait_ld();
-          reg_fence(o);
-#pragma unroll
-          for (int i = 0; i < F4; ++i) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (scale != 0.f)
-              v = make_float4(__uint_as_float(o[4 * i]) * scale, __uint_as_float(o[4 * i + 1]) * scale,
-                              __uint_as_float(o[4 * i + 2]) * scale, __uint_as_float(o[4 * i + 3]) * scale);
-            dst[i ^ swz] = v;
-          }
-        } else {
+        float4* dst = stage + (part * rows + r) * f4;
+#pragma unroll 1
+        for (int x = 0; x < width / 16; ++x) {
           uint32_t o[16];
-          tmem_ld16(tO + c * 16, o);
+          __syncwarp();
+          tmem_ld16(tO + c * width + x * 16, o);
           tmem_wait_ld();
           reg_fence(o);
+          if (r < rows) {
 #pragma unroll
-          for (int i = 0; i < F4; ++i) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (scale != 0.f)
-              v = make_float4(__uint_as_float(o[4 * i]) * scale, __uint_as_float(o[4 * i + 1]) * scale,
-                              __uint_as_float(o[4 * i + 2]) * scale, __uint_as_float(o[4 * i + 3]) * scale);
-            dst[i ^ swz] = v;
+            for (int i = 0; i < 4; ++i) {
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (scale != 0.f)                  // else O may never have been written
+                v = make_float4(__uint_as_float(o[4 * i]) * scale, __uint_as_float(o[4 * i + 1]) * scale,
+                                __uint_as_float(o[4 * i + 2]) * scale, __uint_as_float(o[4 * i + 3]) * scale);
+              dst[(4 * x + i) ^ (r & swz_mask)] = v;
+            }
           }
         }
       }
-      if (!__all_sync(0xffffffffu, mbar_sync(&sm->all_sync, sync_uses, abort_flag, &g_paged_err, code))) return;
-      for (int y = threadIdx.x; y < rows * F4; y += 2 * kBlockM) {
-        const int rr = y / F4, f = y % F4;
+      if (!warps_sync(&sm->all_sync, sync_uses, abort_flag, code)) return;
+      for (int y = threadIdx.x; y < rows * f4; y += 2 * kBlockM) {
+        const int rr = y / f4, f = y - rr * f4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < 2 * copies; ++i) {
-          const int rw = i * span + rr;          // group (i / copies), copy (i % copies): 128 rows apart
-          const int sw = HD == 128 ? rw & 7 : (rw >> 1) & 3;
-          const float4 u = stage[rw * F4 + (f ^ sw)];
+        for (int i = 0; i < parts; ++i) {
+          const float4 u = stage[(i * rows + rr) * f4 + (f ^ (rr & swz_mask))];
           v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
         }
-        const int col = c * (HD / 4) + 4 * f;
-        if (final_rows) {
+        const int col = c * width + 4 * f;
+        if (w.final) {
           const int tk = rr / a.group, h = w.hk * a.group + rr - tk * a.group;
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) +
                                     (static_cast<int64_t>(w.q_row0 + tk) * a.num_heads + h) * HD + col) =
@@ -1023,10 +1044,10 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
           *reinterpret_cast<float4*>(a.o_part + (w.part + rr) * HD + col) = v;
         }
       }
-      if (c == 3) fence_proxy_async_smem();      // the next item's Q may land there after this
-      if (!__all_sync(0xffffffffu, mbar_sync(&sm->all_sync, sync_uses, abort_flag, &g_paged_err, code))) return;
+      fence_proxy_async_smem();                  // TMA may write the stage after this
+      if (!warps_sync(&sm->all_sync, sync_uses, abort_flag, code)) return;
     }
-    if (threadIdx.x == 0) mbar_arrive(&sm->q_empty[0]);
+    if (threadIdx.x == 0) mbar_arrive(&sm->kv_empty[st]);
   }
 }
 
@@ -1046,14 +1067,14 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm->q_full[t], 1);
-      mbar_init(&sm->q_empty[t], PAIR ? 2 : 3);  // its issuers' last S, and the epilogue
+      mbar_init(&sm->q_empty[t], 2);             // PAIR: the last S and the epilogue; SPLIT: both issuers' last S
       mbar_init(&sm->s_full[t], 1);
-      mbar_init(&sm->p_full[t], 128);
+      mbar_init(&sm->p_full[t], 4);              // the group's warps
       mbar_init(&sm->o_full[t], 1);
-      mbar_init(&sm->turn[t], 128);
-      mbar_init(&sm->grp_sync[t], 128);
+      mbar_init(&sm->turn[t], 4);
+      mbar_init(&sm->grp_sync[t], 4);
     }
-    mbar_init(&sm->all_sync, 256);
+    mbar_init(&sm->all_sync, 8);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm->kv_full[s], 1);
       mbar_init(&sm->kv_empty[s], PAIR ? 2 : 1); // PAIR: both issuers pass every stage
