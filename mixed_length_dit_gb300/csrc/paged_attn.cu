@@ -98,7 +98,10 @@ struct PagedSmem {
   Item item[2];                                // what the ring's slots hold
   uint32_t tmem_base;
   int abort_flag;
-  float2 ml[2 * kBlockM];                      // SPLIT: m and l of every group's rows
+  union {
+    float2 ml[2 * kBlockM];                    // SPLIT: m and l of every group's rows
+    int64_t chunk_blocks[kMaxSegs / 32];       // SPLIT, at the start: weights of 32 segments each
+  };
 };
 
 // Block ranges [b0, b1) of 128 keys.
@@ -380,6 +383,20 @@ __device__ __forceinline__ int weight_of(const PagedAttnArgs<N>& a, int seg, int
   return max(1, r.b1 - r.b0);
 }
 
+// SPLIT, all warps: the blocks of every 32 segments.
+template <int HD, int N>
+__device__ __forceinline__ void sum_chunks(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& a) {
+  const int lane = threadIdx.x & 31;
+  for (int chunk = threadIdx.x & ~31; chunk < a.n_segs; chunk += kThreads) {
+    int b0, w = 0;
+    if (chunk + lane < a.n_segs) w = weight_of(a, chunk + lane, length_of(a, chunk + lane), &b0);
+    int64_t sum = static_cast<int64_t>(w) * a.num_kv_heads;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) sm->chunk_blocks[chunk / 32] = sum;
+  }
+}
+
 // SPLIT: the blocks of all (sequence, key head) units stand in one line, which
 // is cut into equal pieces, one per CTA: every SM has the same number of
 // blocks whatever the lengths, and only units that a cut goes through are
@@ -392,20 +409,18 @@ __device__ void produce_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
   const int c = blockIdx.x;
   uint32_t uses0 = 0, uses1 = 0, n = 0;
   int64_t total = 0;
-  for (int s = lane; s < a.n_segs; s += 32) {
-    int b0;
-    total += weight_of(a, s, length_of(a, s), &b0);
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-  total *= a.num_kv_heads;
+  for (int s = 0; s < a.n_segs; s += 32) total += sm->chunk_blocks[s / 32];
   const int64_t per = max(static_cast<int64_t>(kMinBlocks), (total + gridDim.x - 1) / gridDim.x);
   int64_t g = c * per;
   const int64_t end = min(total, g + per);
   PagedJoin join = {0, 0, 0, -1};
-  // the segment that block g lies in: 32 segments at a time
+  // the segments that hold block g: 32 at a time
   int64_t base = 0;            // blocks before the chunk of segments
   int chunk = 0;
+  while (g < end && base + sm->chunk_blocks[chunk / 32] <= g) {
+    base += sm->chunk_blocks[chunk / 32];
+    chunk += 32;
+  }
   int len = 0, w_seg = 0, b0 = 0;
   int64_t incl = 0;
   for (; g < end; chunk += 32) {
@@ -1088,6 +1103,9 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
     tmem_alloc(&sm->tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  if constexpr (!PAIR) sum_chunks<HD, N>(sm, args);
+  // the join may be set up from here on; it waits for this grid's end itself
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1173,6 +1191,7 @@ __device__ __forceinline__ void join_row(const PagedAttnHead& a, int n, F part, 
 // PAIR: one block per (query, head) row; rows of one split were written in place.
 template <int HD, int N>
 __global__ void __launch_bounds__(kJoinThreads) join_pair_kernel(const __grid_constant__ PagedAttnArgs<N> a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t tok_all = blockIdx.x / a.num_heads;
   const int h = static_cast<int>(blockIdx.x - tok_all * a.num_heads);
   int lo = 0, hi = a.n_segs - 1;
@@ -1199,6 +1218,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_pair_kernel(const __grid_co
 template <int HD>
 __global__ void __launch_bounds__(kJoinThreads) join_split_kernel(const __grid_constant__ PagedAttnHead a) {
   const int c = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedJoin j = a.joins[c];
   if (j.last < 0) return;
   for (int r = blockIdx.y; r < j.q_len * a.group; r += kJoinRows) {
@@ -1245,16 +1265,30 @@ cudaError_t attn_kind(const PagedMaps& maps, const PagedAttnArgs<kMaxSegs>& a, c
                               : launch_attn<HD, PAIR, kMaxSegs>(maps, a, stream);
 }
 
+// The join's launch overlaps the attention's last CTAs (programmatic dependent
+// launch); its blocks wait for their results.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int HD>
 cudaError_t join_kind(bool pair, const PagedAttnArgs<kMaxSegs>& a, cudaStream_t stream) {
-  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.tokens) * a.num_heads);
+  const dim3 blocks(static_cast<unsigned>(static_cast<int64_t>(a.tokens) * a.num_heads));
   if (!pair)
-    join_split_kernel<HD><<<dim3(a.n_items, std::min(a.slot_rows, kJoinRows)), kJoinThreads, 0, stream>>>(a);
-  else if (a.n_segs <= kFewSegs)
-    join_pair_kernel<HD, kFewSegs><<<blocks, kJoinThreads, 0, stream>>>(cut<kFewSegs>(a));
-  else
-    join_pair_kernel<HD, kMaxSegs><<<blocks, kJoinThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+    return launch_after(join_split_kernel<HD>, dim3(a.n_items, std::min(a.slot_rows, kJoinRows)), stream,
+                        static_cast<const PagedAttnHead&>(a));
+  return a.n_segs <= kFewSegs ? launch_after(join_pair_kernel<HD, kFewSegs>, blocks, stream, cut<kFewSegs>(a))
+                              : launch_after(join_pair_kernel<HD, kMaxSegs>, blocks, stream, a);
 }
 
 }  // namespace
