@@ -56,29 +56,26 @@ struct RopeArgs : RopeHead {
 };
 static_assert(sizeof(RopeArgs<kMaxSegs>) <= 32764, "rotary arguments exceed the kernel parameter space");
 
-// Most splits of a PAIR sequence's keys, CTAs of a SPLIT launch (one for each
-// of this GPU's SMs), and parts of one row that a join takes.
-constexpr int kMaxSplits = 8;
-constexpr int kSplitCtas = 152;
-constexpr int kMaxParts = kSplitCtas;
+// CTAs of a paged attention launch, one for each of this GPU's SMs; each takes
+// an equal share of the call's key blocks.  A row has a part from as many of
+// them as its keys are spread over.
+constexpr int kPagedCtas = 152;
+constexpr int kMaxParts = kPagedCtas;
 
 // One sequence's queries in a paged attention launch.
 struct PagedSeg {
   int32_t seq;       // row of the page table and of the lengths
   int32_t q_row0;    // packed row of its first query
   int32_t q_len;     // queries, >= 1
-  int32_t item0;     // PAIR: first work item
-  int32_t splits;    // PAIR: splits of its keys, 1 .. kMaxSplits
-  int32_t tok0;      // PAIR: queries of the launch's earlier segments
-  int64_t part0;     // PAIR, splits > 1: its first row in o_part / lse_part
 };
 
-// SPLIT: the unit that begins in a CTA and goes on in the CTAs up to `last`
-// (-1: none).
+// The unit (query tiles from tile0 on of a key head) that begins in a CTA and
+// goes on in the CTAs up to `last` (-1: none).
 struct PagedJoin {
   int32_t q_row0;
   int32_t q_len;
   int32_t hk;
+  int32_t tile0;
   int32_t last;
 };
 
@@ -87,19 +84,17 @@ struct PagedAttnHead {
   const int32_t* kv_lens;
   void* o;                      // [Tq][H][d] bf16
   float* lse;                   // [H][lse_stride]
-  // parts of rows whose keys were split.  PAIR: rows [part0 + split * q_len +
-  // query][H]; SPLIT: [2 * CTAs slots][slot_rows], row token * group + head.
+  // parts of rows whose keys were split: 2 * CTAs slots of slot_rows rows (a
+  // chunk's two tiles: 128 * tile + row; else token * group + head)
   float* o_part;                // [rows][d]
   float* lse_part;              // [rows]
-  PagedJoin* joins;             // SPLIT: [CTAs]
+  PagedJoin* joins;             // [CTAs]
   int64_t lse_stride;           // Tq
-  int32_t tokens;               // queries of this launch
   int32_t num_heads;
   int32_t num_kv_heads;
   int32_t group;                // query heads of a key head
   int32_t tile_tokens;          // tokens of a query tile: 128 / group
-  int32_t split_blocks;         // PAIR: 128-key blocks of a split
-  int32_t slot_rows;            // SPLIT: most rows of a unit
+  int32_t slot_rows;            // rows of a slot
   int32_t table_cols;
   int32_t num_pages;
   int32_t page_shift;
@@ -107,7 +102,6 @@ struct PagedAttnHead {
   int32_t causal;
   int32_t window;
   float scale_log2;             // softmax scale * log2(e)
-  int32_t n_items;              // CTAs to launch: PAIR's work items, SPLIT's kSplitCtas
   int32_t n_segs;
 };
 
@@ -162,7 +156,7 @@ cudaError_t launch_rope(const RopeArgs<kMaxSegs>& args, int num_sms, cudaStream_
 cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, const PagedAttnArgs<kMaxSegs>& args,
                               cudaStream_t stream);
 // Joins the split rows of a launch_paged_attn with the same arguments.
-cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnArgs<kMaxSegs>& args, cudaStream_t stream);
+cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnHead& args, cudaStream_t stream);
 cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const int32_t* dst, int32_t n, int num_sms,
                               cudaStream_t stream);
 cudaError_t launch_pages_extend(const PageTable& t, const int32_t* counts, int32_t* status, cudaStream_t stream);

@@ -30,8 +30,8 @@
 //               take P in V's type), O is rescaled when m grows by more than
 //               2^8
 //   warp 8      producer: all lanes fetch page numbers, each lane issues the
-//               TMA box of its page.  PAIR takes items by cluster launch
-//               control; SPLIT's are the CTA's equal share of all key blocks
+//               TMA box of its page.  The items are the CTA's equal share of
+//               all key blocks of the call
 //   warps 9,10  MMA issuers (S = Q K^T, O += P V) of group t
 //   warp 11     brings the queries, and clears what a sequence's last V block
 //               holds past its length (unwritten rows may be NaN, and 0 * NaN
@@ -56,7 +56,7 @@ constexpr int kAuxWarp = 11;
 constexpr int kReaders = 11;                   // 2 issuer threads, 8 softmax warps, the aux warp
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;
-constexpr int kMinBlocks = 2;                  // SPLIT: key blocks of a CTA at least, one for each group
+constexpr int kMinBlocks = 2;                  // key blocks of a CTA at least (SPLIT: one for each group)
 constexpr float kLn2 = 0.6931471805599453f;
 
 // K/V blocks of 128 keys in shared memory.  PAIR holds two query tiles and
@@ -71,10 +71,12 @@ __host__ __device__ constexpr int stages() { return HD == 128 ? (PAIR ? 4 : 6) :
 
 // A work item as the producer hands it out.
 struct Item {
-  int id;             // PAIR: the item's number, SPLIT: its segment; -1: no item left
-  int len;            // keys of the sequence
-  int hk, s0, s1;     // SPLIT: key head and key blocks
-  int slot;           // SPLIT: partial slot, or -1: the rows are final
+  int seg;            // segment; -1: no item left
+  int len;            // keys of its sequence
+  int hk;             // key head
+  int tile0;          // first query tile
+  int s0, s1;         // key blocks
+  int slot;           // slot of partial rows, or -1: the rows are final
 };
 
 template <int HD, bool PAIR>
@@ -98,10 +100,9 @@ struct PagedSmem {
   Item item[2];                                // what the ring's slots hold
   uint32_t tmem_base;
   int abort_flag;
-  union {
-    float2 ml[2 * kBlockM];                    // SPLIT: m and l of every group's rows
-    int64_t chunk_blocks[kMaxSegs / 32];       // SPLIT, at the start: weights of 32 segments each
-  };
+  // At the start the blocks of every segment (PAIR) or of every 32 (SPLIT);
+  // then SPLIT's m and l of every group's rows.
+  int64_t scratch[PAIR ? kMaxSegs : 2 * kBlockM];
 };
 
 // Block ranges [b0, b1) of 128 keys.
@@ -124,40 +125,18 @@ __device__ __forceinline__ Range blocks_of(const PagedAttnHead& a, int len, int 
   return {lo / kBlockN, (hi + kBlockN - 1) / kBlockN};
 }
 
-// One work item, as every role sees it.
-struct Work {
-  int seq, q_row0, q_len, len;
-  int hk;
-  int tile0;        // first query tile
-  int s0, s1;       // the item's key blocks
-  bool final;       // its rows are final: they go to o and lse
-  int64_t part;     // else: PAIR: the first partial row of the split, SPLIT: of the slot
-  Range tile[2];    // each tile's blocks within [s0, s1)
-  bool has[2];      // the tile exists
-  bool idle;        // PAIR: a split without keys that is not the first
-};
-
-template <int N>
-__device__ __forceinline__ int find_seg(const PagedAttnArgs<N>& a, int it) {
-  int lo = 0, hi = a.n_segs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.segs[mid].item0 <= it) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
 __device__ __forceinline__ Range cut(Range r, int s0, int s1) {
   const int b0 = max(r.b0, s0), b1 = min(r.b1, s1);
   return b1 > b0 ? Range{b0, b1} : Range{s0, s0};
 }
 
-// The blocks that the splits of a PAIR unit (first tile `tile0`) divide: the
-// union of its tiles'.
-__device__ __forceinline__ Range pair_blocks(const PagedAttnHead& a, int len, int q_len, int tile0) {
+// The blocks that a unit (PAIR: two tiles from `tile0` on, SPLIT: the one
+// tile) sees: the union of its tiles'.
+template <bool PAIR>
+__device__ __forceinline__ Range unit_blocks(const PagedAttnHead& a, int len, int q_len, int tile0) {
   const int t0 = tile0 * a.tile_tokens;
   Range r = blocks_of(a, len, q_len, t0, min(q_len, t0 + a.tile_tokens));
-  if (t0 + a.tile_tokens < q_len) {
+  if (PAIR && t0 + a.tile_tokens < q_len) {
     const Range s = blocks_of(a, len, q_len, t0 + a.tile_tokens, min(q_len, t0 + 2 * a.tile_tokens));
     if (r.b1 <= r.b0) return s;
     if (s.b1 > s.b0) r = {min(r.b0, s.b0), max(r.b1, s.b1)};
@@ -165,65 +144,47 @@ __device__ __forceinline__ Range pair_blocks(const PagedAttnHead& a, int len, in
   return r;
 }
 
-// Items of a segment: key head outermost, then the unit, last tokens first
-// (under a causal mask they see the most), then the split.
-template <int N>
-__device__ __forceinline__ Work decode_pair(const PagedAttnArgs<N>& a, const Item& item) {
-  const PagedSeg& s = a.segs[find_seg(a, item.id)];
-  Work w;
-  w.seq = s.seq;
-  w.q_row0 = s.q_row0;
-  w.q_len = s.q_len;
-  w.len = item.len;
-  const int tiles = (s.q_len + a.tile_tokens - 1) / a.tile_tokens;
-  const int units = (tiles + 1) / 2;
-  int x = item.id - s.item0;
-  const int split = x % s.splits;
-  x /= s.splits;
-  const int u = units - 1 - x % units;
-  w.hk = x / units;
-  w.tile0 = 2 * u;
-  const Range r = pair_blocks(a, item.len, s.q_len, w.tile0);
-  w.s0 = min(r.b1, r.b0 + split * a.split_blocks);
-  w.s1 = min(r.b1, w.s0 + a.split_blocks);
-  w.final = r.b1 - r.b0 <= a.split_blocks;
-  w.part = s.part0 + static_cast<int64_t>(split) * s.q_len;
-  w.idle = w.s1 <= w.s0 && split > 0;
-  w.has[0] = true;
-  w.has[1] = w.tile0 + 1 < tiles;
-  const int t0 = w.tile0 * a.tile_tokens;
-  w.tile[0] = cut(blocks_of(a, w.len, s.q_len, t0, min(s.q_len, t0 + a.tile_tokens)), w.s0, w.s1);
-  w.tile[1] = w.tile[0];
-  if (w.has[1])
-    w.tile[1] = cut(blocks_of(a, w.len, s.q_len, t0 + a.tile_tokens, min(s.q_len, t0 + 2 * a.tile_tokens)), w.s0, w.s1);
-  return w;
-}
+// One work item, as every role sees it.
+struct Work {
+  int seq, q_row0, q_len, len;
+  int hk;
+  int tile0;        // first query tile
+  int s0, s1;       // the item's key blocks
+  bool final;       // its rows are final: they go to o and lse
+  int64_t part;     // else: their first row in o_part and lse_part
+  bool has1;        // PAIR: the second tile exists
+  Range r0, r1;     // each tile's blocks within [s0, s1)
 
-template <int N>
-__device__ __forceinline__ Work decode_split(const PagedAttnArgs<N>& a, const Item& item) {
-  const PagedSeg& s = a.segs[item.id];
+  // by selection: an array indexed by the group would live in local memory
+  __device__ __forceinline__ bool has(int t) const { return t == 0 || has1; }
+  __device__ __forceinline__ int b0(int t) const { return t == 0 ? r0.b0 : r1.b0; }
+  __device__ __forceinline__ int b1(int t) const { return t == 0 ? r0.b1 : r1.b1; }
+};
+
+template <bool PAIR, int N>
+__device__ __forceinline__ Work decode(const PagedAttnArgs<N>& a, const Item& item) {
+  const PagedSeg& s = a.segs[item.seg];
   Work w;
   w.seq = s.seq;
   w.q_row0 = s.q_row0;
   w.q_len = s.q_len;
   w.len = item.len;
   w.hk = item.hk;
-  w.tile0 = 0;
+  w.tile0 = item.tile0;
   w.s0 = item.s0;
   w.s1 = item.s1;
   w.final = item.slot < 0;
   w.part = static_cast<int64_t>(item.slot) * a.slot_rows;
-  w.idle = false;
-  w.has[0] = true;
-  w.has[1] = false;
-  w.tile[0] = w.tile[1] = {item.s0, item.s1};
+  w.has1 = false;
+  w.r0 = w.r1 = {item.s0, item.s1};
+  if constexpr (PAIR) {
+    const int t0 = w.tile0 * a.tile_tokens, t1 = t0 + a.tile_tokens;
+    w.has1 = t1 < s.q_len;
+    w.r0 = cut(blocks_of(a, w.len, s.q_len, t0, min(s.q_len, t1)), w.s0, w.s1);
+    if (w.has1)
+      w.r1 = cut(blocks_of(a, w.len, s.q_len, t1, min(s.q_len, t1 + a.tile_tokens)), w.s0, w.s1);
+  }
   return w;
-}
-
-template <bool PAIR, int N>
-__device__ __forceinline__ Work decode(const PagedAttnArgs<N>& a, const Item& item) {
-  if constexpr (PAIR) return decode_pair(a, item);
-  else return decode_split(a, item);
 }
 
 // Copies of a SPLIT tile's rows: 4, 2 or 1, 128 / copies rows apart.
@@ -260,15 +221,16 @@ __device__ __forceinline__ bool take(SM* sm, uint32_t n, uint32_t code, bool war
   if (warp_wide) ok = __all_sync(0xffffffffu, ok);
   if (!ok) return false;
   const volatile Item* i = &sm->item[s];
-  item->id = i->id;
+  item->seg = i->seg;
   item->len = i->len;
   item->hk = i->hk;
+  item->tile0 = i->tile0;
   item->s0 = i->s0;
   item->s1 = i->s1;
   item->slot = i->slot;
   if (warp_wide) __syncwarp();
   if (!warp_wide || (threadIdx.x & 31) == 0) mbar_arrive(&sm->ring.empty[s]);
-  return item->id >= 0;
+  return item->seg >= 0;
 }
 
 // ------------------------------------------------------------------ producer
@@ -296,11 +258,10 @@ __device__ __forceinline__ int length_of(const PagedAttnArgs<N>& a, int seg) {
   return len < 0 ? 0 : a.max_kv_len;
 }
 
-// Brings an item's K/V blocks into the rings; `ask` requests the next PAIR
-// item when the last block is next.  uses0 / uses1: the rings' counts.
+// Brings an item's K/V blocks into the rings.  uses0 / uses1: the rings' counts.
 template <int HD, bool PAIR, int N>
 __device__ __forceinline__ bool load_blocks(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps,
-                                            const Work& w, uint32_t& uses0, uint32_t& uses1, bool ask) {
+                                            const Work& w, uint32_t& uses0, uint32_t& uses1) {
   using Ring = Stages<HD, PAIR>;
   const int lane = threadIdx.x & 31;
   const int page = 1 << a.page_shift;
@@ -313,7 +274,6 @@ __device__ __forceinline__ bool load_blocks(PagedSmem<HD, PAIR>* sm, const Paged
   int cur = e0 + lane < e1 ? __ldg(row + e0 + lane) : 0;
   int nxt = e0 + 32 + lane < e1 ? __ldg(row + e0 + 32 + lane) : 0;
   for (int j = w.s0; j < w.s1; ++j) {
-    if (ask && j == w.s1 - 1 && lane == 0) ring_ask(&sm->ring);
     const int rel = ((j * kBlockN) >> a.page_shift) - e0;
     if ((rel >> 5) != chunk) {
       ++chunk;
@@ -352,122 +312,152 @@ __device__ __forceinline__ bool load_blocks(PagedSmem<HD, PAIR>* sm, const Paged
   return true;
 }
 
-// PAIR: the CTA's own item first, then stolen ones, in launch order.
-template <int HD, int N>
-__device__ void produce_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps) {
-  const int lane = threadIdx.x & 31;
-  uint32_t uses0 = 0, uses1 = 0, steal_ph = 0;
-  Item item = {static_cast<int>(blockIdx.x), 0, 0, 0, 0, 0};
-  for (uint32_t n = 0;; ++n) {
-    if (item.id >= 0) item.len = length_of(a, find_seg(a, item.id));
-    if (!publish(sm, n, item) || item.id < 0) return;
-    const Work w = decode_pair(a, item);
-    if (!load_blocks<HD, true, N>(sm, a, maps, w, uses0, uses1, true)) return;
-    int next = -2;
-    if (lane == 0) {
-      if (w.s1 <= w.s0) ring_ask(&sm->ring);
-      next = ring_answer(&sm->ring, steal_ph, a.n_items, &sm->abort_flag, &g_paged_err, ERR_TIMEOUT_PRODUCER);
-    }
-    next = __shfl_sync(0xffffffffu, next, 0);
-    if (next == -2) return;
-    item.id = next;
-  }
+// Key blocks that a unit counts for (one without keys still has rows to write).
+__device__ __forceinline__ int weight_of(Range r) { return max(1, r.b1 - r.b0); }
+
+template <bool PAIR>
+__device__ __forceinline__ int units_of(const PagedAttnHead& a, int q_len) {
+  return PAIR ? (q_len + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens) : 1;
 }
 
-// Key blocks that one key head of a SPLIT segment counts for (a sequence
-// without keys still has rows to write).
-template <int N>
-__device__ __forceinline__ int weight_of(const PagedAttnArgs<N>& a, int seg, int len, int* b0) {
-  const Range r = blocks_of(a, len, a.segs[seg].q_len, 0, a.segs[seg].q_len);
-  *b0 = r.b0;
-  return max(1, r.b1 - r.b0);
-}
-
-// SPLIT, all warps: the blocks of every 32 segments.
-template <int HD, int N>
-__device__ __forceinline__ void sum_chunks(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& a) {
-  const int lane = threadIdx.x & 31;
-  for (int chunk = threadIdx.x & ~31; chunk < a.n_segs; chunk += kThreads) {
-    int b0, w = 0;
-    if (chunk + lane < a.n_segs) w = weight_of(a, chunk + lane, length_of(a, chunk + lane), &b0);
-    int64_t sum = static_cast<int64_t>(w) * a.num_kv_heads;
+// All warps, at the start: the blocks of one key head of every segment (PAIR),
+// or the sum of 32 segments' (SPLIT, which has no room for more).
+template <int HD, bool PAIR, int N>
+__device__ __forceinline__ void sum_blocks(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if constexpr (PAIR) {
+    for (int s = warp; s < a.n_segs; s += kThreads / 32) {
+      const int len = length_of(a, s), q_len = a.segs[s].q_len;
+      int64_t sum = 0;
+      for (int u = lane; u < units_of<true>(a, q_len); u += 32)
+        sum += weight_of(unit_blocks<true>(a, len, q_len, 2 * u));
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) sm->chunk_blocks[chunk / 32] = sum;
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == 0) sm->scratch[s] = sum;
+    }
+  } else {
+    for (int chunk = warp * 32; chunk < a.n_segs; chunk += kThreads) {
+      int64_t sum = 0;
+      if (chunk + lane < a.n_segs)
+        sum = weight_of(unit_blocks<false>(a, length_of(a, chunk + lane), a.segs[chunk + lane].q_len, 0));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == 0) sm->scratch[chunk / 32] = sum;
+    }
   }
 }
 
-// SPLIT: the blocks of all (sequence, key head) units stand in one line, which
-// is cut into equal pieces, one per CTA: every SM has the same number of
+// Inclusive prefix sum over the warp.
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if (static_cast<int>(threadIdx.x & 31) >= d) x += y;
+  }
+  return x;
+}
+
+// The blocks of all units (sequence, key head, query tiles) stand in one line,
+// which is cut into equal pieces, one per CTA: every SM has the same number of
 // blocks whatever the lengths, and only units that a cut goes through are
 // joined afterwards.  A CTA's piece of the unit that its range starts inside
 // goes to slot 2c, of the unit that goes on behind its range to 2c + 1, and
 // joins[c] tells the join what begins in slot 2c + 1.
-template <int HD, int N>
-__device__ void produce_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps) {
+template <int HD, bool PAIR, int N>
+__device__ void produce(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps) {
   const int lane = threadIdx.x & 31;
   const int c = blockIdx.x;
+  const int nk = a.num_kv_heads;
   uint32_t uses0 = 0, uses1 = 0, n = 0;
   int64_t total = 0;
-  for (int s = 0; s < a.n_segs; s += 32) total += sm->chunk_blocks[s / 32];
+  for (int i = lane; i < (PAIR ? a.n_segs : (a.n_segs + 31) / 32); i += 32) total += sm->scratch[i];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+  total *= nk;
   const int64_t per = max(static_cast<int64_t>(kMinBlocks), (total + gridDim.x - 1) / gridDim.x);
   int64_t g = c * per;
   const int64_t end = min(total, g + per);
-  PagedJoin join = {0, 0, 0, -1};
-  // the segments that hold block g: 32 at a time
-  int64_t base = 0;            // blocks before the chunk of segments
-  int chunk = 0;
-  while (g < end && base + sm->chunk_blocks[chunk / 32] <= g) {
-    base += sm->chunk_blocks[chunk / 32];
-    chunk += 32;
-  }
-  int len = 0, w_seg = 0, b0 = 0;
-  int64_t incl = 0;
-  for (; g < end; chunk += 32) {
-    const int s = chunk + lane;
-    len = 0;
-    w_seg = 0;
-    b0 = 0;
-    if (s < a.n_segs) {
-      len = length_of(a, s);
-      w_seg = weight_of(a, s, len, &b0);
+  PagedJoin join = {0, 0, 0, 0, -1};
+  if (g < end) {
+    // where block g lies: its segment, 32 at a time ...
+    int64_t base = 0;          // blocks before the chunk of segments
+    int chunk = 0, seg = 0;
+    int64_t seg_blocks = 0, off = 0;
+    for (;; chunk += 32) {
+      if constexpr (!PAIR) {
+        if (base + sm->scratch[chunk / 32] * nk <= g) {
+          base += sm->scratch[chunk / 32] * nk;
+          continue;
+        }
+      }
+      int64_t w = 0;
+      if (chunk + lane < a.n_segs) {
+        if constexpr (PAIR) w = sm->scratch[chunk + lane];
+        else w = weight_of(unit_blocks<false>(a, length_of(a, chunk + lane), a.segs[chunk + lane].q_len, 0));
+      }
+      const int64_t incl = base + warp_scan(w * nk);
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > g);
+      if (past != 0) {
+        const int k = __ffs(past) - 1;
+        seg = chunk + k;
+        seg_blocks = __shfl_sync(0xffffffffu, w, k);
+        off = g - (__shfl_sync(0xffffffffu, incl, k) - seg_blocks * nk);
+        break;
+      }
+      base = __shfl_sync(0xffffffffu, incl, 31);
     }
-    incl = static_cast<int64_t>(w_seg) * a.num_kv_heads;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += y;
+    // ... the key head in it, and the unit, 32 at a time
+    int len = length_of(a, seg), q_len = a.segs[seg].q_len;
+    int hk = static_cast<int>(off / seg_blocks), unit = 0;
+    off -= hk * seg_blocks;
+    if constexpr (PAIR) {
+      int64_t before = 0;
+      for (int u0 = 0;; u0 += 32) {
+        const int u = u0 + lane;
+        const int64_t w = u < units_of<true>(a, q_len) ? weight_of(unit_blocks<true>(a, len, q_len, 2 * u)) : 0;
+        const int64_t incl = before + warp_scan(w);
+        const uint32_t past = __ballot_sync(0xffffffffu, incl > off);
+        if (past != 0) {
+          const int k = __ffs(past) - 1;
+          unit = u0 + k;
+          off -= __shfl_sync(0xffffffffu, incl, k) - __shfl_sync(0xffffffffu, w, k);
+          break;
+        }
+        before = __shfl_sync(0xffffffffu, incl, 31);
+      }
     }
-    incl += base;
-    base = __shfl_sync(0xffffffffu, incl, 31);
-    // all units of this chunk that the range meets
-    while (g < end && g < base) {
-      const int k = __ffs(__ballot_sync(0xffffffffu, incl > g)) - 1;      // g's segment in the chunk
-      const int weight = __shfl_sync(0xffffffffu, w_seg, k);
-      const int64_t seg_end = __shfl_sync(0xffffffffu, incl, k);
-      const int64_t off = g - (seg_end - static_cast<int64_t>(weight) * a.num_kv_heads);
-      const int hk = static_cast<int>(off / weight);
-      const int blk = static_cast<int>(off - static_cast<int64_t>(hk) * weight);
+    int blk = static_cast<int>(off);
+    while (true) {
+      const int tile0 = PAIR ? 2 * unit : 0;
+      const Range r = unit_blocks<PAIR>(a, len, q_len, tile0);
+      const int weight = weight_of(r);
       const int cnt = static_cast<int>(min(static_cast<int64_t>(weight - blk), end - g));
-      const int first = __shfl_sync(0xffffffffu, b0, k);
-      Item item;
-      item.id = chunk + k;
-      item.len = __shfl_sync(0xffffffffu, len, k);
-      item.hk = hk;
-      const Range r = blocks_of(a, item.len, a.segs[item.id].q_len, 0, a.segs[item.id].q_len);
-      item.s0 = r.b1 > r.b0 ? first + blk : 0;
-      item.s1 = r.b1 > r.b0 ? first + blk + cnt : 0;
-      item.slot = blk > 0 ? 2 * c : blk + cnt < weight ? 2 * c + 1 : -1;
-      if (blk == 0 && cnt < weight)
-        join = {a.segs[item.id].q_row0, a.segs[item.id].q_len, hk, static_cast<int>((g + weight - 1) / per)};
+      Item item = {seg, len, hk, tile0, 0, 0, -1};
+      if (r.b1 > r.b0) {
+        item.s0 = r.b0 + blk;
+        item.s1 = item.s0 + cnt;
+      }
+      if (cnt < weight) {
+        item.slot = blk > 0 ? 2 * c : 2 * c + 1;
+        if (blk == 0) join = {a.segs[seg].q_row0, q_len, hk, tile0, static_cast<int>((g + weight - 1) / per)};
+      }
       if (!publish(sm, n++, item)) return;
-      const Work w = decode_split(a, item);
-      if (!load_blocks<HD, false, N>(sm, a, maps, w, uses0, uses1, false)) return;
+      const Work w = decode<PAIR>(a, item);
+      if (!load_blocks<HD, PAIR, N>(sm, a, maps, w, uses0, uses1)) return;
       g += cnt;
+      if (g >= end) break;
+      blk = 0;
+      if (++unit < units_of<PAIR>(a, q_len)) continue;
+      unit = 0;
+      if (++hk < nk) continue;
+      hk = 0;
+      ++seg;
+      len = length_of(a, seg);
+      q_len = a.segs[seg].q_len;
     }
   }
   if (lane == 0) a.joins[c] = join;
-  publish(sm, n, Item{-1, 0, 0, 0, 0, 0});
+  publish(sm, n, Item{-1, 0, 0, 0, 0, 0, -1});
 }
 
 // ------------------------------------------------------------------ MMA issuer t
@@ -488,15 +478,16 @@ __device__ void issue(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, uint32
     if (!take(sm, n, code, false, &item)) return;
     const Work w = decode<PAIR>(a, item);
     if (w.s1 <= w.s0) continue;
-    const bool has = PAIR ? w.has[t] : true;
+    const bool has = PAIR ? w.has(t) : true;
     if (has && !mbar_wait(&sm->q_full[qt], q_it & 1u, abort_flag, &g_paged_err, code)) return;
     bool first = true;
     // PAIR: both issuers pass every stage, and each uses the blocks that its
     // tile sees; SPLIT: issuer t's blocks alternate with the other's, in its
     // own ring
-    const int last_mine = PAIR ? w.tile[t].b1 - 1 : w.s1 - 1 - ((w.s1 - 1 - w.s0 - t) & 1);
+    const int mine0 = w.b0(t), mine1 = has ? w.b1(t) : 0;
+    const int last_mine = PAIR ? mine1 - 1 : w.s1 - 1 - ((w.s1 - 1 - w.s0 - t) & 1);
     for (int j = PAIR ? w.s0 : w.s0 + t; j < w.s1; j += PAIR ? 1 : 2) {
-      const bool mine = has && (!PAIR || (j >= w.tile[t].b0 && j < w.tile[t].b1));
+      const bool mine = !PAIR || (j >= mine0 && j < mine1);
       uint32_t st = Ring::stage(t, kv_it);
       if (!mbar_wait(&sm->kv_full[st], Ring::parity(kv_it), abort_flag, &g_paged_err, code)) return;
       if (mine) {
@@ -563,7 +554,7 @@ __device__ void assist(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const
     if (lane == 0) {
 #pragma unroll
       for (int t = 0; t < (PAIR ? 2 : 1); ++t) {
-        if (!w.has[t]) continue;
+        if (!w.has(t)) continue;
         uint32_t& q_it = t ? q_it1 : q_it0;
         if (!mbar_wait(&sm->q_empty[t], (q_it & 1u) ^ 1u, &sm->abort_flag, &g_paged_err, code)) {
           ok = false;
@@ -640,11 +631,14 @@ __device__ __forceinline__ void exp_pack(const uint32_t (&s)[32], float sl2, flo
   }
 }
 
-// Scores of columns [col0, col0 + 32) outside [lo, hi) become -inf.
+// Scores of columns [col0, col0 + 32) outside [lo, hi) become -inf: one bit a
+// column, so that an element costs a test and a select.
 __device__ __forceinline__ void mask32(uint32_t (&s)[32], int col0, int lo, int hi) {
+  const int first = min(max(lo - col0, 0), 32), last = min(max(hi - col0, 0), 32);
+  const uint32_t below = first >= 32 ? 0xffffffffu : (1u << first) - 1u;
+  const uint32_t seen = (last >= 32 ? 0xffffffffu : (1u << last) - 1u) & ~below;
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (col0 + i < lo || col0 + i >= hi) s[i] = __float_as_uint(-INFINITY);
+  for (int i = 0; i < 32; ++i) s[i] = (seen >> i) & 1u ? s[i] : __float_as_uint(-INFINITY);
 }
 
 __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
@@ -695,18 +689,18 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
   const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const uint32_t tS = tmem + 256u * t + lane_off;
   const uint32_t tO = tS + 128u;
-  const float sl2 = a.scale_log2;
   volatile int* abort_flag = &sm->abort_flag;
   const uint32_t code = ERR_TIMEOUT_SOFTMAX;
   const int row_tok = row / a.group, row_head = row - row_tok * a.group;
-  uint32_t blk_it = 0, q_it = 0, turn_it = 0, sync_uses = 0;
+  uint32_t q_it = 0, sync_uses = 0;
+  const float sl2 = a.scale_log2;
+  uint32_t blk_it = 0, turn_it = 0;
   if (t == 1) mbar_arrive(&sm->turn[0]);         // the first turn is group 0's
   for (uint32_t n = 0;; ++n) {
     Item item;
     if (!take(sm, n, code, true, &item)) break;
-    const Work w = decode_pair(a, item);
-    if (w.idle) continue;
-    const bool has = w.has[t];
+    const Work w = decode<true>(a, item);
+    const bool has = w.has(t);
     const int tok0 = (w.tile0 + t) * a.tile_tokens;
     const int tokens = min(a.tile_tokens, w.q_len - tok0);
     const int tok = tok0 + row_tok;
@@ -720,9 +714,10 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
       keys_of(a, w.len, p0 + tok, &lo, &hi);
       keys_of(a, w.len, p0 + tok0, &x, &hi_all);
       keys_of(a, w.len, p0 + tok0 + max(0, tokens - 1), &lo_all, &x);
+      const int mine0 = w.b0(t), mine1 = has ? w.b1(t) : 0;
       bool ok = true;
       for (int j = w.s0; j < w.s1; ++j, ++turn_it) {
-        const bool mine = has && j >= w.tile[t].b0 && j < w.tile[t].b1;
+        const bool mine = j >= mine0 && j < mine1;
         if (!__all_sync(0xffffffffu,
                         (!mine || mbar_wait(&sm->s_full[t], blk_it & 1u, abort_flag, &g_paged_err, code)) &&
                             mbar_wait(&sm->turn[t], turn_it & 1u, abort_flag, &g_paged_err, code))) {
@@ -735,34 +730,26 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
         }
         tc_fence_after();
         uint32_t s[4][32];
-        float m_raw;
+        float r[4];
         const int k0 = j * kBlockN;
-        if (k0 >= lo_all && k0 + kBlockN <= hi_all) {
-          float r[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) r[c] = tmem_ld32_max(tS + c * 32, s[c]);
-          tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) r[c] = tmem_ld32_max(tS + c * 32, s[c]);
+        tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            reg_fence(s[c]);
-            reg_fence_f(r[c]);
-          }
-          m_raw = fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3]));
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
-          tmem_wait_ld();
-          m_raw = -INFINITY;
+        for (int c = 0; c < 4; ++c) {
+          reg_fence(s[c]);
+          reg_fence_f(r[c]);
+        }
+        if (k0 < lo_all || k0 + kBlockN > hi_all) {
+          // the mask goes through this block
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            reg_fence(s[c]);
             mask32(s[c], k0 + c * 32, lo, hi);
-            m_raw = fmaxf(m_raw, max32(s[c]));
+            r[c] = max32(s[c]);
           }
         }
         float alpha;
-        const bool need = raise_max(m_raw * sl2, &m_run, &alpha);
-        l_run *= alpha;
+        const bool need = raise_max(fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3])) * sl2, &m_run, &alpha);
         const float neg_m = neg_or_zero(m_run);
         uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
@@ -780,7 +767,7 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
         ++blk_it;
         float ls0, ls1;
         f2_unpack(f2_add(acc[0], acc[1]), ls0, ls1);
-        l_run += ls0 + ls1;
+        l_run = l_run * alpha + (ls0 + ls1);
       }
       if (!ok) break;
       if (!first) {
@@ -840,7 +827,7 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
     } else {
       const int64_t out = final_rows
           ? (static_cast<int64_t>(w.q_row0 + tok) * a.num_heads + h)
-          : ((w.part + tok) * a.num_heads + h);
+          : w.part + t * kBlockM + row;
 #pragma unroll 1
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t o[32];
@@ -888,6 +875,7 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
 template <int HD, int N>
 __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& a, uint32_t tmem) {
   using Ring = Stages<HD, false>;
+  float2* ml = reinterpret_cast<float2*>(sm->scratch);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = warp >> 2, quad = warp & 3;
   const int row = quad * 32 + lane;
@@ -901,7 +889,7 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
   for (uint32_t n = 0;; ++n) {
     Item item;
     if (!take(sm, n, code, true, &item)) return;
-    const Work w = decode_split(a, item);
+    const Work w = decode<false>(a, item);
     const int rows = w.q_len * a.group;
     const int copies = row_copies(rows);
     const int span = kBlockM / copies;           // rows of a copy
@@ -985,14 +973,14 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
     }
     // ---------------------------------------------------------- join the parts of each row
     // part i: group i / copies, copy i % copies
-    sm->ml[t * kBlockM + row] = make_float2(m_run, l_run);
+    ml[t * kBlockM + row] = make_float2(m_run, l_run);
     if (!warps_sync(&sm->all_sync, sync_uses, abort_flag, code)) return;
     const int parts = 2 * copies;
     float m_all = -INFINITY;
-    for (int i = 0; i < parts; ++i) m_all = fmaxf(m_all, sm->ml[i * span + r].x);
+    for (int i = 0; i < parts; ++i) m_all = fmaxf(m_all, ml[i * span + r].x);
     float l_all = 0.f;
     for (int i = 0; i < parts; ++i) {
-      const float2 v = sm->ml[i * span + r];
+      const float2 v = ml[i * span + r];
       if (v.x != -INFINITY) l_all += v.y * fast_exp2(v.x - m_all);
     }
     const float scale = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_all) / l_all;
@@ -1072,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttnArgs<N> args) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   auto* sm = reinterpret_cast<PagedSmem<HD, PAIR>*>(smem_raw);
-  if (!PAIR && threadIdx.x == 0) args.joins[blockIdx.x].last = -1;   // also when this CTA gives up a wait
+  if (threadIdx.x == 0) args.joins[blockIdx.x].last = -1;   // also when this CTA gives up a wait
   if ((smem_u32(smem_raw) & 1023u) != 0) {       // the declared alignment; the swizzle needs it
     if (threadIdx.x == 0) atomicOr(&g_paged_err, ERR_BAD_WORK);
     return;
@@ -1104,7 +1092,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
     tmem_alloc(&sm->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if constexpr (!PAIR) sum_chunks<HD, N>(sm, args);
+  sum_blocks<HD, PAIR, N>(sm, args);
   // the join may be set up from here on; it waits for this grid's end itself
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
@@ -1112,17 +1100,22 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
 
-  if (warp == kProducerWarp) {
-    if constexpr (PAIR) produce_pair<HD, N>(sm, args, maps);
-    else produce_split<HD, N>(sm, args, maps);
-  } else if (warp == kMmaWarp0 || warp == kMmaWarp0 + 1) {
-    if (lane == 0) issue<HD, PAIR, N>(sm, args, tmem, warp - kMmaWarp0);
-  } else if (warp == kAuxWarp) {
-    assist<HD, PAIR, N>(sm, args, maps);
+  if (warp >= kProducerWarp) {
+    // 384 threads are launched with 168 registers each, 64,512 in all: PAIR's
+    // softmax groups take 200 and leave these warps 104.
+    if constexpr (PAIR) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == kProducerWarp) {
+      produce<HD, PAIR, N>(sm, args, maps);
+    } else if (warp == kAuxWarp) {
+      assist<HD, PAIR, N>(sm, args, maps);
+    } else {
+      if (lane == 0) issue<HD, PAIR, N>(sm, args, tmem, warp - kMmaWarp0);
+    }
   } else if constexpr (PAIR) {
-    softmax_pair<HD, N>(sm, args, maps, tmem);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    softmax_pair<HD>(sm, args, maps, tmem);
   } else {
-    softmax_split<HD, N>(sm, args, tmem);
+    softmax_split<HD>(sm, args, tmem);
   }
 
   __syncwarp();
@@ -1139,7 +1132,8 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
 // The warps of the block take the parts in turn, so that few rows with many
 // parts still have their loads in flight together.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 16;                  // SPLIT: blocks that share a unit's rows
+constexpr int kJoinRows = 16;                  // blocks that share a unit's rows
+constexpr int kFewParts = 4;                   // parts of a row that one warp joins
 
 template <int HD, typename F>
 __device__ __forceinline__ void join_row(const PagedAttnHead& a, int n, F part, int64_t o_row, float* lse_out) {
@@ -1189,45 +1183,67 @@ __device__ __forceinline__ void join_row(const PagedAttnHead& a, int n, F part, 
   if (threadIdx.x == 0) *lse_out = seen ? m + logf(sum) : -INFINITY;
 }
 
-// PAIR: one block per (query, head) row; rows of one split were written in place.
-template <int HD, int N>
-__global__ void __launch_bounds__(kJoinThreads) join_pair_kernel(const __grid_constant__ PagedAttnArgs<N> a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t tok_all = blockIdx.x / a.num_heads;
-  const int h = static_cast<int>(blockIdx.x - tok_all * a.num_heads);
-  int lo = 0, hi = a.n_segs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.segs[mid].tok0 <= tok_all) lo = mid; else hi = mid - 1;
+// The same by one warp, for few parts.
+template <int HD, typename F>
+__device__ __forceinline__ void join_row_warp(const PagedAttnHead& a, int n, F part, int64_t o_row, float* lse_out) {
+  constexpr int C = HD / 32;
+  const int lane = threadIdx.x & 31;
+  float l[kFewParts], x[kFewParts][C];
+#pragma unroll
+  for (int i = 0; i < kFewParts; ++i) {
+    l[i] = -INFINITY;
+    if (i < n) {
+      l[i] = a.lse_part[part(i)];
+      const float* src = a.o_part + part(i) * HD + lane * C;
+      if constexpr (C == 4) *reinterpret_cast<float4*>(x[i]) = *reinterpret_cast<const float4*>(src);
+      else *reinterpret_cast<float2*>(x[i]) = *reinterpret_cast<const float2*>(src);
+    }
   }
-  const PagedSeg& s = a.segs[lo];
-  if (s.splits <= 1) return;
-  const int tok = static_cast<int>(tok_all) - s.tok0;
-  const int len = max(0, min(__ldg(a.kv_lens + s.seq), a.max_kv_len));
-  const Range r = pair_blocks(a, len, s.q_len, tok / a.tile_tokens & ~1);
-  const int n = (r.b1 - r.b0 + a.split_blocks - 1) / a.split_blocks;
-  if (n <= 1) return;
-  const int64_t row0 = (s.part0 + tok) * a.num_heads + h;
-  const int64_t step = static_cast<int64_t>(s.q_len) * a.num_heads;
-  join_row<HD>(a, n, [&](int i) { return row0 + i * step; },
-               static_cast<int64_t>(s.q_row0 + tok) * a.num_heads + h,
-               a.lse + static_cast<int64_t>(h) * a.lse_stride + s.q_row0 + tok);
+  float m = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kFewParts; ++i) m = fmaxf(m, l[i]);
+  float acc[C] = {};
+#pragma unroll
+  for (int i = 0; i < kFewParts; ++i) {
+    if (l[i] == -INFINITY) continue;             // nothing seen in this part
+    const float wgt = expf(l[i] - m);
+    sum += wgt;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = fmaf(wgt, x[i][c], acc[c]);
+  }
+  const bool seen = m != -INFINITY;
+  const float inv = seen ? 1.f / sum : 0.f;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + o_row * HD + lane * C;
+  if constexpr (C == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (lane == 0) *lse_out = seen ? m + logf(sum) : -INFINITY;
 }
 
-// SPLIT: block x looks after the unit that begins in CTA x and goes on in the
-// CTAs behind it; kJoinRows blocks share its rows.
-template <int HD>
-__global__ void __launch_bounds__(kJoinThreads) join_split_kernel(const __grid_constant__ PagedAttnHead a) {
+// Block x looks after the unit that begins in CTA x and goes on in the CTAs
+// behind it; kJoinRows blocks share its rows, a warp or a whole block to a row.
+template <int HD, bool PAIR>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnHead a) {
   const int c = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedJoin j = a.joins[c];
   if (j.last < 0) return;
-  for (int r = blockIdx.y; r < j.q_len * a.group; r += kJoinRows) {
-    const int tok = r / a.group, h = j.hk * a.group + r - tok * a.group;
-    join_row<HD>(a, j.last - c + 1,
-                 [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.slot_rows + r; },
-                 static_cast<int64_t>(j.q_row0 + tok) * a.num_heads + h,
-                 a.lse + static_cast<int64_t>(h) * a.lse_stride + j.q_row0 + tok);
+  const int n = j.last - c + 1;
+  const bool few = n <= kFewParts;
+  constexpr int kWarps = kJoinThreads / 32;
+  for (int r = few ? blockIdx.y * kWarps + threadIdx.x / 32 : blockIdx.y; r < a.slot_rows;
+       r += few ? kJoinRows * kWarps : kJoinRows) {
+    const int row = PAIR ? r % kBlockM : r;                       // of its tile
+    const int tok_t = row / a.group, tok = (j.tile0 + (PAIR ? r / kBlockM : 0)) * a.tile_tokens + tok_t;
+    if (tok_t >= a.tile_tokens || tok >= j.q_len) continue;
+    const int h = j.hk * a.group + row - tok_t * a.group;
+    const auto part = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.slot_rows + r; };
+    const int64_t o_row = static_cast<int64_t>(j.q_row0 + tok) * a.num_heads + h;
+    float* lse = a.lse + static_cast<int64_t>(h) * a.lse_stride + j.q_row0 + tok;
+    if (few) join_row_warp<HD>(a, n, part, o_row, lse);
+    else join_row<HD>(a, n, part, o_row, lse);
   }
 }
 
@@ -1256,7 +1272,7 @@ cudaError_t launch_attn(const PagedMaps& maps, const PagedAttnArgs<N>& a, cudaSt
     if (e != cudaSuccess) return e;
     word.fetch_or(uint64_t(1) << (dev & 63));
   }
-  paged_attn_kernel<HD, PAIR, N><<<a.n_items, kThreads, smem, stream>>>(maps, a);
+  paged_attn_kernel<HD, PAIR, N><<<kPagedCtas, kThreads, smem, stream>>>(maps, a);
   return cudaGetLastError();
 }
 
@@ -1282,16 +1298,6 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, cudaStream_t stream, c
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int HD>
-cudaError_t join_kind(bool pair, const PagedAttnArgs<kMaxSegs>& a, cudaStream_t stream) {
-  const dim3 blocks(static_cast<unsigned>(static_cast<int64_t>(a.tokens) * a.num_heads));
-  if (!pair)
-    return launch_after(join_split_kernel<HD>, dim3(a.n_items, std::min(a.slot_rows, kJoinRows)), stream,
-                        static_cast<const PagedAttnHead&>(a));
-  return a.n_segs <= kFewSegs ? launch_after(join_pair_kernel<HD, kFewSegs>, blocks, stream, cut<kFewSegs>(a))
-                              : launch_after(join_pair_kernel<HD, kMaxSegs>, blocks, stream, a);
-}
-
 }  // namespace
 
 cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, const PagedAttnArgs<kMaxSegs>& a,
@@ -1300,8 +1306,13 @@ cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, co
   return pair ? attn_kind<128, true>(maps, a, stream) : attn_kind<128, false>(maps, a, stream);
 }
 
-cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnArgs<kMaxSegs>& a, cudaStream_t stream) {
-  return head_dim == 64 ? join_kind<64>(pair, a, stream) : join_kind<128>(pair, a, stream);
+cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnHead& a, cudaStream_t stream) {
+  const dim3 grid(kPagedCtas, static_cast<unsigned>(std::min(a.slot_rows, kJoinRows)));
+  if (head_dim == 64)
+    return pair ? launch_after(paged_join_kernel<64, true>, grid, stream, a)
+                : launch_after(paged_join_kernel<64, false>, grid, stream, a);
+  return pair ? launch_after(paged_join_kernel<128, true>, grid, stream, a)
+              : launch_after(paged_join_kernel<128, false>, grid, stream, a);
 }
 
 uint32_t paged_attn_take_error() {

@@ -133,74 +133,39 @@ zl_status check_attn(const int32_t* cu_q, int32_t num_seqs, int32_t max_kv_len, 
   return ZL_OK;
 }
 
-// ------------------------------------------------------------------ the attention's work split
-// What the split depends on.  It does not look at a window: a workspace serves
-// every window.
-struct Shape {
-  int32_t group;         // query heads of a key head: rows of one token in a tile
-  int32_t kv_heads;
-  int32_t max_kv_len;
-
-  int32_t tile_tokens() const { return zl::kBlockM / group; }
-  bool pair(int32_t n) const { return n > tile_tokens(); }
-  int64_t units(int32_t n) const {
-    const int64_t tiles = (n + tile_tokens() - 1) / tile_tokens();
-    return pair(n) ? (tiles + 1) / 2 : 1;
-  }
-  int32_t blocks() const { return std::max(1, max_kv_len / zl::kBlockN + (max_kv_len % zl::kBlockN != 0)); }
-};
-
-// One launch of a kind: up to kMaxSegs sequences.
+// ------------------------------------------------------------------ the attention's launches
+// A call runs its sequences of one query tile (single tokens, drafts) and its
+// longer chunks by two kernels, each as often as its sequences fill launches.
+// The kernels split the work on the device; the workspace holds what a cut
+// through a unit leaves in every CTA, whatever the lengths and the window.
 struct Launch {
   int32_t segs = 0;
-  int64_t items = 0;          // PAIR
-  int32_t split_blocks = 1;   // PAIR
-  int32_t splits = 1;         // PAIR
-  int64_t part_rows = 0;      // rows of o_part and lse_part
-  int32_t slot_rows = 0;      // SPLIT
+  int32_t slot_rows = 0;
 };
 
+int32_t tile_tokens(int32_t group) { return zl::kBlockM / group; }
+
 // The next launch of a kind: as many sequences from *i on as it holds.
-Launch plan_launch(const Shape& sh, const int32_t* cu, int32_t num_seqs, int32_t* i, bool pair) {
+Launch next_launch(const int32_t* cu, int32_t num_seqs, int32_t group, bool pair, int32_t* i) {
   Launch l;
-  int64_t units = 0, tokens = 0;
-  int32_t most = 0;
   for (; *i < num_seqs && l.segs < zl::kMaxSegs; ++*i) {
     const int32_t n = cu[*i + 1] - cu[*i];
-    if (n == 0 || sh.pair(n) != pair) continue;
+    if (n == 0 || (n > tile_tokens(group)) != pair) continue;
     ++l.segs;
-    units += sh.units(n) * sh.kv_heads;
-    tokens += n;
-    most = std::max(most, n);
+    l.slot_rows = pair ? 2 * zl::kBlockM : std::max(l.slot_rows, n * group);
   }
-  if (l.segs == 0) return l;
-  if (!pair) {
-    l.slot_rows = most * sh.group;
-    l.part_rows = int64_t(2) * zl::kSplitCtas * l.slot_rows;
-    return l;
-  }
-  // Long items are fine as long as the last wave of them is full: split only
-  // where it would leave more than 15% of the SMs' time empty.
-  while (l.splits < zl::kMaxSplits && sh.blocks() / (l.splits + 1) >= 16) {
-    const int64_t items = units * l.splits, waves = (items + zl::kSplitCtas - 1) / zl::kSplitCtas;
-    if (items * 100 >= waves * zl::kSplitCtas * 85) break;
-    ++l.splits;
-  }
-  l.split_blocks = (sh.blocks() + l.splits - 1) / l.splits;
-  l.items = units * l.splits;
-  if (l.splits > 1) l.part_rows = l.splits * tokens * sh.group * sh.kv_heads;
   return l;
 }
 
-// The launches of a call run one after another and share their parts' memory.
-size_t attn_workspace(const Shape& sh, const int32_t* cu, int32_t num_seqs, int32_t hd) {
+// The launches run one after another and share the workspace.
+size_t attn_workspace(const int32_t* cu, int32_t num_seqs, int32_t group, int32_t hd) {
   size_t need = 0;
   for (const bool pair : {false, true})
     for (int32_t i = 0; i < num_seqs;) {
-      const Launch l = plan_launch(sh, cu, num_seqs, &i, pair);
-      size_t bytes = static_cast<size_t>(l.part_rows) * (hd + 1) * sizeof(float);
-      if (l.slot_rows > 0) bytes += zl::kSplitCtas * sizeof(zl::PagedJoin);
-      need = std::max(need, bytes);
+      const Launch l = next_launch(cu, num_seqs, group, pair, &i);
+      if (l.segs == 0) continue;
+      const size_t rows = static_cast<size_t>(2) * zl::kPagedCtas * l.slot_rows;
+      need = std::max(need, zl::kPagedCtas * sizeof(zl::PagedJoin) + rows * (hd + 1) * sizeof(float));
     }
   return need;
 }
@@ -390,7 +355,7 @@ zl_status zl_paged_attn_workspace_size(const int32_t* cu_seqlens_q, int32_t num_
   int64_t tq = 0;
   const zl_status st = check_attn(cu_seqlens_q, num_seqs, max_kv_len, num_heads, num_kv_heads, head_dim, &tq);
   if (st != ZL_OK) return st;
-  *bytes = attn_workspace(Shape{num_heads / num_kv_heads, num_kv_heads, max_kv_len}, cu_seqlens_q, num_seqs, head_dim);
+  *bytes = attn_workspace(cu_seqlens_q, num_seqs, num_heads / num_kv_heads, head_dim);
   return ZL_OK;
 }
 
@@ -414,8 +379,8 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
   st = check_rows(q, q_stride, num_heads, hd, tq, 2);
   if (st != ZL_OK) return st;
 
-  const Shape sh{num_heads / cache->num_kv_heads, cache->num_kv_heads, max_kv_len};
-  const size_t need = attn_workspace(sh, cu_seqlens_q, num_seqs, hd);
+  const int32_t group = num_heads / cache->num_kv_heads;
+  const size_t need = attn_workspace(cu_seqlens_q, num_seqs, group, hd);
   if (need > 0 && (!workspace || workspace_bytes < need)) return ZL_EWORKSPACE;
   if (need > 0 && !aligned16(workspace)) return ZL_EALIGN;
   int sms = 0;
@@ -432,8 +397,8 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
   a.lse_stride = tq;
   a.num_heads = num_heads;
   a.num_kv_heads = cache->num_kv_heads;
-  a.group = sh.group;
-  a.tile_tokens = sh.tile_tokens();
+  a.group = group;
+  a.tile_tokens = tile_tokens(group);
   a.table_cols = cache->table_cols;
   a.num_pages = cache->num_pages;
   a.page_shift = shift_of(cache->page_size);
@@ -463,35 +428,22 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
       ok = ok && zl::make_map_heads(&maps.q[i], q, tq, num_heads, hd, q_stride, a.group, zl::kBlockM / (1 << i) / a.group);
   if (!ok) return ZL_ECUDA;
 
+  a.joins = static_cast<zl::PagedJoin*>(workspace);
+  a.o_part = reinterpret_cast<float*>(a.joins + zl::kPagedCtas);
   for (const bool pair : {false, true}) {
     for (int32_t i = 0; i < num_seqs;) {
       const int32_t first = i;
-      const Launch l = plan_launch(sh, cu_seqlens_q, num_seqs, &i, pair);
+      const Launch l = next_launch(cu_seqlens_q, num_seqs, group, pair, &i);
       if (l.segs == 0) continue;
-      if (l.items > INT32_MAX) return ZL_EINVAL;
-      char* ws = static_cast<char*>(workspace);
-      a.joins = reinterpret_cast<zl::PagedJoin*>(ws);
-      if (!pair) ws += zl::kSplitCtas * sizeof(zl::PagedJoin);
-      a.o_part = reinterpret_cast<float*>(ws);
-      a.lse_part = a.o_part + l.part_rows * hd;
-      a.split_blocks = l.split_blocks;
       a.slot_rows = l.slot_rows;
+      a.lse_part = a.o_part + int64_t(2) * zl::kPagedCtas * l.slot_rows * hd;
       a.n_segs = 0;
-      a.n_items = 0;
-      a.tokens = 0;
-      int64_t part0 = 0;
       for (int32_t x = first; x < i; ++x) {
         const int32_t n = cu_seqlens_q[x + 1] - cu_seqlens_q[x];
-        if (n == 0 || sh.pair(n) != pair) continue;
-        a.segs[a.n_segs++] = zl::PagedSeg{x, cu_seqlens_q[x], n, a.n_items, l.splits, a.tokens, part0};
-        a.n_items += static_cast<int32_t>(sh.units(n) * sh.kv_heads * l.splits);
-        a.tokens += n;
-        part0 += int64_t(l.splits) * n;
+        if (n > 0 && (n > a.tile_tokens) == pair) a.segs[a.n_segs++] = zl::PagedSeg{x, cu_seqlens_q[x], n};
       }
-      if (!pair) a.n_items = zl::kSplitCtas;
       st = launch_counted("paged_attn", s, [&] { return zl::launch_paged_attn(hd, pair, maps, a, s); });
       if (st != ZL_OK) return st;
-      if (l.part_rows == 0) continue;
       st = launch_counted("paged_join", s, [&] { return zl::launch_paged_join(hd, pair, a, s); });
       if (st != ZL_OK) return st;
     }
