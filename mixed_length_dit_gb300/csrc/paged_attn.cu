@@ -1102,8 +1102,9 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
 
   if (warp >= kProducerWarp) {
     // 384 threads are launched with 168 registers each, 64,512 in all: PAIR's
-    // softmax groups take 200 and leave these warps 104.
-    if constexpr (PAIR) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    // softmax groups take 208 and leave these warps 88 (at 168 the block loop
+    // spills, or not, with any change of the code around it).
+    if constexpr (PAIR) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kProducerWarp) {
       produce<HD, PAIR, N>(sm, args, maps);
     } else if (warp == kAuxWarp) {
@@ -1112,7 +1113,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
       if (lane == 0) issue<HD, PAIR, N>(sm, args, tmem, warp - kMmaWarp0);
     }
   } else if constexpr (PAIR) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     softmax_pair<HD>(sm, args, maps, tmem);
   } else {
     softmax_split<HD>(sm, args, tmem);
