@@ -4,8 +4,9 @@
 // The tables live on the device, so that a generation loop (or a captured
 // graph) never waits for the host.  What must be decided in one order, which
 // free page goes to whom, is decided by one CTA that scans the reference counts
-// (each thread owns a run of pages, a prefix sum over the threads ranks them):
-// results are the same on every run, lowest page number first, and an
+// (each warp owns a run of pages, read 32 at a time and ranked by ballots; with a
+// run per thread, whose loads do not coalesce, planning 27,500 pages took 12 us
+// more), and a prefix sum over the warps ranks the runs: results are the same on every run, lowest page number first, and an
 // operation that lacks pages changes nothing.  The plan is a list of page
 // moves in the workspace; a second launch over the whole GPU then moves the
 // pages and rewrites the tables.  That launch is bound by HBM (each moved byte
@@ -65,13 +66,49 @@ __device__ __forceinline__ int pages_of(int64_t len, int shift) {
   return static_cast<int>((len + (int64_t(1) << shift) - 1) >> shift);
 }
 
-// A thread's run of pages [first, last).
+// A warp's run of pages [first, last), a multiple of 32 apart.
 __device__ __forceinline__ void page_run(int num_pages, int* first, int* last) {
-  const int64_t per = (static_cast<int64_t>(num_pages) + kPlanThreads - 1) / kPlanThreads;
-  const int64_t f = per * threadIdx.x;
+  constexpr int kWarps = kPlanThreads / 32;
+  const int64_t per = ((static_cast<int64_t>(num_pages) + kWarps - 1) / kWarps + 31) & ~int64_t(31);
+  const int64_t f = per * (threadIdx.x >> 5);
   *first = static_cast<int>(f < num_pages ? f : num_pages);
   *last = static_cast<int>(f + per < num_pages ? f + per : num_pages);
 }
+
+// Pages of the warp's run that `pred` (of a page and its count) holds for.
+template <typename P>
+__device__ __forceinline__ int count_run(const PageTable& t, int first, int last, P pred) {
+  int n = 0;
+#pragma unroll 4
+  for (int p0 = first; p0 < last; p0 += 32) {
+    const int p = p0 + static_cast<int>(threadIdx.x & 31);
+    n += __popc(__ballot_sync(0xffffffffu, p < last && pred(p, t.refs[p])));
+  }
+  return n;
+}
+
+// Calls `take(page, rank)` for those pages in order, ranks from `rank` on, as
+// long as they are below `end`.
+template <typename P, typename F>
+__device__ __forceinline__ void rank_run(const PageTable& t, int first, int last, int rank, int end, P pred, F take) {
+  const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
+#pragma unroll 4
+  for (int p0 = first; p0 < last && rank < end; p0 += 32) {
+    const int p = p0 + static_cast<int>(threadIdx.x & 31);
+    const bool is = p < last && pred(p, t.refs[p]);
+    const uint32_t m = __ballot_sync(0xffffffffu, is);
+    const int r = rank + __popc(m & below);
+    if (is && r < end) take(p, r);
+    rank += __popc(m);
+  }
+}
+
+// Exclusive prefix sum of one value per warp (lane 0's) over the CTA.
+__device__ __forceinline__ int warps_scan(int v, int* total) {
+  return __shfl_sync(0xffffffffu, block_scan((threadIdx.x & 31) == 0 ? v : 0, total), 0);
+}
+
+__device__ __forceinline__ bool is_free(int, int refs) { return refs == 0; }
 
 // ------------------------------------------------------------------ extend
 __global__ void __launch_bounds__(kPlanThreads)
@@ -99,10 +136,9 @@ extend_kernel(PageTable t, const int32_t* counts, int32_t* status) {
   }
   if (!ok) atomicExch(&bad, 1);
   atomicAdd(&wanted, static_cast<unsigned long long>(need));
-  int first, last, free_run = 0;
+  int first, last;
   page_run(t.num_pages, &first, &last);
-  for (int p = first; p < last; ++p) free_run += t.refs[p] == 0;
-  const int rank0 = block_scan(free_run, &total_free);
+  const int rank0 = warps_scan(count_run(t, first, last, is_free), &total_free);
   if (bad || wanted > static_cast<unsigned long long>(total_free)) {
     const unsigned long long lacking = wanted - total_free;
     if (threadIdx.x == 0) *status = bad ? -1 : static_cast<int>(lacking < INT32_MAX ? lacking : INT32_MAX);
@@ -114,9 +150,7 @@ extend_kernel(PageTable t, const int32_t* counts, int32_t* status) {
     at += pages_of(static_cast<int64_t>(t.kv_lens[s]) + counts[s], t.page_shift) - pages_of(t.kv_lens[s], t.page_shift);
   }
   __syncthreads();
-  int rank = rank0;
-  for (int p = first; p < last && rank < total_need; ++p) {
-    if (t.refs[p] != 0) continue;
+  rank_run(t, first, last, rank0, total_need, is_free, [&](int p, int rank) {
     int lo = 0, hi = t.slots - 1;              // the last slot whose new pages start at or before rank
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -124,8 +158,7 @@ extend_kernel(PageTable t, const int32_t* counts, int32_t* status) {
     }
     t.table[static_cast<int64_t>(lo) * t.cols + pages_of(t.kv_lens[lo], t.page_shift) + rank - start[lo]] = p;
     t.refs[p] = 1;
-    ++rank;
-  }
+  });
   __syncthreads();                             // the old lengths were read above
   for (int s = s0; s < s1; ++s) t.kv_lens[s] += counts[s];
   if (threadIdx.x == 0) *status = 0;
@@ -198,11 +231,10 @@ fork_plan_kernel(PageTable t, const int32_t* parents, const int32_t* children, i
     for (int i = i0; i < i1; ++i)
       if (atomicCAS(&t.kv_lens[children[i]], 0, -1 - i) != 0) atomicExch(&bad, 1);
   }
-  int first, last, free_run = 0;
+  int first, last;
   page_run(t.num_pages, &first, &last);
-  for (int p = first; p < last; ++p) free_run += t.refs[p] == 0;
   const int need0 = block_scan(need, &total_need);
-  const int rank0 = block_scan(free_run, &total_free);
+  const int rank0 = warps_scan(count_run(t, first, last, is_free), &total_free);
   if (bad || total_need > total_free) {
     if (in_range)
       for (int i = i0; i < i1; ++i) atomicCAS(&t.kv_lens[children[i]], -1 - i, 0);
@@ -214,9 +246,7 @@ fork_plan_kernel(PageTable t, const int32_t* parents, const int32_t* children, i
   }
   int32_t* src = ws + ws_src();
   int32_t* dst = ws + ws_dst(t.num_pages);
-  int rank = rank0;
-  for (int p = first; p < last && rank < total_need; ++p)
-    if (t.refs[p] == 0) dst[rank++] = p;
+  rank_run(t, first, last, rank0, total_need, is_free, [&](int p, int rank) { dst[rank] = p; });
   __syncthreads();
   int at = need0;
   for (int i = i0; i < i1; ++i) {
@@ -240,33 +270,39 @@ fork_plan_kernel(PageTable t, const int32_t* parents, const int32_t* children, i
 // ------------------------------------------------------------------ compact
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PageTable t, int32_t* ws, int32_t* live_out) {
   __shared__ int live, holes, movers;
-  int first, last, n = 0;
+  int first, last;
   page_run(t.num_pages, &first, &last);
-  for (int p = first; p < last; ++p) n += t.refs[p] > 0;
-  block_scan(n, &live);
+  warps_scan(count_run(t, first, last, [](int, int refs) { return refs > 0; }), &live);
   int32_t* src = ws + ws_src();
   int32_t* dst = ws + ws_dst(t.num_pages);
   int32_t* map = ws + ws_map(t.num_pages);
-  int nh = 0, nm = 0;
-  for (int p = first; p < last; ++p) {
-    const bool used = t.refs[p] > 0;
-    nh += p < live && !used;
-    nm += p >= live && used;
-  }
-  int rh = block_scan(nh, &holes);
-  int rm = block_scan(nm, &movers);
-  for (int p = first; p < last; ++p) {
-    const bool used = t.refs[p] > 0;
-    if (p < live && !used) dst[rh++] = p;
-    if (p >= live && used) src[rm++] = p;
-    map[p] = p;
-  }
+  const int n = live;
+  const auto hole = [n](int p, int refs) { return p < n && refs <= 0; };
+  const auto mover = [n](int p, int refs) { return p >= n && refs > 0; };
+  const int rh = warps_scan(count_run(t, first, last, hole), &holes);
+  const int rm = warps_scan(count_run(t, first, last, mover), &movers);
+  rank_run(t, first, last, rh, INT32_MAX, hole, [&](int p, int rank) { dst[rank] = p; });
+  rank_run(t, first, last, rm, INT32_MAX, mover, [&](int p, int rank) { src[rank] = p; });
+  for (int p = threadIdx.x; p < t.num_pages; p += kPlanThreads) map[p] = p;
   __syncthreads();
-  for (int i = threadIdx.x; i < movers; i += kPlanThreads) {
-    const int s = src[i], d = dst[i];
-    map[s] = d;
-    t.refs[d] = t.refs[s];
-    t.refs[s] = 0;
+  // four moves of a thread at once: their reads depend on one another
+  for (int i0 = threadIdx.x; i0 < movers; i0 += 4 * kPlanThreads) {
+    int s[4], d[4], r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * kPlanThreads;
+      s[u] = i < movers ? src[i] : -1;
+      d[u] = i < movers ? dst[i] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) r[u] = s[u] >= 0 ? t.refs[s[u]] : 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (s[u] < 0) continue;
+      map[s[u]] = d[u];
+      t.refs[d[u]] = r[u];
+      t.refs[s[u]] = 0;
+    }
   }
   if (threadIdx.x == 0) {
     ws[kHdrOk] = 1;
