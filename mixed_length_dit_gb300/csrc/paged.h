@@ -93,6 +93,7 @@ struct PagedAttnHead {
   int32_t num_heads;
   int32_t num_kv_heads;
   int32_t group;                // query heads of a key head
+  int32_t group_inv;            // 65536 / group, rounded up
   int32_t tile_tokens;          // tokens of a query tile: 128 / group
   int32_t slot_rows;            // rows of a slot
   int32_t table_cols;
@@ -103,6 +104,12 @@ struct PagedAttnHead {
   int32_t window;
   float scale_log2;             // softmax scale * log2(e)
   int32_t n_segs;
+
+#ifdef __CUDACC__
+  // The token of a tile's row, row / group: exact for rows and groups up to
+  // 128, because row * (group * group_inv - 65536) < 128 * 128 < 65536.
+  __device__ __forceinline__ int row_token(int row) const { return (row * group_inv) >> 16; }
+#endif
 };
 
 template <int N>

@@ -312,15 +312,24 @@ __device__ __forceinline__ bool load_blocks(PagedSmem<HD, PAIR>* sm, const Paged
   return true;
 }
 
-// Key blocks that a unit counts for (one without keys still has rows to write).
+// Key blocks that a unit counts for (one without keys still has rows to write),
+// and what beginning and ending an item costs, in blocks: the cut is equal in
+// time, not in blocks, when some CTAs get many short sequences.
 __device__ __forceinline__ int weight_of(Range r) { return max(1, r.b1 - r.b0); }
+template <int HD, bool PAIR>
+__host__ __device__ constexpr int item_cost() { return PAIR ? 2 : HD == 128 ? 2 : 4; }
+
+__device__ __forceinline__ int64_t div_nonneg(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 template <bool PAIR>
 __device__ __forceinline__ int units_of(const PagedAttnHead& a, int q_len) {
   return PAIR ? (q_len + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens) : 1;
 }
 
-// All warps, at the start: the blocks of one key head of every segment (PAIR),
+// All warps, at the start: the cost of one key head of every segment (PAIR),
 // or the sum of 32 segments' (SPLIT, which has no room for more).
 template <int HD, bool PAIR, int N>
 __device__ __forceinline__ void sum_blocks(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a) {
@@ -330,7 +339,7 @@ __device__ __forceinline__ void sum_blocks(PagedSmem<HD, PAIR>* sm, const PagedA
       const int len = length_of(a, s), q_len = a.segs[s].q_len;
       int64_t sum = 0;
       for (int u = lane; u < units_of<true>(a, q_len); u += 32)
-        sum += weight_of(unit_blocks<true>(a, len, q_len, 2 * u));
+        sum += item_cost<HD, PAIR>() + weight_of(unit_blocks<true>(a, len, q_len, 2 * u));
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == 0) sm->scratch[s] = sum;
@@ -339,7 +348,8 @@ __device__ __forceinline__ void sum_blocks(PagedSmem<HD, PAIR>* sm, const PagedA
     for (int chunk = warp * 32; chunk < a.n_segs; chunk += kThreads) {
       int64_t sum = 0;
       if (chunk + lane < a.n_segs)
-        sum = weight_of(unit_blocks<false>(a, length_of(a, chunk + lane), a.segs[chunk + lane].q_len, 0));
+        sum = item_cost<HD, PAIR>() +
+              weight_of(unit_blocks<false>(a, length_of(a, chunk + lane), a.segs[chunk + lane].q_len, 0));
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == 0) sm->scratch[chunk / 32] = sum;
@@ -358,9 +368,9 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x) {
 }
 
 // The blocks of all units (sequence, key head, query tiles) stand in one line,
-// which is cut into equal pieces, one per CTA: every SM has the same number of
-// blocks whatever the lengths, and only units that a cut goes through are
-// joined afterwards.  A CTA's piece of the unit that its range starts inside
+// each unit's behind a gap of its item cost, and the line is cut into equal
+// pieces, one per CTA: every SM has the same work whatever the lengths, and only
+// units that a cut goes through are joined afterwards.  A CTA's piece of the unit that its range starts inside
 // goes to slot 2c, of the unit that goes on behind its range to 2c + 1, and
 // joins[c] tells the join what begins in slot 2c + 1.
 template <int HD, bool PAIR, int N>
@@ -374,7 +384,8 @@ __device__ void produce(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, cons
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
   total *= nk;
-  const int64_t per = max(static_cast<int64_t>(kMinBlocks), (total + gridDim.x - 1) / gridDim.x);
+  const int64_t per = max(static_cast<int64_t>(kMinBlocks), div_nonneg(total + gridDim.x - 1, gridDim.x));
+  constexpr int kCost = item_cost<HD, PAIR>();
   int64_t g = c * per;
   const int64_t end = min(total, g + per);
   PagedJoin join = {0, 0, 0, 0, -1};
@@ -393,7 +404,7 @@ __device__ void produce(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, cons
       int64_t w = 0;
       if (chunk + lane < a.n_segs) {
         if constexpr (PAIR) w = sm->scratch[chunk + lane];
-        else w = weight_of(unit_blocks<false>(a, length_of(a, chunk + lane), a.segs[chunk + lane].q_len, 0));
+        else w = kCost + weight_of(unit_blocks<false>(a, length_of(a, chunk + lane), a.segs[chunk + lane].q_len, 0));
       }
       const int64_t incl = base + warp_scan(w * nk);
       const uint32_t past = __ballot_sync(0xffffffffu, incl > g);
@@ -408,13 +419,13 @@ __device__ void produce(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, cons
     }
     // ... the key head in it, and the unit, 32 at a time
     int len = length_of(a, seg), q_len = a.segs[seg].q_len;
-    int hk = static_cast<int>(off / seg_blocks), unit = 0;
+    int hk = static_cast<int>(div_nonneg(off, seg_blocks)), unit = 0;
     off -= hk * seg_blocks;
     if constexpr (PAIR) {
       int64_t before = 0;
       for (int u0 = 0;; u0 += 32) {
         const int u = u0 + lane;
-        const int64_t w = u < units_of<true>(a, q_len) ? weight_of(unit_blocks<true>(a, len, q_len, 2 * u)) : 0;
+        const int64_t w = u < units_of<true>(a, q_len) ? kCost + weight_of(unit_blocks<true>(a, len, q_len, 2 * u)) : 0;
         const int64_t incl = before + warp_scan(w);
         const uint32_t past = __ballot_sync(0xffffffffu, incl > off);
         if (past != 0) {
@@ -426,27 +437,31 @@ __device__ void produce(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, cons
         before = __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    int blk = static_cast<int>(off);
     while (true) {
       const int tile0 = PAIR ? 2 * unit : 0;
       const Range r = unit_blocks<PAIR>(a, len, q_len, tile0);
       const int weight = weight_of(r);
-      const int cnt = static_cast<int>(min(static_cast<int64_t>(weight - blk), end - g));
-      Item item = {seg, len, hk, tile0, 0, 0, -1};
-      if (r.b1 > r.b0) {
-        item.s0 = r.b0 + blk;
-        item.s1 = item.s0 + cnt;
+      const int64_t avail = min(kCost + weight - off, end - g);
+      const int first = static_cast<int>(max(off - kCost, int64_t(0)));          // the piece's blocks of the unit
+      const int last = static_cast<int>(max(off + avail - kCost, int64_t(0)));
+      if (last > first) {
+        Item item = {seg, len, hk, tile0, 0, 0, -1};
+        if (r.b1 > r.b0) {
+          item.s0 = r.b0 + first;
+          item.s1 = r.b0 + last;
+        }
+        if (last - first < weight) {
+          item.slot = first > 0 ? 2 * c : 2 * c + 1;
+          if (first == 0)
+            join = {a.segs[seg].q_row0, q_len, hk, tile0, static_cast<int>(div_nonneg(g - off + kCost + weight - 1, per))};
+        }
+        if (!publish(sm, n++, item)) return;
+        const Work w = decode<PAIR>(a, item);
+        if (!load_blocks<HD, PAIR, N>(sm, a, maps, w, uses0, uses1)) return;
       }
-      if (cnt < weight) {
-        item.slot = blk > 0 ? 2 * c : 2 * c + 1;
-        if (blk == 0) join = {a.segs[seg].q_row0, q_len, hk, tile0, static_cast<int>((g + weight - 1) / per)};
-      }
-      if (!publish(sm, n++, item)) return;
-      const Work w = decode<PAIR>(a, item);
-      if (!load_blocks<HD, PAIR, N>(sm, a, maps, w, uses0, uses1)) return;
-      g += cnt;
+      g += avail;
       if (g >= end) break;
-      blk = 0;
+      off = 0;
       if (++unit < units_of<PAIR>(a, q_len)) continue;
       unit = 0;
       if (++hk < nk) continue;
@@ -870,12 +885,112 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
   if (row == 0) bulk_wait_group0();              // the group's stores, before the CTA leaves
 }
 
+// SPLIT: joins what the groups and copies have summed of each row, 2 * COPIES
+// parts (part i: group i / COPIES, copy i % COPIES), through stage `st` of the
+// rings: the item's last V stage, which its issuer leaves to this epilogue.
+// There it stands as [part][row][width] floats, 16-byte pieces swizzled by the
+// row, in as few passes over the columns as fit (one for eight rows or fewer).
+// With many short sequences a CTA comes here every few microseconds: the loops
+// have fixed lengths, and all TMEM loads of a pass are in flight at once.
+template <int HD, int COPIES>
+__device__ __forceinline__ bool join_parts(PagedSmem<HD, false>* sm, const PagedAttnHead& a, const Work& w,
+                                           uint32_t tO, float m_run, float l_run, uint32_t st, uint32_t& sync_uses) {
+  constexpr int kParts = 2 * COPIES;
+  constexpr int kSpan = kBlockM / COPIES;        // rows of a copy
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = warp >> 2, row = threadIdx.x & 127;
+  const int rows = w.q_len * a.group;
+  const int r = row & (kSpan - 1);
+  const int part = t * COPIES + row / kSpan;
+  const uint32_t code = ERR_TIMEOUT_SOFTMAX;
+  float2* ml = reinterpret_cast<float2*>(sm->scratch);
+  ml[threadIdx.x] = make_float2(m_run, l_run);
+  if (!warps_sync(&sm->all_sync, sync_uses, &sm->abort_flag, code)) return false;
+  float2 v[kParts];
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) v[i] = ml[i * kSpan + r];
+  float m_all = v[0].x;
+#pragma unroll
+  for (int i = 1; i < kParts; ++i) m_all = fmaxf(m_all, v[i].x);
+  float l_all = 0.f;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) l_all += v[i].x == -INFINITY ? 0.f : v[i].y * fast_exp2(v[i].x - m_all);
+  const float scale = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_all) / l_all;
+  if (t == 0 && row < kSpan && r < rows) {       // the first copy's threads know the row's LSE
+    const int tok = a.row_token(r), h = w.hk * a.group + r - tok * a.group;
+    const float lse = l_all > 0.f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
+    if (w.final)
+      a.lse[static_cast<int64_t>(h) * a.lse_stride + w.q_row0 + tok] = lse;
+    else
+      a.lse_part[w.part + r] = lse;
+  }
+  float4* stage = reinterpret_cast<float4*>(sm->kv[st]);
+  const int log_passes = COPIES * rows <= 32 ? 0 : COPIES * rows <= 64 ? 1 : 2;
+  const int width = HD >> log_passes;            // columns of a pass
+  const int log_f4 = (HD == 128 ? 5 : 4) - log_passes;            // 16-byte pieces of a row, 4 at least
+  const int swz_mask = min(7, (1 << log_f4) - 1);
+  const bool warp_rows = (r & ~31) < rows;
+#pragma unroll 1
+  for (int c = 0; c < 1 << log_passes; ++c) {
+    if (warp_rows) {
+      float4* dst = stage + ((part * rows + r) << log_f4);
+#pragma unroll 1
+      for (int x0 = 0; x0 < width; x0 += 32) {   // (a pass of 16 columns loads 16 it does not use)
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld32(tO + (c * width + x0 & HD - 32), o);
+        tmem_wait_ld();
+        reg_fence(o);
+        const int odd = c * width + x0 & 16;     // of HD 64 in passes of 16: the upper half
+        if (r < rows) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (4 * i + x0 >= width) continue;
+            const int e = 4 * i;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (scale != 0.f)                    // else O may never have been written
+              y = odd ? make_float4(__uint_as_float(o[(e + 16) & 31]) * scale, __uint_as_float(o[(e + 17) & 31]) * scale,
+                                    __uint_as_float(o[(e + 18) & 31]) * scale, __uint_as_float(o[(e + 19) & 31]) * scale)
+                      : make_float4(__uint_as_float(o[e]) * scale, __uint_as_float(o[e + 1]) * scale,
+                                    __uint_as_float(o[e + 2]) * scale, __uint_as_float(o[e + 3]) * scale);
+            dst[(x0 / 4 + i) ^ (r & swz_mask)] = y;
+          }
+        }
+      }
+    }
+    if (!warps_sync(&sm->all_sync, sync_uses, &sm->abort_flag, code)) return false;
+    for (int y = threadIdx.x; y < rows << log_f4; y += 2 * kBlockM) {
+      const int rr = y >> log_f4, f = y & ((1 << log_f4) - 1);
+      float4 u[kParts];
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) u[i] = stage[((i * rows + rr) << log_f4) + (f ^ (rr & swz_mask))];
+      float4 sum = u[0];
+#pragma unroll
+      for (int i = 1; i < kParts; ++i) {
+        sum.x += u[i].x; sum.y += u[i].y; sum.z += u[i].z; sum.w += u[i].w;
+      }
+      const int col = c * width + 4 * f;
+      if (w.final) {
+        const int tk = a.row_token(rr), h = w.hk * a.group + rr - tk * a.group;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) +
+                                  (static_cast<int64_t>(w.q_row0 + tk) * a.num_heads + h) * HD + col) =
+            make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+      } else {
+        *reinterpret_cast<float4*>(a.o_part + (w.part + rr) * HD + col) = sum;
+      }
+    }
+    fence_proxy_async_smem();                    // TMA may write the stage after this
+    if (!warps_sync(&sm->all_sync, sync_uses, &sm->abort_flag, code)) return false;
+  }
+  if (threadIdx.x == 0) mbar_arrive(&sm->kv_empty[st]);
+  return true;
+}
+
 // SPLIT: group t takes every other block; with copies of the rows, a warp
 // takes its own part of a block's columns.
 template <int HD, int N>
 __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& a, uint32_t tmem) {
   using Ring = Stages<HD, false>;
-  float2* ml = reinterpret_cast<float2*>(sm->scratch);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = warp >> 2, quad = warp & 3;
   const int row = quad * 32 + lane;
@@ -897,7 +1012,7 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
     const int nch = 4 / copies;                  // 32-column pieces of a block that are this warp's,
     const int ch0 = (quad / nch) * nch;          // from this one on
     const bool warp_rows = (r & ~31) < rows;     // the warp has a row at all
-    const int tok = r / a.group;
+    const int tok = a.row_token(r);
     int lo, hi, lo_all, hi_all, x;
     const int p0 = w.len - w.q_len;
     keys_of(a, w.len, p0 + tok, &lo, &hi);
@@ -971,87 +1086,16 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
       ++q_it;
       tc_fence_after();
     }
-    // ---------------------------------------------------------- join the parts of each row
-    // part i: group i / copies, copy i % copies
-    ml[t * kBlockM + row] = make_float2(m_run, l_run);
-    if (!warps_sync(&sm->all_sync, sync_uses, abort_flag, code)) return;
-    const int parts = 2 * copies;
-    float m_all = -INFINITY;
-    for (int i = 0; i < parts; ++i) m_all = fmaxf(m_all, ml[i * span + r].x);
-    float l_all = 0.f;
-    for (int i = 0; i < parts; ++i) {
-      const float2 v = ml[i * span + r];
-      if (v.x != -INFINITY) l_all += v.y * fast_exp2(v.x - m_all);
-    }
-    const float scale = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_all) / l_all;
-    if (t == 0 && quad * 32 < span && r < rows) {   // the first copy's threads know the row's LSE
-      const int h = w.hk * a.group + r - tok * a.group;
-      const float lse = l_all > 0.f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
-      if (w.final)
-        a.lse[static_cast<int64_t>(h) * a.lse_stride + w.q_row0 + tok] = lse;
-      else
-        a.lse_part[w.part + r] = lse;
-    }
-    // Through the item's last V stage, which its issuer leaves to this
-    // epilogue: [part][row][width] floats, 16-byte pieces swizzled by the
-    // row, in as few passes over the columns as the stage allows (one for
-    // eight rows or fewer).
     const int blocks = w.s1 - w.s0;
     const int ring = (blocks - 1) & 1;
     const uint32_t st = Ring::stage(ring, (ring ? base1 : base0) + 2u * static_cast<uint32_t>((blocks - 1) >> 1) + 1u);
     base0 += 2u * static_cast<uint32_t>((blocks + 1) / 2);
     base1 += 2u * static_cast<uint32_t>(blocks / 2);
-    float4* stage = reinterpret_cast<float4*>(sm->kv[st]);
-    const int passes = copies * rows <= 32 ? 1 : copies * rows <= 64 ? 2 : 4;
-    const int width = HD / passes;               // columns of a pass
-    const int f4 = width / 4;                    // 16-byte pieces of a row, 4 at least
-    const int swz_mask = min(7, f4 - 1);
-    const int part = t * copies + row / span;
-#pragma unroll 1
-    for (int c = 0; c < passes; ++c) {
-      if (warp_rows) {
-        float4* dst = stage + (part * rows + r) * f4;
-#pragma unroll 1
-        for (int x = 0; x < width / 16; ++x) {
-          uint32_t o[16];
-          __syncwarp();
-          tmem_ld16(tO + c * width + x * 16, o);
-          tmem_wait_ld();
-          reg_fence(o);
-          if (r < rows) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (scale != 0.f)                  // else O may never have been written
-                v = make_float4(__uint_as_float(o[4 * i]) * scale, __uint_as_float(o[4 * i + 1]) * scale,
-                                __uint_as_float(o[4 * i + 2]) * scale, __uint_as_float(o[4 * i + 3]) * scale);
-              dst[(4 * x + i) ^ (r & swz_mask)] = v;
-            }
-          }
-        }
-      }
-      if (!warps_sync(&sm->all_sync, sync_uses, abort_flag, code)) return;
-      for (int y = threadIdx.x; y < rows * f4; y += 2 * kBlockM) {
-        const int rr = y / f4, f = y - rr * f4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < parts; ++i) {
-          const float4 u = stage[(i * rows + rr) * f4 + (f ^ (rr & swz_mask))];
-          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-        }
-        const int col = c * width + 4 * f;
-        if (w.final) {
-          const int tk = rr / a.group, h = w.hk * a.group + rr - tk * a.group;
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) +
-                                    (static_cast<int64_t>(w.q_row0 + tk) * a.num_heads + h) * HD + col) =
-              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        } else {
-          *reinterpret_cast<float4*>(a.o_part + (w.part + rr) * HD + col) = v;
-        }
-      }
-      fence_proxy_async_smem();                  // TMA may write the stage after this
-      if (!warps_sync(&sm->all_sync, sync_uses, abort_flag, code)) return;
-    }
-    if (threadIdx.x == 0) mbar_arrive(&sm->kv_empty[st]);
+    bool ok;
+    if (copies == 4) ok = join_parts<HD, 4>(sm, a, w, tO, m_run, l_run, st, sync_uses);
+    else if (copies == 2) ok = join_parts<HD, 2>(sm, a, w, tO, m_run, l_run, st, sync_uses);
+    else ok = join_parts<HD, 1>(sm, a, w, tO, m_run, l_run, st, sync_uses);
+    if (!ok) return;
   }
 }
 

@@ -398,6 +398,7 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
   a.num_heads = num_heads;
   a.num_kv_heads = cache->num_kv_heads;
   a.group = group;
+  a.group_inv = (65536 + group - 1) / group;
   a.tile_tokens = tile_tokens(group);
   a.table_cols = cache->table_cols;
   a.num_pages = cache->num_pages;
