@@ -69,8 +69,7 @@ typedef enum {
                             zl_sync_check)                                      */
   ZL_ENODEVICE = -7,     /* no usable sm_103 device                             */
   ZL_EPAGE = -8          /* a kernel met a page number, slot or length outside
-                            the cache and left it out (reported by
-                            zl_sync_check)                                      */
+                            the cache (reported by zl_sync_check)               */
 } zl_status;
 
 typedef enum {
@@ -458,8 +457,11 @@ zl_status zl_rope_bwd(const zl_rope_t* plan, const void* q, int64_t q_stride, co
  * arrays: a captured graph replays with the lengths and pages of the moment.
  *
  * Kernels check every page number, slot and length that they read from the
- * device: one out of range is left out (its token is not written, its keys
- * are not attended), and the next zl_sync_check reports ZL_EPAGE.
+ * device, and never leave the buffers: a token or page move that is out of
+ * range is left out, attention reads page 0 in place of a page that is not
+ * there and a length within the call's bound (that sequence's outputs are then
+ * undefined, other sequences' are right), and the next zl_sync_check reports
+ * ZL_EPAGE.
  */
 typedef struct {
   void* k_pages;               /* [num_pages][num_kv_heads][page_size][head_dim] bf16 */
@@ -491,8 +493,12 @@ zl_status zl_paged_append(const zl_paged_cache_t* cache, const void* k, int64_t 
                           int32_t num_heads, void* q_out, int64_t q_out_stride, void* stream);
 
 /*
- * Workspace needed by zl_paged_attn for this batch, in bytes (0 when no
- * sequence's keys are split).  Same argument rules as zl_paged_attn.
+ * Workspace needed by zl_paged_attn for this batch, in bytes: what sequences
+ * whose keys are spread over several SMs leave there until they are joined.
+ * It depends on the queries, the heads and head_dim alone, at most 40 MiB, and
+ * a call needs nothing of it from an earlier one: calls that are ordered (the
+ * layers of a model, graphs replayed in turn) may share one workspace, calls
+ * that may overlap must not.  Same argument rules as zl_paged_attn.
  */
 zl_status zl_paged_attn_workspace_size(const int32_t* cu_seqlens_q, int32_t num_seqs, int32_t max_kv_len,
                                        int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, size_t* bytes);
@@ -511,13 +517,17 @@ zl_status zl_paged_attn_workspace_size(const int32_t* cu_seqlens_q, int32_t num_
  * q [Tq, H, d] bf16, q_stride elements between tokens; o [Tq, H, d] bf16,
  * lse [H, Tq] float32 (natural log, as zl_varlen_attn_fwd's, so that results
  * over other keys can be joined with zl_lse_merge).  max_kv_len: an upper
- * bound of kv_lens (a longer sequence is cut there and reported as ZL_EPAGE);
- * the work split is chosen from it.  num_heads is a multiple of num_kv_heads
+ * bound of kv_lens, at most table_cols * page_size (a longer sequence is cut
+ * there and reported as ZL_EPAGE).  num_heads is a multiple of num_kv_heads
  * and at most 128 times as many.  Scores, the running maximum and sum, and the
  * output accumulate in float32; the probabilities are rounded to bf16 once for
- * the tensor cores.  A value row that some query of its 128-key block sees
- * must be finite for the block's other queries too (0 * inf).  Long caches
- * with few query rows are split over the keys and joined in a second launch.
+ * the tensor cores.  The values of a sequence's tokens must be finite: a
+ * product of zero and infinity would reach queries that do not see them (its
+ * keys may be anything where the mask hides them, and rows past its length
+ * anything at all).  The work is spread over the SMs in equal shares whatever
+ * the lengths; results are the same on every run with the same lengths.  Two
+ * launches per 640 sequences of one query tile (up to 128 / (num_heads /
+ * num_kv_heads) queries) and two per 640 longer ones.
  */
 zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_stride, const int32_t* cu_seqlens_q,
                         int32_t num_seqs, int32_t max_kv_len, int32_t num_heads, float softmax_scale, int32_t causal,

@@ -405,7 +405,7 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
   a.page_shift = shift_of(cache->page_size);
   a.max_kv_len = max_kv_len;
   a.causal = causal;
-  a.window = window;
+  a.window = window < max_kv_len ? window : 0;   // one that reaches over every key is none (and stays in 32 bits)
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
 
   // the maps that the call's kinds of sequences use

@@ -291,6 +291,75 @@ def test_two_streams_at_once():
         assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
 
 
+def test_two_graphs_share_a_workspace():
+    bs = [Batch([1, 3], [3000, 700], 8, 2, 128, 16, seed=50), Batch([200, 1], [900, 2000], 8, 2, 128, 16, seed=51)]
+    want = [b.run() for b in bs]
+    size = max(zl.paged_attn_workspace_bytes(b.cu, max(b.lens), 8, 2, 128) for b in bs)
+    ws = zl.alloc_workspace(size, "cuda")
+    outs = [(torch.zeros_like(b.q), torch.zeros((8, b.cu[-1]), device="cuda")) for b in bs]
+    graphs = []
+    for b, (out, lse) in zip(bs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.run(out=out, lse=lse, workspace=ws)
+        graphs.append(g)
+    ws.fill_(255)                           # nothing of an earlier call is needed
+    for i in (0, 1, 1, 0, 0, 1):
+        for t in outs[i]:
+            t.zero_()
+        graphs[i].replay()
+        zl.sync_check()
+        assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+
+
+def test_no_key_at_all():
+    b = Batch([2, 200], [16, 16], 4, 2, 64, 16, seed=52)
+    b.dlens.zero_()
+    for most in (0, 16):
+        o, lse = b.run(most=most)
+        zl.sync_check()
+        assert torch.all(o == 0) and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("new", [1, 20])
+def test_windows_as_large_as_an_int(new):
+    """A window over everything is no window, also for positions below zero."""
+    b = Batch([new, new], [10, 300], 4, 1, 64, 16, seed=53)
+    for causal in (True, False):
+        want = b.run(causal=causal)
+        got = b.run(causal=causal, window=2 ** 31 - 1)
+        zl.sync_check()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        b.check(*got, causal=causal)
+
+
+def test_offsets_past_32_bits():
+    """Pools of more than 2^31 elements, of which the last pages are used: the
+    same bits as with a small pool."""
+    small = Batch([1, 150, 4], [700, 400, 4], 8, 8, 128, 128, seed=54, fill=1.0)
+    k, v = (torch.randn((155, 8, 128), device="cuda").to(BF16) for _ in range(2))
+    plan = zl.RopePlan(128)
+    pages = 2 ** 31 // (8 * 128 * 128) + 40
+    big = [torch.empty((pages, 8, 128, 128), dtype=BF16, device="cuda") for _ in range(2)]
+    assert big[0].numel() > 2 ** 31
+    shift = pages - small.num_pages
+    for x, y in zip(big, (small.k_pages, small.v_pages)):
+        x[shift:] = y
+    used = (torch.arange(small.dtable.shape[1], device="cuda") < (small.dlens[:, None] + 127) // 128)
+    table = torch.where(used, small.dtable + shift, -1).int()
+    q1 = zl.paged_append(k, v, small.k_pages, small.v_pages, small.dtable, small.dlens, small.cu, q=small.q, rope=plan)
+    q2 = zl.paged_append(k, v, *big, table, small.dlens, small.cu, q=small.q, rope=plan)
+    zl.sync_check()
+    assert torch.equal(q1, q2) and torch.equal(big[0][shift:], small.k_pages) and torch.equal(big[1][shift:], small.v_pages)
+    o1, l1 = zl.paged_attn(q1, small.k_pages, small.v_pages, small.dtable, small.dlens, small.cu, 700)
+    o2, l2 = zl.paged_attn(q1, *big, table, small.dlens, small.cu, 700)
+    zl.sync_check()
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    last = torch.tensor([pages - 1], dtype=torch.int32, device="cuda")
+    zl.pages_copy(big[0], last, torch.zeros_like(last))
+    assert torch.equal(big[0][0], big[0][-1])
+
+
 # ------------------------------------------------------------------ append
 @pytest.mark.parametrize("hd,heads,kv_heads,page,axes,il", [
     (64, 4, 2, 16, (64,), False), (128, 10, 2, 64, (128,), True), (128, 3, 3, 256, (64,), False), (64, 2, 1, 32, (6,), True),

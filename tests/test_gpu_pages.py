@@ -61,6 +61,19 @@ def test_extend(page, pages, slots):
         b.same()
 
 
+def test_extend_of_many_slots_in_a_large_pool():
+    slots, pages, page = 8192, 70000, 16
+    rng = np.random.default_rng(8)
+    b = Both([int(x) for x in rng.integers(0, 40, slots)], pages, page, 8, seed=8, groups=1)
+    counts = [int(x) for x in rng.integers(0, 80, slots)]
+    assert int(zl.pages_extend(b.table, b.lens, b.refs, i32(counts), page)) == b.m.extend(counts) == 0
+    b.same()
+    free = b.m.refs.count(0)
+    counts = [16 * (free // slots + 1)] * slots
+    assert int(zl.pages_extend(b.table, b.lens, b.refs, i32(counts), page)) == b.m.extend(counts) != 0
+    b.same()
+
+
 def test_extend_that_cannot_be_met_changes_nothing():
     b = Both([20, 5, 0], 6, 16, 4)
     for counts, want in (([44, 20, 16], 1), ([0, -1, 0], -1), ([45, 0, 0], -1), ([2 ** 31 - 1, 0, 0], -1),
@@ -139,6 +152,18 @@ def test_compact(pages, lens, groups, elems):
     assert int(live) == b.m.compact()
     b.same()
     b.same_data()
+
+
+def test_compact_a_large_pool():
+    b = Both([16 * 9] * 3000, 60000, 16, 9, seed=9, groups=1)
+    rng = np.random.default_rng(9)
+    gone = [int(x) for x in rng.permutation(3000)[:1200]]
+    zl.pages_free(b.table, b.lens, b.refs, i32(gone), 16)
+    b.m.release(gone)
+    assert int(zl.pages_compact(b.cache, b.table, b.lens, b.refs)) == b.m.compact()
+    b.same()
+    got = b.cache.view(torch.int32).view(60000, -1)[:, 0].tolist()
+    assert all(got[p] == d * 8 for p, d in enumerate(b.m.data) if b.m.refs[p] > 0)
 
 
 def test_compact_of_shared_pages():
