@@ -10,7 +10,6 @@ cu_seqlens are host sequences of ints, or host_int32 of one.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import struct
@@ -18,7 +17,7 @@ import struct
 import torch
 
 from . import _lib
-from .attention import _check_like, alloc_workspace
+from .attention import _check_like
 
 _BF16, _I32 = torch.bfloat16, torch.int32
 
@@ -61,9 +60,13 @@ def _call(name, index, stream, *args):
         _lib.check(fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream), name)
 
 
-def _given(stream):
-    """What a call allocates belongs to the stream it is given."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty(like, shape, dtype, stream):
+    """A new tensor on the device of `like`; it belongs to the stream that the
+    call is given."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _rows(t, name, tokens, heads, dim, dtype, device):
@@ -175,32 +178,31 @@ def _rope(name, q, k, positions, plan, q_out, k_out, stream):
     if hd != plan.head_dim:
         raise ValueError(f"the plan is for head_dim {plan.head_dim}, q has {hd}")
     qs = _rows(q, "q", tokens, nq, hd, dtype, dev)
-    nk = kp = ks = kop = kos = 0
+    nk = kp = ks = kop = 0
     if k is not None:
         nk = k.shape[1]
         ks = _rows(k, "k", tokens, nk, hd, dtype, dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
     pos, pos_stride = _positions(positions, plan, tokens, dev)
+    qos, kos = nq * hd, nk * hd
     if q_out is not None or k_out is not None:
         if q_out is not None:
-            _rows(q_out, "q_out", tokens, nq, hd, dtype, dev)
+            qos = _rows(q_out, "q_out", tokens, nq, hd, dtype, dev)
         if k_out is not None:
-            _rows(k_out, "k_out", tokens, nk, hd, dtype, dev)
+            kos = _rows(k_out, "k_out", tokens, nk, hd, dtype, dev)
         _check_outputs((q_out, k_out), (q, k))
     index = q.get_device()
-    with _given(stream):
-        if q_out is None:
-            q_out = torch.empty((tokens, nq, hd), dtype=dtype, device=dev)
-        if k is not None and k_out is None:
-            k_out = torch.empty((tokens, nk, hd), dtype=dtype, device=dev)
+    if q_out is None:
+        q_out = _empty(q, (tokens, nq, hd), dtype, stream)
+    if k is not None and k_out is None:
+        k_out = _empty(q, (tokens, nk, hd), dtype, stream)
     if tokens == 0:
         return q_out, k_out
     if k is not None:
-        kp, kop, kos = k.data_ptr(), k_out.data_ptr(), k_out.stride(0) if tokens > 1 else nk * hd
+        kp, kop = k.data_ptr(), k_out.data_ptr()
     _call(name, index, stream, plan.ref, q.data_ptr(), qs, kp, ks, pos, pos_stride, tokens, nq, nk,
-          _lib.ZL_BF16 if dtype is _BF16 else _lib.ZL_FP32, q_out.data_ptr(),
-          q_out.stride(0) if tokens > 1 else nq * hd, kop, kos)
+          _lib.ZL_BF16 if dtype is _BF16 else _lib.ZL_FP32, q_out.data_ptr(), qos, kop, kos)
     return q_out, k_out
 
 
@@ -256,8 +258,7 @@ def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None
         nq = q.shape[1]
         qs = _rows(q, "q", tokens, nq, hd, _BF16, dev)
         if q_out is None:
-            with _given(stream):
-                q_out = torch.empty((tokens, nq, hd), dtype=_BF16, device=dev)
+            q_out = _empty(q, (tokens, nq, hd), _BF16, stream)
             qos = nq * hd
         else:
             qos = _rows(q_out, "q_out", tokens, nq, hd, _BF16, dev)
@@ -307,14 +308,12 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, max_kv_le
     index = q.get_device()
     if index < 0:
         raise ValueError("tensors must be CUDA tensors")
-    if out is None or lse is None or workspace is None:
-        with _given(stream):
-            if out is None:
-                out = torch.empty((tq, nh, hd), dtype=_BF16, device=dev)
-            if lse is None:
-                lse = torch.empty((nh, tq), dtype=torch.float32, device=dev)
-            if workspace is None:
-                workspace = alloc_workspace(paged_attn_workspace_bytes(cu, max_kv_len, nh, nk, hd), dev)
+    if out is None:
+        out = _empty(q, (tq, nh, hd), _BF16, stream)
+    if lse is None:
+        lse = _empty(q, (nh, tq), torch.float32, stream)
+    if workspace is None:
+        workspace = _empty(q, (paged_attn_workspace_bytes(cu, max_kv_len, nh, nk, hd),), torch.uint8, stream)
     ws, ws_bytes = _scratch(workspace, dev)
     _call("zl_paged_attn", index, stream, cache, q.data_ptr(), qs, cu.array, cu.n - 1, max_kv_len, nh,
           1.0 / math.sqrt(hd) if softmax_scale is None else softmax_scale, 1 if causal else 0, window, out.data_ptr(),
@@ -362,19 +361,17 @@ def _list(t, name, device):
     return t.shape[0]
 
 
-def _status(status, device, stream):
+def _status(status, like, stream):
     if status is None:
-        with _given(stream):
-            return torch.empty(1, dtype=_I32, device=device)
-    _exact(status, "status", (1,), _I32, device)
+        return _empty(like, (1,), _I32, stream)
+    _exact(status, "status", (1,), _I32, like.device)
     return status
 
 
-def _pages_scratch(workspace, num_pages, device, stream):
+def _pages_scratch(workspace, like, num_pages, stream):
     if workspace is None:
-        with _given(stream):
-            workspace = alloc_workspace(pages_workspace_bytes(num_pages), device)
-    ws, size = _scratch(workspace, device)
+        workspace = _empty(like, (pages_workspace_bytes(num_pages),), torch.uint8, stream)
+    ws, size = _scratch(workspace, like.device)
     return workspace, ws, size
 
 
@@ -391,7 +388,7 @@ def pages_extend(page_table, kv_lens, page_refs, counts, page_size, status=None,
     negative or do not fit a row; unless it is 0 nothing was changed."""
     t, dev = _tables(page_table, kv_lens, page_refs, page_size)
     _exact(counts, "counts", kv_lens.shape, _I32, dev)
-    status = _status(status, dev, stream)
+    status = _status(status, kv_lens, stream)
     _call("zl_pages_extend", kv_lens.get_device(), stream, t, counts.data_ptr(), status.data_ptr())
     return status
 
@@ -406,8 +403,8 @@ def pages_fork(cache, page_table, kv_lens, page_refs, parents, children, status=
     n = _list(parents, "parents", dev)
     if _list(children, "children", dev) != n:
         raise ValueError("parents and children differ in length")
-    status = _status(status, dev, stream)
-    workspace, ws, size = _pages_scratch(workspace, page_refs.shape[0], dev, stream)
+    status = _status(status, kv_lens, stream)
+    workspace, ws, size = _pages_scratch(workspace, kv_lens, page_refs.shape[0], stream)
     _call("zl_pages_fork", kv_lens.get_device(), stream, p, t, parents.data_ptr(), children.data_ptr(), n,
           status.data_ptr(), ws, size)
     return status
@@ -425,8 +422,8 @@ def pages_compact(cache, page_table, kv_lens, page_refs, live=None, workspace=No
     of cache [..., P, Hk, page, d].  Returns their number, a device int32 [1]."""
     t, dev = _tables(page_table, kv_lens, page_refs, cache.shape[-2] if cache.dim() >= 2 else 0)
     p = _pool(cache, page_refs.shape[0], dev)
-    live = _status(live, dev, stream)
-    workspace, ws, size = _pages_scratch(workspace, page_refs.shape[0], dev, stream)
+    live = _status(live, kv_lens, stream)
+    workspace, ws, size = _pages_scratch(workspace, kv_lens, page_refs.shape[0], stream)
     _call("zl_pages_compact", kv_lens.get_device(), stream, p, t, live.data_ptr(), ws, size)
     return live
 
