@@ -3,8 +3,9 @@
 //
 //     angle = pos * f,   (a, b) -> m (a cos - b sin, a sin + b cos)
 //
-// Memory-bound: every element is read and written once (90% of the measured copy
-// rate on the backward of 190,288 tokens x 80 heads, 97% on appended chunks), with three float32
+// Memory-bound: every element is read and written once (7.1 TB/s on the backward
+// of 190,288 tokens x 80 heads, 6.9 on the image mix's 28,672 x 48, where a
+// plain copy measures 6.8), with three float32
 // operations in between.  What would cost more than the traffic is the angle,
 // so a block computes the cosines and sines of its tokens once, into shared
 // memory, and all of their heads use them.  The angle itself is a 64-bit
@@ -16,8 +17,7 @@
 // A thread's unit is 16 columns for bf16, 8 for float32, as two 16-byte loads
 // and stores (the two halves' pieces, or two neighbours), so a head's units are
 // consecutive threads and a token's heads are one run.  Two units of a thread
-// are in flight, the first two while the block makes its cosines (one at a time
-// took 1,329 us on that backward).
+// are in flight, the first two while the block makes its cosines.
 // Plans whose pairs do not fill such units take units of one pair.
 #include "common.cuh"
 #include "paged.h"
@@ -28,7 +28,7 @@ namespace {
 __device__ uint32_t g_rope_err;
 
 constexpr int kRopeThreads = 256;
-constexpr int kTokensMax = 4;                  // tokens of a block
+constexpr int kTokensMax = 2;                  // tokens of a block (4: 1-2% slower, 8: 1-5%)
 
 template <typename T>
 struct Vec16;
@@ -66,6 +66,18 @@ __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// Where the cosine and sine of pair i stand in their row: units of N pairs are
+// read as 16-byte pieces (two pairs) by consecutive threads, whose pieces are
+// 8 N bytes apart; swizzled by the unit, eight threads' pieces fall into
+// different banks (unswizzled, conflicts filled two thirds of the cycles).
+template <int N>
+__device__ __forceinline__ int cs_at(int i) {
+  if constexpr (N == 1) return i;
+  const int unit = i / N, piece = i % N / 2;
+  const int swz = N == 8 ? (unit >> 1) & 3 : (unit >> 2) & 1;
+  return 2 * (unit * (N / 2) + (piece ^ swz)) + (i & 1);
+}
+
 // One unit of a head: N pairs turned, or 2N columns kept (past rot_dim).
 // Loading and finishing are apart, so that a thread has two units' loads in
 // flight.  VECTOR: N = 8 for bf16, 4 for float32; else one pair.
@@ -98,10 +110,10 @@ struct Unit {
         float u[N], v[N];
         Vec16<T>::unpack(x, u);
         Vec16<T>::unpack(y, v);
-        const float4* w4 = reinterpret_cast<const float4*>(cs + N * unit);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-          const float4 w = w4[i / 2];          // cos, sin of two pairs
+          // cos, sin of two pairs
+          const float4 w = *reinterpret_cast<const float4*>(cs + cs_at<N>(N * unit + i));
           if constexpr (INTERLEAVED) {
             // pairs i, i+1 of the unit: columns 2i .. 2i+3 of the 2N loaded ones
             float* z = 2 * i < N ? u + 2 * i : v + 2 * i - N;
@@ -132,9 +144,7 @@ struct Unit {
 };
 
 // SEQS: sequences of an append's parameters; 0: no append.
-// Five blocks an SM: of 4, 5 and 6 the fastest on both large cases (backward of
-// 190,288 tokens x 80 heads 1,285, 1,277 and 1,349 us; chunks appended 172, 167
-// and 176 us).
+// Five blocks an SM: 1,097 us on that backward, 6 blocks 1,117, 4 the same.
 template <typename T, bool VECTOR, bool INTERLEAVED, int SEQS>
 __global__ void __launch_bounds__(kRopeThreads, 5)
 rope_kernel(const __grid_constant__ RopeArgs<SEQS> a, int tokens_per_block, int heads_per_block) {
@@ -236,7 +246,7 @@ rope_kernel(const __grid_constant__ RopeArgs<SEQS> a, int tokens_per_block, int 
     float s, c;
     sincospif(x2, &s, &c);
     const float m = a.rope.magnitude;
-    cs[tp][i] = make_float2(c * m, (a.inverse ? -s : s) * m);
+    cs[tp][cs_at<U::N>(i)] = make_float2(c * m, (a.inverse ? -s : s) * m);
   }
   __syncthreads();
   while (has0) {                               // units come in order: no u1 without a u0
