@@ -95,6 +95,7 @@ class ZlError(RuntimeError):
 
 
 _lib = None
+_bind = None
 
 
 def load() -> ctypes.CDLL:
@@ -174,6 +175,20 @@ def load() -> ctypes.CDLL:
     return lib
 
 
+def bind():
+    """The compiled binding (binding/bind.cpp), on top of the library."""
+    global _bind
+    if _bind is None:
+        load()
+        try:
+            from . import _bind as module
+        except ImportError as e:
+            raise RuntimeError(f"{PKG}/_bind.so is missing or does not fit this PyTorch: run "
+                               "`python -m mixed_length_dit_gb300.build --force`") from e
+        _bind = module
+    return _bind
+
+
 def status_string(status: int) -> str:
     return load().zl_status_string(int(status)).decode()
 
@@ -186,10 +201,11 @@ def check(status: int, where: str) -> None:
 class HostInt32:
     """A host int32 array made once and passed to many calls (the cu_seqlens
     of a batch that every layer shares)."""
-    __slots__ = ("array", "n", "last")
+    __slots__ = ("array", "n", "last", "address")
 
     def __init__(self, values):
         self.array, self.n = int32_array(values)
+        self.address = ctypes.addressof(self.array)
         self.last = int(self.array[self.n - 1]) if self.n else None
 
     def __len__(self):

@@ -42,6 +42,25 @@ def _cu(values):
     return values
 
 
+def _short(name, *args):
+    """The call by the compiled binding, if all is as it should be: its result;
+    None if the long way has to be taken."""
+    r = getattr(_lib._bind or _lib.bind(), name)(*args)
+    if type(r) is int:
+        _lib.check(r, "zl_" + _NAMES[name])
+    return r
+
+
+_NAMES = {"rope": "rope", "append": "paged_append", "attn": "paged_attn", "extend": "pages_extend",
+          "fork": "pages_fork", "compact": "pages_compact"}
+
+
+def _int32(value, name):
+    """ctypes keeps the low 32 bits of a larger number."""
+    if not -2**31 <= value < 2**31:
+        raise ValueError(f"{name} must fit 32 bits, got {value}")
+
+
 def _call(name, index, stream, *args):
     """Calls the library with the device `index` of the call's tensors as the
     current one (its launches go there) and that device's current stream."""
@@ -123,6 +142,7 @@ class RopePlan:
         _lib.check(_lib.load().zl_rope_init(ctypes.byref(self.struct), self.head_dim, int(bool(interleaved)), n, arr,
                                             float(base), float(factor), ramp_arr, float(magnitude)), "zl_rope_init")
         self.ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
 
 def _positions(positions, plan, tokens, device):
@@ -210,12 +230,20 @@ def rope_fwd(q, k, positions, plan, q_out=None, k_out=None, stream=None):
     """Turns q [T, Hq, d] and k [T, Hk, d] (or None) by their tokens' positions
     (int32 [T], or [n_axes, T]).  Returns (q_out, k_out); an output may be its
     own input."""
+    if stream is None and q_out is None and k_out is None:
+        r = _short("rope", False, q, k, positions, plan.address, plan.n_axes, plan.head_dim)
+        if r is not None:
+            return r
     return _rope("zl_rope_fwd", q, k, positions, plan, q_out, k_out, stream)
 
 
 def rope_bwd(dq, dk, positions, plan, dq_out=None, dk_out=None, stream=None):
     """Gradient of rope_fwd: from the gradients of its outputs to those of its
     inputs.  Returns (dq_out, dk_out)."""
+    if stream is None and dq_out is None and dk_out is None:
+        r = _short("rope", True, dq, dk, positions, plan.address, plan.n_axes, plan.head_dim)
+        if r is not None:
+            return r
     return _rope("zl_rope_bwd", dq, dk, positions, plan, dq_out, dk_out, stream)
 
 
@@ -247,6 +275,11 @@ def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None
     RopePlan the keys (and q [T, H, d], if given) are turned at their cache
     positions, or at `positions`.  Returns the turned q (or None)."""
     cu = _cu(cu_seqlens)
+    if stream is None and q_out is None and positions is None:
+        r = _short("append", k, v, k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last, q,
+                   0 if rope is None else rope.address)
+        if r is not None:
+            return r[0]
     cache, nk, hd = _cache(k_pages, v_pages, page_table, kv_lens, cu.n - 1)
     tokens, dev = cu.last, k_pages.device
     ks = _rows(k, "k", tokens, nk, hd, _BF16, dev)
@@ -281,6 +314,7 @@ def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None
 def paged_attn_workspace_bytes(cu_seqlens_q, max_kv_len, num_heads, num_kv_heads, head_dim) -> int:
     lib = _lib.load()
     cu = _cu(cu_seqlens_q)
+    _int32(max_kv_len, "max_kv_len")
     out = ctypes.c_size_t(0)
     _lib.check(lib.zl_paged_attn_workspace_size(cu.array, cu.n - 1, max_kv_len, num_heads, num_kv_heads, head_dim,
                                                 ctypes.byref(out)), "zl_paged_attn_workspace_size")
@@ -293,6 +327,13 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, max_kv_le
     keys and values.  The queries stand at the last positions below kv_lens;
     max_kv_len (host) bounds kv_lens.  Returns (o [Tq, H, d], lse [H, Tq])."""
     cu = _cu(cu_seqlens_q)
+    if stream is None:
+        r = _short("attn", q, k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last, max_kv_len, causal,
+                   window, softmax_scale, out, lse, workspace)
+        if r is not None:
+            return r
+    _int32(max_kv_len, "max_kv_len")
+    _int32(window, "window")
     cache, nk, hd = _cache(k_pages, v_pages, page_table, kv_lens, cu.n - 1)
     if q.dim() != 3:
         raise ValueError("q must be [Tq, H, d]")
@@ -326,6 +367,7 @@ def _tables(page_table, kv_lens, page_refs, page_size):
     """The checked zl_page_tables_t, and the device."""
     if page_table.dim() != 2 or page_refs.dim() != 1:
         raise ValueError("page_table must be [S, cols] and page_refs [P]")
+    _int32(page_size, "page_size")
     dev = page_table.device
     slots, cols = page_table.shape
     pages = page_refs.shape[0]
@@ -376,6 +418,7 @@ def _pages_scratch(workspace, like, num_pages, stream):
 
 
 def pages_workspace_bytes(num_pages) -> int:
+    _int32(num_pages, "num_pages")
     out = ctypes.c_size_t(0)
     _lib.check(_lib.load().zl_pages_workspace_size(num_pages, ctypes.byref(out)), "zl_pages_workspace_size")
     return int(out.value)
@@ -386,6 +429,10 @@ def pages_extend(page_table, kv_lens, page_refs, counts, page_size, status=None,
     place: kv_lens grows, free pages (lowest first) enter the rows.  Returns a
     device int32 [1]: 0, or the pages lacking, or -1 for counts that are
     negative or do not fit a row; unless it is 0 nothing was changed."""
+    if stream is None and status is None:
+        r = _short("extend", page_table, kv_lens, page_refs, counts, page_size)
+        if r is not None:
+            return r
     t, dev = _tables(page_table, kv_lens, page_refs, page_size)
     _exact(counts, "counts", kv_lens.shape, _I32, dev)
     status = _status(status, kv_lens, stream)
@@ -398,6 +445,10 @@ def pages_fork(cache, page_table, kv_lens, page_refs, parents, children, status=
     device), in place: full pages are shared, a part-filled last page is copied
     in every group of cache [..., P, Hk, page, d].  Returns a device int32 [1]
     as pages_extend does."""
+    if stream is None and status is None and workspace is not None:
+        r = _short("fork", cache, page_table, kv_lens, page_refs, parents, children, workspace)
+        if r is not None:
+            return r
     t, dev = _tables(page_table, kv_lens, page_refs, cache.shape[-2] if cache.dim() >= 2 else 0)
     p = _pool(cache, page_refs.shape[0], dev)
     n = _list(parents, "parents", dev)
@@ -420,6 +471,10 @@ def pages_free(page_table, kv_lens, page_refs, slots, page_size, stream=None):
 def pages_compact(cache, page_table, kv_lens, page_refs, live=None, workspace=None, stream=None):
     """Moves the used pages to the front of the pool, in place, in every group
     of cache [..., P, Hk, page, d].  Returns their number, a device int32 [1]."""
+    if stream is None and live is None and workspace is not None:
+        r = _short("compact", cache, page_table, kv_lens, page_refs, workspace)
+        if r is not None:
+            return r
     t, dev = _tables(page_table, kv_lens, page_refs, cache.shape[-2] if cache.dim() >= 2 else 0)
     p = _pool(cache, page_refs.shape[0], dev)
     live = _status(live, kv_lens, stream)

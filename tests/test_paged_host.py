@@ -370,3 +370,44 @@ def test_oracle_pages_facts():
     assert p.extend([33, 0, 0]) == 0 and p.table[0] == [3, 4, 5]
     p.release([1])
     assert p.compact() == 5 and p.table[0] == [3, 4, 0]
+
+
+def test_numbers_past_32_bits_are_refused():
+    # ctypes would keep their low bits: a window of 2**32 + 5 would be one of 5
+    k, v, t, n = (torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16), torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16),
+                  torch.zeros(1, 2, dtype=torch.int32), torch.ones(1, dtype=torch.int32))
+    q = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="window"):
+        zl.paged_attn(q, k, v, t, n, [0, 1], 16, window=2**32 + 5)
+    with pytest.raises(ValueError, match="max_kv_len"):
+        zl.paged_attn(q, k, v, t, n, [0, 1], 2**32 + 16)
+    with pytest.raises(ValueError, match="max_kv_len"):
+        zl.paged_attn_workspace_bytes([0, 1], 2**32 + 16, 1, 1, 64)
+    with pytest.raises(ValueError, match="page_size"):
+        zl.pages_extend(t, n, torch.zeros(2, dtype=torch.int32), n, 2**32 + 16)
+    with pytest.raises(ValueError, match="num_pages"):
+        zl.pages_workspace_bytes(2**32 + 1)
+
+
+def test_compiled_binding_leaves_unusual_calls_alone():
+    """It does nothing with what is not as it should be: the long way says why."""
+    b = zl._lib.bind()
+    cpu = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    pages, i1, i2 = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16), torch.ones(1, dtype=torch.int32), torch.zeros(
+        1, 2, dtype=torch.int32)
+    plan, cu = zl.RopePlan(64), zl.host_int32([0, 1])
+    good = {
+        "rope": [False, cpu, None, i1, plan.address, 1, 64],
+        "append": [cpu, cpu, pages, pages, i2, i1, cu.address, 2, 1, None, 0],
+        "attn": [cpu, pages, pages, i2, i1, cu.address, 2, 1, 16, True, 0, None, None, None, None],
+        "extend": [i2, i1, i1, i1, 16],
+        "fork": [pages, i2, i1, torch.zeros(2, dtype=torch.int32), i1, i1, i1],
+        "compact": [pages, i2, i1, torch.zeros(2, dtype=torch.int32), i1],
+    }
+    for name, args in good.items():
+        fn = getattr(b, name)
+        assert fn(*args) is None                  # tensors of the CPU
+        assert fn() is None and fn(*args[:-1]) is None and fn(*args, 1) is None
+        for i in range(len(args)):
+            for bad in (None, "x", 2**80, 1.5, torch.zeros(0), [1]):
+                assert fn(*args[:i], bad, *args[i + 1:]) is None
