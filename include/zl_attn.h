@@ -590,6 +590,15 @@ zl_status zl_pages_fork(const zl_page_pool_t* pool, const zl_page_tables_t* tabl
 zl_status zl_pages_free(const zl_page_tables_t* tables, const int32_t* slots, int32_t n, void* stream);
 
 /*
+ * Shortens every slot that is longer than lens[s] (device, >= 0) to it, as when
+ * drafted tokens are taken back: the pages behind lose a reference, their table
+ * entries become -1.  (A caller that only lowered kv_lens would lose those
+ * pages.)  A slot cut inside a page that another slot holds too must not be
+ * appended to before it has a copy of its own, as a fork makes one.
+ */
+zl_status zl_pages_truncate(const zl_page_tables_t* tables, const int32_t* lens, void* stream);
+
+/*
  * Packs the pool: with L pages in use, those numbered L and up move to the
  * free pages below L (both in ascending order), in every group of the pool,
  * and the tables and counts follow.  *live (device) = L.

@@ -11,6 +11,6 @@ from .attention import (  # noqa: F401
 )
 from .paged import (  # noqa: F401
     RopePlan, host_int32, paged_append, paged_attn, paged_attn_workspace_bytes, pages_compact, pages_copy, pages_extend,
-    pages_fork, pages_free, pages_workspace_bytes, rope_bwd, rope_fwd,
+    pages_fork, pages_free, pages_truncate, pages_workspace_bytes, rope_bwd, rope_fwd,
 )
 from ._lib import ZlError, load  # noqa: F401

@@ -33,7 +33,7 @@ EXPORTS = (
     "zl_varlen_attn_fwd_ex", "zl_lse_merge_ex", "zl_varlen_attn_fwd_schedule", "zl_varlen_attn_bwd_schedule",
     "zl_selftest_wait_timeout", "zl_rope_init", "zl_rope_fwd", "zl_rope_bwd", "zl_paged_append",
     "zl_paged_attn_workspace_size", "zl_paged_attn", "zl_pages_workspace_size", "zl_pages_extend", "zl_pages_fork",
-    "zl_pages_free", "zl_pages_compact", "zl_pages_copy",
+    "zl_pages_free", "zl_pages_truncate", "zl_pages_compact", "zl_pages_copy",
 )
 
 ZL_FWD_FUSED_MERGE = 1
@@ -167,6 +167,7 @@ def load() -> ctypes.CDLL:
     lib.zl_pages_extend.argtypes = [tabp, vp, vp, vp]
     lib.zl_pages_fork.argtypes = [poolp, tabp, vp, vp, c_i32, vp, vp, c_sz, vp]
     lib.zl_pages_free.argtypes = [tabp, vp, c_i32, vp]
+    lib.zl_pages_truncate.argtypes = [tabp, vp, vp]
     lib.zl_pages_compact.argtypes = [poolp, tabp, vp, vp, c_sz, vp]
     lib.zl_pages_copy.argtypes = [poolp, vp, vp, c_i32, vp]
     for name in EXPORTS[-12:]:

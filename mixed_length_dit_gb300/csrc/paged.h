@@ -168,6 +168,7 @@ cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const in
                               cudaStream_t stream);
 cudaError_t launch_pages_extend(const PageTable& t, const int32_t* counts, int32_t* status, cudaStream_t stream);
 cudaError_t launch_pages_free(const PageTable& t, const int32_t* slots, int32_t n, cudaStream_t stream);
+cudaError_t launch_pages_truncate(const PageTable& t, const int32_t* lens, cudaStream_t stream);
 cudaError_t launch_pages_fork_plan(const PageTable& t, const int32_t* parents, const int32_t* children, int32_t n,
                                    int32_t* ws, int32_t* status, cudaStream_t stream);
 cudaError_t launch_pages_fork_move(const PagePool& pool, const PageTable& t, const int32_t* parents,

@@ -512,6 +512,19 @@ zl_status zl_pages_free(const zl_page_tables_t* tables, const int32_t* slots, in
   return launch_counted("pages_free", s, [&] { return zl::launch_pages_free(t, slots, n, s); });
 }
 
+zl_status zl_pages_truncate(const zl_page_tables_t* tables, const int32_t* lens, void* stream) {
+  zl::PageTable t;
+  zl_status st = check_tables(tables, &t);
+  if (st != ZL_OK) return st;
+  if (!lens) return ZL_EINVAL;
+  if (misaligned4(lens)) return ZL_EALIGN;
+  int sms = 0;
+  st = device_sms(&sms);
+  if (st != ZL_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return launch_counted("pages_truncate", s, [&] { return zl::launch_pages_truncate(t, lens, s); });
+}
+
 zl_status zl_pages_compact(const zl_page_pool_t* pool, const zl_page_tables_t* tables, int32_t* live, void* workspace,
                            size_t workspace_bytes, void* stream) {
   zl::PageTable t;

@@ -468,6 +468,14 @@ def pages_free(page_table, kv_lens, page_refs, slots, page_size, stream=None):
     _call("zl_pages_free", kv_lens.get_device(), stream, t, slots.data_ptr(), n)
 
 
+def pages_truncate(page_table, kv_lens, page_refs, lens, page_size, stream=None):
+    """Shortens every slot that is longer than lens[s] (int32, device) to it, in
+    place, as when drafted tokens are taken back; the pages behind are freed."""
+    t, dev = _tables(page_table, kv_lens, page_refs, page_size)
+    _exact(lens, "lens", kv_lens.shape, _I32, dev)
+    _call("zl_pages_truncate", kv_lens.get_device(), stream, t, lens.data_ptr())
+
+
 def pages_compact(cache, page_table, kv_lens, page_refs, live=None, workspace=None, stream=None):
     """Moves the used pages to the front of the pool, in place, in every group
     of cache [..., P, Hk, page, d].  Returns their number, a device int32 [1]."""

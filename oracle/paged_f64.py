@@ -186,6 +186,13 @@ class Pages:
                 self.table[s][j] = -1
             self.lens[s] = 0
 
+    def truncate(self, lens):
+        for s, n in enumerate(lens):
+            for j in range(self.used(n), self.used(self.lens[s])):
+                self.refs[self.table[s][j]] -= 1
+                self.table[s][j] = -1
+            self.lens[s] = min(self.lens[s], n)
+
     def compact(self):
         live = sum(r > 0 for r in self.refs)
         holes = [p for p in range(live) if self.refs[p] == 0]

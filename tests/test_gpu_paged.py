@@ -494,3 +494,49 @@ def test_generation_loop():
     for s in range(slots):
         assert table[s, :host.used(host.lens[s])].tolist() == host.table[s][:host.used(host.lens[s])]
     step([17, 1, 1, 1, 1, 40])
+
+
+def test_drafts_taken_back_leave_what_was_never_drafted():
+    """Drafted tokens appended, attended to, and in part taken back: the cache
+    goes on as if only the accepted ones had been there, bit for bit."""
+    page, hd, heads, kv, slots, pages = 16, 128, 8, 2, 3, 40
+    g = torch.Generator(device="cuda").manual_seed(41)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    plan = zl.RopePlan(hd)
+    rand = lambda n, h: torch.randn((n, h, hd), generator=g, device="cuda").to(BF16)
+
+    class Cache:
+        def __init__(self):
+            self.kv = torch.zeros((2, pages, kv, page, hd), dtype=BF16, device="cuda")
+            self.table = torch.full((slots, 12), -1, dtype=torch.int32, device="cuda")
+            self.lens, self.refs = i32([0] * slots), i32([0] * pages)
+
+        def step(self, q, k, v, cu):
+            counts = [b - a for a, b in zip(cu, cu[1:])]
+            assert int(zl.pages_extend(self.table, self.lens, self.refs, i32(counts), page)) == 0
+            qr = zl.paged_append(k, v, self.kv[0], self.kv[1], self.table, self.lens, cu, q=q, rope=plan)
+            return zl.paged_attn(qr, self.kv[0], self.kv[1], self.table, self.lens, cu, 12 * page)
+
+    drafted, plain = Cache(), Cache()
+    start = [30, 16, 47]
+    cu = [0, 30, 46, 93]
+    first = rand(93, heads), rand(93, kv), rand(93, kv)
+    for c in (drafted, plain):
+        c.step(*first, cu)
+    for accepted in ([0, 1, 4], [5, 0, 2], [1, 1, 1]):
+        q, k, v = rand(15, heads), rand(15, kv), rand(15, kv)
+        drafted.step(q, k, v, [0, 5, 10, 15])
+        start = [n + a for n, a in zip(start, accepted)]
+        zl.pages_truncate(drafted.table, drafted.lens, drafted.refs, i32(start), page)
+        rows = [5 * s + i for s in range(slots) for i in range(accepted[s])]
+        cu = [0]
+        for a in accepted:
+            cu.append(cu[-1] + a)
+        plain.step(q[rows], k[rows], v[rows], cu)
+        assert drafted.lens.tolist() == plain.lens.tolist() == start
+        assert int(drafted.refs.sum()) == int(plain.refs.sum())
+        q, k, v = rand(slots, heads), rand(slots, kv), rand(slots, kv)
+        o, o2 = (c.step(q, k, v, [0, 1, 2, 3]) for c in (drafted, plain))
+        zl.sync_check()
+        start = [n + 1 for n in start]
+        assert torch.equal(o[0], o2[0]) and torch.equal(o[1], o2[1])

@@ -217,3 +217,48 @@ def test_a_captured_loop():
         assert b.m.extend([3, 1, 0, 2]) == int(status[1]) == 0
         b.m.release([3, 2])
         b.same()
+
+
+@pytest.mark.parametrize("page,slots", [(16, 5), (32, 300), (256, 8)])
+def test_truncate(page, slots):
+    rng = np.random.default_rng(page)
+    cols = 300 if slots == 5 else 7            # of 300 pages some threads take two
+    b = Both([int(x) for x in rng.integers(0, cols * page, slots - 1)] + [0], cols * slots, page, cols)
+    for most in (cols * page, cols * page // 2, 2 * page, page, 1, 0):
+        keep = [int(x) for x in rng.integers(0, most + 1, slots)]
+        zl.pages_truncate(b.table, b.lens, b.refs, i32(keep), page)
+        b.m.truncate(keep)
+        b.same()
+        assert sum(b.m.refs) == sum(b.m.used(n) for n in b.m.lens)   # no page is lost
+        counts = [int(x) for x in rng.integers(0, page, slots)]
+        assert int(zl.pages_extend(b.table, b.lens, b.refs, i32(counts), page)) == b.m.extend(counts)
+        b.same()
+
+
+def test_truncate_shared_pages_bad_lengths_and_graphs():
+    b = Both([70, 16, 8], 30, 16, 6, spare_slots=3)
+    zl.pages_fork(b.cache, b.table, b.lens, b.refs, i32([0, 0]), i32([3, 4]))
+    b.m.fork([0, 0], [3, 4])
+    keep = i32([32, 99, 0, 33, 70, 5])
+    before = [x.clone() for x in (b.table, b.lens, b.refs)]
+    zl.pages_truncate(b.table, b.lens, b.refs, keep, 16)
+    b.m.truncate(keep.tolist())
+    b.same()
+    want = [x.clone() for x in (b.table, b.lens, b.refs)]
+    for x, y in zip((b.table, b.lens, b.refs), before):
+        x.copy_(y)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        zl.pages_truncate(b.table, b.lens, b.refs, keep, 16)
+    for _ in range(2):                         # the second finds nothing left to do
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((b.table, b.lens, b.refs), want))
+    # a negative length is flagged, and leaves its slot alone
+    zl.pages_truncate(b.table, b.lens, b.refs, i32([-1, 16, 0, 0, 70, 0]), 16)
+    b.m.truncate([32, 16, 0, 0, 70, 0])
+    with pytest.raises(zl.ZlError) as e:
+        b.same()
+    assert e.value.status == -8
+    b.same()

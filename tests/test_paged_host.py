@@ -411,3 +411,18 @@ def test_compiled_binding_leaves_unusual_calls_alone():
         for i in range(len(args)):
             for bad in (None, "x", 2**80, 1.5, torch.zeros(0), [1]):
                 assert fn(*args[:i], bad, *args[i + 1:]) is None
+
+
+@pytest.mark.parametrize("fault,status", [
+    (dict(page_size=24), _lib.ZL_EUNSUPPORTED), (dict(slots=0), _lib.ZL_EINVAL), (dict(page_refs=0), _lib.ZL_EINVAL),
+    (dict(kv_lens=65), _lib.ZL_EALIGN), (dict(table_cols=1 << 28), _lib.ZL_EINVAL),
+])
+def test_truncate_refusals(lib, fault, status):
+    assert lib.zl_pages_truncate(ctypes.byref(_tables(**fault)), P64, None) == status
+    assert lib.zl_pages_truncate(None, P64, None) == _lib.ZL_EINVAL
+    assert lib.zl_pages_truncate(ctypes.byref(_tables()), None, None) == _lib.ZL_EINVAL
+    assert lib.zl_pages_truncate(ctypes.byref(_tables()), 66, None) == _lib.ZL_EALIGN
+    with pytest.raises(ValueError, match="lens"):
+        zl.pages_truncate(_i(3, 4), _i(3), _i(20), _i(2), 16)
+    with pytest.raises(ValueError, match="CUDA"):
+        zl.pages_truncate(_i(3, 4), _i(3), _i(20), _i(3), 16)
