@@ -370,9 +370,10 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x) {
 // The blocks of all units (sequence, key head, query tiles) stand in one line,
 // each unit's behind a gap of its item cost, and the line is cut into equal
 // pieces, one per CTA: every SM has the same work whatever the lengths, and only
-// units that a cut goes through are joined afterwards.  A CTA's piece of the unit that its range starts inside
-// goes to slot 2c, of the unit that goes on behind its range to 2c + 1, and
-// joins[c] tells the join what begins in slot 2c + 1.
+// units that a cut goes through are joined afterwards.  A CTA's piece of the
+// unit that its range starts inside goes to slot 2c, of the unit that goes on
+// behind its range to 2c + 1, and joins[c] tells the join what begins in slot
+// 2c + 1.
 template <int HD, bool PAIR, int N>
 __device__ void produce(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps) {
   const int lane = threadIdx.x & 31;
