@@ -794,7 +794,7 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
     }
     if (!has) continue;
     // ---------------------------------------------------------- epilogue
-    const bool seen = l_run > 0.f;
+    const bool seen = l_run != 0.f;             // (a NaN is handed on)
     const float inv_l = seen ? 1.f / l_run : 0.f;
     const float lse = seen ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
     const int h = w.hk * a.group + row_head;
@@ -915,11 +915,13 @@ __device__ __forceinline__ bool join_parts(PagedSmem<HD, false>* sm, const Paged
   for (int i = 1; i < kParts; ++i) m_all = fmaxf(m_all, v[i].x);
   float l_all = 0.f;
 #pragma unroll
-  for (int i = 0; i < kParts; ++i) l_all += v[i].x == -INFINITY ? 0.f : v[i].y * fast_exp2(v[i].x - m_all);
-  const float scale = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_all) / l_all;
+  for (int i = 0; i < kParts; ++i) l_all += v[i].y == 0.f ? 0.f : v[i].y * fast_exp2(v[i].x - m_all);
+  // a part has seen something if its sum is not zero; one of NaN (whose maximum
+  // may be -inf: NaN scores do not raise it) makes the row NaN
+  const float scale = l_run == 0.f ? 0.f : fast_exp2(m_run - m_all) / l_all;
   if (t == 0 && row < kSpan && r < rows) {       // the first copy's threads know the row's LSE
     const int tok = a.row_token(r), h = w.hk * a.group + r - tok * a.group;
-    const float lse = l_all > 0.f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
+    const float lse = l_all != 0.f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
     if (w.final)
       a.lse[static_cast<int64_t>(h) * a.lse_stride + w.q_row0 + tok] = lse;
     else
@@ -1192,10 +1194,14 @@ __device__ __forceinline__ void join_row(const PagedAttnHead& a, int n, F part, 
   for (int i = threadIdx.x; i < n; i += kJoinThreads) lse_s[i] = a.lse_part[part(i)];
   __syncthreads();
   float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, lse_s[i]);
+  bool any = false;                            // a part that has seen a key, or is NaN
+  for (int i = lane; i < n; i += 32) {
+    any = any || lse_s[i] != -INFINITY;
+    m = fmaxf(m, lse_s[i]);
+  }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  const bool seen = m != -INFINITY;
+  const bool seen = __any_sync(0xffffffffu, any);
   float sum = 0.f;
   for (int i = lane; i < n; i += 32) sum += seen ? expf(lse_s[i] - m) : 0.f;
 #pragma unroll
@@ -1257,7 +1263,7 @@ __device__ __forceinline__ void join_row_warp(const PagedAttnHead& a, int n, F p
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = fmaf(wgt, x[i][c], acc[c]);
   }
-  const bool seen = m != -INFINITY;
+  const bool seen = sum != 0.f;                // (a NaN is handed on)
   const float inv = seen ? 1.f / sum : 0.f;
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + o_row * HD + lane * C;
   if constexpr (C == 4)

@@ -540,3 +540,32 @@ def test_drafts_taken_back_leave_what_was_never_drafted():
         zl.sync_check()
         start = [n + 1 for n in start]
         assert torch.equal(o[0], o2[0]) and torch.equal(o[1], o2[1])
+
+
+@pytest.mark.parametrize("new,lens,heads,kv_heads,hd", [
+    ([1, 1], [40, 300], 8, 2, 128), ([12, 3], [200, 90], 10, 2, 64), ([100], [260], 1, 1, 128), ([300, 70], [300, 900], 4, 2, 64),
+    ([1], [20000], 6, 2, 128), ([150], [9000], 2, 1, 64),
+])
+def test_nan_is_handed_on(new, lens, heads, kv_heads, hd):
+    """A query or a visible key of NaN makes its rows NaN, as the formula does,
+    and no other row's bits change."""
+    b = Batch(new, lens, heads, kv_heads, hd, 16, seed=11)
+    o1, l1 = b.run()
+    q = b.q.clone()
+    rows = [0, b.cu[-1] - 1]
+    q[rows, heads - 1, 3] = float("nan")
+    o2, l2 = b.run(q=q)
+    nan = torch.zeros((b.cu[-1], heads), dtype=torch.bool, device="cuda")
+    nan[rows, heads - 1] = True
+    for hit, o, lse in ((nan, o2, l2),):
+        assert o[hit].isnan().all() and lse.T[hit].isnan().all()
+        assert torch.equal(o[~hit], o1[~hit]) and torch.equal(lse.T[~hit], l1.T[~hit])
+    # the last sequence's newest key: its last query alone sees it
+    s, n = len(lens) - 1, lens[-1]
+    b.k_pages[int(b.table[s, (n - 1) // 16]), 0, (n - 1) % 16, 0] = float("nan")
+    o3, l3 = b.run()
+    zl.sync_check()
+    nan[:] = False
+    nan[-1, :heads // kv_heads] = True
+    assert o3[nan].isnan().all() and l3.T[nan].isnan().all()
+    assert torch.equal(o3[~nan], o1[~nan]) and torch.equal(l3.T[~nan], l1.T[~nan])
