@@ -391,8 +391,9 @@ zl_status zl_varlen_attn_bwd_static(
  *
  * so that with a ramp the pairs that turn more than `high` times over
  * `length` positions keep their frequency and those that turn less than `low`
- * times take the scaled one.  Angles are exact to 2^-31 of a turn at every
- * int32 position (fixed-point fractions of a turn), positions may be negative.
+ * times take the scaled one.  Frequencies are rounded to float64 once; beside
+ * that, angles are exact to 2^-31 of a turn at every int32 position
+ * (fixed-point fractions of a turn).  Positions may be negative.
  */
 #define ZL_ROPE_MAX_PAIRS 64
 #define ZL_ROPE_MAX_AXES 4
