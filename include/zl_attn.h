@@ -526,9 +526,10 @@ zl_status zl_paged_attn_workspace_size(const int32_t* cu_seqlens_q, int32_t num_
  * product of zero and infinity would reach queries that do not see them (its
  * keys may be anything where the mask hides them, and rows past its length
  * anything at all).  The work is spread over the SMs in equal shares whatever
- * the lengths; results are the same on every run with the same lengths.  Two
+ * the lengths (short ones, by max_kv_len and the window, are left whole); results
+ * are the same on every run with the same lengths and arguments.  One or two
  * launches per 640 sequences of one query tile (up to 128 / (num_heads /
- * num_kv_heads) queries) and two per 640 longer ones.
+ * num_kv_heads) queries) and one or two per 640 longer ones.
  */
 zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_stride, const int32_t* cu_seqlens_q,
                         int32_t num_seqs, int32_t max_kv_len, int32_t num_heads, float softmax_scale, int32_t causal,

@@ -31,7 +31,7 @@
 //               2^8
 //   warp 8      producer: all lanes fetch page numbers, each lane issues the
 //               TMA box of its page.  The items are the CTA's equal share of
-//               all key blocks of the call
+//               all key blocks of the call, or, of few short units, one whole
 //   warps 9,10  MMA issuers (S = Q K^T, O += P V) of group t
 //   warp 11     brings the queries, and clears what a sequence's last V block
 //               holds past its length (unwritten rows may be NaN, and 0 * NaN
@@ -367,9 +367,30 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x) {
   return x;
 }
 
-// The blocks of all units (sequence, key head, query tiles) stand in one line,
-// each unit's behind a gap of its item cost, and the line is cut into equal
-// pieces, one per CTA: every SM has the same work whatever the lengths, and only
+// A launch of few units with few blocks each: CTA c takes the c-th whole, and
+// neither the sums before nor the join behind it is needed.
+template <int HD, bool PAIR, int N>
+__device__ void produce_whole(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps) {
+  const int nk = a.num_kv_heads;
+  int seg = 0, x = blockIdx.x;
+  if constexpr (PAIR) {
+    for (; x >= units_of<true>(a, a.segs[seg].q_len) * nk; ++seg) x -= units_of<true>(a, a.segs[seg].q_len) * nk;
+  } else {
+    seg = x / nk;
+    x -= seg * nk;
+  }
+  const int unit = x / nk, len = length_of(a, seg);
+  const Range r = unit_blocks<PAIR>(a, len, a.segs[seg].q_len, PAIR ? 2 * unit : 0);
+  const Item item = {seg, len, x - unit * nk, PAIR ? 2 * unit : 0, r.b0, max(r.b0, r.b1), -1};
+  if (!publish(sm, 0, item)) return;
+  uint32_t uses0 = 0, uses1 = 0;
+  if (!load_blocks<HD, PAIR, N>(sm, a, maps, decode<PAIR>(a, item), uses0, uses1)) return;
+  publish(sm, 1, Item{-1, 0, 0, 0, 0, 0, -1});
+}
+
+// Otherwise the blocks of all units (sequence, key head, query tiles) stand in
+// one line, each unit's behind a gap of its item cost, and the line is cut into
+// equal pieces, one per CTA: every SM has the same work whatever the lengths, and only
 // units that a cut goes through are joined afterwards.  A CTA's piece of the
 // unit that its range starts inside goes to slot 2c, of the unit that goes on
 // behind its range to 2c + 1, and joins[c] tells the join what begins in slot
@@ -1107,7 +1128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttnArgs<N> args) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   auto* sm = reinterpret_cast<PagedSmem<HD, PAIR>*>(smem_raw);
-  if (threadIdx.x == 0) args.joins[blockIdx.x].last = -1;   // also when this CTA gives up a wait
+  if (args.whole == 0 && threadIdx.x == 0) args.joins[blockIdx.x].last = -1;   // also when this CTA gives up a wait
   if ((smem_u32(smem_raw) & 1023u) != 0) {       // the declared alignment; the swizzle needs it
     if (threadIdx.x == 0) atomicOr(&g_paged_err, ERR_BAD_WORK);
     return;
@@ -1139,7 +1160,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
     tmem_alloc(&sm->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  sum_blocks<HD, PAIR, N>(sm, args);
+  if (args.whole == 0) sum_blocks<HD, PAIR, N>(sm, args);
   // the join may be set up from here on; it waits for this grid's end itself
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
@@ -1153,7 +1174,8 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
     // spills, or not, with any change of the code around it).
     if constexpr (PAIR) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kProducerWarp) {
-      produce<HD, PAIR, N>(sm, args, maps);
+      if (args.whole > 0) produce_whole<HD, PAIR, N>(sm, args, maps);
+      else produce<HD, PAIR, N>(sm, args, maps);
     } else if (warp == kAuxWarp) {
       assist<HD, PAIR, N>(sm, args, maps);
     } else {
@@ -1274,19 +1296,80 @@ __device__ __forceinline__ void join_row_warp(const PagedAttnHead& a, int n, F p
   if (lane == 0) *lse_out = seen ? m + logf(sum) : -INFINITY;
 }
 
+// And for many parts: the lanes take the parts' lse, then the warp goes through
+// them with kManyLoads rows in flight.  (A block to a row, for hundreds of rows,
+// took twice as long as the attention: 35 us for 200 queries over 1,536 keys.)
+constexpr int kManyLoads = 8;
+template <int HD, typename F>
+__device__ __forceinline__ void join_row_many(const PagedAttnHead& a, int n, F part, int64_t o_row, float* lse_out) {
+  constexpr int C = HD / 32;
+  constexpr int kLane = (kMaxParts + 31) / 32;
+  const int lane = threadIdx.x & 31;
+  float l[kLane], m = -INFINITY, sum = 0.f;
+  bool any = false;
+#pragma unroll
+  for (int k = 0; k < kLane; ++k) {
+    const int i = 32 * k + lane;
+    l[k] = i < n ? a.lse_part[part(i)] : -INFINITY;
+    any = any || l[k] != -INFINITY;
+    m = fmaxf(m, l[k]);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const bool seen = __any_sync(0xffffffffu, any);
+#pragma unroll
+  for (int k = 0; k < kLane; ++k) {
+    l[k] = l[k] == -INFINITY ? 0.f : expf(l[k] - m);             // the part's weight
+    sum += l[k];
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  float acc[C] = {};
+#pragma unroll
+  for (int k = 0; k < kLane; ++k) {
+    for (int i0 = 32 * k; i0 < min(n, 32 * k + 32); i0 += kManyLoads) {
+      float x[kManyLoads][C];
+#pragma unroll
+      for (int u = 0; u < kManyLoads; ++u) {
+        const float* src = a.o_part + part(min(i0 + u, n - 1)) * HD + lane * C;
+        if constexpr (C == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(src);
+        else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(src);
+      }
+#pragma unroll
+      for (int u = 0; u < kManyLoads; ++u) {
+        const float wgt = __shfl_sync(0xffffffffu, l[k], (i0 + u) & 31);   // 0 behind the last part
+        if (wgt == 0.f) continue;
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = fmaf(wgt, x[u][c], acc[c]);
+      }
+    }
+  }
+  const float inv = seen ? 1.f / sum : 0.f;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + o_row * HD + lane * C;
+  if constexpr (C == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (lane == 0) *lse_out = seen ? m + logf(sum) : -INFINITY;
+}
+
 // Block x looks after the unit that begins in CTA x and goes on in the CTAs
-// behind it; kJoinRows blocks share its rows, a warp or a whole block to a row.
+// behind it; kJoinRows blocks share its rows, a warp to a row or, where that
+// leaves one for each block, a whole block.  Four blocks an SM (64 registers):
+// at two, most of the time is blocks that find nothing to join (48 units of a
+// chunk over 2,048 keys: 30 against 33 us with the attention).
 template <int HD, bool PAIR>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnHead a) {
+__global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const __grid_constant__ PagedAttnHead a) {
   const int c = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedJoin j = a.joins[c];
   if (j.last < 0) return;
   const int n = j.last - c + 1;
-  const bool few = n <= kFewParts;
+  const bool few = n <= kFewParts, by_warp = few || a.slot_rows > kJoinRows;
   constexpr int kWarps = kJoinThreads / 32;
-  for (int r = few ? blockIdx.y * kWarps + threadIdx.x / 32 : blockIdx.y; r < a.slot_rows;
-       r += few ? kJoinRows * kWarps : kJoinRows) {
+  for (int r = by_warp ? blockIdx.y * kWarps + threadIdx.x / 32 : blockIdx.y; r < a.slot_rows;
+       r += by_warp ? kJoinRows * kWarps : kJoinRows) {
     const int row = PAIR ? r % kBlockM : r;                       // of its tile
     const int tok_t = row / a.group, tok = (j.tile0 + (PAIR ? r / kBlockM : 0)) * a.tile_tokens + tok_t;
     if (tok_t >= a.tile_tokens || tok >= j.q_len) continue;
@@ -1295,6 +1378,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const int64_t o_row = static_cast<int64_t>(j.q_row0 + tok) * a.num_heads + h;
     float* lse = a.lse + static_cast<int64_t>(h) * a.lse_stride + j.q_row0 + tok;
     if (few) join_row_warp<HD>(a, n, part, o_row, lse);
+    else if (by_warp) join_row_many<HD>(a, n, part, o_row, lse);
     else join_row<HD>(a, n, part, o_row, lse);
   }
 }
@@ -1324,7 +1408,7 @@ cudaError_t launch_attn(const PagedMaps& maps, const PagedAttnArgs<N>& a, cudaSt
     if (e != cudaSuccess) return e;
     word.fetch_or(uint64_t(1) << (dev & 63));
   }
-  paged_attn_kernel<HD, PAIR, N><<<kPagedCtas, kThreads, smem, stream>>>(maps, a);
+  paged_attn_kernel<HD, PAIR, N><<<a.whole > 0 ? a.whole : kPagedCtas, kThreads, smem, stream>>>(maps, a);
   return cudaGetLastError();
 }
 

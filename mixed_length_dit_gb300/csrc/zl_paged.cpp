@@ -170,6 +170,31 @@ size_t attn_workspace(const int32_t* cu, int32_t num_seqs, int32_t group, int32_
   return need;
 }
 
+// The launch's units if each is left whole, one CTA to a unit; 0 if they are cut
+// into equal shares.  Whole units do without the sums over all lengths and
+// without the join, equal shares finish earlier when there are fewer units than
+// SMs or lengths differ.  L key blocks bound a unit (the lengths themselves are
+// on the device), half of them is taken for the mean, so a share is about
+// `share`; whole is taken while L is at most 4 blocks (chunks: 5), and one for
+// every 16 units to be joined, above it.  Measured, whole and cut (us; 128
+// columns; L = 2, 4, 8, 16):
+//   8 units of a token       8.3 11.4   10.1 10.9   13.8 10.9   21.4 12.6
+//   32 units of a token      8.2 11.6   10.4 12.6   14.2 14.6   21.5 16.7
+//   128 units of 5 rows      8.8 12.1   11.1 14.5   15.2 21.9   27.1 33.9
+//   8 units of a chunk      10.6 14.9   14.2 18.5   20.9 19.1   34.3 21.7
+//   48 units of a chunk     10.7 15.3   14.1 22.9   20.8 25.9   34.2 30.1
+int32_t whole_units(const zl::PagedAttnArgs<zl::kMaxSegs>& a, bool pair) {
+  const int32_t span = pair ? 2 * a.tile_tokens : a.tile_tokens;     // queries of a unit, at most
+  int64_t units = 0;
+  for (int32_t i = 0; i < a.n_segs; ++i)
+    units += int64_t(pair ? (a.segs[i].q_len + span - 1) / span : 1) * a.num_kv_heads;
+  if (units > zl::kPagedCtas) return 0;
+  int64_t blocks = (int64_t(a.max_kv_len) + zl::kBlockN - 1) / zl::kBlockN;
+  if (a.window > 0 && a.causal) blocks = std::min(blocks, (int64_t(a.window) + span) / zl::kBlockN + 2);
+  const int64_t share = std::max<int64_t>(2, units * (blocks / 2 + 2) / zl::kPagedCtas);
+  return blocks - share <= (pair ? 5 : 4) + units / 16 ? static_cast<int32_t>(units) : 0;
+}
+
 zl_status check_tables(const zl_page_tables_t* t, zl::PageTable* out) {
   if (!t) return ZL_EINVAL;
   if (!page_size_ok(t->page_size)) return ZL_EUNSUPPORTED;
@@ -443,8 +468,10 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
         const int32_t n = cu_seqlens_q[x + 1] - cu_seqlens_q[x];
         if (n > 0 && (n > a.tile_tokens) == pair) a.segs[a.n_segs++] = zl::PagedSeg{x, cu_seqlens_q[x], n};
       }
+      a.whole = whole_units(a, pair);
       st = launch_counted("paged_attn", s, [&] { return zl::launch_paged_attn(hd, pair, maps, a, s); });
       if (st != ZL_OK) return st;
+      if (a.whole > 0) continue;
       st = launch_counted("paged_join", s, [&] { return zl::launch_paged_join(hd, pair, a, s); });
       if (st != ZL_OK) return st;
     }

@@ -569,3 +569,36 @@ def test_nan_is_handed_on(new, lens, heads, kv_heads, hd):
     nan[-1, :heads // kv_heads] = True
     assert o3[nan].isnan().all() and l3.T[nan].isnan().all()
     assert torch.equal(o3[~nan], o1[~nan]) and torch.equal(l3.T[~nan], l1.T[~nan])
+
+
+@pytest.mark.parametrize("new,lens,heads,kv_heads,hd", [
+    ([1], [700], 8, 8, 64), ([1] * 19, [130] * 18 + [1000], 16, 8, 128), ([3, 1, 2], [3, 0, 600], 12, 4, 64),
+    ([200], [600], 4, 4, 128), ([600, 129, 300], [620, 129, 1], 3, 1, 64), ([90, 1, 400, 2], [90, 500, 700, 7], 20, 4, 128),
+    ([130] * 5, [0, 1, 200, 640, 64], 6, 2, 64),
+])
+def test_whole_and_cut_units_agree(new, lens, heads, kv_heads, hd):
+    """A bound of the lengths decides whether units are left whole; either way
+    the result is the formula's, and the order of units does not matter."""
+    b = Batch(new, lens, heads, kv_heads, hd, 32, seed=12, spare_cols=2000)
+    for kw in ({}, {"causal": False}, {"window": 100}):
+        for most in (max(lens), 60000):
+            before = zl.launch_count()
+            o, lse = b.run(most=most, **kw)
+            launches = zl.launch_count() - before
+            zl.sync_check()
+            b.check(o, lse, **kw)
+            kinds = len({n * (heads // kv_heads) > 128 // (heads // kv_heads) * (heads // kv_heads) for n in new})
+            if most == 60000 and "window" not in kw:
+                assert launches == 2 * kinds
+            else:
+                assert kinds <= launches <= 2 * kinds
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_many_rows_of_many_parts(hd):
+    """Chunks and drafts of many rows, each row's keys spread over many SMs."""
+    for new, lens, heads, kv in (([250], [9000], 1, 1), ([64], [20000], 1, 1), ([30, 25], [15000, 40], 3, 1)):
+        b = Batch(new, lens, heads, kv, hd, 64, seed=13)
+        o, lse = b.run()
+        zl.sync_check()
+        b.check(o, lse)
