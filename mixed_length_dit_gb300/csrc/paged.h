@@ -104,7 +104,8 @@ struct PagedAttnHead {
   int32_t window;
   float scale_log2;             // softmax scale * log2(e)
   int32_t n_segs;
-  int32_t whole;                // > 0: units of this launch, one CTA each and none cut (no join follows)
+  int32_t whole;                // > 0: the launch's units, of kFewSegs sequences at most; each has a CTA
+                                // to itself and no join follows
 
 #ifdef __CUDACC__
   // The token of a tile's row, row / group: exact for rows and groups up to

@@ -367,8 +367,9 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x) {
   return x;
 }
 
-// A launch of few units with few blocks each: CTA c takes the c-th whole, and
-// neither the sums before nor the join behind it is needed.
+// WHOLE, a launch of few units with few blocks each: CTA c takes the c-th whole,
+// and neither the sums before nor the join behind it is needed.  (Both ways in
+// one kernel cost the other launches 0.5 to 1.7 us of instruction fetches.)
 template <int HD, bool PAIR, int N>
 __device__ void produce_whole(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const PagedMaps& maps) {
   const int nk = a.num_kv_heads;
@@ -1123,12 +1124,12 @@ __device__ void softmax_split(PagedSmem<HD, false>* sm, const PagedAttnArgs<N>& 
   }
 }
 
-template <int HD, bool PAIR, int N>
+template <int HD, bool PAIR, bool WHOLE, int N>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttnArgs<N> args) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   auto* sm = reinterpret_cast<PagedSmem<HD, PAIR>*>(smem_raw);
-  if (args.whole == 0 && threadIdx.x == 0) args.joins[blockIdx.x].last = -1;   // also when this CTA gives up a wait
+  if (!WHOLE && threadIdx.x == 0) args.joins[blockIdx.x].last = -1;   // also when this CTA gives up a wait
   if ((smem_u32(smem_raw) & 1023u) != 0) {       // the declared alignment; the swizzle needs it
     if (threadIdx.x == 0) atomicOr(&g_paged_err, ERR_BAD_WORK);
     return;
@@ -1160,9 +1161,11 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
     tmem_alloc(&sm->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if (args.whole == 0) sum_blocks<HD, PAIR, N>(sm, args);
-  // the join may be set up from here on; it waits for this grid's end itself
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (!WHOLE) {
+    sum_blocks<HD, PAIR, N>(sm, args);
+    // the join may be set up from here on; it waits for this grid's end itself
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1174,7 +1177,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant_
     // spills, or not, with any change of the code around it).
     if constexpr (PAIR) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kProducerWarp) {
-      if (args.whole > 0) produce_whole<HD, PAIR, N>(sm, args, maps);
+      if constexpr (WHOLE) produce_whole<HD, PAIR, N>(sm, args, maps);
       else produce<HD, PAIR, N>(sm, args, maps);
     } else if (warp == kAuxWarp) {
       assist<HD, PAIR, N>(sm, args, maps);
@@ -1359,14 +1362,15 @@ __device__ __forceinline__ void join_row_many(const PagedAttnHead& a, int n, F p
 // leaves one for each block, a whole block.  Four blocks an SM (64 registers):
 // at two, most of the time is blocks that find nothing to join (48 units of a
 // chunk over 2,048 keys: 30 against 33 us with the attention).
-template <int HD, bool PAIR>
+// FEW_ROWS: slot_rows <= kJoinRows.
+template <int HD, bool PAIR, bool FEW_ROWS>
 __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const __grid_constant__ PagedAttnHead a) {
   const int c = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedJoin j = a.joins[c];
   if (j.last < 0) return;
   const int n = j.last - c + 1;
-  const bool few = n <= kFewParts, by_warp = few || a.slot_rows > kJoinRows;
+  const bool few = n <= kFewParts, by_warp = few || !FEW_ROWS;
   constexpr int kWarps = kJoinThreads / 32;
   for (int r = by_warp ? blockIdx.y * kWarps + threadIdx.x / 32 : blockIdx.y; r < a.slot_rows;
        r += by_warp ? kJoinRows * kWarps : kJoinRows) {
@@ -1378,8 +1382,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const __gri
     const int64_t o_row = static_cast<int64_t>(j.q_row0 + tok) * a.num_heads + h;
     float* lse = a.lse + static_cast<int64_t>(h) * a.lse_stride + j.q_row0 + tok;
     if (few) join_row_warp<HD>(a, n, part, o_row, lse);
-    else if (by_warp) join_row_many<HD>(a, n, part, o_row, lse);
-    else join_row<HD>(a, n, part, o_row, lse);
+    else if constexpr (FEW_ROWS) join_row<HD>(a, n, part, o_row, lse);
+    else join_row_many<HD>(a, n, part, o_row, lse);
   }
 }
 
@@ -1392,7 +1396,7 @@ PagedAttnArgs<N> cut(const PagedAttnArgs<kMaxSegs>& a) {
   return r;
 }
 
-template <int HD, bool PAIR, int N>
+template <int HD, bool PAIR, bool WHOLE, int N>
 cudaError_t launch_attn(const PagedMaps& maps, const PagedAttnArgs<N>& a, cudaStream_t stream) {
   constexpr size_t smem = sizeof(PagedSmem<HD, PAIR>);
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
@@ -1403,19 +1407,20 @@ cudaError_t launch_attn(const PagedMaps& maps, const PagedAttnArgs<N>& a, cudaSt
   if (e != cudaSuccess) return e;
   std::atomic<uint64_t>& word = done[(dev >> 6) & 1];
   if (!(word.load() >> (dev & 63) & 1)) {
-    e = cudaFuncSetAttribute(paged_attn_kernel<HD, PAIR, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(paged_attn_kernel<HD, PAIR, WHOLE, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     word.fetch_or(uint64_t(1) << (dev & 63));
   }
-  paged_attn_kernel<HD, PAIR, N><<<a.whole > 0 ? a.whole : kPagedCtas, kThreads, smem, stream>>>(maps, a);
+  paged_attn_kernel<HD, PAIR, WHOLE, N><<<WHOLE ? a.whole : kPagedCtas, kThreads, smem, stream>>>(maps, a);
   return cudaGetLastError();
 }
 
 template <int HD, bool PAIR>
 cudaError_t attn_kind(const PagedMaps& maps, const PagedAttnArgs<kMaxSegs>& a, cudaStream_t stream) {
-  return a.n_segs <= kFewSegs ? launch_attn<HD, PAIR, kFewSegs>(maps, cut<kFewSegs>(a), stream)
-                              : launch_attn<HD, PAIR, kMaxSegs>(maps, a, stream);
+  if (a.whole > 0) return launch_attn<HD, PAIR, true, kFewSegs>(maps, cut<kFewSegs>(a), stream);
+  return a.n_segs <= kFewSegs ? launch_attn<HD, PAIR, false, kFewSegs>(maps, cut<kFewSegs>(a), stream)
+                              : launch_attn<HD, PAIR, false, kMaxSegs>(maps, a, stream);
 }
 
 // The join's launch overlaps the attention's last CTAs (programmatic dependent
@@ -1444,11 +1449,14 @@ cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, co
 
 cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnHead& a, cudaStream_t stream) {
   const dim3 grid(kPagedCtas, static_cast<unsigned>(std::min(a.slot_rows, kJoinRows)));
+  const bool few = a.slot_rows <= kJoinRows;   // never of a chunk: its slots are two tiles
   if (head_dim == 64)
-    return pair ? launch_after(paged_join_kernel<64, true>, grid, stream, a)
-                : launch_after(paged_join_kernel<64, false>, grid, stream, a);
-  return pair ? launch_after(paged_join_kernel<128, true>, grid, stream, a)
-              : launch_after(paged_join_kernel<128, false>, grid, stream, a);
+    return pair  ? launch_after(paged_join_kernel<64, true, false>, grid, stream, a)
+           : few ? launch_after(paged_join_kernel<64, false, true>, grid, stream, a)
+                 : launch_after(paged_join_kernel<64, false, false>, grid, stream, a);
+  return pair  ? launch_after(paged_join_kernel<128, true, false>, grid, stream, a)
+         : few ? launch_after(paged_join_kernel<128, false, true>, grid, stream, a)
+               : launch_after(paged_join_kernel<128, false, false>, grid, stream, a);
 }
 
 uint32_t paged_attn_take_error() {

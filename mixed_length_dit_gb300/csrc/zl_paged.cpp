@@ -178,17 +178,17 @@ size_t attn_workspace(const int32_t* cu, int32_t num_seqs, int32_t group, int32_
 // `share`; whole is taken while L is at most 4 blocks (chunks: 5), and one for
 // every 16 units to be joined, above it.  Measured, whole and cut (us; 128
 // columns; L = 2, 4, 8, 16):
-//   8 units of a token       8.3 11.4   10.1 10.9   13.8 10.9   21.4 12.6
-//   32 units of a token      8.2 11.6   10.4 12.6   14.2 14.6   21.5 16.7
-//   128 units of 5 rows      8.8 12.1   11.1 14.5   15.2 21.9   27.1 33.9
-//   8 units of a chunk      10.6 14.9   14.2 18.5   20.9 19.1   34.3 21.7
-//   48 units of a chunk     10.7 15.3   14.1 22.9   20.8 25.9   34.2 30.1
+//   8 units of a token       7.7 11.4    9.4 10.9   13.8 10.6   21.4 12.2
+//   32 units of a token      8.0 11.6   10.1 12.6   14.2 14.4   21.5 16.5
+//   128 units of 5 rows      8.9 12.1   10.9 14.5   15.2 21.9   26.7 33.9
+//   8 units of a chunk      10.2 14.9   13.7 18.5   20.9 18.9   34.3 21.2
+//   48 units of a chunk     10.4 15.3   13.8 22.9   20.5 25.9   34.2 29.9
 int32_t whole_units(const zl::PagedAttnArgs<zl::kMaxSegs>& a, bool pair) {
   const int32_t span = pair ? 2 * a.tile_tokens : a.tile_tokens;     // queries of a unit, at most
   int64_t units = 0;
   for (int32_t i = 0; i < a.n_segs; ++i)
     units += int64_t(pair ? (a.segs[i].q_len + span - 1) / span : 1) * a.num_kv_heads;
-  if (units > zl::kPagedCtas) return 0;
+  if (units > zl::kPagedCtas || a.n_segs > zl::kFewSegs) return 0;
   int64_t blocks = (int64_t(a.max_kv_len) + zl::kBlockN - 1) / zl::kBlockN;
   if (a.window > 0 && a.causal) blocks = std::min(blocks, (int64_t(a.window) + span) / zl::kBlockN + 2);
   const int64_t share = std::max<int64_t>(2, units * (blocks / 2 + 2) / zl::kPagedCtas);
