@@ -56,7 +56,10 @@ constexpr int kAuxWarp = 11;
 constexpr int kReaders = 11;                   // 2 issuer threads, 8 softmax warps, the aux warp
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;
-constexpr int kMinBlocks = 2;                  // key blocks of a CTA at least (SPLIT: one for each group)
+// Key blocks of a CTA at least (SPLIT: one for each group).  With three, a token
+// over 1,000 keys takes 12.7 us instead of 11.5, a chunk of 200 over 1,536 21.6
+// instead of 20.7.
+constexpr int kMinBlocks = 2;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // K/V blocks of 128 keys in shared memory.  PAIR holds two query tiles and
