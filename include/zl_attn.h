@@ -454,8 +454,10 @@ zl_status zl_rope_bwd(const zl_rope_t* plan, const void* q, int64_t q_stride, co
  * and token j of it lies in page_table[s][j / page_size] at j % page_size.
  * Entries past a sequence's pages, and pool rows past its length, are never
  * used, whatever they hold.  page_refs[p] counts the sequences that hold page
- * p (0: free); a shared page is always a full one.  All tables are DEVICE
- * arrays: a captured graph replays with the lengths and pages of the moment.
+ * p (0: free).  New tokens are never written into a page that another sequence
+ * holds: forks share full pages only, and a sequence truncated inside a shared
+ * page is not extended (see zl_pages_truncate).  All tables are DEVICE arrays:
+ * a captured graph replays with the lengths and pages of the moment.
  *
  * Kernels check every page number, slot and length that they read from the
  * device, and never leave the buffers: a token or page move that is out of
@@ -566,9 +568,10 @@ zl_status zl_pages_workspace_size(int32_t num_pages, size_t* bytes);
  * Makes room for counts[s] (device, >= 0) new tokens in every slot: kv_lens
  * grows by counts, and the pages that the new lengths need are taken from the
  * free ones, lowest number first, in the order of slots and positions.
- * *status (device): 0; or the number of pages that were lacking, or -1 for a
- * negative count or a length that does not fit a table row; unless it is 0
- * nothing was changed.
+ * *status (device): 0; or the number of pages that were lacking; or -1 for a
+ * negative count or a length that does not fit a table row; or -2 for a slot
+ * whose new tokens would begin inside a page that another slot holds (it was
+ * truncated there).  Unless it is 0 nothing was changed.
  */
 zl_status zl_pages_extend(const zl_page_tables_t* tables, const int32_t* counts, int32_t* status, void* stream);
 
@@ -595,8 +598,9 @@ zl_status zl_pages_free(const zl_page_tables_t* tables, const int32_t* slots, in
  * Shortens every slot that is longer than lens[s] (device, >= 0) to it, as when
  * drafted tokens are taken back: the pages behind lose a reference, their table
  * entries become -1.  (A caller that only lowered kv_lens would lose those
- * pages.)  A slot cut inside a page that another slot holds too must not be
- * appended to before it has a copy of its own, as a fork makes one.
+ * pages.)  A slot cut inside a page that another slot holds too cannot grow
+ * (zl_pages_extend: -2) until it has a copy of that page of its own: fork it to
+ * an empty slot and free it, or free the others.
  */
 zl_status zl_pages_truncate(const zl_page_tables_t* tables, const int32_t* lens, void* stream);
 

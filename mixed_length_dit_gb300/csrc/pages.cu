@@ -115,10 +115,10 @@ __device__ __forceinline__ bool is_free(int, int refs) { return refs == 0; }
 __global__ void __launch_bounds__(kPlanThreads)
 extend_kernel(PageTable t, const int32_t* counts, int32_t* status) {
   __shared__ int start[kMaxSlots];             // first rank of each slot's new pages
-  __shared__ int bad, total_need, total_free;
+  __shared__ int bad, shared_end, total_need, total_free;
   __shared__ unsigned long long wanted;        // 64 bits: more than there are pages may be asked for
   if (threadIdx.x == 0) {
-    bad = 0;
+    bad = shared_end = 0;
     wanted = 0;
   }
   __syncthreads();
@@ -126,7 +126,7 @@ extend_kernel(PageTable t, const int32_t* counts, int32_t* status) {
   const int per = (t.slots + kPlanThreads - 1) / kPlanThreads;
   const int s0 = min(t.slots, static_cast<int>(threadIdx.x) * per), s1 = min(t.slots, s0 + per);
   int64_t need = 0;
-  bool ok = true;
+  bool ok = true, own_end = true;
   for (int s = s0; s < s1; ++s) {
     const int64_t len = t.kv_lens[s], c = counts[s];
     if (len < 0 || c < 0 || len + c > INT32_MAX || pages_of(len + c, t.page_shift) > t.cols) {
@@ -134,15 +134,23 @@ extend_kernel(PageTable t, const int32_t* counts, int32_t* status) {
       continue;
     }
     need += pages_of(len + c, t.page_shift) - pages_of(len, t.page_shift);
+    // a slot that was truncated inside a page which another one holds too: new
+    // tokens would be written over the other's
+    if (c > 0 && (len & ((1 << t.page_shift) - 1)) != 0) {
+      const int p = t.table[static_cast<int64_t>(s) * t.cols + (len >> t.page_shift)];
+      if (p >= 0 && p < t.num_pages && t.refs[p] > 1) own_end = false;
+    }
   }
   if (!ok) atomicExch(&bad, 1);
+  if (!own_end) atomicExch(&shared_end, 1);
   atomicAdd(&wanted, static_cast<unsigned long long>(need));
   int first, last;
   page_run(t.num_pages, &first, &last);
   const int rank0 = warps_scan(count_run(t, first, last, is_free), &total_free);
-  if (bad || wanted > static_cast<unsigned long long>(total_free)) {
+  if (bad || shared_end || wanted > static_cast<unsigned long long>(total_free)) {
     const unsigned long long lacking = wanted - total_free;
-    if (threadIdx.x == 0) *status = bad ? -1 : static_cast<int>(lacking < INT32_MAX ? lacking : INT32_MAX);
+    if (threadIdx.x == 0)
+      *status = bad ? -1 : shared_end ? -2 : static_cast<int>(lacking < INT32_MAX ? lacking : INT32_MAX);
     return;
   }
   int at = block_scan(static_cast<int>(need), &total_need);

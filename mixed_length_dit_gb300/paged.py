@@ -428,7 +428,9 @@ def pages_extend(page_table, kv_lens, page_refs, counts, page_size, status=None,
     """Makes room for counts[s] (int32, device) new tokens in every slot, in
     place: kv_lens grows, free pages (lowest first) enter the rows.  Returns a
     device int32 [1]: 0, or the pages lacking, or -1 for counts that are
-    negative or do not fit a row; unless it is 0 nothing was changed."""
+    negative or do not fit a row, or -2 for a slot that would grow inside a page
+    that another one holds (it was truncated there); unless it is 0 nothing was
+    changed."""
     if stream is None and status is None:
         r = _short("extend", page_table, kv_lens, page_refs, counts, page_size)
         if r is not None:
@@ -470,7 +472,10 @@ def pages_free(page_table, kv_lens, page_refs, slots, page_size, stream=None):
 
 def pages_truncate(page_table, kv_lens, page_refs, lens, page_size, stream=None):
     """Shortens every slot that is longer than lens[s] (int32, device) to it, in
-    place, as when drafted tokens are taken back; the pages behind are freed."""
+    place, as when drafted tokens are taken back; the pages behind are freed.
+    A slot cut inside a page that another one holds (a fork's parent or child,
+    shortened to before the fork) cannot be extended until it has that page to
+    itself: fork it to an empty slot and free it."""
     t, dev = _tables(page_table, kv_lens, page_refs, page_size)
     _exact(lens, "lens", kv_lens.shape, _I32, dev)
     _call("zl_pages_truncate", kv_lens.get_device(), stream, t, lens.data_ptr())

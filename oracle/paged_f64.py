@@ -144,6 +144,9 @@ class Pages:
         need = [self.used(n + c) - self.used(n) for n, c in zip(self.lens, counts)]
         if min(counts) < 0 or any(self.used(n + c) > len(self.table[0]) for n, c in zip(self.lens, counts)):
             return -1
+        if any(c > 0 and n % self.page and self.refs[row[n // self.page]] > 1
+               for n, c, row in zip(self.lens, counts, self.table)):
+            return -2
         free = self.free_pages()
         if sum(need) > len(free):
             return sum(need) - len(free)

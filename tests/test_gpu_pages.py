@@ -262,3 +262,64 @@ def test_truncate_shared_pages_bad_lengths_and_graphs():
         b.same()
     assert e.value.status == -8
     b.same()
+
+
+def test_a_slot_cut_inside_a_shared_page_does_not_grow_over_the_other():
+    """Fork, truncate to before the fork, go on: the sibling keeps its tokens,
+    and a fork gives the shortened slot a page of its own."""
+    b = Both([70, 8], 30, 16, 6, spare_slots=3)
+    zl.pages_fork(b.cache, b.table, b.lens, b.refs, i32([0]), i32([2]))
+    b.m.fork([0], [2])
+    keep = [70, 8, 40, 0, 0]                     # slot 2: 8 tokens into a page that slot 0 holds too
+    zl.pages_truncate(b.table, b.lens, b.refs, i32(keep), 16)
+    b.m.truncate(keep)
+    b.same()
+    for counts, want in (([0, 0, 1, 0, 0], -2), ([3, 2, 8, 1, 0], -2), ([0, 0, 9, 0, 500], -1), ([1, 1, 0, 1, 1], 0),
+                         ([0, 0, 2, 0, 0], -2), ([0, 0, 1, 16 * 90, 0], -1)):
+        st = zl.pages_extend(b.table, b.lens, b.refs, i32(counts), 16)
+        assert int(st) == b.m.extend(counts) == want, counts
+        b.same()
+    zl.pages_free(b.table, b.lens, b.refs, i32([3, 4]), 16)
+    b.m.release([3, 4])
+    assert int(zl.pages_fork(b.cache, b.table, b.lens, b.refs, i32([2]), i32([4]))) == b.m.fork([2], [4]) == 0
+    zl.pages_free(b.table, b.lens, b.refs, i32([2]), 16)
+    b.m.release([2])
+    b.same()
+    b.same_data()
+    assert int(b.table[4, 2]) != int(b.table[0, 2])
+    assert int(zl.pages_extend(b.table, b.lens, b.refs, i32([0, 0, 0, 0, 30]), 16)) == b.m.extend([0, 0, 0, 0, 30]) == 0
+    b.same()
+    b.same_data()
+    # a cut at a page's end shares full pages only, and a page whose other holder is gone is one's own again
+    zl.pages_fork(b.cache, b.table, b.lens, b.refs, i32([0]), i32([2]))
+    b.m.fork([0], [2])
+    keep = [71, 9, 32, 0, 70]
+    zl.pages_truncate(b.table, b.lens, b.refs, i32(keep), 16)
+    b.m.truncate(keep)
+    assert int(zl.pages_extend(b.table, b.lens, b.refs, i32([0, 0, 20, 0, 0]), 16)) == b.m.extend([0, 0, 20, 0, 0]) == 0
+    b.same()
+    zl.pages_truncate(b.table, b.lens, b.refs, i32([71, 9, 25, 0, 70]), 16)
+    b.m.truncate([71, 9, 25, 0, 70])
+    assert int(zl.pages_extend(b.table, b.lens, b.refs, i32([0, 0, 1, 0, 0]), 16)) == b.m.extend([0, 0, 1, 0, 0]) == -2
+    zl.pages_free(b.table, b.lens, b.refs, i32([0, 4]), 16)
+    b.m.release([0, 4])
+    assert int(zl.pages_extend(b.table, b.lens, b.refs, i32([0, 0, 9, 0, 0]), 16)) == b.m.extend([0, 0, 9, 0, 0]) == 0
+    b.same()
+
+
+def test_tokens_appended_after_a_cut_leave_the_sibling_alone():
+    """The loop that a search runs: fork, cut, extend, append.  What the refused
+    extend left is what it was, and the sibling's keys stay."""
+    page, kv, hd = 16, 2, 64
+    cache = torch.zeros((2, 20, kv, page, hd), dtype=torch.bfloat16, device="cuda")
+    table, lens, refs = torch.full((2, 6), -1, dtype=torch.int32, device="cuda"), i32([0, 0]), i32([0] * 20)
+    plan = zl.RopePlan(hd)
+    first = torch.randn((40, kv, hd), device="cuda").to(torch.bfloat16)
+    assert int(zl.pages_extend(table, lens, refs, i32([40, 0]), page)) == 0
+    zl.paged_append(first, first, *cache, table, lens, [0, 40, 40], rope=plan)
+    assert int(zl.pages_fork(cache, table, lens, refs, i32([0]), i32([1]))) == 0
+    zl.pages_truncate(table, lens, refs, i32([40, 20]), page)
+    before = [x.clone() for x in (cache, table, lens, refs)]
+    assert int(zl.pages_extend(table, lens, refs, i32([0, 4]), page)) == -2
+    zl.sync_check()
+    assert all(torch.equal(x, y) for x, y in zip((cache, table, lens, refs), before))

@@ -426,3 +426,12 @@ def test_truncate_refusals(lib, fault, status):
         zl.pages_truncate(_i(3, 4), _i(3), _i(20), _i(2), 16)
     with pytest.raises(ValueError, match="CUDA"):
         zl.pages_truncate(_i(3, 4), _i(3), _i(20), _i(3), 16)
+
+
+def test_oracle_pages_shared_ends():
+    p = ref.Pages([[0, 1, 2], [-1] * 3], [40, 0], [1, 1, 1, 0, 0], 16)
+    assert p.fork([0], [1]) == 0
+    p.truncate([40, 20])
+    assert p.refs[1] == 2 and p.extend([0, 1]) == -2 and p.lens == [40, 20] and p.extend([3, 0]) == 0
+    p.truncate([43, 16])
+    assert p.refs[1] == 1 and p.extend([0, 5]) == 0 and p.table[1][1] != p.table[0][1]
