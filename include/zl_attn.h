@@ -120,7 +120,8 @@ const char* zl_status_string(int32_t status);
 /* ABI version of this header: (major << 16) | minor.  2.0: head-sharded
  * tiles; 2.1 adds ZL_FWD_BF16_PARTIALS, zl_lse_merge_ex and the schedule
  * queries; 2.2 adds rotary positions (zl_rope_*) and the paged key/value cache
- * (zl_paged_*, zl_pages_*) (no existing entry changed). */
+ * (zl_paged_*, zl_pages_*); 2.3 adds zl_paged_append_ex (no existing entry
+ * changed). */
 int32_t zl_version(void);
 
 /*
@@ -489,11 +490,29 @@ typedef struct {
  * zl_rope_fwd) when given; a plan of more than one axis needs them.  The
  * pages that the tokens go to must not be shared.  One launch per 640
  * sequences.
+ *
+ * The lengths have to count the new tokens.  Where zl_pages_extend lacked pages
+ * they do not, and the tokens would be written over the sequences' last ones:
+ * check its status before, or, where the host does not wait for it (a captured
+ * graph), hand it to zl_paged_append_ex.
  */
 zl_status zl_paged_append(const zl_paged_cache_t* cache, const void* k, int64_t k_stride, const void* v,
                           int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs, const zl_rope_t* plan,
                           const int32_t* positions, int64_t pos_stride, const void* q, int64_t q_stride,
                           int32_t num_heads, void* q_out, int64_t q_out_stride, void* stream);
+
+/*
+ * The same behind a zl_pages_extend whose status the host has not read: status
+ * (device int32, or NULL) is read by the launch, and unless it is 0 no key or
+ * value is written and the next zl_sync_check reports ZL_EPAGE.  (q_out is
+ * written either way; of attention over the cache the call's outputs then mean
+ * nothing, but the cache is as it was.)
+ */
+zl_status zl_paged_append_ex(const zl_paged_cache_t* cache, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs, const zl_rope_t* plan,
+                             const int32_t* positions, int64_t pos_stride, const void* q, int64_t q_stride,
+                             int32_t num_heads, void* q_out, int64_t q_out_stride, const int32_t* status,
+                             void* stream);
 
 /*
  * Workspace needed by zl_paged_attn for this batch, in bytes: what sequences

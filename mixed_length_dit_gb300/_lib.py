@@ -32,7 +32,7 @@ EXPORTS = (
     "zl_launch_count", "zl_profile_begin", "zl_profile_end", "zl_varlen_attn_bwd_static",
     "zl_varlen_attn_fwd_ex", "zl_lse_merge_ex", "zl_varlen_attn_fwd_schedule", "zl_varlen_attn_bwd_schedule",
     "zl_selftest_wait_timeout", "zl_rope_init", "zl_rope_fwd", "zl_rope_bwd", "zl_paged_append",
-    "zl_paged_attn_workspace_size", "zl_paged_attn", "zl_pages_workspace_size", "zl_pages_extend", "zl_pages_fork",
+    "zl_paged_append_ex", "zl_paged_attn_workspace_size", "zl_paged_attn", "zl_pages_workspace_size", "zl_pages_extend", "zl_pages_fork",
     "zl_pages_free", "zl_pages_truncate", "zl_pages_compact", "zl_pages_copy",
 )
 
@@ -158,8 +158,9 @@ def load() -> ctypes.CDLL:
     rope_args = [ropep, vp, c_i64, vp, c_i64, vp, c_i64, c_i64, c_i32, c_i32, c_i32, vp, c_i64, vp, c_i64, vp]
     lib.zl_rope_fwd.argtypes = rope_args
     lib.zl_rope_bwd.argtypes = rope_args
-    lib.zl_paged_append.argtypes = [cachep, vp, c_i64, vp, c_i64, i32p, c_i32, ropep, vp, c_i64, vp, c_i64, c_i32,
-                                    vp, c_i64, vp]
+    append_args = [cachep, vp, c_i64, vp, c_i64, i32p, c_i32, ropep, vp, c_i64, vp, c_i64, c_i32, vp, c_i64]
+    lib.zl_paged_append.argtypes = append_args + [vp]
+    lib.zl_paged_append_ex.argtypes = append_args + [vp, vp]
     lib.zl_paged_attn_workspace_size.argtypes = [i32p, c_i32, c_i32, c_i32, c_i32, c_i32, szp]
     lib.zl_paged_attn.argtypes = [cachep, vp, c_i64, i32p, c_i32, c_i32, c_i32, c_f32, c_i32, c_i32, vp, vp, vp, c_sz,
                                   vp]

@@ -186,8 +186,9 @@ bool cache_of(Args& a, zl_paged_cache_t* c, c10::Device* dev) {
   return true;
 }
 
-// k, v, the cache, its tables, cu (address, entries, last), q | None, plan | 0,
-// its axes, its head_dim
+// k, v, the cache, its tables, cu (address, entries, last), q | None, plan | 0;
+// STATUS: and the status of the extend before it
+template <bool STATUS>
 PyObject* append(Args& a) {
   const at::Tensor* k = a.t();
   const at::Tensor* v = a.t();
@@ -200,7 +201,9 @@ PyObject* append(Args& a) {
   const int64_t tokens = a.integer();
   const at::Tensor* q = a.maybe();
   const auto* plan = static_cast<const zl_rope_t*>(a.pointer());
+  const at::Tensor* extended = STATUS ? a.t() : nullptr;
   if (!a.done() || lens->size(0) != n - 1 || tokens == 0) return none();
+  if (extended && (!ints(*extended, dev) || extended->dim() != 1 || extended->size(0) != 1)) return none();
   const int64_t ks = rows(*k, tokens, c.num_kv_heads, c.head_dim, at::kBFloat16, dev);
   const int64_t vs = rows(*v, tokens, c.num_kv_heads, c.head_dim, at::kBFloat16, dev);
   int64_t qs = 0, nq = 0;
@@ -215,9 +218,9 @@ PyObject* append(Args& a) {
   {
     Unlocked u;
     if (q) qo = fresh(*q, {tokens, nq, c.head_dim}, at::kBFloat16);
-    st = zl_paged_append(&c, k->data_ptr(), ks, v->data_ptr(), vs, cu, n - 1, plan, nullptr, 0,
-                         q ? q->data_ptr() : nullptr, qs, static_cast<int32_t>(nq), q ? qo.data_ptr() : nullptr,
-                         nq * c.head_dim, stream_of(dev));
+    st = zl_paged_append_ex(&c, k->data_ptr(), ks, v->data_ptr(), vs, cu, n - 1, plan, nullptr, 0,
+                            q ? q->data_ptr() : nullptr, qs, static_cast<int32_t>(nq), q ? qo.data_ptr() : nullptr,
+                            nq * c.head_dim, extended ? extended->data_ptr<int32_t>() : nullptr, stream_of(dev));
   }
   if (st != ZL_OK) return status(st);
   // what was asked for, in a tuple: None alone means the long way
@@ -407,7 +410,8 @@ PyCFunction fast() {
 }
 
 PyMethodDef methods[] = {
-    {"rope", fast<rope>(), METH_FASTCALL, nullptr},       {"append", fast<append>(), METH_FASTCALL, nullptr},
+    {"rope", fast<rope>(), METH_FASTCALL, nullptr},       {"append", fast<append<false>>(), METH_FASTCALL, nullptr},
+    {"append_after", fast<append<true>>(), METH_FASTCALL, nullptr},
     {"attn", fast<attn>(), METH_FASTCALL, nullptr},       {"extend", fast<extend>(), METH_FASTCALL, nullptr},
     {"fork", fast<fork>(), METH_FASTCALL, nullptr},       {"compact", fast<compact>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -41,6 +41,7 @@ struct RopeHead {
   // append: the cache
   const int32_t* page_table;    // [seqs][table_cols]
   const int32_t* kv_lens;       // [seqs]
+  const int32_t* status;        // or null; not 0: nothing is appended
   int32_t table_cols;
   int32_t num_pages;
   int32_t page_shift;

@@ -171,7 +171,8 @@ rope_kernel(const __grid_constant__ RopeArgs<SEQS> a, int tokens_per_block, int 
       const int len = a.kv_lens[seq];
       const int64_t p = static_cast<int64_t>(len) - n + (t - a.cu[lo]);
       int64_t row = -1;
-      if (p >= 0 && (p >> a.page_shift) < a.table_cols) {
+      const bool room = !a.status || *a.status == 0;   // else the lengths do not count the new tokens
+      if (room && p >= 0 && (p >> a.page_shift) < a.table_cols) {
         const int page = a.page_table[seq * a.table_cols + (p >> a.page_shift)];
         if (page >= 0 && page < a.num_pages)
           row = ((static_cast<int64_t>(page) * a.nk) << a.page_shift) + (p & ((1 << a.page_shift) - 1));

@@ -489,7 +489,7 @@ const char* zl_status_string(int32_t status) {
   }
 }
 
-int32_t zl_version(void) { return (2 << 16) | 2; }
+int32_t zl_version(void) { return (2 << 16) | 3; }
 
 int64_t zl_launch_count(void) { return g_launches.load(); }
 

@@ -311,6 +311,15 @@ zl_status zl_paged_append(const zl_paged_cache_t* cache, const void* k, int64_t 
                           int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs, const zl_rope_t* plan,
                           const int32_t* positions, int64_t pos_stride, const void* q, int64_t q_stride,
                           int32_t num_heads, void* q_out, int64_t q_out_stride, void* stream) {
+  return zl_paged_append_ex(cache, k, k_stride, v, v_stride, cu_seqlens, num_seqs, plan, positions, pos_stride, q,
+                            q_stride, num_heads, q_out, q_out_stride, nullptr, stream);
+}
+
+zl_status zl_paged_append_ex(const zl_paged_cache_t* cache, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs, const zl_rope_t* plan,
+                             const int32_t* positions, int64_t pos_stride, const void* q, int64_t q_stride,
+                             int32_t num_heads, void* q_out, int64_t q_out_stride, const int32_t* status,
+                             void* stream) {
   zl_status st = check_cache(cache);
   if (st != ZL_OK) return st;
   int64_t tokens = 0;
@@ -323,7 +332,7 @@ zl_status zl_paged_append(const zl_paged_cache_t* cache, const void* k, int64_t 
   if (tokens == 0) return ZL_OK;
   st = check_cache_pointers(cache);
   if (st != ZL_OK) return st;
-  if (positions && misaligned4(positions)) return ZL_EALIGN;
+  if (misaligned4(positions) || misaligned4(status)) return ZL_EALIGN;
   const int32_t hd = cache->head_dim;
   st = check_rows(k, k_stride, cache->num_kv_heads, hd, tokens, 2);
   if (st == ZL_OK) st = check_rows(v, v_stride, cache->num_kv_heads, hd, tokens, 2);
@@ -355,6 +364,7 @@ zl_status zl_paged_append(const zl_paged_cache_t* cache, const void* k, int64_t 
   a.skip_kept = q && q == q_out && q_stride == q_out_stride;
   a.page_table = cache->page_table;
   a.kv_lens = cache->kv_lens;
+  a.status = status;
   a.table_cols = cache->table_cols;
   a.num_pages = cache->num_pages;
   a.page_shift = shift_of(cache->page_size);

@@ -51,7 +51,7 @@ def _short(name, *args):
     return r
 
 
-_NAMES = {"rope": "rope", "append": "paged_append", "attn": "paged_attn", "extend": "pages_extend",
+_NAMES = {"rope": "rope", "append": "paged_append", "append_after": "paged_append_ex", "attn": "paged_attn", "extend": "pages_extend",
           "fork": "pages_fork", "compact": "pages_compact"}
 
 
@@ -269,15 +269,26 @@ def _cache(k_pages, v_pages, page_table, kv_lens, seqs):
 
 
 def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None, q_out=None, rope=None,
-                 positions=None, stream=None):
+                 positions=None, stream=None, status=None):
     """Writes a batch's new tokens k, v [T, Hk, d] into the pages: sequence s's
     rows of cu_seqlens become its last positions below kv_lens[s].  With a
     RopePlan the keys (and q [T, H, d], if given) are turned at their cache
-    positions, or at `positions`.  Returns the turned q (or None)."""
+    positions, or at `positions`.  Returns the turned q (or None).
+
+    kv_lens has to count the new tokens, and the pages they go to must be the
+    sequence's own, as pages_extend sees to.  Where it reported anything but 0
+    the lengths are the old ones, and the tokens would be written over the last
+    ones of each sequence: unless the host has read 0 from it, give the tensor
+    that it returned as `status`.  Then nothing is written unless it holds 0,
+    and the next sync_check raises."""
     cu = _cu(cu_seqlens)
     if stream is None and q_out is None and positions is None:
-        r = _short("append", k, v, k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last, q,
-                   0 if rope is None else rope.address)
+        plan = 0 if rope is None else rope.address
+        if status is None:
+            r = _short("append", k, v, k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last, q, plan)
+        else:
+            r = _short("append_after", k, v, k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last, q, plan,
+                       status)
         if r is not None:
             return r[0]
     cache, nk, hd = _cache(k_pages, v_pages, page_table, kv_lens, cu.n - 1)
@@ -303,11 +314,14 @@ def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None
         if rope is None:
             raise ValueError("positions without a rope plan")
         pos, pos_stride = _positions(positions, rope, tokens, dev)
+    if status is not None:
+        _exact(status, "status", (1,), _I32, dev)
     index = k_pages.get_device()
     if tokens == 0 and index >= 0:
         return q_out
-    _call("zl_paged_append", index, stream, cache, k.data_ptr(), ks, v.data_ptr(), vs, cu.array, cu.n - 1,
-          None if rope is None else rope.ref, pos, pos_stride, qp, qs, nq, qop, qos)
+    _call("zl_paged_append_ex", index, stream, cache, k.data_ptr(), ks, v.data_ptr(), vs, cu.array, cu.n - 1,
+          None if rope is None else rope.ref, pos, pos_stride, qp, qs, nq, qop, qos,
+          None if status is None else status.data_ptr())
     return q_out
 
 

@@ -602,3 +602,93 @@ def test_many_rows_of_many_parts(hd):
         o, lse = b.run()
         zl.sync_check()
         b.check(o, lse)
+
+
+# ------------------------------------------------------------------ an append behind a refused extend
+def _small_cache(slots, pages, page=16, kv=2, hd=64):
+    cache = torch.zeros((2, pages, kv, page, hd), dtype=BF16, device="cuda")
+    table = torch.full((slots, 8), -1, dtype=torch.int32, device="cuda")
+    return cache, table, *(torch.zeros(n, dtype=torch.int32, device="cuda") for n in (slots, pages))
+
+
+@pytest.mark.parametrize("way", ["short", "stream", "positions", "q_out"])
+def test_append_behind_a_refused_extend_writes_nothing(way):
+    """The lengths are the old ones then: without the status the new tokens
+    would replace the last ones, also in pages that a fork shares."""
+    page, kv, hd = 16, 2, 64
+    cache, table, lens, refs = _small_cache(3, 4)
+    plan = zl.RopePlan(hd)
+    g = torch.Generator(device="cuda").manual_seed(60)
+    rand = lambda n, h: torch.randn((n, h, hd), generator=g, device="cuda").to(BF16)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    kw = {}
+    if way == "stream":
+        kw["stream"] = torch.cuda.Stream()
+    elif way == "positions":
+        kw["positions"] = i32(list(range(22)))
+
+    def append(n, cu, status):
+        k, v, q = rand(n, kv), rand(n, kv), rand(n, 4)
+        if way == "positions":
+            kw["positions"] = i32(list(range(n)))
+        if way == "q_out":
+            kw["q_out"] = torch.empty_like(q)
+        torch.cuda.synchronize()
+        zl.paged_append(k, v, *cache, table, lens, cu, q=q, rope=plan, status=status, **kw)
+        torch.cuda.synchronize()
+
+    status = zl.pages_extend(table, lens, refs, i32([32, 16, 0]), page)
+    assert int(status) == 0
+    append(48, [0, 32, 48, 48], status)
+    zl.sync_check()
+    assert cache[:, :3].float().abs().sum((2, 3, 4)).min() > 0
+    assert int(zl.pages_fork(cache, table, lens, refs, i32([0]), i32([2]))) == 0     # full pages, shared
+    before = [x.clone() for x in (cache, table, lens, refs)]
+    status = zl.pages_extend(table, lens, refs, i32([1, 1, 20]), page)
+    assert int(status) == 3
+    append(22, [0, 1, 2, 22], status)
+    with pytest.raises(zl.ZlError) as e:
+        zl.sync_check()
+    assert e.value.status == -8
+    assert all(torch.equal(x, y) for x, y in zip((cache, table, lens, refs), before))
+    status = zl.pages_extend(table, lens, refs, i32([1, 0, 0]), page)                # one page is left
+    assert int(status) == 0
+    append(1, [0, 1, 1, 1], status)
+    zl.sync_check()
+    changed = (cache != before[0]).flatten(2).any(2).any(0).tolist()
+    assert changed == [p == int(table[0, 2]) for p in range(4)]
+
+
+def test_a_replayed_loop_that_runs_out_of_pages():
+    """Extend and append in one graph: once the pool is full every replay leaves
+    the cache as it was, and reports it."""
+    page, kv, hd, slots = 16, 2, 64, 700                 # two launches an append
+    cache, table, lens, refs = _small_cache(slots, 2 * slots)
+    g = torch.Generator(device="cuda").manual_seed(61)
+    k, v = (torch.randn((slots * 11, kv, hd), generator=g, device="cuda").to(BF16) for _ in range(2))
+    counts = torch.full((slots,), 11, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = zl.host_int32([11 * i for i in range(slots + 1)])
+
+    def once():
+        zl.pages_extend(table, lens, refs, counts, page, status=status)
+        zl.paged_append(k, v, *cache, table, lens, cu, status=status)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        once()
+    for n in (11, 22):
+        k.add_(1)
+        graph.replay()
+        zl.sync_check()
+        assert int(status) == 0 and lens.tolist() == [n] * slots
+        last = table[:, (n - 1) // page].long()
+        assert torch.equal(cache[0][last, :, (n - 1) % page], k[10::11])
+    before = [x.clone() for x in (cache, table, lens, refs)]
+    for _ in range(2):                                   # 33 tokens take three pages a slot
+        k.add_(1)
+        graph.replay()
+        with pytest.raises(zl.ZlError):
+            zl.sync_check()
+        assert int(status) == slots
+        assert all(torch.equal(x, y) for x, y in zip((cache, table, lens, refs), before))

@@ -435,3 +435,27 @@ def test_oracle_pages_shared_ends():
     assert p.refs[1] == 2 and p.extend([0, 1]) == -2 and p.lens == [40, 20] and p.extend([3, 0]) == 0
     p.truncate([43, 16])
     assert p.refs[1] == 1 and p.extend([0, 5]) == 0 and p.table[1][1] != p.table[0][1]
+
+
+def test_append_with_a_status_refusals(lib):
+    cu, n = _lib.int32_array([0, 3])
+    c = _cache()
+
+    def call(status, k=64):
+        return lib.zl_paged_append_ex(ctypes.byref(c), k, 128, P64, 128, cu, n - 1, None, None, 0, None, 0, 0, None, 0,
+                                      status, None)
+    assert call(66) == _lib.ZL_EALIGN
+    assert call(64, k=None) == _lib.ZL_EINVAL
+    kp, table, lens, k = _b(10, 2, 16, 64), _i(2, 4), _i(2), _b(5, 2, 64)
+    for status in (_i(2), _i(1, 1), _i(1).long()):
+        with pytest.raises(ValueError, match="status must be"):
+            zl.paged_append(k, k, kp, kp, table, lens, [0, 2, 5], status=status)
+    with pytest.raises(ValueError, match="CUDA"):
+        zl.paged_append(k, k, kp, kp, table, lens, [0, 2, 5], status=_i(1))
+    plan, hcu = zl.RopePlan(64), zl.host_int32([0, 2, 5])
+    args = [k, k, kp, kp, table, lens, hcu.address, 3, 5, None, plan.address, _i(1)]
+    fn = zl._lib.bind().append_after
+    assert fn(*args) is None and fn() is None and fn(*args[:-1]) is None and fn(*args, 1) is None
+    for i in range(len(args)):
+        for bad in (None, "x", 2**80, 1.5, torch.zeros(0), [1]):
+            assert fn(*args[:i], bad, *args[i + 1:]) is None
