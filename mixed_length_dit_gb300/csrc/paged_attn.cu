@@ -162,6 +162,10 @@ struct Work {
   __device__ __forceinline__ bool has(int t) const { return t == 0 || has1; }
   __device__ __forceinline__ int b0(int t) const { return t == 0 ? r0.b0 : r1.b0; }
   __device__ __forceinline__ int b1(int t) const { return t == 0 ? r0.b1 : r1.b1; }
+  // Tile t has a block in the item.  One that has none takes no part in its
+  // queries' coming and going: its softmax group would release them without
+  // having waited for its issuer, twice before a slow one came by.
+  __device__ __forceinline__ bool uses_q(int t) const { return has(t) && b1(t) > b0(t); }
 };
 
 template <bool PAIR, int N>
@@ -519,13 +523,13 @@ __device__ void issue(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, uint32
     if (!take(sm, n, code, false, &item)) return;
     const Work w = decode<PAIR>(a, item);
     if (w.s1 <= w.s0) continue;
-    const bool has = PAIR ? w.has(t) : true;
-    if (has && !mbar_wait(&sm->q_full[qt], q_it & 1u, abort_flag, &g_paged_err, code)) return;
+    const bool uses = PAIR ? w.uses_q(t) : true;
+    if (uses && !mbar_wait(&sm->q_full[qt], q_it & 1u, abort_flag, &g_paged_err, code)) return;
     bool first = true;
     // PAIR: both issuers pass every stage, and each uses the blocks that its
     // tile sees; SPLIT: issuer t's blocks alternate with the other's, in its
     // own ring
-    const int mine0 = w.b0(t), mine1 = has ? w.b1(t) : 0;
+    const int mine0 = w.b0(t), mine1 = uses ? w.b1(t) : 0;
     const int last_mine = PAIR ? mine1 - 1 : w.s1 - 1 - ((w.s1 - 1 - w.s0 - t) & 1);
     for (int j = PAIR ? w.s0 : w.s0 + t; j < w.s1; j += PAIR ? 1 : 2) {
       const bool mine = !PAIR || (j >= mine0 && j < mine1);
@@ -564,10 +568,10 @@ __device__ void issue(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, uint32
       }
       ++kv_it;
     }
-    if (has) {
-      // An issuer without a block in this item does not wait for the softmax
-      // group's work on the one before: it must not complete o_full, or could
-      // complete it a second time before the group has seen the first.
+    if (uses) {
+      // SPLIT's issuer without a block in this item does not wait for the
+      // softmax group's work on the one before: it must not complete o_full, or
+      // could complete it a second time before the group has seen the first.
       if (first) umma_commit(&sm->q_empty[qt]);
       else umma_commit(&sm->o_full[t]);
       ++q_it;
@@ -595,7 +599,7 @@ __device__ void assist(PagedSmem<HD, PAIR>* sm, const PagedAttnArgs<N>& a, const
     if (lane == 0) {
 #pragma unroll
       for (int t = 0; t < (PAIR ? 2 : 1); ++t) {
-        if (!w.has(t)) continue;
+        if (!w.uses_q(t)) continue;
         uint32_t& q_it = t ? q_it1 : q_it0;
         if (!mbar_wait(&sm->q_empty[t], (q_it & 1u) ^ 1u, &sm->abort_flag, &g_paged_err, code)) {
           ok = false;
@@ -823,11 +827,10 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
     const float inv_l = seen ? 1.f / l_run : 0.f;
     const float lse = seen ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
     const int h = w.hk * a.group + row_head;
-    const bool loaded = w.s1 > w.s0;            // this item's Q went through q[t]
+    const bool loaded = !first;                 // the tile had a block: this item's Q is in q[t], and O was written
     const bool final_rows = w.final;
-    // a full tile of final rows leaves by TMA through the tile's own Q
-    // buffer; rows without keys would read O as it was: per thread
-    const bool by_tma = final_rows && loaded && !first && tokens == a.tile_tokens;
+    // a full tile of final rows leaves by TMA through the tile's own Q buffer
+    const bool by_tma = final_rows && loaded && tokens == a.tile_tokens;
     if (loaded && !by_tma && row == 0) mbar_arrive(&sm->q_empty[t]);
     if (by_tma) {
       const uint32_t r7 = static_cast<uint32_t>(row & 7);
@@ -872,7 +875,7 @@ __device__ void softmax_pair(PagedSmem<HD, true>* sm, const PagedAttnArgs<N>& a,
 #pragma unroll 1
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t o[32];
-        if (loaded && !first) {
+        if (loaded) {
           tmem_ld32(tO + c * 32, o);
           tmem_wait_ld();
           reg_fence(o);

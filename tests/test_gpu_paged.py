@@ -692,3 +692,23 @@ def test_a_replayed_loop_that_runs_out_of_pages():
             zl.sync_check()
         assert int(status) == slots
         assert all(torch.equal(x, y) for x, y in zip((cache, table, lens, refs), before))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads,new,lens,kw", [
+    (40, 40, [512, 512], [90, 40], {}),               # of each pair of tiles that sees a key, the first sees none
+    (48, 16, [200, 160, 85], [60, 20, 1], {}),        # three heads to a row's token: tiles of 42
+    (32, 32, [512] * 3, [300, 100, 512], {"window": 5}),
+    (64, 64, [256] * 3, [100, 120, 90], {"window": 3}),
+])
+def test_items_whose_tiles_see_nothing_in_turn(heads, kv_heads, new, lens, kw, hd):
+    """Lengths shorter than the chunk, of many key heads: a CTA meets one item
+    after the other in which one of its two tiles has no key block."""
+    b = Batch(new, lens, heads, kv_heads, hd, 16, seed=62, spare_cols=2000)
+    o, lse = b.run(most=30000, **kw)
+    zl.sync_check()
+    b.check(o, lse, **kw)
+    for _ in range(30):
+        o2, l2 = b.run(most=30000, **kw)
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+    zl.sync_check()
