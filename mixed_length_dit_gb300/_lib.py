@@ -210,6 +210,10 @@ class HostInt32:
         self.address = ctypes.addressof(self.array)
         self.last = int(self.array[self.n - 1]) if self.n else None
 
+    def __reduce__(self):
+        # copies and pickles are made anew: `address` is this array's alone
+        return HostInt32, (list(self),)
+
     def __len__(self):
         return self.n
 

@@ -141,8 +141,23 @@ class RopePlan:
         ramp_arr = None if ramp is None else (ctypes.c_double * 3)(*(float(x) for x in ramp))
         _lib.check(_lib.load().zl_rope_init(ctypes.byref(self.struct), self.head_dim, int(bool(interleaved)), n, arr,
                                             float(base), float(factor), ramp_arr, float(magnitude)), "zl_rope_init")
+        self._point()
+
+    def _point(self):
         self.ref = ctypes.byref(self.struct)
         self.address = ctypes.addressof(self.struct)
+
+    def __reduce__(self):
+        # copies and pickles point at a struct of their own
+        return _plan_of, (bytes(self.struct),)
+
+
+def _plan_of(data):
+    plan = RopePlan.__new__(RopePlan)
+    plan.struct = _lib.Rope.from_buffer_copy(data)
+    plan.n_axes, plan.head_dim = plan.struct.n_axes, plan.struct.head_dim
+    plan._point()
+    return plan
 
 
 def _positions(positions, plan, tokens, device):

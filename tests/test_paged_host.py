@@ -1,7 +1,10 @@
 """Host checks of rotary positions and the paged cache, without a GPU: plans,
 refusals of the C ABI and of the binding, and the oracle's own facts."""
+import copy
 import ctypes
+import gc
 import math
+import pickle
 
 import numpy as np
 import pytest
@@ -459,3 +462,22 @@ def test_append_with_a_status_refusals(lib):
     for i in range(len(args)):
         for bad in (None, "x", 2**80, 1.5, torch.zeros(0), [1]):
             assert fn(*args[:i], bad, *args[i + 1:]) is None
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, lambda x: pickle.loads(pickle.dumps(x))])
+def test_copies_of_plans_and_host_arrays_point_at_their_own_memory(how):
+    """A model that holds them is copied and pickled with them."""
+    a = zl.host_int32([0, 3, 7])
+    plan = zl.RopePlan(128, axes=(44, 42, 42), interleaved=True, factor=4.0, magnitude=1.25)
+    b, c = how(a), how(plan)
+    assert b.address == ctypes.addressof(b.array) and list(b) == [0, 3, 7] and (b.n, b.last) == (3, 7)
+    assert c.address == ctypes.addressof(c.struct) and bytes(c.struct) == bytes(plan.struct)
+    assert (c.n_axes, c.head_dim) == (plan.n_axes, plan.head_dim) == (3, 128)
+    want, address = bytes(plan.struct), c.address
+    del a, plan
+    gc.collect()
+    assert ctypes.string_at(address, len(want)) == want
+    if how is not copy.copy:
+        assert how({"plan": c})["plan"].address != c.address
+    assert zl._lib.load().zl_rope_fwd(c.ref, 64, 128, 64, 128, 64, 10, 0, 1, 1, _lib.ZL_BF16, 64, 128, 64, 128,
+                                      None) == _lib.ZL_OK
