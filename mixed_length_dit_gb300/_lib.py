@@ -223,10 +223,13 @@ class HostInt32:
 
 def int32_array(values):
     """Host int32 array for cu_seqlens (list, tuple, numpy or CPU tensor; an
-    array made by an earlier call is taken as it is)."""
+    array made by an earlier call is taken as it is).  ctypes would keep the low
+    bits of a number that does not fit."""
     if isinstance(values, HostInt32):
         return values.array, values.n
     vals = [int(x) for x in (values.tolist() if hasattr(values, "tolist") else values)]
+    if vals and not (-2**31 <= min(vals) and max(vals) < 2**31):
+        raise ValueError(f"numbers must fit 32 bits, got {max(vals, key=abs)}")
     return (ctypes.c_int32 * max(1, len(vals)))(*vals), len(vals)
 
 

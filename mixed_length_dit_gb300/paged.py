@@ -343,7 +343,9 @@ def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None
 def paged_attn_workspace_bytes(cu_seqlens_q, max_kv_len, num_heads, num_kv_heads, head_dim) -> int:
     lib = _lib.load()
     cu = _cu(cu_seqlens_q)
-    _int32(max_kv_len, "max_kv_len")
+    for value, name in ((max_kv_len, "max_kv_len"), (num_heads, "num_heads"), (num_kv_heads, "num_kv_heads"),
+                        (head_dim, "head_dim")):
+        _int32(value, name)
     out = ctypes.c_size_t(0)
     _lib.check(lib.zl_paged_attn_workspace_size(cu.array, cu.n - 1, max_kv_len, num_heads, num_kv_heads, head_dim,
                                                 ctypes.byref(out)), "zl_paged_attn_workspace_size")
@@ -400,6 +402,8 @@ def _tables(page_table, kv_lens, page_refs, page_size):
     dev = page_table.device
     slots, cols = page_table.shape
     pages = page_refs.shape[0]
+    for value, name in ((slots, "the table's rows"), (cols, "the table's columns"), (pages, "the number of pages")):
+        _int32(value, name)
     _exact(page_table, "page_table", (slots, cols), _I32, dev)
     _exact(kv_lens, "kv_lens", (slots,), _I32, dev)
     _exact(page_refs, "page_refs", (pages,), _I32, dev)
@@ -428,6 +432,7 @@ def _pool(cache, num_pages=None, device=None):
 def _list(t, name, device):
     if t.dim() != 1:
         raise ValueError(f"{name} must be a vector")
+    _int32(t.shape[0], f"the length of {name}")
     _exact(t, name, t.shape, _I32, device)
     return t.shape[0]
 

@@ -481,3 +481,28 @@ def test_copies_of_plans_and_host_arrays_point_at_their_own_memory(how):
         assert how({"plan": c})["plan"].address != c.address
     assert zl._lib.load().zl_rope_fwd(c.ref, 64, 128, 64, 128, 64, 10, 0, 1, 1, _lib.ZL_BF16, 64, 128, 64, 128,
                                       None) == _lib.ZL_OK
+
+
+def test_lists_and_sizes_past_32_bits_are_refused():
+    for bad in ([0, 2**32 + 5], [0, -2**32], [0, 2**31]):
+        with pytest.raises(ValueError, match="32 bits"):
+            zl.host_int32(bad)
+        with pytest.raises(ValueError, match="32 bits"):
+            zl.fwd_workspace_bytes(bad, [0, 5], 4, 64)
+    assert list(zl.host_int32([-2**31, 2**31 - 1])) == [-2**31, 2**31 - 1]
+    with pytest.raises(ValueError, match="32 bits"):
+        zl.RopePlan(64, axes=(2**32 + 64,))
+    for args, name in ((([0, 1], 16, 2**32 + 8, 8, 64), "num_heads"), (([0, 1], 16, 8, 2**32 + 8, 64), "num_kv_heads"),
+                       (([0, 1], 16, 8, 8, 2**32 + 64), "head_dim")):
+        with pytest.raises(ValueError, match=name):
+            zl.paged_attn_workspace_bytes(*args)
+    meta = lambda *s, dtype=torch.int32: torch.empty(s, dtype=dtype, device="meta")   # shapes without memory
+    cache, long = meta(1, 1, 16, 64, dtype=torch.bfloat16), meta(2**32 + 1)
+    with pytest.raises(ValueError, match="length of src"):
+        zl.pages_copy(cache, long, long)
+    with pytest.raises(ValueError, match="length of slots"):
+        zl.pages_free(meta(2, 4), meta(2), meta(8), long, 16)
+    with pytest.raises(ValueError, match="number of pages"):
+        zl.pages_extend(meta(2, 4), meta(2), long, meta(2), 16)
+    with pytest.raises(ValueError, match="columns"):
+        zl.pages_truncate(meta(2, 2**31), meta(2), meta(8), meta(2), 16)
