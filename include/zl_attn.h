@@ -539,8 +539,8 @@ zl_status zl_paged_attn_workspace_size(const int32_t* cu_seqlens_q, int32_t num_
  * q [Tq, H, d] bf16, q_stride elements between tokens; o [Tq, H, d] bf16,
  * lse [H, Tq] float32 (natural log, as zl_varlen_attn_fwd's, so that results
  * over other keys can be joined with zl_lse_merge).  max_kv_len: an upper
- * bound of kv_lens, at most table_cols * page_size (a longer sequence is cut
- * there and reported as ZL_EPAGE).  num_heads is a multiple of num_kv_heads
+ * bound of kv_lens, at most table_cols * page_size and 2^31 - 257 (a longer
+ * sequence is cut there and reported as ZL_EPAGE).  num_heads is a multiple of num_kv_heads
  * and at most 128 times as many.  Scores, the running maximum and sum, and the
  * output accumulate in float32; the probabilities are rounded to bf16 once for
  * the tensor cores.  The values of a sequence's tokens must be finite: a

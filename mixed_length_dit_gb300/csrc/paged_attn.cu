@@ -116,7 +116,7 @@ struct Range {
 // Keys [lo, hi) that the query at position p of a sequence of `len` sees.
 __device__ __forceinline__ void keys_of(const PagedAttnHead& a, int len, int p, int* lo, int* hi) {
   *hi = a.causal ? max(0, min(len, p + 1)) : len;
-  *lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+  *lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;   // p may be far below zero
 }
 
 // Blocks that queries [t0, t1) of the sequence see.

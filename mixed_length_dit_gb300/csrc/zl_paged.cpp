@@ -125,7 +125,8 @@ zl_status check_cu(const int32_t* cu, int32_t b, int64_t* total) {
 zl_status check_attn(const int32_t* cu_q, int32_t num_seqs, int32_t max_kv_len, int32_t nh, int32_t nk, int32_t hd,
                      int64_t* tq) {
   if (hd != 64 && hd != 128) return ZL_EUNSUPPORTED;
-  if (nk < 1 || nh < nk || nh > 4096 || nh % nk != 0 || max_kv_len < 0) return ZL_EINVAL;
+  if (nk < 1 || nh < nk || nh > 4096 || nh % nk != 0) return ZL_EINVAL;
+  if (max_kv_len < 0 || max_kv_len > zl::kMaxTokens) return ZL_EINVAL;   // the last block's end stays in int32
   if (nh / nk > zl::kBlockM) return ZL_EUNSUPPORTED;
   const zl_status st = check_cu(cu_q, num_seqs, tq);
   if (st != ZL_OK) return st;

@@ -506,3 +506,14 @@ def test_lists_and_sizes_past_32_bits_are_refused():
         zl.pages_extend(meta(2, 4), meta(2), long, meta(2), 16)
     with pytest.raises(ValueError, match="columns"):
         zl.pages_truncate(meta(2, 2**31), meta(2), meta(8), meta(2), 16)
+
+
+def test_attn_bounds_whose_last_block_ends_past_32_bits(lib):
+    arr, n = _lib.int32_array([0, 3])
+    c = _cache(table_cols=2**27 - 1)                  # a row holds 2^31 - 16 tokens
+    out = ctypes.c_size_t(0)
+    for most in (2**31 - 256, 2**31 - 17):
+        assert lib.zl_paged_attn_workspace_size(arr, n - 1, most, 4, 2, 64, ctypes.byref(out)) == _lib.ZL_EINVAL
+        assert lib.zl_paged_attn(ctypes.byref(c), P64, 256, arr, n - 1, most, 4, 0.125, 1, 0, P64, P64, P64, 1 << 40,
+                                 None) == _lib.ZL_EINVAL
+    assert lib.zl_paged_attn_workspace_size(arr, n - 1, 2**31 - 257, 4, 2, 64, ctypes.byref(out)) == _lib.ZL_OK
