@@ -414,9 +414,10 @@ typedef struct {
 
 /*
  * Fills *plan.  axis_dims (host, n_axes entries): the rotated columns of each
- * axis, even and >= 2, their sum rot_dim <= head_dim.  base > 1, factor > 0,
- * magnitude finite and not 0.  ramp: NULL, or {low, high, length} with
- * 0 <= low < high and length > 0.  Host only.
+ * axis, even and >= 2, their sum rot_dim <= head_dim.  base > 1, factor > 0 (the
+ * scaled frequencies must be finite), magnitude finite and not 0 in float32.
+ * ramp: NULL, or {low, high, length} with 0 <= low < high and length > 0.  Host
+ * only.
  */
 zl_status zl_rope_init(zl_rope_t* plan, int32_t head_dim, int32_t interleaved, int32_t n_axes,
                        const int32_t* axis_dims, double base, double factor, const double* ramp,

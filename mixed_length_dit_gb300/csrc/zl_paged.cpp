@@ -248,7 +248,8 @@ zl_status zl_rope_init(zl_rope_t* plan, int32_t head_dim, int32_t interleaved, i
   if (interleaved != 0 && interleaved != 1) return ZL_EINVAL;
   if (n_axes < 1 || n_axes > ZL_ROPE_MAX_AXES) return ZL_EINVAL;
   if (!(base > 1.0) || !std::isfinite(base) || !(factor > 0.0) || !std::isfinite(factor)) return ZL_EINVAL;
-  if (!std::isfinite(magnitude) || magnitude == 0.0 || !std::isfinite(static_cast<float>(magnitude))) return ZL_EINVAL;
+  const float m = static_cast<float>(magnitude);     // what the kernels multiply by
+  if (!std::isfinite(m) || m == 0.f) return ZL_EINVAL;
   if (ramp) {
     for (int i = 0; i < 3; ++i)
       if (!std::isfinite(ramp[i])) return ZL_EINVAL;
@@ -266,7 +267,7 @@ zl_status zl_rope_init(zl_rope_t* plan, int32_t head_dim, int32_t interleaved, i
   p.rot_dim = static_cast<int32_t>(rot);
   p.interleaved = interleaved;
   p.n_axes = n_axes;
-  p.magnitude = static_cast<float>(magnitude);
+  p.magnitude = m;
   const double two_pi = 6.283185307179586476925;
   int32_t pair = 0;
   for (int32_t a = 0; a < n_axes; ++a) {
@@ -279,6 +280,7 @@ zl_status zl_rope_init(zl_rope_t* plan, int32_t head_dim, int32_t interleaved, i
       } else {
         f /= factor;
       }
+      if (!std::isfinite(f)) return ZL_EINVAL;         // a factor near zero
       // turns per position, whole turns dropped, as a 64-bit fraction
       double t = f / two_pi;
       t -= std::floor(t);

@@ -517,3 +517,11 @@ def test_attn_bounds_whose_last_block_ends_past_32_bits(lib):
         assert lib.zl_paged_attn(ctypes.byref(c), P64, 256, arr, n - 1, most, 4, 0.125, 1, 0, P64, P64, P64, 1 << 40,
                                  None) == _lib.ZL_EINVAL
     assert lib.zl_paged_attn_workspace_size(arr, n - 1, 2**31 - 257, 4, 2, 64, ctypes.byref(out)) == _lib.ZL_OK
+
+
+@pytest.mark.parametrize("kw", [{"factor": 1e-320}, {"factor": 1e-320, "ramp": (1.0, 4.0, 1.0)}, {"magnitude": 1e-60},
+                                {"magnitude": -1e-60}, {"magnitude": float("nan")}])
+def test_plans_whose_numbers_overflow_or_vanish(kw):
+    with pytest.raises(zl.ZlError) as e:
+        zl.RopePlan(64, **kw)
+    assert e.value.status == _lib.ZL_EINVAL
