@@ -171,7 +171,7 @@ def load() -> ctypes.CDLL:
     lib.zl_pages_truncate.argtypes = [tabp, vp, vp]
     lib.zl_pages_compact.argtypes = [poolp, tabp, vp, vp, c_sz, vp]
     lib.zl_pages_copy.argtypes = [poolp, vp, vp, c_i32, vp]
-    for name in EXPORTS[-12:]:
+    for name in EXPORTS[EXPORTS.index("zl_rope_init"):]:
         getattr(lib, name).restype = c_i32
     _lib = lib
     return lib

@@ -525,3 +525,11 @@ def test_plans_whose_numbers_overflow_or_vanish(kw):
     with pytest.raises(zl.ZlError) as e:
         zl.RopePlan(64, **kw)
     assert e.value.status == _lib.ZL_EINVAL
+
+
+def test_every_entry_is_declared_to_ctypes(lib):
+    """No call falls back on what ctypes makes of undeclared arguments."""
+    for name in _lib.EXPORTS:
+        fn = getattr(lib, name)
+        assert fn.argtypes is not None, name
+        assert fn.restype in (ctypes.c_int32, ctypes.c_int64, ctypes.c_char_p), name
