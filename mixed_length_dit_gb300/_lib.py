@@ -182,11 +182,15 @@ def bind():
     global _bind
     if _bind is None:
         load()
+        import torch
+        mend = "run `python -m mixed_length_dit_gb300.build --force`"
         try:
             from . import _bind as module
         except ImportError as e:
-            raise RuntimeError(f"{PKG}/_bind.so is missing or does not fit this PyTorch: run "
-                               "`python -m mixed_length_dit_gb300.build --force`") from e
+            raise RuntimeError(f"{PKG}/_bind.so is missing or does not fit this PyTorch: {mend}") from e
+        built_for = getattr(module, "torch_version", "another PyTorch")
+        if built_for != str(torch.__version__):
+            raise RuntimeError(f"{PKG}/_bind.so was built for {built_for}, this is {torch.__version__}: {mend}")
         _bind = module
     return _bind
 

@@ -419,4 +419,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, null
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bind() { return PyModule_Create(&module); }
+// It lays tensors out as the PyTorch did that it was compiled against.
+PyMODINIT_FUNC PyInit__bind() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", ZL_TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    m = nullptr;
+  }
+  return m;
+}

@@ -26,6 +26,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libzl_attn.so")
 BIND_SRC = os.path.join(PKG, "binding", "bind.cpp")
 BIND = os.path.join(PKG, "_bind.so")
+BIND_FOR = os.path.join(BUILD, "bind.torch")    # the version of PyTorch that _bind.so was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -54,6 +55,19 @@ def _stale(obj, src, hdr_mtime):
     return os.path.getmtime(obj) < max(os.path.getmtime(src), hdr_mtime)
 
 
+def _torch_version():
+    from importlib.metadata import version
+    return version("torch")
+
+
+def _bind_stale(hdr_mtime):
+    """Sources newer than _bind.so, or another PyTorch than the one it was built for."""
+    if _stale(BIND, BIND_SRC, hdr_mtime) or not os.path.exists(BIND_FOR):
+        return True
+    with open(BIND_FOR) as f:
+        return f.read() != _torch_version()
+
+
 def _bind_commands():
     """Compiles and links _bind.so, against the PyTorch that runs this."""
     import sysconfig
@@ -65,6 +79,7 @@ def _bind_commands():
     cxx = shutil.which("g++") or "g++"
     obj = os.path.join(BUILD, "bind.cpp.o")
     return ([cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             f'-DZL_TORCH_VERSION="{torch.__version__}"',
              *(f"-I{p}" for p in inc), "-c", BIND_SRC, "-o", obj],
             [cxx, "-shared", obj, "-o", BIND + ".tmp", "-L" + os.path.join(base, "lib"), "-L" + PKG, "-lzl_attn",
              "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
@@ -93,7 +108,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             jobs.append(cmd)
     units = len(jobs)
     bind_link = None
-    if force or _stale(BIND, BIND_SRC, hdr_mtime):
+    if force or _bind_stale(hdr_mtime):
         compile_, bind_link = _bind_commands()
         jobs.insert(0, compile_)
     if jobs:
@@ -112,6 +127,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if bind_link:
         _link(bind_link)
         os.replace(BIND + ".tmp", BIND)
+        with open(BIND_FOR, "w") as f:
+            f.write(_torch_version())
     return LIB
 
 

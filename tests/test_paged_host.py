@@ -533,3 +533,17 @@ def test_every_entry_is_declared_to_ctypes(lib):
         fn = getattr(lib, name)
         assert fn.argtypes is not None, name
         assert fn.restype in (ctypes.c_int32, ctypes.c_int64, ctypes.c_char_p), name
+
+
+def test_a_binding_of_another_pytorch_is_refused_and_rebuilt(monkeypatch):
+    from mixed_length_dit_gb300 import build
+    assert _lib.bind().torch_version == torch.__version__
+    monkeypatch.setattr(_lib, "_bind", None)
+    monkeypatch.setattr(torch, "__version__", "1.0")
+    with pytest.raises(RuntimeError, match="built for .* this is 1.0: run"):
+        _lib.bind()
+    with pytest.raises(RuntimeError, match="built for"):
+        zl.paged_append(_b(1, 1, 64), _b(1, 1, 64), _b(1, 1, 16, 64), _b(1, 1, 16, 64), _i(1, 1), _i(1), [0, 1])
+    assert not build._bind_stale(0.0)
+    monkeypatch.setattr(build, "_torch_version", lambda: "1.0")
+    assert build._bind_stale(0.0)
