@@ -712,3 +712,14 @@ def test_items_whose_tiles_see_nothing_in_turn(heads, kv_heads, new, lens, kw, h
         o2, l2 = b.run(most=30000, **kw)
         assert torch.equal(o, o2) and torch.equal(lse, l2)
     zl.sync_check()
+
+
+@pytest.mark.parametrize("slots", [70, 700])
+def test_more_chunks_than_few_and_than_one_launch_holds(slots):
+    rng = np.random.default_rng(63)
+    new = [int(x) for x in rng.choice([0, 1, 129, 140], slots)]
+    lens = [n + int(x) for n, x in zip(new, rng.integers(0, 60, slots))]
+    b = Batch(new, lens, 1, 1, 64, 16, seed=63)
+    o, lse = b.run()
+    zl.sync_check()
+    b.check(o, lse)
