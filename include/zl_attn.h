@@ -392,9 +392,10 @@ zl_status zl_varlen_attn_bwd_static(
  *
  * so that with a ramp the pairs that turn more than `high` times over
  * `length` positions keep their frequency and those that turn less than `low`
- * times take the scaled one.  Frequencies are rounded to float64 once; beside
- * that, angles are exact to 2^-31 of a turn at every int32 position
- * (fixed-point fractions of a turn).  Positions may be negative.
+ * times take the scaled one.  A frequency in turns is computed in float64, a few
+ * roundings of 2^-53 of it each; beside that an angle is off by at most 2^-26 of
+ * a turn at every int32 position (a fixed-point product, exact mod 1, whose
+ * upper 32 bits become a float32).  Positions may be negative.
  */
 #define ZL_ROPE_MAX_PAIRS 64
 #define ZL_ROPE_MAX_AXES 4
@@ -549,7 +550,10 @@ zl_status zl_paged_attn_workspace_size(const int32_t* cu_seqlens_q, int32_t num_
  * keys may be anything where the mask hides them, and rows past its length
  * anything at all).  The work is spread over the SMs in equal shares whatever
  * the lengths (short ones, by max_kv_len and the window, are left whole); results
- * are the same on every run with the same lengths and arguments.  One or two
+ * are the same on every run with the same lengths and arguments.  Where a
+ * sequence's keys are cut follows from the whole batch, so its last bits may
+ * change with the sequences beside it and with max_kv_len.  o and lse overlap no
+ * other operand.  One or two
  * launches per 640 sequences of one query tile (up to 128 / (num_heads /
  * num_kv_heads) queries) and one or two per 640 longer ones.
  */

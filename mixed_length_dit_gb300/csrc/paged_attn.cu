@@ -57,8 +57,8 @@ constexpr int kReaders = 11;                   // 2 issuer threads, 8 softmax wa
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;
 // Key blocks of a CTA at least (SPLIT: one for each group).  With three, a token
-// over 1,000 keys takes 12.7 us instead of 11.5, a chunk of 200 over 1,536 21.6
-// instead of 20.7.
+// over 1,000 keys (24 / 8 heads, pages of 64; a call repeated on the same inputs)
+// takes 12.8 us instead of 11.7, a chunk of 200 over 1,536 21.7 instead of 20.6.
 constexpr int kMinBlocks = 2;
 constexpr float kLn2 = 0.6931471805599453f;
 

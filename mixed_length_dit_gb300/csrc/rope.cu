@@ -13,7 +13,7 @@
 // of step itself (made in float64: below 2^-54 of a turn, so 2^-34 at position
 // 2^20).  A float32 product pos * f would be off by 2^-24 of all the turns so
 // far, and float64 runs on a unit that this GPU has few of.  The top 32 bits go
-// to sincospi.
+// to sincospi as a float32, off by 2^-26 of a turn at most.
 //
 // A thread's unit is 16 columns for bf16, 8 for float32, as two 16-byte loads
 // and stores (the two halves' pieces, or two neighbours), so a head's units are

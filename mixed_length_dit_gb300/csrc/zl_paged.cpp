@@ -177,13 +177,21 @@ size_t attn_workspace(const int32_t* cu, int32_t num_seqs, int32_t group, int32_
 // SMs or lengths differ.  L key blocks bound a unit (the lengths themselves are
 // on the device), half of them is taken for the mean, so a share is about
 // `share`; whole is taken while L is at most 4 blocks (chunks: 5), and one for
-// every 16 units to be joined, above it.  Measured, whole and cut (us; 128
-// columns; L = 2, 4, 8, 16):
-//   8 units of a token       7.7 11.4    9.4 10.9   13.8 10.6   21.4 12.2
-//   32 units of a token      8.0 11.6   10.1 12.6   14.2 14.4   21.5 16.5
-//   128 units of 5 rows      8.9 12.1   10.9 14.5   15.2 21.9   26.7 33.9
-//   8 units of a chunk      10.2 14.9   13.7 18.5   20.9 18.9   34.3 21.2
-//   48 units of a chunk     10.4 15.3   13.8 22.9   20.5 25.9   34.2 29.9
+// every 16 units to be joined, above it.  Measured, whole and cut (us of the
+// GPU, a call repeated on the same inputs; d = 128, pages of 64; L = 2, 4, 8, 16,
+// every length at its bound):
+//   8 units of a token       7.9 10.6    9.8 11.2   13.2 11.7   21.9 13.6
+//   32 units of a token      8.0 11.1   10.2 12.7   14.3 14.4   22.0 16.7
+//   128 units of 5 rows      8.9 11.9   11.0 14.4   15.0 21.7   27.3 32.2
+//   8 units of a chunk      10.1 14.5   13.5 18.5   20.2 18.7   33.5 21.3
+//   48 units of a chunk     10.1 14.6   13.6 22.8   20.3 26.5   33.6 30.1
+// With pages of 16 a token's whole units are slower (eight boxes to a block), and
+// at 32 units and L = 8 the rule takes the slower way:
+//   8 units of a token       8.8 11.4   11.4 12.2   17.0 12.1   28.3 13.5
+//   32 units of a token      9.0 11.7   12.1 12.7   17.6 14.7   29.1 17.0
+//   128 units of 5 rows      9.5 12.3   12.6 15.0   18.1 23.0   30.8 33.7
+// It goes by the bound alone: a captured call whose bound is its table's width
+// is cut whatever the lengths come to.
 int32_t whole_units(const zl::PagedAttnArgs<zl::kMaxSegs>& a, bool pair) {
   const int32_t span = pair ? 2 * a.tile_tokens : a.tile_tokens;     // queries of a unit, at most
   int64_t units = 0;

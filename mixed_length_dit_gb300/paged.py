@@ -356,7 +356,12 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, max_kv_le
                softmax_scale=None, out=None, lse=None, workspace=None, stream=None):
     """Attention of each sequence's new queries q [Tq, H, d] over its cached
     keys and values.  The queries stand at the last positions below kv_lens;
-    max_kv_len (host) bounds kv_lens.  Returns (o [Tq, H, d], lse [H, Tq])."""
+    max_kv_len (host) bounds kv_lens.  Returns (o [Tq, H, d], lse [H, Tq]).
+
+    The same batch gives the same bits on every run; another batch around a
+    sequence, or another bound, may change its last ones.  Behind a refused
+    pages_extend the queries are taken for the last cached tokens: nothing is
+    written to the cache, and the results mean nothing."""
     cu = _cu(cu_seqlens_q)
     if stream is None:
         r = _short("attn", q, k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last, max_kv_len, causal,
