@@ -120,8 +120,8 @@ const char* zl_status_string(int32_t status);
 /* ABI version of this header: (major << 16) | minor.  2.0: head-sharded
  * tiles; 2.1 adds ZL_FWD_BF16_PARTIALS, zl_lse_merge_ex and the schedule
  * queries; 2.2 adds rotary positions (zl_rope_*) and the paged key/value cache
- * (zl_paged_*, zl_pages_*); 2.3 adds zl_paged_append_ex (no existing entry
- * changed). */
+ * (zl_paged_*, zl_pages_*); 2.3 adds zl_paged_append_ex; 2.4 the cache held in
+ * 4 bits (zl_paged_*_q4; no existing entry changed). */
 int32_t zl_version(void);
 
 /*
@@ -560,6 +560,77 @@ zl_status zl_paged_attn_workspace_size(const int32_t* cu_seqlens_q, int32_t num_
 zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_stride, const int32_t* cu_seqlens_q,
                         int32_t num_seqs, int32_t max_kv_len, int32_t num_heads, float softmax_scale, int32_t causal,
                         int32_t window, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A paged cache held in 4 bits.
+ *
+ * The same cache (zl_paged_cache_t, its tables and the page operations), whose
+ * pools hold a token's head in d / 2 + d / 32 bytes instead of 2 d.  Every 32
+ * columns (a group) of a key's or value's head share a step s, and x is held as
+ *
+ *     c = floor(x / s + 1/2), clamped to [-8, 7]     (0 where s is 0)
+ *
+ * and reads c s, a number that bf16 holds exactly.  s is the largest |x| of the
+ * group divided by 7 and rounded to four significant bits (halves up), a byte
+ * b = 8 e + m:
+ *
+ *     s = (8 + m) / 8 * 2^(e - 15),  or m / 8 * 2^-14 where e is 0;  s <= 61,440
+ *
+ * so that groups below 2^-18 * 7 in magnitude read as zero and those above
+ * 7 * 61,440 are clamped.  A group with an element that is not finite has the
+ * byte 255 and reads as NaN.
+ *
+ * k_pages and v_pages are [num_pages][Hk] blocks of page_size * (d/2 + d/32)
+ * bytes: the codes of the page's tokens, d/2 bytes each, and behind them their
+ * steps, d/32 bytes each, in the order of the groups.  A code is kept as c + 8 in
+ * four bits; eight columns, the first in the lowest bits, are a word W[q][i]
+ * (group q of d/32, i of 4).  A key's codes are its words in the order
+ * W[0][0], W[1][0], .. W[0][1], W[1][1], ..; a value's are its words' 16-bit
+ * halves H[q][i] (i of 8, the lower half of a word first) in the order H[0][0],
+ * H[1][0], .. H[0][1], ...  A pool's page_bytes, for zl_page_pool_t, are
+ * Hk * page_size * (d/2 + d/32).
+ */
+
+/*
+ * zl_paged_append_ex into a cache held in 4 bits: same arguments.  Turned keys
+ * are rounded to bf16 and then quantised, values and keys that are not turned
+ * as they are given.
+ */
+zl_status zl_paged_append_q4(const zl_paged_cache_t* cache, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs, const zl_rope_t* plan,
+                             const int32_t* positions, int64_t pos_stride, const void* q, int64_t q_stride,
+                             int32_t num_heads, void* q_out, int64_t q_out_stride, const int32_t* status,
+                             void* stream);
+
+/*
+ * Reads the last tokens of each sequence back, as the append has written them:
+ * sequence s's positions kv_lens[s] - n_s .. kv_lens[s] - 1 become the rows
+ * [cu_seqlens[s], cu_seqlens[s+1]) of k and v, bf16 [T, Hk, d] with k_stride /
+ * v_stride elements between tokens, exactly the values that are held.  A token
+ * that is not in the cache (a length below n_s, a page number out of range)
+ * reads as zeros and is reported as ZL_EPAGE.  One launch per 640 sequences.
+ */
+zl_status zl_paged_read_q4(const zl_paged_cache_t* cache, const int32_t* cu_seqlens, int32_t num_seqs, void* k,
+                           int64_t k_stride, void* v, int64_t v_stride, void* stream);
+
+/*
+ * Workspace needed by zl_paged_attn_q4 for this batch, in bytes.  Same argument
+ * rules as zl_paged_attn_q4.  Sequences of many rows take memory for their keys
+ * and values in bf16, of what max_kv_len and the window let them see: 4 d Hk
+ * bytes a token, 1 GiB or one sequence at a time.  Calls that are ordered may
+ * share a workspace, calls that may overlap must not.
+ */
+zl_status zl_paged_attn_q4_workspace_size(const int32_t* cu_seqlens_q, int32_t num_seqs, int32_t max_kv_len,
+                                          int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t window,
+                                          size_t* bytes);
+
+/*
+ * zl_paged_attn over a cache held in 4 bits: same arguments and rules.
+ */
+zl_status zl_paged_attn_q4(const zl_paged_cache_t* cache, const void* q, int64_t q_stride, const int32_t* cu_seqlens_q,
+                           int32_t num_seqs, int32_t max_kv_len, int32_t num_heads, float softmax_scale,
+                           int32_t causal, int32_t window, void* o, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 /* The tables of a cache as the page operations change them. */
 typedef struct {

@@ -33,7 +33,8 @@ EXPORTS = (
     "zl_varlen_attn_fwd_ex", "zl_lse_merge_ex", "zl_varlen_attn_fwd_schedule", "zl_varlen_attn_bwd_schedule",
     "zl_selftest_wait_timeout", "zl_rope_init", "zl_rope_fwd", "zl_rope_bwd", "zl_paged_append",
     "zl_paged_append_ex", "zl_paged_attn_workspace_size", "zl_paged_attn", "zl_pages_workspace_size", "zl_pages_extend", "zl_pages_fork",
-    "zl_pages_free", "zl_pages_truncate", "zl_pages_compact", "zl_pages_copy",
+    "zl_pages_free", "zl_pages_truncate", "zl_pages_compact", "zl_pages_copy", "zl_paged_append_q4", "zl_paged_read_q4",
+    "zl_paged_attn_q4_workspace_size", "zl_paged_attn_q4",
 )
 
 ZL_FWD_FUSED_MERGE = 1
@@ -164,6 +165,10 @@ def load() -> ctypes.CDLL:
     lib.zl_paged_attn_workspace_size.argtypes = [i32p, c_i32, c_i32, c_i32, c_i32, c_i32, szp]
     lib.zl_paged_attn.argtypes = [cachep, vp, c_i64, i32p, c_i32, c_i32, c_i32, c_f32, c_i32, c_i32, vp, vp, vp, c_sz,
                                   vp]
+    lib.zl_paged_append_q4.argtypes = append_args + [vp, vp]
+    lib.zl_paged_read_q4.argtypes = [cachep, i32p, c_i32, vp, c_i64, vp, c_i64, vp]
+    lib.zl_paged_attn_q4_workspace_size.argtypes = [i32p, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, szp]
+    lib.zl_paged_attn_q4.argtypes = lib.zl_paged_attn.argtypes
     lib.zl_pages_workspace_size.argtypes = [c_i32, szp]
     lib.zl_pages_extend.argtypes = [tabp, vp, vp, vp]
     lib.zl_pages_fork.argtypes = [poolp, tabp, vp, vp, c_i32, vp, vp, c_sz, vp]

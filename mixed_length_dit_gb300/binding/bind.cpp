@@ -166,7 +166,9 @@ PyObject* rope(Args& a) {
   return r;
 }
 
-// k_pages, v_pages, page_table, kv_lens of `seqs` sequences, checked.
+// k_pages, v_pages, page_table, kv_lens, checked.  Q4: pools held in 4 bits,
+// 17 bytes for every 32 columns of a head.
+template <bool Q4>
 bool cache_of(Args& a, zl_paged_cache_t* c, c10::Device* dev) {
   const at::Tensor* kp = a.t();
   const at::Tensor* vp = a.t();
@@ -174,34 +176,37 @@ bool cache_of(Args& a, zl_paged_cache_t* c, c10::Device* dev) {
   const at::Tensor* lens = a.t();
   if (!a.ok || kp->dim() != 4 || table->dim() != 2 || lens->dim() != 1 || !current(kp->device())) return false;
   *dev = kp->device();
-  if (kp->scalar_type() != at::kBFloat16 || vp->scalar_type() != at::kBFloat16 || vp->device() != *dev) return false;
+  constexpr auto type = Q4 ? at::kByte : at::kBFloat16;
+  if (kp->scalar_type() != type || vp->scalar_type() != type || vp->device() != *dev) return false;
   if (kp->sizes() != vp->sizes() || !kp->is_contiguous() || !vp->is_contiguous()) return false;
   if (!ints(*table, *dev) || !ints(*lens, *dev) || lens->size(0) != table->size(0)) return false;
   for (const int64_t x : {kp->size(0), kp->size(1), kp->size(2), kp->size(3), table->size(0), table->size(1)})
     if (x > INT32_MAX) return false;
+  const int64_t row = kp->size(3);
+  if (Q4 && row != 34 && row != 68) return false;
   *c = zl_paged_cache_t{kp->data_ptr(), vp->data_ptr(), table->data_ptr<int32_t>(), lens->data_ptr<int32_t>(),
                         static_cast<int32_t>(table->size(1)), static_cast<int32_t>(kp->size(0)),
                         static_cast<int32_t>(kp->size(2)), static_cast<int32_t>(kp->size(1)),
-                        static_cast<int32_t>(kp->size(3)), 0};
+                        static_cast<int32_t>(Q4 ? row / 17 * 32 : row), 0};
   return true;
 }
 
 // k, v, the cache, its tables, cu (address, entries, last), q | None, plan | 0;
-// STATUS: and the status of the extend before it
-template <bool STATUS>
+// STATUS: and the status of the extend before it (Q4: or None)
+template <bool STATUS, bool Q4>
 PyObject* append(Args& a) {
   const at::Tensor* k = a.t();
   const at::Tensor* v = a.t();
   zl_paged_cache_t c;
   c10::Device dev(c10::kCPU);
   const at::Tensor* lens = a.ok && a.i + 3 < a.n ? tensor(a.v[a.i + 3]) : nullptr;
-  if (!lens || !cache_of(a, &c, &dev)) return none();
+  if (!lens || !cache_of<Q4>(a, &c, &dev)) return none();
   const auto* cu = static_cast<const int32_t*>(a.pointer());
   const int32_t n = a.int32();
   const int64_t tokens = a.integer();
   const at::Tensor* q = a.maybe();
   const auto* plan = static_cast<const zl_rope_t*>(a.pointer());
-  const at::Tensor* extended = STATUS ? a.t() : nullptr;
+  const at::Tensor* extended = !STATUS ? nullptr : Q4 ? a.maybe() : a.t();
   if (!a.done() || lens->size(0) != n - 1 || tokens == 0) return none();
   if (extended && (!ints(*extended, dev) || extended->dim() != 1 || extended->size(0) != 1)) return none();
   const int64_t ks = rows(*k, tokens, c.num_kv_heads, c.head_dim, at::kBFloat16, dev);
@@ -218,9 +223,10 @@ PyObject* append(Args& a) {
   {
     Unlocked u;
     if (q) qo = fresh(*q, {tokens, nq, c.head_dim}, at::kBFloat16);
-    st = zl_paged_append_ex(&c, k->data_ptr(), ks, v->data_ptr(), vs, cu, n - 1, plan, nullptr, 0,
-                            q ? q->data_ptr() : nullptr, qs, static_cast<int32_t>(nq), q ? qo.data_ptr() : nullptr,
-                            nq * c.head_dim, extended ? extended->data_ptr<int32_t>() : nullptr, stream_of(dev));
+    const auto fn = Q4 ? zl_paged_append_q4 : zl_paged_append_ex;
+    st = fn(&c, k->data_ptr(), ks, v->data_ptr(), vs, cu, n - 1, plan, nullptr, 0, q ? q->data_ptr() : nullptr, qs,
+            static_cast<int32_t>(nq), q ? qo.data_ptr() : nullptr, nq * c.head_dim,
+            extended ? extended->data_ptr<int32_t>() : nullptr, stream_of(dev));
   }
   if (st != ZL_OK) return status(st);
   // what was asked for, in a tuple: None alone means the long way
@@ -230,14 +236,44 @@ PyObject* append(Args& a) {
   return r;
 }
 
+// the cache, its tables, cu (address, entries, last)
+PyObject* read_q4(Args& a) {
+  zl_paged_cache_t c;
+  c10::Device dev(c10::kCPU);
+  const at::Tensor* like = a.n > 3 ? tensor(a.v[0]) : nullptr;
+  const at::Tensor* lens = a.n > 3 ? tensor(a.v[3]) : nullptr;
+  if (!like || !lens || !cache_of<true>(a, &c, &dev)) return none();
+  const auto* cu = static_cast<const int32_t*>(a.pointer());
+  const int32_t n = a.int32();
+  const int64_t tokens = a.integer();
+  if (!a.done() || lens->size(0) != n - 1) return none();
+  at::Tensor k, v;
+  zl_status st;
+  {
+    Unlocked u;
+    k = fresh(*like, {tokens, c.num_kv_heads, c.head_dim}, at::kBFloat16);
+    v = fresh(*like, {tokens, c.num_kv_heads, c.head_dim}, at::kBFloat16);
+    const int64_t stride = int64_t(c.num_kv_heads) * c.head_dim;
+    st = zl_paged_read_q4(&c, cu, n - 1, k.data_ptr(), stride, v.data_ptr(), stride, stream_of(dev));
+  }
+  if (st != ZL_OK) return status(st);
+  PyObject* x = THPVariable_Wrap(std::move(k));
+  PyObject* y = THPVariable_Wrap(std::move(v));
+  PyObject* r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
+  Py_XDECREF(x);
+  Py_XDECREF(y);
+  return r;
+}
+
 // q, the cache, its tables, cu (address, entries, last), max_kv_len, causal,
 // window, scale, out | None, lse | None, workspace | None
+template <bool Q4>
 PyObject* attn(Args& a) {
   const at::Tensor* q = a.t();
   zl_paged_cache_t c;
   c10::Device dev(c10::kCPU);
   const at::Tensor* lens = a.ok && a.i + 3 < a.n ? tensor(a.v[a.i + 3]) : nullptr;
-  if (!lens || !cache_of(a, &c, &dev)) return none();
+  if (!lens || !cache_of<Q4>(a, &c, &dev)) return none();
   const auto* cu = static_cast<const int32_t*>(a.pointer());
   const int32_t n = a.int32();
   const int64_t tq = a.integer();
@@ -273,13 +309,15 @@ PyObject* attn(Args& a) {
     if (!lse) l = fresh(*q, {nh, tq}, at::kFloat);
     if (!ws) {
       size_t bytes = 0;
-      st = zl_paged_attn_workspace_size(cu, n - 1, most, heads, c.num_kv_heads, c.head_dim, &bytes);
+      st = Q4 ? zl_paged_attn_q4_workspace_size(cu, n - 1, most, heads, c.num_kv_heads, c.head_dim, window, &bytes)
+              : zl_paged_attn_workspace_size(cu, n - 1, most, heads, c.num_kv_heads, c.head_dim, &bytes);
       if (st == ZL_OK) w = fresh(*q, {static_cast<int64_t>(bytes)}, at::kByte);
     }
     if (st == ZL_OK) {
       const Scratch scratch(&w, dev);
-      st = zl_paged_attn(&c, q->data_ptr(), qs, cu, n - 1, most, heads, static_cast<float>(scale), causal ? 1 : 0,
-                         window, o.data_ptr(), l.data_ptr<float>(), scratch.p, scratch.bytes, stream_of(dev));
+      const auto fn = Q4 ? zl_paged_attn_q4 : zl_paged_attn;
+      st = fn(&c, q->data_ptr(), qs, cu, n - 1, most, heads, static_cast<float>(scale), causal ? 1 : 0, window,
+              o.data_ptr(), l.data_ptr<float>(), scratch.p, scratch.bytes, stream_of(dev));
     }
   }
   if (st != ZL_OK) return status(st);
@@ -410,9 +448,13 @@ PyCFunction fast() {
 }
 
 PyMethodDef methods[] = {
-    {"rope", fast<rope>(), METH_FASTCALL, nullptr},       {"append", fast<append<false>>(), METH_FASTCALL, nullptr},
-    {"append_after", fast<append<true>>(), METH_FASTCALL, nullptr},
-    {"attn", fast<attn>(), METH_FASTCALL, nullptr},       {"extend", fast<extend>(), METH_FASTCALL, nullptr},
+    {"rope", fast<rope>(), METH_FASTCALL, nullptr},
+    {"append", fast<append<false, false>>(), METH_FASTCALL, nullptr},
+    {"append_after", fast<append<true, false>>(), METH_FASTCALL, nullptr},
+    {"append_q4", fast<append<true, true>>(), METH_FASTCALL, nullptr},
+    {"read_q4", fast<read_q4>(), METH_FASTCALL, nullptr},
+    {"attn", fast<attn<false>>(), METH_FASTCALL, nullptr},
+    {"attn_q4", fast<attn<true>>(), METH_FASTCALL, nullptr}, {"extend", fast<extend>(), METH_FASTCALL, nullptr},
     {"fork", fast<fork>(), METH_FASTCALL, nullptr},       {"compact", fast<compact>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

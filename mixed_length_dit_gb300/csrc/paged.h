@@ -53,6 +53,7 @@ struct RopeHead {
 // N sequences; N = 0: no append.
 template <int N>
 struct RopeArgs : RopeHead {
+  using Head = RopeHead;
   int32_t cu[N + 1];            // append: first token of each sequence of the launch
 };
 static_assert(sizeof(RopeArgs<kMaxSegs>) <= 32764, "rotary arguments exceed the kernel parameter space");
@@ -130,6 +131,60 @@ struct PagedMaps {
 };
 static_assert(sizeof(PagedAttnArgs<kMaxSegs>) + sizeof(PagedMaps) <= 32764, "paged attention arguments exceed the kernel parameter space");
 
+// Tokens read back from a cache held in 4 bits.
+struct ReadQ4Head {
+  const uint8_t* k_pages;       // [num_pages][nk] blocks of page_size tokens
+  const uint8_t* v_pages;
+  const int32_t* page_table;    // [seqs][table_cols]
+  const int32_t* kv_lens;       // [seqs]
+  void* k_out;                  // [T][nk][d] bf16
+  void* v_out;
+  int64_t k_stride, v_stride;   // elements between tokens
+  int64_t token0;               // first token of this launch
+  int64_t tokens;               // tokens of this launch
+  int32_t nk;
+  int32_t head_dim;
+  int32_t table_cols;
+  int32_t num_pages;
+  int32_t page_shift;
+  int32_t n_seqs;               // sequences of this launch
+  int32_t seq0;                 // table row of the launch's first sequence
+};
+
+template <int N>
+struct ReadQ4Args : ReadQ4Head {
+  using Head = ReadQ4Head;
+  int32_t cu[N + 1];            // first token of each sequence of the launch
+};
+
+// Sequences of a 4-bit cache unpacked for the bf16 attention: what each one's
+// queries see goes to seg_pages pages of kScratchPage tokens of its own.
+constexpr int kScratchPage = kBlockN;
+
+struct UnpackQ4Head {
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const int32_t* page_table;    // [seqs][table_cols]
+  const int32_t* kv_lens;       // [seqs]
+  void* k_out;                  // [segs * seg_pages][nk][kScratchPage][d] bf16
+  void* v_out;
+  int32_t* table;               // [seqs][scratch_cols]: the pages' numbers among those
+  int32_t nk;
+  int32_t table_cols;
+  int32_t num_pages;
+  int32_t page_shift;
+  int32_t max_kv_len;
+  int32_t window;
+  int32_t seg_pages;
+  int32_t scratch_cols;
+  int32_t n_segs;
+};
+
+template <int N>
+struct UnpackQ4Args : UnpackQ4Head {
+  PagedSeg segs[N];
+};
+
 // A pool of pages seen by the kernels that move whole pages.
 struct PagePool {
   uint8_t* base;                // groups x num_pages x page_bytes
@@ -167,6 +222,10 @@ cudaError_t launch_paged_attn(int head_dim, bool pair, const PagedMaps& maps, co
                               cudaStream_t stream);
 // Joins the split rows of a launch_paged_attn with the same arguments.
 cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnHead& args, cudaStream_t stream);
+// As launch_rope with args.append, into a cache held in 4 bits.
+cudaError_t launch_append_q4(const RopeArgs<kMaxSegs>& args, int num_sms, cudaStream_t stream);
+cudaError_t launch_read_q4(const ReadQ4Args<kMaxSegs>& args, int num_sms, cudaStream_t stream);
+cudaError_t launch_unpack_q4(int head_dim, const UnpackQ4Args<kMaxSegs>& args, cudaStream_t stream);
 cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const int32_t* dst, int32_t n, int num_sms,
                               cudaStream_t stream);
 cudaError_t launch_pages_extend(const PageTable& t, const int32_t* counts, int32_t* status, cudaStream_t stream);
@@ -188,6 +247,7 @@ constexpr uint32_t kErrBadPage = 32u;
 uint32_t rope_take_error();
 uint32_t pages_take_error();
 uint32_t paged_attn_take_error();
+uint32_t pages_q4_take_error();
 uint32_t paged_take_error();
 
 }  // namespace zl

@@ -22,6 +22,7 @@
 // Plans whose pairs do not fill such units take units of one pair.
 #include "common.cuh"
 #include "paged.h"
+#include "rope.cuh"
 
 namespace zl {
 namespace {
@@ -160,26 +161,14 @@ rope_kernel(const __grid_constant__ RopeArgs<SEQS> a, int tokens_per_block, int 
 
   if constexpr (APPEND) {
     if (threadIdx.x < nt) {
-      const int64_t t = a.token0 + t0 + threadIdx.x;
-      int lo = 0, hi = a.n_seqs - 1;           // the last sequence that starts at or before t
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
-      }
-      const int64_t seq = a.seq0 + lo;
-      const int n = a.cu[lo + 1] - a.cu[lo];
-      const int len = a.kv_lens[seq];
-      const int64_t p = static_cast<int64_t>(len) - n + (t - a.cu[lo]);
-      int64_t row = -1;
+      const Place at = place_of(a, a.token0 + t0 + threadIdx.x);
       const bool room = !a.status || *a.status == 0;   // else the lengths do not count the new tokens
-      if (room && p >= 0 && (p >> a.page_shift) < a.table_cols) {
-        const int page = a.page_table[seq * a.table_cols + (p >> a.page_shift)];
-        if (page >= 0 && page < a.num_pages)
-          row = ((static_cast<int64_t>(page) * a.nk) << a.page_shift) + (p & ((1 << a.page_shift) - 1));
-      }
+      const int64_t row = room && at.page >= 0 ? ((static_cast<int64_t>(at.page) * a.nk) << a.page_shift) +
+                                                     (at.pos & ((1 << a.page_shift) - 1))
+                                               : -1;
       if (row < 0) atomicOr(&g_rope_err, ERR_BAD_PAGE);
       page_row[threadIdx.x] = row;
-      pos_of[threadIdx.x] = static_cast<int32_t>(p);
+      pos_of[threadIdx.x] = static_cast<int32_t>(at.pos);
     }
     __syncthreads();
   }
@@ -236,20 +225,12 @@ rope_kernel(const __grid_constant__ RopeArgs<SEQS> a, int tokens_per_block, int 
 
   for (int y = threadIdx.x; y < nt * half; y += kRopeThreads) {
     const int tp = y / half, i = y - tp * half;
-    int axis = 0;
-    while (axis < a.rope.n_axes - 1 && i >= a.rope.pair_end[axis]) ++axis;
     int64_t p;
     if (APPEND && !a.positions)
       p = pos_of[tp];
     else
-      p = a.positions[axis * a.pos_stride + a.token0 + t0 + tp];
-    const uint64_t phase = static_cast<uint64_t>(p) * a.rope.step[i];
-    // signed fraction of a turn in the top 32 bits; in half turns for sincospi
-    const float x2 = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;
-    float s, c;
-    sincospif(x2, &s, &c);
-    const float m = a.rope.magnitude;
-    cs[tp][cs_at<U::N>(i)] = make_float2(c * m, (a.inverse ? -s : s) * m);
+      p = a.positions[rope_axis(a.rope, i) * a.pos_stride + a.token0 + t0 + tp];
+    cs[tp][cs_at<U::N>(i)] = rope_turn(a.rope, p, i, a.inverse != 0);
   }
   __syncthreads();
   while (has0) {                               // units come in order: no u1 without a u0

@@ -146,12 +146,19 @@ struct Launch {
 
 int32_t tile_tokens(int32_t group) { return zl::kBlockM / group; }
 
+// The sequences of a call that a launch takes: of [first, end) those with more
+// than `above` rows (queries times the heads of a key head).
+struct Chosen {
+  int32_t first, end;
+  int64_t above;
+};
+
 // The next launch of a kind: as many sequences from *i on as it holds.
-Launch next_launch(const int32_t* cu, int32_t num_seqs, int32_t group, bool pair, int32_t* i) {
+Launch next_launch(const int32_t* cu, const Chosen& from, int32_t group, bool pair, int32_t* i) {
   Launch l;
-  for (; *i < num_seqs && l.segs < zl::kMaxSegs; ++*i) {
+  for (; *i < from.end && l.segs < zl::kMaxSegs; ++*i) {
     const int32_t n = cu[*i + 1] - cu[*i];
-    if (n == 0 || (n > tile_tokens(group)) != pair) continue;
+    if (n == 0 || int64_t(n) * group <= from.above || (n > tile_tokens(group)) != pair) continue;
     ++l.segs;
     l.slot_rows = pair ? 2 * zl::kBlockM : std::max(l.slot_rows, n * group);
   }
@@ -159,11 +166,11 @@ Launch next_launch(const int32_t* cu, int32_t num_seqs, int32_t group, bool pair
 }
 
 // The launches run one after another and share the workspace.
-size_t attn_workspace(const int32_t* cu, int32_t num_seqs, int32_t group, int32_t hd) {
+size_t attn_workspace(const int32_t* cu, const Chosen& from, int32_t group, int32_t hd) {
   size_t need = 0;
   for (const bool pair : {false, true})
-    for (int32_t i = 0; i < num_seqs;) {
-      const Launch l = next_launch(cu, num_seqs, group, pair, &i);
+    for (int32_t i = from.first; i < from.end;) {
+      const Launch l = next_launch(cu, from, group, pair, &i);
       if (l.segs == 0) continue;
       const size_t rows = static_cast<size_t>(2) * zl::kPagedCtas * l.slot_rows;
       need = std::max(need, zl::kPagedCtas * sizeof(zl::PagedJoin) + rows * (hd + 1) * sizeof(float));
@@ -232,6 +239,281 @@ zl_status check_workspace(int32_t num_pages, const void* ws, size_t bytes) {
   return aligned16(ws) ? ZL_OK : ZL_EALIGN;
 }
 
+// Appends to a cache in bf16, or in 4 bits.
+zl_status append(const zl_paged_cache_t* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                 const int32_t* cu_seqlens, int32_t num_seqs, const zl_rope_t* plan, const int32_t* positions,
+                 int64_t pos_stride, const void* q, int64_t q_stride, int32_t num_heads, void* q_out,
+                 int64_t q_out_stride, const int32_t* status, void* stream, bool q4) {
+  zl_status st = check_cache(cache);
+  if (st != ZL_OK) return st;
+  int64_t tokens = 0;
+  st = check_cu(cu_seqlens, num_seqs, &tokens);
+  if (st != ZL_OK) return st;
+  if (plan && (!plan_ok(*plan) || plan->head_dim != cache->head_dim)) return ZL_EINVAL;
+  if (plan && plan->n_axes > 1 && !positions) return ZL_EINVAL;
+  if (positions && (!plan || pos_stride < (plan->n_axes > 1 ? tokens : 0))) return ZL_EINVAL;
+  if (num_heads < 0 || num_heads > 4096 || (num_heads > 0) != (q != nullptr)) return ZL_EINVAL;
+  if (tokens == 0) return ZL_OK;
+  st = check_cache_pointers(cache);
+  if (st != ZL_OK) return st;
+  if (misaligned4(positions) || misaligned4(status)) return ZL_EALIGN;
+  const int32_t hd = cache->head_dim;
+  st = check_rows(k, k_stride, cache->num_kv_heads, hd, tokens, 2);
+  if (st == ZL_OK) st = check_rows(v, v_stride, cache->num_kv_heads, hd, tokens, 2);
+  if (st == ZL_OK && q) st = check_rows(q, q_stride, num_heads, hd, tokens, 2);
+  if (st == ZL_OK && q) st = check_rows(q_out, q_out_stride, num_heads, hd, tokens, 2);
+  if (st != ZL_OK) return st;
+  int sms = 0;
+  st = device_sms(&sms);
+  if (st != ZL_OK) return st;
+  static thread_local RopeArgs a;
+  static_cast<zl::RopeHead&>(a) = zl::RopeHead();
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.k_out = cache->k_pages;
+  a.v_out = cache->v_pages;
+  a.positions = positions;
+  a.pos_stride = pos_stride;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out_stride = q_out_stride;
+  a.nq = num_heads;
+  a.nk = cache->num_kv_heads;
+  a.head_dim = hd;
+  a.elem_bytes = 2;
+  a.append = 1;
+  a.skip_kept = q && q == q_out && q_stride == q_out_stride;
+  a.page_table = cache->page_table;
+  a.kv_lens = cache->kv_lens;
+  a.status = status;
+  a.table_cols = cache->table_cols;
+  a.num_pages = cache->num_pages;
+  a.page_shift = shift_of(cache->page_size);
+  if (plan) a.rope = *plan;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  for (int32_t s0 = 0; s0 < num_seqs; s0 += zl::kMaxSegs) {
+    a.seq0 = s0;
+    a.n_seqs = std::min(num_seqs - s0, zl::kMaxSegs);
+    for (int32_t i = 0; i <= a.n_seqs; ++i) a.cu[i] = cu_seqlens[s0 + i];
+    a.token0 = a.cu[0];
+    a.tokens = a.cu[a.n_seqs] - a.cu[0];
+    if (a.tokens == 0) continue;
+    st = q4 ? launch_counted("paged_append_q4", s, [&] { return zl::launch_append_q4(a, sms, s); })
+            : launch_counted("paged_append", s, [&] { return zl::launch_rope(a, sms, s); });
+    if (st != ZL_OK) return st;
+  }
+  return ZL_OK;
+}
+
+// The arguments of an attention over a cache, and the checks of a call.
+struct Attend {
+  const zl_paged_cache_t* cache;
+  const void* q;
+  int64_t q_stride;
+  const int32_t* cu;
+  int32_t num_seqs;
+  int32_t max_kv_len;
+  int32_t num_heads;
+  float scale;
+  int32_t causal;
+  int32_t window;
+  void* o;
+  float* lse;
+  cudaStream_t stream;
+  int64_t tq = 0;
+
+  int32_t group() const { return num_heads / cache->num_kv_heads; }
+  int32_t queries(int32_t s) const { return cu[s + 1] - cu[s]; }
+  zl_status check();
+};
+
+zl_status Attend::check() {
+  zl_status st = check_cache(cache);
+  if (st != ZL_OK) return st;
+  st = check_attn(cu, num_seqs, max_kv_len, num_heads, cache->num_kv_heads, cache->head_dim, &tq);
+  if (st != ZL_OK) return st;
+  if (max_kv_len > int64_t(cache->table_cols) * cache->page_size) return ZL_EINVAL;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ZL_EINVAL;
+  if ((causal != 0 && causal != 1) || window < 0) return ZL_EINVAL;
+  if (tq == 0) return ZL_OK;
+  st = check_cache_pointers(cache);
+  if (st != ZL_OK) return st;
+  if (!o || !lse) return ZL_EINVAL;
+  if (!aligned16(o) || misaligned4(lse)) return ZL_EALIGN;
+  return check_rows(q, q_stride, num_heads, cache->head_dim, tq, 2);
+}
+
+// The bf16 attention's launches over `cache`, the call's own or one that has been
+// unpacked from it.
+zl_status launch_attn(const Attend& c, const zl_paged_cache_t& cache, const Chosen& from, void* workspace) {
+  const int32_t hd = cache.head_dim, group = c.group();
+  cudaStream_t s = c.stream;
+  static thread_local zl::PagedAttnArgs<zl::kMaxSegs> a;      // ~21 KB: kept off the stack
+  static_cast<zl::PagedAttnHead&>(a) = zl::PagedAttnHead();
+  a.page_table = cache.page_table;
+  a.kv_lens = cache.kv_lens;
+  a.o = c.o;
+  a.lse = c.lse;
+  a.lse_stride = c.tq;
+  a.num_heads = c.num_heads;
+  a.num_kv_heads = cache.num_kv_heads;
+  a.group = group;
+  a.group_inv = (65536 + group - 1) / group;
+  a.tile_tokens = tile_tokens(group);
+  a.table_cols = cache.table_cols;
+  a.num_pages = cache.num_pages;
+  a.page_shift = shift_of(cache.page_size);
+  a.max_kv_len = c.max_kv_len;
+  a.causal = c.causal;
+  a.window = c.window < c.max_kv_len ? c.window : 0;   // one that reaches over every key is none (and stays in 32 bits)
+  a.scale_log2 = c.scale * 1.4426950408889634f;
+
+  // the maps that the call's kinds of sequences use
+  bool copies[3] = {false, false, false}, pairs = false;
+  for (int32_t i = from.first; i < from.end; ++i) {
+    const int64_t n = c.queries(i);
+    if (n == 0 || n * a.group <= from.above) continue;
+    pairs = pairs || n > a.tile_tokens;
+    const int64_t tile_rows = n * a.group;
+    copies[n > a.tile_tokens || tile_rows > 64 ? 0 : tile_rows > 32 ? 1 : 2] = true;
+  }
+  zl::PagedMaps maps;
+  const int64_t pool_rows = int64_t(cache.num_pages) * cache.num_kv_heads * cache.page_size;
+  const int box_rows = std::min(cache.page_size, zl::kBlockN);
+  bool ok = zl::make_map(&maps.k, cache.k_pages, pool_rows, 1, hd, box_rows) &&
+            zl::make_map(&maps.v, cache.v_pages, pool_rows, 1, hd, box_rows);
+  if (pairs)
+    ok = ok && zl::make_map_heads(&maps.o, c.o, c.tq, c.num_heads, hd, int64_t(c.num_heads) * hd, a.group, a.tile_tokens);
+  for (int i = 0; i < 3; ++i)
+    if (copies[i])
+      ok = ok && zl::make_map_heads(&maps.q[i], c.q, c.tq, c.num_heads, hd, c.q_stride, a.group,
+                                    zl::kBlockM / (1 << i) / a.group);
+  if (!ok) return ZL_ECUDA;
+
+  a.joins = static_cast<zl::PagedJoin*>(workspace);
+  a.o_part = reinterpret_cast<float*>(a.joins + zl::kPagedCtas);
+  for (const bool pair : {false, true}) {
+    for (int32_t i = from.first; i < from.end;) {
+      const int32_t first = i;
+      const Launch l = next_launch(c.cu, from, group, pair, &i);
+      if (l.segs == 0) continue;
+      a.slot_rows = l.slot_rows;
+      a.lse_part = a.o_part + int64_t(2) * zl::kPagedCtas * l.slot_rows * hd;
+      a.n_segs = 0;
+      for (int32_t x = first; x < i; ++x) {
+        const int32_t n = c.queries(x);
+        if (n > 0 && int64_t(n) * group > from.above && (n > a.tile_tokens) == pair)
+          a.segs[a.n_segs++] = zl::PagedSeg{x, c.cu[x], n};
+      }
+      a.whole = whole_units(a, pair);
+      zl_status st = launch_counted("paged_attn", s, [&] { return zl::launch_paged_attn(hd, pair, maps, a, s); });
+      if (st != ZL_OK) return st;
+      if (a.whole > 0) continue;
+      st = launch_counted("paged_join", s, [&] { return zl::launch_paged_join(hd, pair, a, s); });
+      if (st != ZL_OK) return st;
+    }
+  }
+  return ZL_OK;
+}
+
+// ------------------------------------------------------------------ attention over 4 bits
+// Sequences of more than kQ4Rows rows are unpacked to bf16, once for all of their
+// queries, and handed to the bf16 attention, a batch at a time: as many as
+// kScratchBytes hold, or one.
+constexpr int64_t kQ4Rows = 0;
+constexpr int64_t kScratchBytes = int64_t(1) << 30;
+
+struct Q4Plan {
+  int32_t chunks = 0;      // sequences that are unpacked
+  int32_t batch = 0;       // of them at a time
+  int32_t seg_pages = 0;   // pages of each
+  int32_t cols = 0;        // of the scratch table
+  size_t attn = 0;         // bytes of what the attentions leave to their joins
+  size_t table = 0;        // bytes of the scratch table
+  size_t pool = 0;         // bytes of the scratch keys, and of the values
+  size_t bytes() const { return attn + table + 2 * pool; }
+};
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+zl_status plan_q4(const int32_t* cu, int32_t num_seqs, int32_t max_kv_len, int32_t nh, int32_t nk, int32_t hd,
+                  int32_t window, Q4Plan* p) {
+  const int32_t group = nh / nk;
+  int32_t most = 0;
+  for (int32_t i = 0; i < num_seqs; ++i) {
+    const int32_t n = cu[i + 1] - cu[i];
+    if (int64_t(n) * group <= kQ4Rows) continue;
+    ++p->chunks;
+    most = std::max(most, n);
+  }
+  if (p->chunks > 0) {
+    const int64_t page = zl::kScratchPage;
+    const int64_t cols = (int64_t(max_kv_len) + page - 1) / page;
+    int64_t pages = cols;
+    if (window > 0) pages = std::min(pages, (int64_t(most) + window) / page + 2);
+    pages = std::max<int64_t>(pages, 1);
+    if (pages * nk * page > INT32_MAX) return ZL_EUNSUPPORTED;     // the pool's rows are numbered in int32
+    const int64_t each = pages * nk * page * hd * 2;               // keys, or values
+    p->seg_pages = static_cast<int32_t>(pages);
+    p->cols = static_cast<int32_t>(std::max<int64_t>(cols, 1));
+    p->batch = static_cast<int32_t>(std::min<int64_t>({kScratchBytes / (2 * each), INT32_MAX / (pages * nk * page),
+                                                       zl::kMaxSegs, p->chunks}));
+    p->batch = std::max(p->batch, 1);
+    p->table = up256(size_t(num_seqs) * p->cols * sizeof(int32_t));
+    p->pool = up256(size_t(p->batch) * each);
+  }
+  p->attn = up256(attn_workspace(cu, Chosen{0, num_seqs, kQ4Rows}, group, hd));
+  return ZL_OK;
+}
+
+zl_status launch_attn_q4(const Attend& c, const Q4Plan& p, void* workspace) {
+  const zl_paged_cache_t& cache = *c.cache;
+  auto* at = static_cast<uint8_t*>(workspace) + p.attn;
+  zl_paged_cache_t scratch = cache;
+  scratch.page_table = reinterpret_cast<int32_t*>(at);
+  scratch.k_pages = at + p.table;
+  scratch.v_pages = at + p.table + p.pool;
+  scratch.table_cols = p.cols;
+  scratch.page_size = zl::kScratchPage;
+  static thread_local zl::UnpackQ4Args<zl::kMaxSegs> a;
+  static_cast<zl::UnpackQ4Head&>(a) = zl::UnpackQ4Head();
+  a.k_pages = static_cast<const uint8_t*>(cache.k_pages);
+  a.v_pages = static_cast<const uint8_t*>(cache.v_pages);
+  a.page_table = cache.page_table;
+  a.kv_lens = cache.kv_lens;
+  a.k_out = scratch.k_pages;
+  a.v_out = scratch.v_pages;
+  a.table = reinterpret_cast<int32_t*>(at);
+  a.nk = cache.num_kv_heads;
+  a.table_cols = cache.table_cols;
+  a.num_pages = cache.num_pages;
+  a.page_shift = shift_of(cache.page_size);
+  a.max_kv_len = c.max_kv_len;
+  a.window = c.window < c.max_kv_len ? c.window : 0;
+  a.seg_pages = p.seg_pages;
+  a.scratch_cols = p.cols;
+  for (int32_t i = 0; i < c.num_seqs;) {
+    Chosen part{i, i, kQ4Rows};
+    a.n_segs = 0;
+    for (; i < c.num_seqs; ++i) {
+      if (int64_t(c.queries(i)) * c.group() <= kQ4Rows) continue;
+      if (a.n_segs == p.batch) break;
+      a.segs[a.n_segs++] = zl::PagedSeg{i, c.cu[i], c.queries(i)};
+    }
+    part.end = i;
+    if (a.n_segs == 0) break;
+    scratch.num_pages = a.n_segs * p.seg_pages;
+    zl_status st = launch_counted("paged_unpack_q4", c.stream,
+                                  [&] { return zl::launch_unpack_q4(cache.head_dim, a, c.stream); });
+    if (st == ZL_OK) st = launch_attn(c, scratch, part, workspace);
+    if (st != ZL_OK) return st;
+  }
+  return ZL_OK;
+}
+
 }  // namespace
 
 namespace zl {
@@ -240,8 +522,10 @@ uint32_t paged_take_error() {
   const uint32_t a = rope_take_error();
   const uint32_t b = pages_take_error();
   const uint32_t c = paged_attn_take_error();
-  if (a == 0xFFFFFFFFu || b == 0xFFFFFFFFu || c == 0xFFFFFFFFu) return 0xFFFFFFFFu;
-  return a | b | c;
+  const uint32_t d = pages_q4_take_error();
+  for (const uint32_t x : {a, b, c, d})
+    if (x == 0xFFFFFFFFu) return x;
+  return a | b | c | d;
 }
 
 }  // namespace zl
@@ -331,55 +615,48 @@ zl_status zl_paged_append_ex(const zl_paged_cache_t* cache, const void* k, int64
                              const int32_t* positions, int64_t pos_stride, const void* q, int64_t q_stride,
                              int32_t num_heads, void* q_out, int64_t q_out_stride, const int32_t* status,
                              void* stream) {
+  return append(cache, k, k_stride, v, v_stride, cu_seqlens, num_seqs, plan, positions, pos_stride, q, q_stride,
+                num_heads, q_out, q_out_stride, status, stream, false);
+}
+
+zl_status zl_paged_append_q4(const zl_paged_cache_t* cache, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs, const zl_rope_t* plan,
+                             const int32_t* positions, int64_t pos_stride, const void* q, int64_t q_stride,
+                             int32_t num_heads, void* q_out, int64_t q_out_stride, const int32_t* status,
+                             void* stream) {
+  return append(cache, k, k_stride, v, v_stride, cu_seqlens, num_seqs, plan, positions, pos_stride, q, q_stride,
+                num_heads, q_out, q_out_stride, status, stream, true);
+}
+
+zl_status zl_paged_read_q4(const zl_paged_cache_t* cache, const int32_t* cu_seqlens, int32_t num_seqs, void* k,
+                           int64_t k_stride, void* v, int64_t v_stride, void* stream) {
   zl_status st = check_cache(cache);
   if (st != ZL_OK) return st;
   int64_t tokens = 0;
   st = check_cu(cu_seqlens, num_seqs, &tokens);
-  if (st != ZL_OK) return st;
-  if (plan && (!plan_ok(*plan) || plan->head_dim != cache->head_dim)) return ZL_EINVAL;
-  if (plan && plan->n_axes > 1 && !positions) return ZL_EINVAL;
-  if (positions && (!plan || pos_stride < (plan->n_axes > 1 ? tokens : 0))) return ZL_EINVAL;
-  if (num_heads < 0 || num_heads > 4096 || (num_heads > 0) != (q != nullptr)) return ZL_EINVAL;
-  if (tokens == 0) return ZL_OK;
+  if (st != ZL_OK || tokens == 0) return st;
   st = check_cache_pointers(cache);
-  if (st != ZL_OK) return st;
-  if (misaligned4(positions) || misaligned4(status)) return ZL_EALIGN;
-  const int32_t hd = cache->head_dim;
-  st = check_rows(k, k_stride, cache->num_kv_heads, hd, tokens, 2);
-  if (st == ZL_OK) st = check_rows(v, v_stride, cache->num_kv_heads, hd, tokens, 2);
-  if (st == ZL_OK && q) st = check_rows(q, q_stride, num_heads, hd, tokens, 2);
-  if (st == ZL_OK && q) st = check_rows(q_out, q_out_stride, num_heads, hd, tokens, 2);
+  if (st == ZL_OK) st = check_rows(k, k_stride, cache->num_kv_heads, cache->head_dim, tokens, 2);
+  if (st == ZL_OK) st = check_rows(v, v_stride, cache->num_kv_heads, cache->head_dim, tokens, 2);
   if (st != ZL_OK) return st;
   int sms = 0;
   st = device_sms(&sms);
   if (st != ZL_OK) return st;
-  static thread_local RopeArgs a;
-  static_cast<zl::RopeHead&>(a) = zl::RopeHead();
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.q_out = q_out;
-  a.k_out = cache->k_pages;
-  a.v_out = cache->v_pages;
-  a.positions = positions;
-  a.pos_stride = pos_stride;
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.q_out_stride = q_out_stride;
-  a.nq = num_heads;
-  a.nk = cache->num_kv_heads;
-  a.head_dim = hd;
-  a.elem_bytes = 2;
-  a.append = 1;
-  a.skip_kept = q && q == q_out && q_stride == q_out_stride;
+  static thread_local zl::ReadQ4Args<zl::kMaxSegs> a;
+  static_cast<zl::ReadQ4Head&>(a) = zl::ReadQ4Head();
+  a.k_pages = static_cast<const uint8_t*>(cache->k_pages);
+  a.v_pages = static_cast<const uint8_t*>(cache->v_pages);
   a.page_table = cache->page_table;
   a.kv_lens = cache->kv_lens;
-  a.status = status;
+  a.k_out = k;
+  a.v_out = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.nk = cache->num_kv_heads;
+  a.head_dim = cache->head_dim;
   a.table_cols = cache->table_cols;
   a.num_pages = cache->num_pages;
   a.page_shift = shift_of(cache->page_size);
-  if (plan) a.rope = *plan;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int32_t s0 = 0; s0 < num_seqs; s0 += zl::kMaxSegs) {
     a.seq0 = s0;
@@ -388,7 +665,7 @@ zl_status zl_paged_append_ex(const zl_paged_cache_t* cache, const void* k, int64
     a.token0 = a.cu[0];
     a.tokens = a.cu[a.n_seqs] - a.cu[0];
     if (a.tokens == 0) continue;
-    st = launch_counted("paged_append", s, [&] { return zl::launch_rope(a, sms, s); });
+    st = launch_counted("paged_read_q4", s, [&] { return zl::launch_read_q4(a, sms, s); });
     if (st != ZL_OK) return st;
   }
   return ZL_OK;
@@ -401,103 +678,55 @@ zl_status zl_paged_attn_workspace_size(const int32_t* cu_seqlens_q, int32_t num_
   int64_t tq = 0;
   const zl_status st = check_attn(cu_seqlens_q, num_seqs, max_kv_len, num_heads, num_kv_heads, head_dim, &tq);
   if (st != ZL_OK) return st;
-  *bytes = attn_workspace(cu_seqlens_q, num_seqs, num_heads / num_kv_heads, head_dim);
+  *bytes = attn_workspace(cu_seqlens_q, Chosen{0, num_seqs, 0}, num_heads / num_kv_heads, head_dim);
   return ZL_OK;
 }
 
 zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_stride, const int32_t* cu_seqlens_q,
                         int32_t num_seqs, int32_t max_kv_len, int32_t num_heads, float softmax_scale, int32_t causal,
                         int32_t window, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-  zl_status st = check_cache(cache);
-  if (st != ZL_OK) return st;
-  int64_t tq = 0;
-  st = check_attn(cu_seqlens_q, num_seqs, max_kv_len, num_heads, cache->num_kv_heads, cache->head_dim, &tq);
-  if (st != ZL_OK) return st;
-  if (max_kv_len > int64_t(cache->table_cols) * cache->page_size) return ZL_EINVAL;
-  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return ZL_EINVAL;
-  if ((causal != 0 && causal != 1) || window < 0) return ZL_EINVAL;
-  if (tq == 0) return ZL_OK;
-  st = check_cache_pointers(cache);
-  if (st != ZL_OK) return st;
-  if (!o || !lse) return ZL_EINVAL;
-  if (!aligned16(o) || misaligned4(lse)) return ZL_EALIGN;
-  const int32_t hd = cache->head_dim;
-  st = check_rows(q, q_stride, num_heads, hd, tq, 2);
-  if (st != ZL_OK) return st;
-
-  const int32_t group = num_heads / cache->num_kv_heads;
-  const size_t need = attn_workspace(cu_seqlens_q, num_seqs, group, hd);
+  Attend c{cache, q, q_stride, cu_seqlens_q, num_seqs, max_kv_len, num_heads, softmax_scale, causal, window, o, lse,
+           static_cast<cudaStream_t>(stream)};
+  zl_status st = c.check();
+  if (st != ZL_OK || c.tq == 0) return st;
+  const Chosen all{0, num_seqs, 0};
+  const size_t need = attn_workspace(cu_seqlens_q, all, c.group(), cache->head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need)) return ZL_EWORKSPACE;
   if (need > 0 && !aligned16(workspace)) return ZL_EALIGN;
   int sms = 0;
   st = device_sms(&sms);
+  return st != ZL_OK ? st : launch_attn(c, *cache, all, workspace);
+}
+
+zl_status zl_paged_attn_q4_workspace_size(const int32_t* cu_seqlens_q, int32_t num_seqs, int32_t max_kv_len,
+                                          int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t window,
+                                          size_t* bytes) {
+  if (!bytes || window < 0) return ZL_EINVAL;
+  int64_t tq = 0;
+  zl_status st = check_attn(cu_seqlens_q, num_seqs, max_kv_len, num_heads, num_kv_heads, head_dim, &tq);
   if (st != ZL_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Q4Plan p;
+  st = plan_q4(cu_seqlens_q, num_seqs, max_kv_len, num_heads, num_kv_heads, head_dim, window, &p);
+  if (st == ZL_OK) *bytes = p.bytes();
+  return st;
+}
 
-  static thread_local zl::PagedAttnArgs<zl::kMaxSegs> a;      // ~21 KB: kept off the stack
-  static_cast<zl::PagedAttnHead&>(a) = zl::PagedAttnHead();
-  a.page_table = cache->page_table;
-  a.kv_lens = cache->kv_lens;
-  a.o = o;
-  a.lse = lse;
-  a.lse_stride = tq;
-  a.num_heads = num_heads;
-  a.num_kv_heads = cache->num_kv_heads;
-  a.group = group;
-  a.group_inv = (65536 + group - 1) / group;
-  a.tile_tokens = tile_tokens(group);
-  a.table_cols = cache->table_cols;
-  a.num_pages = cache->num_pages;
-  a.page_shift = shift_of(cache->page_size);
-  a.max_kv_len = max_kv_len;
-  a.causal = causal;
-  a.window = window < max_kv_len ? window : 0;   // one that reaches over every key is none (and stays in 32 bits)
-  a.scale_log2 = softmax_scale * 1.4426950408889634f;
-
-  // the maps that the call's kinds of sequences use
-  bool copies[3] = {false, false, false}, pairs = false;
-  for (int32_t i = 0; i < num_seqs; ++i) {
-    const int64_t n = cu_seqlens_q[i + 1] - cu_seqlens_q[i];
-    if (n == 0) continue;
-    pairs = pairs || n > a.tile_tokens;
-    const int64_t tile_rows = n * a.group;
-    copies[n > a.tile_tokens || tile_rows > 64 ? 0 : tile_rows > 32 ? 1 : 2] = true;
-  }
-  zl::PagedMaps maps;
-  const int64_t pool_rows = int64_t(cache->num_pages) * cache->num_kv_heads * cache->page_size;
-  const int box_rows = std::min(cache->page_size, zl::kBlockN);
-  bool ok = zl::make_map(&maps.k, cache->k_pages, pool_rows, 1, hd, box_rows) &&
-            zl::make_map(&maps.v, cache->v_pages, pool_rows, 1, hd, box_rows);
-  if (pairs)
-    ok = ok && zl::make_map_heads(&maps.o, o, tq, num_heads, hd, int64_t(num_heads) * hd, a.group, a.tile_tokens);
-  for (int i = 0; i < 3; ++i)
-    if (copies[i])
-      ok = ok && zl::make_map_heads(&maps.q[i], q, tq, num_heads, hd, q_stride, a.group, zl::kBlockM / (1 << i) / a.group);
-  if (!ok) return ZL_ECUDA;
-
-  a.joins = static_cast<zl::PagedJoin*>(workspace);
-  a.o_part = reinterpret_cast<float*>(a.joins + zl::kPagedCtas);
-  for (const bool pair : {false, true}) {
-    for (int32_t i = 0; i < num_seqs;) {
-      const int32_t first = i;
-      const Launch l = next_launch(cu_seqlens_q, num_seqs, group, pair, &i);
-      if (l.segs == 0) continue;
-      a.slot_rows = l.slot_rows;
-      a.lse_part = a.o_part + int64_t(2) * zl::kPagedCtas * l.slot_rows * hd;
-      a.n_segs = 0;
-      for (int32_t x = first; x < i; ++x) {
-        const int32_t n = cu_seqlens_q[x + 1] - cu_seqlens_q[x];
-        if (n > 0 && (n > a.tile_tokens) == pair) a.segs[a.n_segs++] = zl::PagedSeg{x, cu_seqlens_q[x], n};
-      }
-      a.whole = whole_units(a, pair);
-      st = launch_counted("paged_attn", s, [&] { return zl::launch_paged_attn(hd, pair, maps, a, s); });
-      if (st != ZL_OK) return st;
-      if (a.whole > 0) continue;
-      st = launch_counted("paged_join", s, [&] { return zl::launch_paged_join(hd, pair, a, s); });
-      if (st != ZL_OK) return st;
-    }
-  }
-  return ZL_OK;
+zl_status zl_paged_attn_q4(const zl_paged_cache_t* cache, const void* q, int64_t q_stride, const int32_t* cu_seqlens_q,
+                           int32_t num_seqs, int32_t max_kv_len, int32_t num_heads, float softmax_scale,
+                           int32_t causal, int32_t window, void* o, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  Attend c{cache, q, q_stride, cu_seqlens_q, num_seqs, max_kv_len, num_heads, softmax_scale, causal, window, o, lse,
+           static_cast<cudaStream_t>(stream)};
+  zl_status st = c.check();
+  if (st != ZL_OK || c.tq == 0) return st;
+  Q4Plan p;
+  st = plan_q4(cu_seqlens_q, num_seqs, max_kv_len, num_heads, cache->num_kv_heads, cache->head_dim, window, &p);
+  if (st != ZL_OK) return st;
+  if (p.bytes() > 0 && (!workspace || workspace_bytes < p.bytes())) return ZL_EWORKSPACE;
+  if (p.bytes() > 0 && !aligned16(workspace)) return ZL_EALIGN;
+  int sms = 0;
+  st = device_sms(&sms);
+  return st != ZL_OK ? st : launch_attn_q4(c, p, workspace);
 }
 
 // ------------------------------------------------------------------ pages

@@ -7,6 +7,11 @@ parts of one projection's rows.  A layer's pools are k_pages and v_pages
 [P, Hk, page, d] bf16; page_table [S, cols], kv_lens [S] and page_refs [P] are
 int32 tensors on the same device.  kv_lens counts the new tokens of a call.
 cu_seqlens are host sequences of ints, or host_int32 of one.
+
+A cache held in 4 bits has the same tables; its pools are uint8
+[P, Hk, page, q4_row_bytes(d)], of which a page's head is one block of bytes
+(include/zl_attn.h says how they lie).  paged_append_q4, paged_read_q4 and
+paged_attn_q4 work on it, and the page operations on any pool.
 """
 from __future__ import annotations
 
@@ -51,7 +56,8 @@ def _short(name, *args):
     return r
 
 
-_NAMES = {"rope": "rope", "append": "paged_append", "append_after": "paged_append_ex", "attn": "paged_attn", "extend": "pages_extend",
+_NAMES = {"rope": "rope", "append": "paged_append", "append_after": "paged_append_ex", "attn": "paged_attn",
+          "append_q4": "paged_append_q4", "read_q4": "paged_read_q4", "attn_q4": "paged_attn_q4", "extend": "pages_extend",
           "fork": "pages_fork", "compact": "pages_compact"}
 
 
@@ -263,22 +269,35 @@ def rope_bwd(dq, dk, positions, plan, dq_out=None, dk_out=None, stream=None):
 
 
 # ------------------------------------------------------------------ the cache
-def _cache(k_pages, v_pages, page_table, kv_lens, seqs):
+def q4_row_bytes(head_dim) -> int:
+    """Bytes that a token's head takes in a 4-bit cache: two codes to a byte and
+    a step for every 32 columns."""
+    if head_dim not in (64, 128):
+        raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+    return head_dim // 2 + head_dim // 32
+
+
+def _cache(k_pages, v_pages, page_table, kv_lens, seqs, q4=False):
     """The checked zl_paged_cache_t, its key heads and head_dim."""
     if k_pages.dim() != 4 or page_table.dim() != 2:
-        raise ValueError("k_pages must be [P, Hk, page, d] and page_table [S, cols]")
+        raise ValueError(f"k_pages must be [P, Hk, page, {'q4_row_bytes(d)' if q4 else 'd'}] and page_table [S, cols]")
     dev, shape = k_pages.device, k_pages.shape
-    if k_pages.dtype is not _BF16:
-        raise TypeError("the pages must be bf16")
+    dtype = torch.uint8 if q4 else _BF16
+    if k_pages.dtype is not dtype:
+        raise TypeError("the pages must be " + ("uint8" if q4 else "bf16"))
     cols = page_table.shape[1]
     if page_table.shape[0] != seqs:
         raise ValueError(f"page_table has {page_table.shape[0]} rows, the batch {seqs} sequences")
     if not k_pages.is_contiguous():
         raise ValueError("k_pages must be contiguous")
-    _exact(v_pages, "v_pages", shape, _BF16, dev)
+    _exact(v_pages, "v_pages", shape, dtype, dev)
     _exact(page_table, "page_table", (seqs, cols), _I32, dev)
     _exact(kv_lens, "kv_lens", (seqs,), _I32, dev)
     p, nk, page, hd = shape
+    if q4:
+        if hd not in (34, 68):
+            raise ValueError(f"the pages' last dimension must be q4_row_bytes(64) = 34 or q4_row_bytes(128) = 68, got {hd}")
+        hd = hd * 32 // 17
     return _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cols, p,
                        page, nk, hd, 0), nk, hd
 
@@ -296,17 +315,35 @@ def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None
     ones of each sequence: unless the host has read 0 from it, give the tensor
     that it returned as `status`.  Then nothing is written unless it holds 0,
     and the next sync_check raises."""
+    return _append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q, q_out, rope, positions, stream, status,
+                   False)
+
+
+def paged_append_q4(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None, q_out=None, rope=None,
+                    positions=None, stream=None, status=None):
+    """paged_append into a cache held in 4 bits.  Keys that are turned are rounded
+    to bf16 first; what is held is a group's values to the nearest of 16 steps,
+    the step its largest one's seventh (paged_read_q4 gives the values).  A group
+    of 32 columns with an element that is not finite reads as NaN."""
+    return _append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q, q_out, rope, positions, stream, status,
+                   True)
+
+
+def _append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q, q_out, rope, positions, stream, status, q4):
     cu = _cu(cu_seqlens)
     if stream is None and q_out is None and positions is None:
         plan = 0 if rope is None else rope.address
-        if status is None:
+        if q4:
+            r = _short("append_q4", k, v, k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last, q, plan,
+                       status)
+        elif status is None:
             r = _short("append", k, v, k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last, q, plan)
         else:
             r = _short("append_after", k, v, k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last, q, plan,
                        status)
         if r is not None:
             return r[0]
-    cache, nk, hd = _cache(k_pages, v_pages, page_table, kv_lens, cu.n - 1)
+    cache, nk, hd = _cache(k_pages, v_pages, page_table, kv_lens, cu.n - 1, q4)
     tokens, dev = cu.last, k_pages.device
     ks = _rows(k, "k", tokens, nk, hd, _BF16, dev)
     vs = _rows(v, "v", tokens, nk, hd, _BF16, dev)
@@ -334,22 +371,62 @@ def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None
     index = k_pages.get_device()
     if tokens == 0 and index >= 0:
         return q_out
-    _call("zl_paged_append_ex", index, stream, cache, k.data_ptr(), ks, v.data_ptr(), vs, cu.array, cu.n - 1,
+    _call("zl_paged_append_q4" if q4 else "zl_paged_append_ex", index, stream, cache, k.data_ptr(), ks, v.data_ptr(), vs, cu.array, cu.n - 1,
           None if rope is None else rope.ref, pos, pos_stride, qp, qs, nq, qop, qos,
           None if status is None else status.data_ptr())
     return q_out
 
 
-def paged_attn_workspace_bytes(cu_seqlens_q, max_kv_len, num_heads, num_kv_heads, head_dim) -> int:
+def paged_read_q4(k_pages, v_pages, page_table, kv_lens, cu_seqlens, k_out=None, v_out=None, stream=None):
+    """Reads the last tokens of each sequence of a 4-bit cache back, exactly the
+    values that are held: the rows of cu_seqlens are the positions below
+    kv_lens[s].  Returns (k, v), bf16 [T, Hk, d]; rows that are not in the cache
+    are zero, and the next sync_check raises."""
+    cu = _cu(cu_seqlens)
+    if stream is None and k_out is None and v_out is None:
+        r = _short("read_q4", k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last)
+        if r is not None:
+            return r
+    cache, nk, hd = _cache(k_pages, v_pages, page_table, kv_lens, cu.n - 1, True)
+    shape, dev = (cu.last, nk, hd), k_pages.device
+    index = k_pages.get_device()
+    if index < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    strides = []
+    for x, name in ((k_out, "k_out"), (v_out, "v_out")):
+        strides.append(nk * hd if x is None else _rows(x, name, *shape, _BF16, dev))
+    if k_out is not None and v_out is not None and _overlap(k_out, v_out):
+        raise ValueError("k_out and v_out overlap")
+    if k_out is None:
+        k_out = _empty(k_pages, shape, _BF16, stream)
+    if v_out is None:
+        v_out = _empty(k_pages, shape, _BF16, stream)
+    if cu.last == 0:
+        return k_out, v_out
+    _call("zl_paged_read_q4", index, stream, cache, cu.array, cu.n - 1, k_out.data_ptr(), strides[0], v_out.data_ptr(),
+          strides[1])
+    return k_out, v_out
+
+
+def _attn_bytes(name, cu_seqlens_q, max_kv_len, num_heads, num_kv_heads, head_dim, *window) -> int:
     lib = _lib.load()
     cu = _cu(cu_seqlens_q)
-    for value, name in ((max_kv_len, "max_kv_len"), (num_heads, "num_heads"), (num_kv_heads, "num_kv_heads"),
-                        (head_dim, "head_dim")):
-        _int32(value, name)
+    for value, what in ((max_kv_len, "max_kv_len"), (num_heads, "num_heads"), (num_kv_heads, "num_kv_heads"),
+                        (head_dim, "head_dim"), *((w, "window") for w in window)):
+        _int32(value, what)
     out = ctypes.c_size_t(0)
-    _lib.check(lib.zl_paged_attn_workspace_size(cu.array, cu.n - 1, max_kv_len, num_heads, num_kv_heads, head_dim,
-                                                ctypes.byref(out)), "zl_paged_attn_workspace_size")
+    _lib.check(getattr(lib, name)(cu.array, cu.n - 1, max_kv_len, num_heads, num_kv_heads, head_dim, *window,
+                                  ctypes.byref(out)), name)
     return int(out.value)
+
+
+def paged_attn_workspace_bytes(cu_seqlens_q, max_kv_len, num_heads, num_kv_heads, head_dim) -> int:
+    return _attn_bytes("zl_paged_attn_workspace_size", cu_seqlens_q, max_kv_len, num_heads, num_kv_heads, head_dim)
+
+
+def paged_attn_q4_workspace_bytes(cu_seqlens_q, max_kv_len, num_heads, num_kv_heads, head_dim, window=0) -> int:
+    return _attn_bytes("zl_paged_attn_q4_workspace_size", cu_seqlens_q, max_kv_len, num_heads, num_kv_heads, head_dim,
+                       window)
 
 
 def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, max_kv_len, causal=True, window=0,
@@ -362,15 +439,30 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, max_kv_le
     sequence, or another bound, may change its last ones.  Behind a refused
     pages_extend the queries are taken for the last cached tokens: nothing is
     written to the cache, and the results mean nothing."""
+    return _attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, max_kv_len, causal, window, softmax_scale, out,
+                 lse, workspace, stream, False)
+
+
+def paged_attn_q4(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, max_kv_len, causal=True, window=0,
+                  softmax_scale=None, out=None, lse=None, workspace=None, stream=None):
+    """paged_attn over a cache held in 4 bits.  A call with long chunks takes a
+    workspace for their sequences' keys and values in bf16
+    (paged_attn_q4_workspace_bytes): one tensor can serve all layers."""
+    return _attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, max_kv_len, causal, window, softmax_scale, out,
+                 lse, workspace, stream, True)
+
+
+def _attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, max_kv_len, causal, window, softmax_scale, out, lse,
+          workspace, stream, q4):
     cu = _cu(cu_seqlens_q)
     if stream is None:
-        r = _short("attn", q, k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last, max_kv_len, causal,
-                   window, softmax_scale, out, lse, workspace)
+        r = _short("attn_q4" if q4 else "attn", q, k_pages, v_pages, page_table, kv_lens, cu.address, cu.n, cu.last,
+                   max_kv_len, causal, window, softmax_scale, out, lse, workspace)
         if r is not None:
             return r
     _int32(max_kv_len, "max_kv_len")
     _int32(window, "window")
-    cache, nk, hd = _cache(k_pages, v_pages, page_table, kv_lens, cu.n - 1)
+    cache, nk, hd = _cache(k_pages, v_pages, page_table, kv_lens, cu.n - 1, q4)
     if q.dim() != 3:
         raise ValueError("q must be [Tq, H, d]")
     tq, nh, _ = q.shape
@@ -390,9 +482,11 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, max_kv_le
     if lse is None:
         lse = _empty(q, (nh, tq), torch.float32, stream)
     if workspace is None:
-        workspace = _empty(q, (paged_attn_workspace_bytes(cu, max_kv_len, nh, nk, hd),), torch.uint8, stream)
+        need = (paged_attn_q4_workspace_bytes(cu, max_kv_len, nh, nk, hd, window) if q4
+                else paged_attn_workspace_bytes(cu, max_kv_len, nh, nk, hd))
+        workspace = _empty(q, (need,), torch.uint8, stream)
     ws, ws_bytes = _scratch(workspace, dev)
-    _call("zl_paged_attn", index, stream, cache, q.data_ptr(), qs, cu.array, cu.n - 1, max_kv_len, nh,
+    _call("zl_paged_attn_q4" if q4 else "zl_paged_attn", index, stream, cache, q.data_ptr(), qs, cu.array, cu.n - 1, max_kv_len, nh,
           1.0 / math.sqrt(hd) if softmax_scale is None else softmax_scale, 1 if causal else 0, window, out.data_ptr(),
           lse.data_ptr(), ws, ws_bytes)
     return out, lse
