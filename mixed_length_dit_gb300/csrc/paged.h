@@ -2,6 +2,7 @@
 // (zl_paged.cpp) and its kernels.  Not part of the public C ABI.
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -185,6 +186,56 @@ struct UnpackQ4Args : UnpackQ4Head {
   PagedSeg segs[N];
 };
 
+// A launch of the attention of few rows over a 4-bit cache.  A CTA's piece of the
+// line of units: it begins `off` into the unit (seg, hk, rt), at g of the line.
+struct Q4Piece {
+  int32_t seg, hk, rt;
+  int64_t off, g, end;
+  int64_t per;                  // of every CTA
+};
+
+// The unit (rows from row0 on) that begins in a CTA and goes on in the CTAs up to
+// `last` (-1: none).
+struct Q4Join {
+  int32_t q_row0;
+  int32_t row0;
+  int32_t rows;
+  int32_t hk;
+  int32_t last;
+};
+
+struct AttnQ4Head {
+  const __nv_bfloat16* q;
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const int32_t* page_table;
+  const int32_t* kv_lens;
+  __nv_bfloat16* o;             // [Tq][H][d]
+  float* lse;                   // [H][lse_stride]
+  float* o_part;                // [2 * CTAs][rows of a unit][d]: slots of cut units
+  float* lse_part;
+  Q4Join* joins;                // [CTAs]
+  int64_t q_stride;
+  int64_t lse_stride;
+  int32_t num_heads;
+  int32_t num_kv_heads;
+  int32_t group;                // query heads of a key head
+  int32_t table_cols;
+  int32_t num_pages;
+  int32_t page_shift;
+  int32_t max_kv_len;
+  int32_t causal;
+  int32_t window;
+  float scale_log2;             // softmax scale * log2(e)
+  int32_t n_segs;
+  int32_t whole;                // > 0: the launch's units; each has a CTA to itself, and no join follows
+};
+
+template <int N>
+struct AttnQ4Args : AttnQ4Head {
+  PagedSeg segs[N];
+};
+
 // A pool of pages seen by the kernels that move whole pages.
 struct PagePool {
   uint8_t* base;                // groups x num_pages x page_bytes
@@ -226,6 +277,11 @@ cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnHead& args
 cudaError_t launch_append_q4(const RopeArgs<kMaxSegs>& args, int num_sms, cudaStream_t stream);
 cudaError_t launch_read_q4(const ReadQ4Args<kMaxSegs>& args, int num_sms, cudaStream_t stream);
 cudaError_t launch_unpack_q4(int head_dim, const UnpackQ4Args<kMaxSegs>& args, cudaStream_t stream);
+// nt: tiles of 8 rows in a unit, 1, 2 or 4; attn_q4_ctas: CTAs of such a launch.
+int attn_q4_ctas(int nt);
+cudaError_t launch_attn_q4(int head_dim, int nt, const AttnQ4Args<kMaxSegs>& args, cudaStream_t stream);
+// Joins the cut units of a launch_attn_q4 with the same arguments.
+cudaError_t launch_join_q4(int head_dim, int nt, const AttnQ4Head& args, cudaStream_t stream);
 cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const int32_t* dst, int32_t n, int num_sms,
                               cudaStream_t stream);
 cudaError_t launch_pages_extend(const PageTable& t, const int32_t* counts, int32_t* status, cudaStream_t stream);
@@ -248,6 +304,7 @@ uint32_t rope_take_error();
 uint32_t pages_take_error();
 uint32_t paged_attn_take_error();
 uint32_t pages_q4_take_error();
+uint32_t attn_q4_take_error();
 uint32_t paged_take_error();
 
 }  // namespace zl

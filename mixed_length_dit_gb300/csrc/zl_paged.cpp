@@ -420,10 +420,11 @@ zl_status launch_attn(const Attend& c, const zl_paged_cache_t& cache, const Chos
 }
 
 // ------------------------------------------------------------------ attention over 4 bits
-// Sequences of more than kQ4Rows rows are unpacked to bf16, once for all of their
-// queries, and handed to the bf16 attention, a batch at a time: as many as
+// Sequences of at most kQ4Rows rows (queries times the heads of a key head) run
+// over the codes as they are.  Longer ones are unpacked to bf16, once for all of
+// their queries, and handed to the bf16 attention, a batch at a time: as many as
 // kScratchBytes hold, or one.
-constexpr int64_t kQ4Rows = 0;
+constexpr int64_t kQ4Rows = 64;
 constexpr int64_t kScratchBytes = int64_t(1) << 30;
 
 struct Q4Plan {
@@ -438,6 +439,46 @@ struct Q4Plan {
 };
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The next launch over codes: sequences from *i on, units of nt tiles of 8 rows.
+struct Few {
+  int32_t segs = 0;
+  int32_t nt = 1;
+  int64_t row_tiles = 0;   // of one key head
+};
+
+Few next_few(const int32_t* cu, int32_t num_seqs, int32_t group, int32_t* i) {
+  Few f;
+  const int32_t first = *i;
+  int64_t most = 0;
+  for (; *i < num_seqs && f.segs < zl::kMaxSegs; ++*i) {
+    const int64_t rows = int64_t(cu[*i + 1] - cu[*i]) * group;
+    if (rows == 0 || rows > kQ4Rows) continue;
+    ++f.segs;
+    most = std::max(most, rows);
+  }
+  f.nt = most <= 8 ? 1 : most <= 16 ? 2 : 4;
+  for (int32_t x = first; x < *i; ++x) {
+    const int64_t rows = int64_t(cu[x + 1] - cu[x]) * group;
+    if (rows <= kQ4Rows) f.row_tiles += (rows + 8 * f.nt - 1) / (8 * f.nt);
+  }
+  return f;
+}
+
+size_t few_workspace(int32_t nt, int32_t hd) {
+  const size_t ctas = zl::attn_q4_ctas(nt);
+  return up256(ctas * sizeof(zl::Q4Join)) + 2 * ctas * 8 * nt * (hd + 1) * sizeof(float);
+}
+
+// The launch's units if each is left whole, one CTA to a unit (no sums over the
+// lengths, no join); 0 if they are cut into equal shares.
+int32_t whole_q4(const zl::AttnQ4Head& a, const Few& f, int ctas) {
+  const int64_t units = f.row_tiles * a.num_kv_heads;
+  if (units > ctas) return 0;
+  int64_t keys = a.max_kv_len;
+  if (a.window > 0 && a.causal) keys = std::min(keys, int64_t(a.window) + 64);
+  return keys <= 1024 ? static_cast<int32_t>(units) : 0;
+}
 
 zl_status plan_q4(const int32_t* cu, int32_t num_seqs, int32_t max_kv_len, int32_t nh, int32_t nk, int32_t hd,
                   int32_t window, Q4Plan* p) {
@@ -465,12 +506,67 @@ zl_status plan_q4(const int32_t* cu, int32_t num_seqs, int32_t max_kv_len, int32
     p->table = up256(size_t(num_seqs) * p->cols * sizeof(int32_t));
     p->pool = up256(size_t(p->batch) * each);
   }
-  p->attn = up256(attn_workspace(cu, Chosen{0, num_seqs, kQ4Rows}, group, hd));
+  p->attn = attn_workspace(cu, Chosen{0, num_seqs, kQ4Rows}, group, hd);
+  for (int32_t i = 0; i < num_seqs;) {
+    const Few f = next_few(cu, num_seqs, group, &i);
+    if (f.segs > 0) p->attn = std::max(p->attn, few_workspace(f.nt, hd));
+  }
+  p->attn = up256(p->attn);
+  return ZL_OK;
+}
+
+// The launches over codes.
+zl_status launch_few_q4(const Attend& c, void* workspace) {
+  const zl_paged_cache_t& cache = *c.cache;
+  static thread_local zl::AttnQ4Args<zl::kMaxSegs> a;
+  static_cast<zl::AttnQ4Head&>(a) = zl::AttnQ4Head();
+  a.q = static_cast<const __nv_bfloat16*>(c.q);
+  a.k_pages = static_cast<const uint8_t*>(cache.k_pages);
+  a.v_pages = static_cast<const uint8_t*>(cache.v_pages);
+  a.page_table = cache.page_table;
+  a.kv_lens = cache.kv_lens;
+  a.o = static_cast<__nv_bfloat16*>(c.o);
+  a.lse = c.lse;
+  a.q_stride = c.q_stride;
+  a.lse_stride = c.tq;
+  a.num_heads = c.num_heads;
+  a.num_kv_heads = cache.num_kv_heads;
+  a.group = c.group();
+  a.table_cols = cache.table_cols;
+  a.num_pages = cache.num_pages;
+  a.page_shift = shift_of(cache.page_size);
+  a.max_kv_len = c.max_kv_len;
+  a.causal = c.causal;
+  a.window = c.window < c.max_kv_len ? c.window : 0;
+  a.scale_log2 = c.scale * 1.4426950408889634f;
+  for (int32_t i = 0; i < c.num_seqs;) {
+    const int32_t first = i;
+    const Few f = next_few(c.cu, c.num_seqs, a.group, &i);
+    if (f.segs == 0) continue;
+    a.n_segs = 0;
+    for (int32_t x = first; x < i; ++x) {
+      const int32_t n = c.queries(x);
+      if (n > 0 && int64_t(n) * a.group <= kQ4Rows) a.segs[a.n_segs++] = zl::PagedSeg{x, c.cu[x], n};
+    }
+    const int ctas = zl::attn_q4_ctas(f.nt);
+    a.joins = static_cast<zl::Q4Join*>(workspace);
+    a.o_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up256(ctas * sizeof(zl::Q4Join)));
+    a.lse_part = a.o_part + int64_t(2) * ctas * 8 * f.nt * cache.head_dim;
+    a.whole = whole_q4(a, f, ctas);
+    zl_status st = launch_counted("paged_attn_q4", c.stream,
+                                  [&] { return zl::launch_attn_q4(cache.head_dim, f.nt, a, c.stream); });
+    if (st == ZL_OK && a.whole == 0)
+      st = launch_counted("paged_join_q4", c.stream,
+                          [&] { return zl::launch_join_q4(cache.head_dim, f.nt, a, c.stream); });
+    if (st != ZL_OK) return st;
+  }
   return ZL_OK;
 }
 
 zl_status launch_attn_q4(const Attend& c, const Q4Plan& p, void* workspace) {
   const zl_paged_cache_t& cache = *c.cache;
+  zl_status few = launch_few_q4(c, workspace);
+  if (few != ZL_OK || p.chunks == 0) return few;
   auto* at = static_cast<uint8_t*>(workspace) + p.attn;
   zl_paged_cache_t scratch = cache;
   scratch.page_table = reinterpret_cast<int32_t*>(at);
@@ -523,9 +619,10 @@ uint32_t paged_take_error() {
   const uint32_t b = pages_take_error();
   const uint32_t c = paged_attn_take_error();
   const uint32_t d = pages_q4_take_error();
-  for (const uint32_t x : {a, b, c, d})
+  const uint32_t e = attn_q4_take_error();
+  for (const uint32_t x : {a, b, c, d, e})
     if (x == 0xFFFFFFFFu) return x;
-  return a | b | c | d;
+  return a | b | c | d | e;
 }
 
 }  // namespace zl
