@@ -217,6 +217,7 @@ struct AttnQ4Head {
   Q4Join* joins;                // [CTAs]
   int64_t q_stride;
   int64_t lse_stride;
+  int64_t page_bytes;           // of a pool's page, all heads
   int32_t num_heads;
   int32_t num_kv_heads;
   int32_t group;                // query heads of a key head

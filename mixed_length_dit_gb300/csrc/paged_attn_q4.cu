@@ -3,30 +3,39 @@
 //
 //     S = q K^T scale,  o = softmax(S) V,   K = c_k s_k,  V = c_v s_v
 //
-// with a step s for every 32 columns (a group) of a token's head.  The codes are
-// not made into bf16 values: a code n = c + 8 becomes the bf16 128 + n by one
-// logical operation (its last four bits), and the products go
+// with a step s for every 32 columns (a group) of a token's head.  The codes
+// n = c + 8 are not made into values: the products run over n itself,
 //
-//     S = scale sum_g s_k[g] (sum_(i in g) q_i (128 + n_i) - 136 sum_(i in g) q_i)
-//     o_i = sum_j (p_j s_v[j, g]) ((128 + n_ji) - 136)
+//     S = scale sum_g s_k[g] (sum_(i in g) q_i n_i - 8 sum_(i in g) q_i)
+//     o_i = sum_j (p_j s_v[j, g]) n_ji - 8 sum_j (p_j s_v[j, g])
 //
 // so that a key's steps multiply four sums instead of 128 codes, and a value's
 // steps the probability before it is rounded to bf16 (the one rounding, as in the
 // bf16 attention: the tensor cores take P in V's type).
 //
 // Bound by HBM at best, by instructions otherwise: an SM's share of HBM is 43
-// codes a clock.  So K and V are the A operands of warp-level products
-// (mma.m16n8k16: 16 keys, or 16 columns, by the 8 rows of a query tile by 16),
-// unpacked in registers where they are used.  The 5th-generation tensor cores
-// take B from shared memory only, and A from there or from TMEM: unpacked codes
-// would cross shared memory twice, 170 bytes a clock of its 128.
+// codes a clock.  So K and V are the A operands of warp-level products (16 keys,
+// or 16 columns, by the 8 rows of a query tile), unpacked in registers where they
+// are used.  The 5th-generation tensor cores take B from shared memory only, and A
+// from there or from TMEM: unpacked codes would cross shared memory twice, 170
+// bytes a clock of its 128.
+//
+// The codes become operands by masks alone.  A 16-bit pattern below 256 is, as a
+// bf16, its number times 2^-133 (subnormal, or with the lowest exponent), and the
+// products take such numbers as they are.  So a code in bits 0 to 3 is n, one in
+// bits 4 to 7 is 16 n, and the other factor brings the size: a row of q is scaled
+// by a power of two so that its largest element lies at 2^120 (columns whose codes
+// come 16 times over by 1/16 of it), a value's steps by 2^100.  All of it is exact.
+// A word's codes are four operands after five logical operations; two tokens' codes
+// of a column, as V wants them, take a byte permutation more for each.
 //
 // A unit is (sequence, key head, tile of 8 NT rows: queries times the heads that
 // share the key head).  The tiles of 32 keys of all units stand in one line that
 // is cut into equal pieces, one a CTA, as in the bf16 attention; the warps of a
-// CTA take a unit's tiles in turn, each with copies (TMA bulk) of its own in
-// flight, and are joined in shared memory; units that a cut goes through are
-// joined by a second launch.
+// CTA take a unit's tiles in turn, each with copies of its own in flight, and are
+// joined in shared memory; units that a cut goes through are joined by a second
+// launch.  The copies are 16 bytes a lane: bulk copies (TMA), four to a tile, took
+// their warp through a loop over the lanes that issue them.
 #include <algorithm>
 #include <atomic>
 
@@ -41,7 +50,12 @@ __device__ uint32_t g_attn_q4_err;
 constexpr int kTile = 32;                      // keys of a warp's step
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;                // the running maximum lags by this much (base 2) at most
-constexpr uint32_t kMagic = 0x43004300u;       // 128 as bf16, twice
+constexpr uint32_t kLow = 0x000f000fu;         // of codes: n, and 16 n
+constexpr uint32_t kHigh = 0x00f000f0u;
+constexpr uint32_t kMinus8 = 0x80088008u;      // -8 n's unit, twice, and 16 times that
+constexpr uint32_t kMinus128 = 0x80808080u;
+constexpr float kStepScale = 0x1p100f;         // a value's steps
+constexpr float kOutScale = 0x1p33f;           // from sums of codes to the output
 
 template <int HD, int NT>
 struct Cfg {
@@ -51,33 +65,33 @@ struct Cfg {
   static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
   static constexpr int kStages = NT == 1 ? 2 : 3;
   static constexpr int kRegion = kTile * kQ4Row<HD>;           // keys, or values, of a stage
-  static constexpr bool kQInSmem = NT > 2;
+  static constexpr int kSteps = kTile * kQ4Codes<HD>;          // its steps, behind the codes
+  // -8 sum_j: by a product with a constant, the sums of a tile apart (of few rows,
+  // whose products cost little), or by subtraction from the codes
+  static constexpr bool kOffsetByProduct = NT == 1;
   static constexpr int kPad = HD + 4;          // floats of a row to be joined (rows 2c of four lanes in different banks)
 };
 
-template <int HD, int NT>
-struct Smem {
-  using C = Cfg<HD, NT>;
-  alignas(128) uint8_t stage[C::W][C::kStages][2][C::kRegion];
-  alignas(16) float part[C::W][8][C::kPad];    // 8 rows of every warp
-  float m[C::W][C::RT], l[C::W][C::RT];
-  uint2 q[C::kQInSmem ? C::W : 1][C::kQInSmem ? NT : 1][C::G][2][32];
-  float2 q_sum[C::kQInSmem ? C::W : 1][C::kQInSmem ? NT : 1][C::G][4];
-  alignas(8) uint64_t full[C::W][C::kStages];
-  int64_t sums[32];
-  Q4Piece piece;
-  int abort_flag;
-};
+template <int TO, int FROM>
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;"
+               :: "r"(dst), "l"(__cvta_generic_to_global(src)), "n"(TO), "n"(FROM) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               :: "r"(dst), "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+// d = a b + c.
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint2& b, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint2& b) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -85,9 +99,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-
-// Codes j and j + 4 of a word, as 128 + n each.
-__device__ __forceinline__ uint32_t pair_of(uint32_t w, int j) { return ((w >> (4 * j)) & 0x000f000fu) | kMagic; }
 
 template <int G>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[G]) {
@@ -99,20 +110,27 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[G]) {
     w[0] = u.x; w[1] = u.y;
   }
 }
-
-// The steps of a token's groups.
 template <int G>
-__device__ __forceinline__ void load_steps(const uint8_t* p, float (&s)[G]) {
-  uint32_t w;
-  if constexpr (G == 4) w = *reinterpret_cast<const uint32_t*>(p);
-  else w = *reinterpret_cast<const uint16_t*>(p);
-  const float2 a = q4_steps01(w);
-  s[0] = a.x;
-  s[1] = a.y;
+__device__ __forceinline__ void load_floats(const float* p, float (&w)[G]) {
   if constexpr (G == 4) {
-    const float2 b = q4_steps23(w);
-    s[2] = b.x;
-    s[3] = b.y;
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else {
+    const float2 u = *reinterpret_cast<const float2*>(p);
+    w[0] = u.x; w[1] = u.y;
+  }
+}
+
+// A token's steps from its bytes to floats.
+template <int G>
+__device__ __forceinline__ void spread_steps(float* to, const uint8_t* p, float times) {
+  if constexpr (G == 4) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    const float2 a = q4_steps01(w), b = q4_steps23(w);
+    *reinterpret_cast<float4*>(to) = make_float4(a.x * times, a.y * times, b.x * times, b.y * times);
+  } else {
+    const float2 a = q4_steps01(*reinterpret_cast<const uint16_t*>(p));
+    *reinterpret_cast<float2*>(to) = make_float2(a.x * times, a.y * times);
   }
 }
 
@@ -245,12 +263,12 @@ struct Item {
 
 // Walks a CTA's items; every warp for itself, once for its copies and once for
 // its products.
-template <int W, int RT, int N>
 struct Walk {
   int seg, hk, rt;
   int64_t off, g, end;
   int len, q_len;
 
+  template <int N>
   __device__ __forceinline__ void start(const AttnQ4Args<N>& a, const Q4Piece& p) {
     seg = p.seg; hk = p.hk; rt = p.rt; off = p.off; g = p.g; end = p.end;
     if (g < end) {
@@ -259,7 +277,7 @@ struct Walk {
     }
   }
 
-  // The next item; false: none left.
+  template <int W, int RT, int N>
   __device__ __forceinline__ bool next(const AttnQ4Args<N>& a, Item* it) {
     while (g < end) {
       const int rows = q_len * a.group, r0 = rt * RT;
@@ -304,190 +322,278 @@ struct Walk {
   }
 };
 
-// ------------------------------------------------------------------ copies
-// Where the 16 keys of half a tile lie in a region: pages of 16 tokens are copied
-// with their steps behind their codes, larger pages' codes and steps apart.
-struct Layout {
-  int codes_half, steps, steps_half;
+// A warp's place in the CTA's piece, and the item there.  It changes once in many
+// tiles, so it is kept in shared memory.
+struct Spot {
+  Walk walk;
+  Item item;
+  // of the copies: the first token's codes in page 0, keys' and values', its steps
+  // behind the first code of the block, and the sequence's row of the table
+  const uint8_t* k;
+  const uint8_t* v;
+  int32_t steps;
+  const int32_t* entries;
 };
 
+template <int HD, int NT>
+struct Smem {
+  using C = Cfg<HD, NT>;
+  alignas(128) uint8_t stage[C::W][C::kStages][2][C::kRegion];
+  alignas(16) float part[C::W][8][C::kPad];    // 8 rows of every warp
+  float m[C::W][C::RT], l[C::W][C::RT];
+  // Of the item's queries, the same for all warps (each writes them, so that none
+  // waits for another): fragments of q^T for a group's two products, and their first
+  // sums, -8 sum q of rows 2c, 2c + 1 for keys g and g + 8.
+  uint4 q[NT][C::G][32];
+  float4 q_sum[NT][C::G][4];
+  float q_scale[C::RT];                        // a row's scores from its sums: scale and log2 e, its own scale
+  Q4Piece piece;
+  Spot spot[2][C::W];                        // of every warp's copies, and of its products
+};
+
+// The next item, by all lanes of the warp; false: none left.
+template <int W, int RT, int N>
+__device__ __forceinline__ bool next_item(const AttnQ4Args<N>& a, Spot* at) {
+  Walk walk = at->walk;
+  Item it;
+  const bool ok = walk.next<W, RT>(a, &it);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    at->walk = walk;
+    at->item = it;
+  }
+  __syncwarp();
+  return ok;
+}
+
+// ------------------------------------------------------------------ copies
+// Where 16 bytes (chunk) of a token's codes lie in a region: a value's chunks of
+// the rows that four neighbouring lanes read are in different banks.
 template <int HD>
-__device__ __forceinline__ Layout layout_of(const AttnQ4Head& a) {
-  if (a.page_shift == 4) return {16 * kQ4Row<HD>, 16 * kQ4Codes<HD>, 16 * kQ4Row<HD>};
-  return {16 * kQ4Codes<HD>, kTile * kQ4Codes<HD>, 16 * kQ4Steps<HD>};
+__device__ __forceinline__ int chunk_at(int row, int chunk, bool values) {
+  return row * kQ4Codes<HD> + 16 * (HD == 128 && values ? chunk ^ ((row >> 1) & 3) : chunk);
 }
 
 // A warp's tiles, one after another: a copy is set off as soon as a stage is free,
-// with the page number that was fetched when the one before was.
+// with the page numbers that were fetched when the one before was.  A unit's tiles
+// of a warp are W tiles (256 keys) apart, the largest page's length, so they begin
+// at the same row of their pages.
 template <int HD, int NT, int N>
 struct Loader {
   using C = Cfg<HD, NT>;
-  Walk<C::W, C::RT, N> walk;
-  Item it;
-  int tile;                                    // of the item; >= it.s1: none left
-  int page;                                    // lane's page number of that tile
+  static constexpr int kLanes = kQ4Codes<HD> / 16;             // that copy a token's codes
+  static constexpr int kRows = 32 / kLanes;                    // tokens of a warp's copy
+  static constexpr int kStepLanes = kTile * kQ4Steps<HD> / 16; // that copy a tile's steps
+  Spot* at;
+  int tile, end;                               // of the item; tile >= end: none left
+  int page[2];                                 // of its first and its second 16 tokens
   uint32_t stage = 0;
+  static_assert(C::W * kTile == 256, "tiles of a warp begin at the same row of a page");
 
+  __device__ __forceinline__ void fetch(const AttnQ4Args<N>& a) {
+    const int32_t* e = at->entries + ((tile * kTile) >> a.page_shift);
+    page[0] = __ldg(e);
+    page[1] = a.page_shift > 4 ? page[0] : tile * kTile + 16 < at->item.len ? __ldg(e + 1) : 0;
+  }
+
+  // The next item with a tile for this warp.
   __device__ __forceinline__ void settle(const AttnQ4Args<N>& a) {
-    while (tile >= it.s1) {
-      if (!walk.next(a, &it)) return;
-      tile = it.s0 + (threadIdx.x >> 5);
+    do {
+      if (!next_item<C::W, C::RT>(a, at)) return;
+      tile = at->item.s0 + (threadIdx.x >> 5);
+      end = at->item.s1;
+    } while (tile >= end);
+    if ((threadIdx.x & 31) == 0) {
+      const int ps = 1 << a.page_shift, row = (tile * kTile) & (ps - 1);
+      const int64_t codes = ((static_cast<int64_t>(at->item.hk) * kQ4Row<HD>) << a.page_shift) + row * kQ4Codes<HD>;
+      at->k = a.k_pages + codes;
+      at->v = a.v_pages + codes;
+      at->steps = ps * kQ4Codes<HD> + row * (kQ4Steps<HD> - kQ4Codes<HD>);
+      at->entries = a.page_table + static_cast<int64_t>(a.segs[at->item.seg].seq) * a.table_cols;
     }
-    const int lane = threadIdx.x & 31;
-    const int pos = tile * kTile + (a.page_shift == 4 ? (lane & 1) * 16 : 0);
-    page = -1;
-    if (lane < 4 && pos < it.len && (pos >> a.page_shift) < a.table_cols)
-      page = __ldg(a.page_table + static_cast<int64_t>(a.segs[it.seg].seq) * a.table_cols + (pos >> a.page_shift));
-  }
-
-  __device__ __forceinline__ void start(const AttnQ4Args<N>& a, const Q4Piece& p) {
-    walk.start(a, p);
-    it.s1 = 0;
-    tile = 0;
-    settle(a);
-  }
-
-  // Lanes 0-3: keys' codes and steps, values' codes and steps (pages of 16: the
-  // first and second page of each; of 32: one copy of each).
-  __device__ __forceinline__ void issue(const AttnQ4Args<N>& a, Smem<HD, NT>* sm) {
-    if (tile >= it.s1) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int part = lane & 1, ps = 1 << a.page_shift;
-    const int pos = tile * kTile;
-    uint64_t* bar = &sm->full[warp][stage];
-    uint32_t bytes = 0, from = 0, to = 0;
-    if (a.page_shift == 4) {
-      if (lane < 4 && pos + 16 * part < it.len) bytes = 16 * kQ4Row<HD>;
-      to = part * 16 * kQ4Row<HD>;
-    } else if (a.page_shift == 5) {
-      if (lane < 4 && part == 0) bytes = kTile * kQ4Row<HD>;
-    } else if (lane < 4) {
-      const int row = pos & (ps - 1);
-      bytes = part ? kTile * kQ4Steps<HD> : kTile * kQ4Codes<HD>;
-      from = part ? ps * kQ4Codes<HD> + row * kQ4Steps<HD> : row * kQ4Codes<HD>;
-      to = part ? kTile * kQ4Codes<HD> : 0;
-    }
-    int pg = page;
-    if (bytes > 0 && (pg < 0 || pg >= a.num_pages)) {
-      atomicOr(&g_attn_q4_err, ERR_BAD_PAGE);  // reads page 0 in its place
-      pg = 0;
-    }
-    const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
-    if (lane == 0) mbar_arrive_expect_tx(bar, all);
     __syncwarp();
-    if (bytes > 0) {
-      const int64_t block = static_cast<int64_t>(pg) * a.num_kv_heads + it.hk;
-      const uint8_t* src = (lane < 2 ? a.k_pages : a.v_pages) + ((block * kQ4Row<HD>) << a.page_shift) + from;
-      bulk_load(smem_u32(sm->stage[warp][stage][lane >> 1]) + to, src, bytes, bar);
-    }
-    if (++stage == C::kStages) stage = 0;
-    tile += C::W;
+    fetch(a);
+  }
+
+  __device__ __forceinline__ void start(const AttnQ4Args<N>& a, Spot* spot) {
+    at = spot;
+    tile = end = 0;
     settle(a);
+  }
+
+  // One tile's copies, and the next one's page numbers.
+  __device__ __forceinline__ void issue(const AttnQ4Args<N>& a, Smem<HD, NT>* sm) {
+    if (tile < end) {
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+      const bool both = a.page_shift > 4 || tile * kTile + 16 < at->item.len;  // else the second page is not there
+      if (static_cast<uint32_t>(page[0]) >= static_cast<uint32_t>(a.num_pages) ||
+          static_cast<uint32_t>(page[1]) >= static_cast<uint32_t>(a.num_pages)) {
+        atomicOr(&g_attn_q4_err, ERR_BAD_PAGE);                // reads page 0 in its place
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (static_cast<uint32_t>(page[i]) >= static_cast<uint32_t>(a.num_pages)) page[i] = 0;
+      }
+      const uint32_t to = smem_u32(sm->stage[warp][stage][0]);
+      const uint32_t to_k = to + 16 * lane, to_v = to + C::kRegion + chunk_at<HD>(lane / kLanes, lane % kLanes, true);
+      const int64_t p0 = static_cast<int64_t>(page[0]) * a.page_bytes;
+      const uint8_t* k0 = at->k + p0;
+      const uint8_t* v0 = at->v + p0;
+      const uint8_t* k1 = k0 + 16 * kQ4Codes<HD>;
+      const uint8_t* v1 = v0 + 16 * kQ4Codes<HD>;
+      int64_t on = 16 * kQ4Steps<HD>;          // from the first 16 tokens' steps to the second's
+      if (a.page_shift == 4) {                 // they are in a page of their own
+        on = static_cast<int64_t>(page[1] - page[0]) * a.page_bytes;
+        k1 = k0 + on;
+        v1 = v0 + on;
+      }
+      constexpr int kHalf = 16 * kQ4Codes<HD>;
+      copy16<0, 0>(to_k, k0 + 16 * lane);
+      copy16<0, 0>(to_v, v0 + 16 * lane);
+      if constexpr (kRows < 16) {
+        copy16<512, 512>(to_k, k0 + 16 * lane);
+        copy16<512, 512>(to_v, v0 + 16 * lane);
+      }
+      if (both) {
+        copy16<kHalf, 0>(to_k, k1 + 16 * lane);
+        copy16<kHalf, 0>(to_v, v1 + 16 * lane);
+        if constexpr (kRows < 16) {
+          copy16<kHalf + 512, 512>(to_k, k1 + 16 * lane);
+          copy16<kHalf + 512, 512>(to_v, v1 + 16 * lane);
+        }
+      }
+      if (lane < 2 * kStepLanes) {
+        const bool values = lane >= kStepLanes, second = lane % kStepLanes >= kStepLanes / 2;
+        if (both || !second)
+          copy16<C::kSteps, 0>(to + (values ? C::kRegion : 0) + 16 * (lane % kStepLanes),
+                               (values ? v0 : k0) + at->steps + (second ? on : 0) + 16 * (lane % (kStepLanes / 2)));
+      }
+      tile += C::W;
+      if (tile < end) fetch(a);
+      else settle(a);
+    }
+    copies_commit();
+    if (++stage == C::kStages) stage = 0;
   }
 };
 
 // ------------------------------------------------------------------ products
 // A warp's share of a unit: lane (g, c) = (lane / 4, lane % 4) of the products'
 // fragments.  Scores are S^T (keys g, g + 8 by rows 2c, 2c + 1), the output o^T
-// (columns 32 q + 4 g + (0 .. 3) by rows 2c, 2c + 1).
+// (columns 32 q + 4 g + (0 .. 3) by rows 2c, 2c + 1; 2^-33 of it, of the odd
+// columns 2^-29).
 template <int HD, int NT>
 struct Rows {
   using C = Cfg<HD, NT>;
   static constexpr int G = C::G;
   float o[NT][G][2][4];                        // [tile of 16 columns][fragment]
   float m[NT][2], l[NT][2];                    // of rows 2c, 2c + 1; l: the lane's keys alone
-  uint2 q[C::kQInSmem ? 1 : NT][G][2];         // fragments of q^T
-  float q_sum[C::kQInSmem ? 1 : NT][G][2];     // -136 times the sum of a group's q
+  float f[NT][2];                              // their q_scale
 
   template <int N>
   __device__ __forceinline__ void start(const AttnQ4Args<N>& a, const Item& it, Smem<HD, NT>* sm) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-#pragma unroll
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll 1
     for (int n = 0; n < NT; ++n) {
       const int r = 8 * n + g;
       const int row = it.rt * C::RT + r, tok = row / a.group;
       const __nv_bfloat16* src = a.q + (a.segs[it.seg].q_row0 + static_cast<int64_t>(tok)) * a.q_stride +
                                  (it.hk * a.group + row - tok * a.group) * HD + 8 * c;
+      uint4 u[G];
+      uint32_t top = 0;
 #pragma unroll
       for (int x = 0; x < G; ++x) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (r < it.rows) u = __ldg(reinterpret_cast<const uint4*>(src + 32 * x));
-        // columns j and j + 4 of the 8 beside one another, as a word's codes are taken
-        const uint2 b0 = make_uint2(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632));
-        const uint2 b1 = make_uint2(__byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632));
-        float2 f = bf16x2_to_float2(u.x);
-        float sum = f.x + f.y;
-        f = bf16x2_to_float2(u.y); sum += f.x + f.y;
-        f = bf16x2_to_float2(u.z); sum += f.x + f.y;
-        f = bf16x2_to_float2(u.w); sum += f.x + f.y;
+        u[x] = make_uint4(0, 0, 0, 0);
+        if (r < it.rows) u[x] = __ldg(reinterpret_cast<const uint4*>(src + 32 * x));
+        top = __vmaxu2(top, q4_top(u[x]));
+      }
+      top = max(top & 0xffffu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // The row's scale, 2^(up_exp - 127): its largest element goes to 2^120, or is
+      // below 2^-7 and goes up by 2^127.  Codes are n 2^-133.
+      const int up_exp = min(374 - static_cast<int>(top >> 7), 254);
+      const float up = __uint_as_float(static_cast<uint32_t>(up_exp) << 23);
+      const float down = top >= 0x7f80u ? __uint_as_float(0x7fffffffu)
+                                        : __uint_as_float(static_cast<uint32_t>(min(387 - up_exp, 254)) << 23) * a.scale_log2;
+      if (c == 0) sm->q_scale[r] = down;
+#pragma unroll
+      for (int x = 0; x < G; ++x) {
+        const float2 x0 = bf16x2_to_float2(u[x].x), x1 = bf16x2_to_float2(u[x].y), x2 = bf16x2_to_float2(u[x].z),
+                     x3 = bf16x2_to_float2(u[x].w);
+        // columns j and j + 4 beside one another, as a word's codes are taken; the odd ones' codes come 16 times over
+        const float odd = up * 0.0625f;
+        const uint4 b = make_uint4(pack_bf16x2(x0.x * up, x2.x * up), pack_bf16x2(x0.y * odd, x2.y * odd),
+                                   pack_bf16x2(x1.x * up, x3.x * up), pack_bf16x2(x1.y * odd, x3.y * odd));
+        float sum = ((x0.x + x0.y) + (x1.x + x1.y)) + ((x2.x + x2.y) + (x3.x + x3.y));
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= -136.f;
+        sum = sum * up * (-8.f * 0x1p-66f) * 0x1p-67f;
         const float s0 = __shfl_sync(0xffffffffu, sum, 8 * c), s1 = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
-        if constexpr (C::kQInSmem) {
-          sm->q[warp][n][x][0][lane] = b0;
-          sm->q[warp][n][x][1][lane] = b1;
-          if (g == 0) sm->q_sum[warp][n][x][c] = make_float2(s0, s1);
-        } else {
-          q[n][x][0] = b0;
-          q[n][x][1] = b1;
-          q_sum[n][x][0] = s0;
-          q_sum[n][x][1] = s1;
-        }
+        sm->q[n][x][lane] = b;
+        if (g == 0) sm->q_sum[n][x][c] = make_float4(s0, s1, s0, s1);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        f[n][e] = sm->q_scale[8 * n + 2 * c + e];
+        m[n][e] = -INFINITY;
+        l[n][e] = 0.f;
+      }
+#pragma unroll
+      for (int x = 0; x < G; ++x)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[n][x][t][i] = 0.f;
-      }
-      m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.f;
     }
-    __syncwarp();
   }
 
-  // A tile of 32 keys from position `pos` on.  EDGE: some row does not see all of them.
+  // A tile of 32 keys from position `pos` on.  EDGE: some row does not see all of
+  // them.  `steps`: room for 64 tokens' steps.
   template <bool EDGE>
   __device__ __forceinline__ void tile(const AttnQ4Head& a, const Item& it, const Smem<HD, NT>* sm, const uint8_t* kr,
-                                       const uint8_t* vr, const Layout& lay, int pos) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+                                       const uint8_t* vr, float* steps, int pos) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    spread_steps<G>(steps + lane * G, kr + C::kSteps + lane * G, 1.f);
+    spread_steps<G>(steps + (kTile + lane) * G, vr + C::kSteps + lane * G, kStepScale);
+    __syncwarp();
     float s[2][NT][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {              // 16 keys
+      asm volatile("" ::: "memory");
       uint32_t wa[G], wb[G];
       float sa[G], sb[G];
-      const uint8_t* codes = kr + h * lay.codes_half + c * (4 * G);
-      load_words<G>(codes + g * kQ4Codes<HD>, wa);
-      load_words<G>(codes + (g + 8) * kQ4Codes<HD>, wb);
-      const uint8_t* steps = kr + lay.steps + h * lay.steps_half;
-      load_steps<G>(steps + g * G, sa);
-      load_steps<G>(steps + (g + 8) * G, sb);
+      const uint8_t* codes = kr + (16 * h + g) * kQ4Codes<HD> + c * (4 * G);
+      load_words<G>(codes, wa);
+      load_words<G>(codes + 8 * kQ4Codes<HD>, wb);
+      load_floats<G>(steps + (16 * h + g) * G, sa);
+      load_floats<G>(steps + (16 * h + 8 + g) * G, sb);
 #pragma unroll
       for (int x = 0; x < G; ++x) {
-        const uint32_t a0[4] = {pair_of(wa[x], 0), pair_of(wb[x], 0), pair_of(wa[x], 1), pair_of(wb[x], 1)};
-        const uint32_t a1[4] = {pair_of(wa[x], 2), pair_of(wb[x], 2), pair_of(wa[x], 3), pair_of(wb[x], 3)};
+        const uint32_t w0[4] = {wa[x] & kLow, wb[x] & kLow, wa[x] & kHigh, wb[x] & kHigh};
+        const uint32_t ua = wa[x] >> 8, ub = wb[x] >> 8;
+        const uint32_t w1[4] = {ua & kLow, ub & kLow, ua & kHigh, ub & kHigh};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float s0, s1;
-          uint2 b0, b1;
-          if constexpr (C::kQInSmem) {
-            const float2 f = sm->q_sum[warp][n][x][c];
-            s0 = f.x;
-            s1 = f.y;
-            b0 = sm->q[warp][n][x][0][lane];
-            b1 = sm->q[warp][n][x][1][lane];
-          } else {
-            s0 = q_sum[n][x][0];
-            s1 = q_sum[n][x][1];
-            b0 = q[n][x][0];
-            b1 = q[n][x][1];
-          }
-          float d[4] = {s0, s1, s0, s1};
-          mma(d, a0, b0);
-          mma(d, a1, b1);
+          float d[4];
+          const float4 z = sm->q_sum[n][x][c];
+          const float first[4] = {z.x, z.y, z.z, z.w};
+          const uint4 b = sm->q[n][x][lane];
+          mma(d, w0, make_uint2(b.x, b.y), first);
+          mma(d, w1, make_uint2(b.z, b.w), d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float st = i < 2 ? sa[x] : sb[x];
-            s[h][n][i] = x == 0 ? st * d[i] : fmaf(st, d[i], s[h][n][i]);
+          for (int k = 0; k < 2; ++k) {        // keys g, g + 8
+            const float st = k ? sb[x] : sa[x];
+            float* to = &s[h][n][2 * k];
+            if (x == 0) {
+              to[0] = st * d[2 * k];
+              to[1] = st * d[2 * k + 1];
+            } else {
+              f2_unpack(f2_fma(f2_pack(st, st), f2_pack(d[2 * k], d[2 * k + 1]), f2_pack(to[0], to[1])), to[0], to[1]);
+            }
           }
         }
       }
@@ -509,8 +615,9 @@ struct Rows {
               if (key < lo || key >= hi) s[h][n][2 * k + e] = -INFINITY;
             }
         }
-        const float top = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e])) * a.scale_log2;
-        raise = raise || top > m[n][e] + kRescale;
+        // (a mask's -inf stays -inf: f is above zero, NaN, or 0 for a row of zeros)
+        const float top = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+        raise = raise || top * f[n][e] > m[n][e] + kRescale;
       }
     }
     if (__any_sync(0xffffffffu, raise)) {
@@ -518,7 +625,7 @@ struct Rows {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float top = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e])) * a.scale_log2;
+          float top = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e])) * f[n][e];
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           // a row's own scores decide, so that its bits do not depend on the rows beside it
@@ -545,57 +652,87 @@ struct Rows {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float& p = s[h][n][2 * k + e];
-            p = fast_exp2(fmaf(p, a.scale_log2, neg));
+            p = fast_exp2(fmaf(p, f[n][e], neg));
             l[n][e] += p;
           }
       }
-    const __nv_bfloat162 off = __float2bfloat162_rn(136.f);
+    uint32_t w[2][4];
+    float2 st[2][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // the codes of keys 2c, 2c + 1 and 2c + 8, 2c + 9: four columns of each group
-      uint32_t w[4][G / 2];
-      const uint8_t* codes = vr + h * lay.codes_half + g * (2 * G);
+    for (int x = 0; x < G; ++x) {
+      // the codes of keys 2c, 2c + 1 and 2c + 8, 2c + 9 of each 16, and the steps of
+      // keys g, g + 8, for two groups: four columns of a group are half a word
+      if ((x & 1) == 0) {
+        asm volatile("" ::: "memory");         // not loaded further ahead: registers
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint8_t* p = codes + (2 * c + (k & 1) + 8 * (k >> 1)) * kQ4Codes<HD>;
-        if constexpr (G == 4) {
-          const uint2 u = *reinterpret_cast<const uint2*>(p);
-          w[k][0] = u.x;
-          w[k][1] = u.y;
-        } else {
-          w[k][0] = *reinterpret_cast<const uint32_t*>(p);
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = 16 * h + 2 * c + (k & 1) + 8 * (k >> 1);
+            w[h][k] = *reinterpret_cast<const uint32_t*>(vr + (G == 4 ? chunk_at<HD>(row, g >> 1, true) + 8 * (g & 1) + 2 * x
+                                                                      : row * kQ4Codes<HD> + 4 * g));
+          }
+          st[h][0] = *reinterpret_cast<const float2*>(steps + (kTile + 16 * h + g) * G + x);
+          st[h][1] = *reinterpret_cast<const float2*>(steps + (kTile + 16 * h + 8 + g) * G + x);
         }
       }
-      float sa[G], sb[G];
-      const uint8_t* steps = vr + lay.steps + h * lay.steps_half;
-      load_steps<G>(steps + g * G, sa);
-      load_steps<G>(steps + (g + 8) * G, sb);
+      uint2 b[2][NT];
 #pragma unroll
-      for (int x = 0; x < G; ++x) {
-        const uint32_t sel = x & 1 ? 0x7632 : 0x5410;
-        const uint32_t u = __byte_perm(w[0][x / 2], w[1][x / 2], sel), v = __byte_perm(w[2][x / 2], w[3][x / 2], sel);
-        uint2 b[NT];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float t[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float st = i < 2 ? sa[x] : sb[x];
-            // a key that is not seen may have any step
-            t[i] = EDGE && s[h][n][i] == 0.f ? 0.f : s[h][n][i] * st;
+          for (int k = 0; k < 2; ++k) {
+            const float step = x & 1 ? st[h][k].y : st[h][k].x;
+            t[2 * k] = s[h][n][2 * k] * step;
+            t[2 * k + 1] = s[h][n][2 * k + 1] * step;
           }
-          b[n] = make_uint2(transpose8(pack_bf16x2(t[0], t[1])), transpose8(pack_bf16x2(t[2], t[3])));
+          if constexpr (EDGE) {                // a key that is not seen may have any step
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (s[h][n][i] == 0.f) t[i] = 0.f;
+          }
+          b[h][n] = make_uint2(transpose8(pack_bf16x2(t[0], t[1])), transpose8(pack_bf16x2(t[2], t[3])));
         }
+      float base[4];
+      if constexpr (C::kOffsetByProduct) {
+        const uint32_t minus[4] = {kMinus8, kMinus128, kMinus8, kMinus128};
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        mma(base, minus, b[0][0], zero);
+        mma(base, minus, b[1][0], base);
+      }
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          uint32_t f[4] = {pair_of(u, 2 * t), pair_of(u, 2 * t + 1), pair_of(v, 2 * t), pair_of(v, 2 * t + 1)};
+      for (int t = 0; t < 2; ++t) {
+        const int byte = 2 * (x & 1) + t;      // of each word: the codes of rows g and (16 times) g + 8 of the tile
+        uint32_t v[2][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 z = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&f[i]), off);
-            f[i] = *reinterpret_cast<const uint32_t*>(&z);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t u = __byte_perm(w[h][2 * k], w[h][2 * k + 1], byte | (4 + byte) << 8);
+            v[h][2 * k] = u & kLow;
+            v[h][2 * k + 1] = u & kHigh;
+            if constexpr (!C::kOffsetByProduct) {
+              v[h][2 * k] = add_bf16x2(v[h][2 * k], kMinus8);
+              v[h][2 * k + 1] = add_bf16x2(v[h][2 * k + 1], kMinus128);
+            }
           }
+        if constexpr (C::kOffsetByProduct) {
+          float d[4];
+          mma(d, v[0], b[0][0], base);
+          mma(d, v[1], b[1][0], d);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma(o[n][x][t], f, b[n]);
+          for (int i = 0; i < 4; i += 2) {
+            float* to = &o[0][x][t][i];
+            f2_unpack(f2_add(f2_pack(to[0], to[1]), f2_pack(d[i], d[i + 1])), to[0], to[1]);
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma(o[n][x][t], v[0], b[0][n], o[n][x][t]);
+            mma(o[n][x][t], v[1], b[1][n], o[n][x][t]);
+          }
         }
       }
     }
@@ -629,7 +766,8 @@ __device__ __forceinline__ void finish(const AttnQ4Args<N>& a, const Item& it, S
 #pragma unroll
         for (int x = 0; x < C::G; ++x)
           *reinterpret_cast<float4*>(&sm->part[warp][2 * c + e][32 * x + 4 * g]) =
-              make_float4(r.o[n][x][0][e], r.o[n][x][0][2 + e], r.o[n][x][1][e], r.o[n][x][1][2 + e]);
+              make_float4(r.o[n][x][0][e] * kOutScale, r.o[n][x][0][2 + e] * (kOutScale / 16), r.o[n][x][1][e] * kOutScale,
+                          r.o[n][x][1][2 + e] * (kOutScale / 16));
     }
     __syncthreads();
     constexpr int F4 = HD / 4;
@@ -675,30 +813,27 @@ paged_attn_q4_kernel(const __grid_constant__ AttnQ4Args<N> a) {
   using C = Cfg<HD, NT>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   auto* sm = reinterpret_cast<Smem<HD, NT>*>(smem_raw);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5;
   if (a.whole == 0 && threadIdx.x == 0) a.joins[blockIdx.x].last = -1;
-  if (lane == 0)
-    for (int s = 0; s < C::kStages; ++s) mbar_init(&sm->full[warp][s], 1);
-  if (threadIdx.x == 0) sm->abort_flag = 0;
-  fence_mbar_init();
   if (warp == 0) find_piece<C::W, C::RT, N>(a, &sm->piece);
   // the join may be set up from here on; it waits for this grid's end itself
   if (a.whole == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
   const Q4Piece piece = sm->piece;
-  const Layout lay = layout_of<HD>(a);
+
+  if ((threadIdx.x & 31) == 0)
+    for (int i = 0; i < 2; ++i) sm->spot[i][warp].walk.start(a, piece);
+  __syncwarp();
 
   Loader<HD, NT, N> load;
-  load.start(a, piece);
+  load.start(a, &sm->spot[0][warp]);
 #pragma unroll 1
   for (int s = 0; s < C::kStages; ++s) load.issue(a, sm);
 
-  Walk<C::W, C::RT, N> walk;
-  walk.start(a, piece);
-  Item it;
   Rows<HD, NT> rows;
-  uint32_t stage = 0, parity = 0;
-  while (walk.next(a, &it)) {
+  uint32_t stage = 0;
+  const Item& it = sm->spot[1][warp].item;
+  while (next_item<C::W, C::RT>(a, &sm->spot[1][warp])) {
     rows.start(a, it, sm);
     // keys that every row sees
     int lo, hi, x;
@@ -707,32 +842,22 @@ paged_attn_q4_kernel(const __grid_constant__ AttnQ4Args<N> a) {
     keys_of(a, it.len, it.len - it.q_len + last / a.group, &lo, &x);
 #pragma unroll 1
     for (int t = it.s0 + warp; t < it.s1; t += C::W) {
-      // (a wait that runs out is recorded, and the rows' values are wrong)
-      mbar_wait(&sm->full[warp][stage], parity, &sm->abort_flag, &g_attn_q4_err, ERR_TIMEOUT_OTHER);
+      copies_wait<C::kStages - 1>();
       __syncwarp();
       const uint8_t* kr = sm->stage[warp][stage][0];
       const uint8_t* vr = sm->stage[warp][stage][1];
+      float* steps = &sm->part[warp][0][0];    // free until the unit's end
       const int pos = t * kTile;
-      if (pos >= lo && pos + kTile <= hi) rows.template tile<false>(a, it, sm, kr, vr, lay, pos);
-      else rows.template tile<true>(a, it, sm, kr, vr, lay, pos);
+      if (pos >= lo && pos + kTile <= hi) rows.template tile<false>(a, it, sm, kr, vr, steps, pos);
+      else rows.template tile<true>(a, it, sm, kr, vr, steps, pos);
       __syncwarp();                            // the stage has been read
       load.issue(a, sm);
-      if (++stage == C::kStages) {
-        stage = 0;
-        parity ^= 1u;
-      }
+      if (++stage == C::kStages) stage = 0;
     }
     finish<HD, NT, N>(a, it, sm, rows);
     if (it.slot >= 0 && it.first && threadIdx.x == 0)
       a.joins[blockIdx.x] = {a.segs[it.seg].q_row0, it.rt * C::RT, it.rows, it.hk,
                              static_cast<int32_t>((it.behind - 1) / piece.per)};
-  }
-  // after a wait that ran out, copies may still be on their way
-  __syncthreads();
-  if (*reinterpret_cast<volatile int*>(&sm->abort_flag)) {
-    const uint64_t t0 = globaltimer();
-    while (globaltimer() - t0 < 2000000ull) {
-    }
   }
 }
 
