@@ -187,10 +187,11 @@ struct UnpackQ4Args : UnpackQ4Head {
 };
 
 // A launch of the attention of few rows over a 4-bit cache.  A CTA's piece of the
-// line of units: it begins `off` into the unit (seg, hk, rt), at g of the line.
+// line of units: it begins `off` into the unit (seg, hk, rt).
 struct Q4Piece {
   int32_t seg, hk, rt;
-  int64_t off, g, end;
+  int32_t off;
+  int64_t left;                 // its length
   int64_t per;                  // of every CTA
 };
 
@@ -217,7 +218,7 @@ struct AttnQ4Head {
   Q4Join* joins;                // [CTAs]
   int64_t q_stride;
   int64_t lse_stride;
-  int64_t page_bytes;           // of a pool's page, all heads
+  int32_t page_bytes;           // of a pool's page, all heads
   int32_t num_heads;
   int32_t num_kv_heads;
   int32_t group;                // query heads of a key head

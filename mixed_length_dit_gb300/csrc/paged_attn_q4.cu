@@ -25,7 +25,7 @@
 // products take such numbers as they are.  So a code in bits 0 to 3 is n, one in
 // bits 4 to 7 is 16 n, and the other factor brings the size: a row of q is scaled
 // by a power of two so that its largest element lies at 2^120 (columns whose codes
-// come 16 times over by 1/16 of it), a value's steps by 2^100.  All of it is exact.
+// come 16 times over by 1/16 of it), P by 2^60.  All of it is exact.
 // A word's codes are four operands after five logical operations; two tokens' codes
 // of a column, as V wants them, take a byte permutation more for each.
 //
@@ -54,8 +54,8 @@ constexpr uint32_t kLow = 0x000f000fu;         // of codes: n, and 16 n
 constexpr uint32_t kHigh = 0x00f000f0u;
 constexpr uint32_t kMinus8 = 0x80088008u;      // -8 n's unit, twice, and 16 times that
 constexpr uint32_t kMinus128 = 0x80808080u;
-constexpr float kStepScale = 0x1p100f;         // a value's steps
-constexpr float kOutScale = 0x1p33f;           // from sums of codes to the output
+constexpr float kPScale = 60.f;                // P comes 2^60 times over
+constexpr float kOutScale = 0x1p73f;           // from sums of codes to the output
 
 template <int HD, int NT>
 struct Cfg {
@@ -76,6 +76,9 @@ template <int TO, int FROM>
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
   asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;"
                :: "r"(dst), "l"(__cvta_generic_to_global(src)), "n"(TO), "n"(FROM) : "memory");
+}
+__device__ __forceinline__ const uint8_t* in_page(const uint8_t* p, int page, int page_bytes) {
+  return p + static_cast<int64_t>(page) * page_bytes;
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -123,14 +126,13 @@ __device__ __forceinline__ void load_floats(const float* p, float (&w)[G]) {
 
 // A token's steps from its bytes to floats.
 template <int G>
-__device__ __forceinline__ void spread_steps(float* to, const uint8_t* p, float times) {
+__device__ __forceinline__ void spread_steps(float* to, const uint8_t* p) {
   if constexpr (G == 4) {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
     const float2 a = q4_steps01(w), b = q4_steps23(w);
-    *reinterpret_cast<float4*>(to) = make_float4(a.x * times, a.y * times, b.x * times, b.y * times);
+    *reinterpret_cast<float4*>(to) = make_float4(a.x, a.y, b.x, b.y);
   } else {
-    const float2 a = q4_steps01(*reinterpret_cast<const uint16_t*>(p));
-    *reinterpret_cast<float2*>(to) = make_float2(a.x * times, a.y * times);
+    *reinterpret_cast<float2*>(to) = q4_steps01(*reinterpret_cast<const uint16_t*>(p));
   }
 }
 
@@ -184,6 +186,11 @@ __device__ __forceinline__ int64_t seg_weight(const AttnQ4Head& a, int len, int 
   return sum;
 }
 
+__device__ __forceinline__ int64_t div_nonneg(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 __device__ __forceinline__ int64_t warp_sum(int64_t x) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
@@ -195,7 +202,7 @@ template <int W, int RT, int N>
 __device__ void find_piece(const AttnQ4Args<N>& a, Q4Piece* out) {
   const int lane = threadIdx.x & 31;
   const int c = blockIdx.x, nk = a.num_kv_heads;
-  Q4Piece p = {0, 0, 0, 0, 0, 0, 0};
+  Q4Piece p = {0, 0, 0, 0, 0, 1};
   if (a.whole > 0) {                           // few short units: each CTA has one to itself
     int x = c;
     for (;; ++p.seg) {
@@ -206,18 +213,17 @@ __device__ void find_piece(const AttnQ4Args<N>& a, Q4Piece* out) {
     const int rts = row_tiles<RT>(a, a.segs[p.seg].q_len);
     p.hk = x / rts;
     p.rt = x - p.hk * rts;
-    p.end = 1;                                 // any piece ends within its first unit
-    p.per = 0;
+    p.left = 1;                                // any piece ends within its first unit
     if (lane == 0) *out = p;
     return;
   }
   int64_t total = 0;
   for (int s = lane; s < a.n_segs; s += 32) total += seg_weight<W, RT>(a, length_of(a, s), a.segs[s].q_len);
   total = warp_sum(total) * nk;
-  p.per = max(int64_t(1 + kUnitCost), (total + gridDim.x - 1) / gridDim.x);
-  p.g = c * p.per;
-  p.end = min(total, p.g + p.per);
-  if (p.g < p.end) {
+  p.per = max(int64_t(1 + kUnitCost), div_nonneg(total + gridDim.x - 1, gridDim.x));
+  const int64_t g = c * p.per;
+  p.left = max(int64_t(0), min(total - g, p.per));
+  if (p.left > 0) {
     int64_t base = 0;
     for (int chunk = 0;; chunk += 32) {
       int64_t w = 0;
@@ -229,23 +235,24 @@ __device__ void find_piece(const AttnQ4Args<N>& a, Q4Piece* out) {
         if (lane >= d) incl += y;
       }
       incl += base;
-      const uint32_t past = __ballot_sync(0xffffffffu, incl > p.g);
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > g);
       if (past != 0) {
         const int k = __ffs(past) - 1;
         const int64_t one = __shfl_sync(0xffffffffu, w, k);
+        int64_t off = g - (__shfl_sync(0xffffffffu, incl, k) - one * nk);
         p.seg = chunk + k;
-        p.off = p.g - (__shfl_sync(0xffffffffu, incl, k) - one * nk);
-        p.hk = static_cast<int>(p.off / one);
-        p.off -= p.hk * one;
+        p.hk = static_cast<int>(div_nonneg(off, one));
+        off -= p.hk * one;
+        const int len = length_of(a, p.seg), q_len = a.segs[p.seg].q_len;
+        for (;; ++p.rt) {
+          const int weight = unit_weight<W, RT>(a, len, q_len, p.rt);
+          if (off < weight) break;
+          off -= weight;
+        }
+        p.off = static_cast<int>(off);
         break;
       }
       base = __shfl_sync(0xffffffffu, incl, 31);
-    }
-    const int len = length_of(a, p.seg), q_len = a.segs[p.seg].q_len;
-    for (;; ++p.rt) {
-      const int w = unit_weight<W, RT>(a, len, q_len, p.rt);
-      if (p.off < w) break;
-      p.off -= w;
     }
   }
   if (lane == 0) *out = p;
@@ -257,29 +264,30 @@ struct Item {
   int len, q_len, rows;                        // rows of the unit
   int s0, s1;
   int slot;                                    // slot of partial rows; -1: the rows are final
-  bool first;                                  // slot >= 0: the unit begins here
-  int64_t behind;                              // and where the line's next unit begins
+  int behind;                                  // of a unit that begins here: what it weighs behind the piece, else 0
 };
 
 // Walks a CTA's items; every warp for itself, once for its copies and once for
 // its products.
 struct Walk {
   int seg, hk, rt;
-  int64_t off, g, end;
+  int off;                                     // into the unit
+  int64_t left;                                // of the piece
   int len, q_len;
 
   template <int N>
   __device__ __forceinline__ void start(const AttnQ4Args<N>& a, const Q4Piece& p) {
-    seg = p.seg; hk = p.hk; rt = p.rt; off = p.off; g = p.g; end = p.end;
-    if (g < end) {
+    seg = p.seg; hk = p.hk; rt = p.rt; off = p.off; left = p.left;
+    if (left > 0) {
       len = length_of(a, seg);
       q_len = a.segs[seg].q_len;
     }
   }
 
+  // The next item; false: none left.
   template <int W, int RT, int N>
   __device__ __forceinline__ bool next(const AttnQ4Args<N>& a, Item* it) {
-    while (g < end) {
+    while (left > 0) {
       const int rows = q_len * a.group, r0 = rt * RT;
       it->seg = seg; it->hk = hk; it->rt = rt;
       it->len = len; it->q_len = q_len;
@@ -288,29 +296,28 @@ struct Walk {
       it->s0 = t.t0;
       it->s1 = t.t1;
       it->slot = -1;
+      it->behind = 0;
       if (a.whole > 0) {
-        g = end;
+        left = 0;
         return true;
       }
-      const int waves = waves_of<W>(t);
-      const int64_t avail = min(kUnitCost + waves - off, end - g);
-      const int w0 = static_cast<int>(max(off - kUnitCost, int64_t(0)));       // the piece's waves of the unit
-      const int w1 = static_cast<int>(max(off + avail - kUnitCost, int64_t(0)));
-      it->behind = g - off + kUnitCost + waves;
+      const int waves = waves_of<W>(t), rest = kUnitCost + waves - off;
+      const int avail = left < rest ? static_cast<int>(left) : rest;
+      const int w0 = max(off - kUnitCost, 0), w1 = max(off + avail - kUnitCost, 0);      // the piece's waves of the unit
       if (w1 - w0 < waves) {
-        it->first = w0 == 0;
-        it->slot = it->first ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
+        it->slot = w0 == 0 ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
+        if (w0 == 0) it->behind = rest - avail;
         it->s0 = t.t0 + w0 * W;
         it->s1 = min(t.t1, t.t0 + w1 * W);
       }
-      g += avail;
+      left -= avail;
       off = 0;
-      if (++rt >= row_tiles<RT>(a, q_len)) {
+      if (++rt * RT >= rows) {
         rt = 0;
         if (++hk >= a.num_kv_heads) {
           hk = 0;
           ++seg;
-          if (g < end) {
+          if (left > 0) {
             len = length_of(a, seg);
             q_len = a.segs[seg].q_len;
           }
@@ -329,10 +336,9 @@ struct Spot {
   Item item;
   // of the copies: the first token's codes in page 0, keys' and values', its steps
   // behind the first code of the block, and the sequence's row of the table
-  const uint8_t* k;
-  const uint8_t* v;
-  int32_t steps;
+  const uint8_t* kv[2];
   const int32_t* entries;
+  int32_t steps;
 };
 
 template <int HD, int NT>
@@ -341,8 +347,7 @@ struct Smem {
   alignas(128) uint8_t stage[C::W][C::kStages][2][C::kRegion];
   alignas(16) float part[C::W][8][C::kPad];    // 8 rows of every warp
   float m[C::W][C::RT], l[C::W][C::RT];
-  // Of the item's queries, the same for all warps (each writes them, so that none
-  // waits for another): fragments of q^T for a group's two products, and their first
+  // Of the item's queries: fragments of q^T for a group's two products, and their first
   // sums, -8 sum q of rows 2c, 2c + 1 for keys g and g + 8.
   uint4 q[NT][C::G][32];
   float4 q_sum[NT][C::G][4];
@@ -406,8 +411,8 @@ struct Loader {
     if ((threadIdx.x & 31) == 0) {
       const int ps = 1 << a.page_shift, row = (tile * kTile) & (ps - 1);
       const int64_t codes = ((static_cast<int64_t>(at->item.hk) * kQ4Row<HD>) << a.page_shift) + row * kQ4Codes<HD>;
-      at->k = a.k_pages + codes;
-      at->v = a.v_pages + codes;
+      at->kv[0] = a.k_pages + codes;
+      at->kv[1] = a.v_pages + codes;
       at->steps = ps * kQ4Codes<HD> + row * (kQ4Steps<HD> - kQ4Codes<HD>);
       at->entries = a.page_table + static_cast<int64_t>(a.segs[at->item.seg].seq) * a.table_cols;
     }
@@ -435,37 +440,41 @@ struct Loader {
       }
       const uint32_t to = smem_u32(sm->stage[warp][stage][0]);
       const uint32_t to_k = to + 16 * lane, to_v = to + C::kRegion + chunk_at<HD>(lane / kLanes, lane % kLanes, true);
-      const int64_t p0 = static_cast<int64_t>(page[0]) * a.page_bytes;
-      const uint8_t* k0 = at->k + p0;
-      const uint8_t* v0 = at->v + p0;
-      const uint8_t* k1 = k0 + 16 * kQ4Codes<HD>;
-      const uint8_t* v1 = v0 + 16 * kQ4Codes<HD>;
-      int64_t on = 16 * kQ4Steps<HD>;          // from the first 16 tokens' steps to the second's
-      if (a.page_shift == 4) {                 // they are in a page of their own
-        on = static_cast<int64_t>(page[1] - page[0]) * a.page_bytes;
-        k1 = k0 + on;
-        v1 = v0 + on;
-      }
       constexpr int kHalf = 16 * kQ4Codes<HD>;
-      copy16<0, 0>(to_k, k0 + 16 * lane);
-      copy16<0, 0>(to_v, v0 + 16 * lane);
+      const uint8_t* k = at->kv[0] + 16 * lane;
+      const uint8_t* v = at->kv[1] + 16 * lane;
+      const uint8_t* k0 = in_page(k, page[0], a.page_bytes);
+      const uint8_t* v0 = in_page(v, page[0], a.page_bytes);
+      copy16<0, 0>(to_k, k0);
+      copy16<0, 0>(to_v, v0);
       if constexpr (kRows < 16) {
-        copy16<512, 512>(to_k, k0 + 16 * lane);
-        copy16<512, 512>(to_v, v0 + 16 * lane);
+        copy16<512, 512>(to_k, k0);
+        copy16<512, 512>(to_v, v0);
       }
-      if (both) {
-        copy16<kHalf, 0>(to_k, k1 + 16 * lane);
-        copy16<kHalf, 0>(to_v, v1 + 16 * lane);
+      if (a.page_shift > 4) {
+        copy16<kHalf, kHalf>(to_k, k0);
+        copy16<kHalf, kHalf>(to_v, v0);
         if constexpr (kRows < 16) {
-          copy16<kHalf + 512, 512>(to_k, k1 + 16 * lane);
-          copy16<kHalf + 512, 512>(to_v, v1 + 16 * lane);
+          copy16<kHalf + 512, kHalf + 512>(to_k, k0);
+          copy16<kHalf + 512, kHalf + 512>(to_v, v0);
+        }
+      } else if (both) {                       // the second 16 tokens are in a page of their own
+        const uint8_t* k1 = in_page(k, page[1], a.page_bytes);
+        const uint8_t* v1 = in_page(v, page[1], a.page_bytes);
+        copy16<kHalf, 0>(to_k, k1);
+        copy16<kHalf, 0>(to_v, v1);
+        if constexpr (kRows < 16) {
+          copy16<kHalf + 512, 512>(to_k, k1);
+          copy16<kHalf + 512, 512>(to_v, v1);
         }
       }
       if (lane < 2 * kStepLanes) {
-        const bool values = lane >= kStepLanes, second = lane % kStepLanes >= kStepLanes / 2;
+        const int values = lane / kStepLanes, of = lane % kStepLanes;
+        const bool second = a.page_shift == 4 && of >= kStepLanes / 2;
         if (both || !second)
-          copy16<C::kSteps, 0>(to + (values ? C::kRegion : 0) + 16 * (lane % kStepLanes),
-                               (values ? v0 : k0) + at->steps + (second ? on : 0) + 16 * (lane % (kStepLanes / 2)));
+          copy16<C::kSteps, 0>(to + values * C::kRegion + 16 * of,
+                               in_page(at->kv[values] + (at->steps + 16 * (second ? of - kStepLanes / 2 : of)),
+                                       second ? page[1] : page[0], a.page_bytes));
       }
       tile += C::W;
       if (tile < end) fetch(a);
@@ -479,32 +488,32 @@ struct Loader {
 // ------------------------------------------------------------------ products
 // A warp's share of a unit: lane (g, c) = (lane / 4, lane % 4) of the products'
 // fragments.  Scores are S^T (keys g, g + 8 by rows 2c, 2c + 1), the output o^T
-// (columns 32 q + 4 g + (0 .. 3) by rows 2c, 2c + 1; 2^-33 of it, of the odd
-// columns 2^-29).
+// (columns 32 q + 4 g + (0 .. 3) by rows 2c, 2c + 1; 2^-73 of it, of the odd
+// columns 2^-69).
 template <int HD, int NT>
 struct Rows {
   using C = Cfg<HD, NT>;
   static constexpr int G = C::G;
   float o[NT][G][2][4];                        // [tile of 16 columns][fragment]
-  float m[NT][2], l[NT][2];                    // of rows 2c, 2c + 1; l: the lane's keys alone
+  float m[NT][2], l[NT][2];                    // of rows 2c, 2c + 1; l: the lane's keys alone, 2^60 times
   float f[NT][2];                              // their q_scale
 
   template <int N>
   __device__ __forceinline__ void start(const AttnQ4Args<N>& a, const Item& it, Smem<HD, NT>* sm) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    // the warps make the fragments of a group of 8 rows each
 #pragma unroll 1
-    for (int n = 0; n < NT; ++n) {
-      const int r = 8 * n + g;
+    for (int i = threadIdx.x >> 5; i < NT * G; i += C::W) {
+      const int n = i / G, x = i % G, r = 8 * n + g;
       const int row = it.rt * C::RT + r, tok = row / a.group;
       const __nv_bfloat16* src = a.q + (a.segs[it.seg].q_row0 + static_cast<int64_t>(tok)) * a.q_stride +
                                  (it.hk * a.group + row - tok * a.group) * HD + 8 * c;
-      uint4 u[G];
+      uint4 u = make_uint4(0, 0, 0, 0);
       uint32_t top = 0;
+      if (r < it.rows) {
+        u = __ldg(reinterpret_cast<const uint4*>(src + 32 * x));
 #pragma unroll
-      for (int x = 0; x < G; ++x) {
-        u[x] = make_uint4(0, 0, 0, 0);
-        if (r < it.rows) u[x] = __ldg(reinterpret_cast<const uint4*>(src + 32 * x));
-        top = __vmaxu2(top, q4_top(u[x]));
+        for (int y = 0; y < G; ++y) top = __vmaxu2(top, q4_top(__ldg(reinterpret_cast<const uint4*>(src + 32 * y))));
       }
       top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -515,25 +524,20 @@ struct Rows {
       const float up = __uint_as_float(static_cast<uint32_t>(up_exp) << 23);
       const float down = top >= 0x7f80u ? __uint_as_float(0x7fffffffu)
                                         : __uint_as_float(static_cast<uint32_t>(min(387 - up_exp, 254)) << 23) * a.scale_log2;
-      if (c == 0) sm->q_scale[r] = down;
-#pragma unroll
-      for (int x = 0; x < G; ++x) {
-        const float2 x0 = bf16x2_to_float2(u[x].x), x1 = bf16x2_to_float2(u[x].y), x2 = bf16x2_to_float2(u[x].z),
-                     x3 = bf16x2_to_float2(u[x].w);
-        // columns j and j + 4 beside one another, as a word's codes are taken; the odd ones' codes come 16 times over
-        const float odd = up * 0.0625f;
-        const uint4 b = make_uint4(pack_bf16x2(x0.x * up, x2.x * up), pack_bf16x2(x0.y * odd, x2.y * odd),
-                                   pack_bf16x2(x1.x * up, x3.x * up), pack_bf16x2(x1.y * odd, x3.y * odd));
-        float sum = ((x0.x + x0.y) + (x1.x + x1.y)) + ((x2.x + x2.y) + (x3.x + x3.y));
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum = sum * up * (-8.f * 0x1p-66f) * 0x1p-67f;
-        const float s0 = __shfl_sync(0xffffffffu, sum, 8 * c), s1 = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
-        sm->q[n][x][lane] = b;
-        if (g == 0) sm->q_sum[n][x][c] = make_float4(s0, s1, s0, s1);
-      }
+      if (c == 0 && x == 0) sm->q_scale[r] = down;
+      const float2 x0 = bf16x2_to_float2(u.x), x1 = bf16x2_to_float2(u.y), x2 = bf16x2_to_float2(u.z), x3 = bf16x2_to_float2(u.w);
+      // columns j and j + 4 beside one another, as a word's codes are taken; the odd ones' codes come 16 times over
+      const float odd = up * 0.0625f;
+      sm->q[n][x][lane] = make_uint4(pack_bf16x2(x0.x * up, x2.x * up), pack_bf16x2(x0.y * odd, x2.y * odd),
+                                     pack_bf16x2(x1.x * up, x3.x * up), pack_bf16x2(x1.y * odd, x3.y * odd));
+      float sum = ((x0.x + x0.y) + (x1.x + x1.y)) + ((x2.x + x2.y) + (x3.x + x3.y));
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      sum = sum * up * (-8.f * 0x1p-66f) * 0x1p-67f;
+      const float s0 = __shfl_sync(0xffffffffu, sum, 8 * c), s1 = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+      if (g == 0) sm->q_sum[n][x][c] = make_float4(s0, s1, s0, s1);
     }
-    __syncwarp();
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -557,13 +561,12 @@ struct Rows {
   __device__ __forceinline__ void tile(const AttnQ4Head& a, const Item& it, const Smem<HD, NT>* sm, const uint8_t* kr,
                                        const uint8_t* vr, float* steps, int pos) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    spread_steps<G>(steps + lane * G, kr + C::kSteps + lane * G, 1.f);
-    spread_steps<G>(steps + (kTile + lane) * G, vr + C::kSteps + lane * G, kStepScale);
+    spread_steps<G>(steps + lane * G, kr + C::kSteps + lane * G);
+    spread_steps<G>(steps + (kTile + lane) * G, vr + C::kSteps + lane * G);
     __syncwarp();
     float s[2][NT][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {              // 16 keys
-      asm volatile("" ::: "memory");
       uint32_t wa[G], wb[G];
       float sa[G], sb[G];
       const uint8_t* codes = kr + (16 * h + g) * kQ4Codes<HD> + c * (4 * G);
@@ -588,12 +591,8 @@ struct Rows {
           for (int k = 0; k < 2; ++k) {        // keys g, g + 8
             const float st = k ? sb[x] : sa[x];
             float* to = &s[h][n][2 * k];
-            if (x == 0) {
-              to[0] = st * d[2 * k];
-              to[1] = st * d[2 * k + 1];
-            } else {
-              f2_unpack(f2_fma(f2_pack(st, st), f2_pack(d[2 * k], d[2 * k + 1]), f2_pack(to[0], to[1])), to[0], to[1]);
-            }
+            const uint64_t st2 = f2_pack(st, st), d2 = f2_pack(d[2 * k], d[2 * k + 1]);
+            f2_unpack(x == 0 ? f2_mul(st2, d2) : f2_fma(st2, d2, f2_pack(to[0], to[1])), to[0], to[1]);
           }
         }
       }
@@ -646,7 +645,7 @@ struct Rows {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float neg = m[n][e] == -INFINITY ? 0.f : -m[n][e];
+        const float neg = m[n][e] == -INFINITY ? 0.f : kPScale - m[n][e];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -685,8 +684,7 @@ struct Rows {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float step = x & 1 ? st[h][k].y : st[h][k].x;
-            t[2 * k] = s[h][n][2 * k] * step;
-            t[2 * k + 1] = s[h][n][2 * k + 1] * step;
+            f2_unpack(f2_mul(f2_pack(s[h][n][2 * k], s[h][n][2 * k + 1]), f2_pack(step, step)), t[2 * k], t[2 * k + 1]);
           }
           if constexpr (EDGE) {                // a key that is not seen may have any step
 #pragma unroll
@@ -754,7 +752,7 @@ __device__ __forceinline__ void finish(const AttnQ4Args<N>& a, const Item& it, S
       for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
       if (g == 0) {
         sm->m[warp][8 * n + 2 * c + e] = r.m[n][e];
-        sm->l[warp][8 * n + 2 * c + e] = l;
+        sm->l[warp][8 * n + 2 * c + e] = l * 0x1p-60f;
       }
     }
   }
@@ -855,9 +853,9 @@ paged_attn_q4_kernel(const __grid_constant__ AttnQ4Args<N> a) {
       if (++stage == C::kStages) stage = 0;
     }
     finish<HD, NT, N>(a, it, sm, rows);
-    if (it.slot >= 0 && it.first && threadIdx.x == 0)
+    if (it.behind > 0 && threadIdx.x == 0)     // the CTAs behind have a whole piece each
       a.joins[blockIdx.x] = {a.segs[it.seg].q_row0, it.rt * C::RT, it.rows, it.hk,
-                             static_cast<int32_t>((it.behind - 1) / piece.per)};
+                             static_cast<int32_t>(blockIdx.x + div_nonneg(it.behind + piece.per - 1, piece.per))};
   }
 }
 

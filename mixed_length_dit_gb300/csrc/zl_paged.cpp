@@ -529,7 +529,7 @@ zl_status launch_few_q4(const Attend& c, void* workspace) {
   a.lse = c.lse;
   a.q_stride = c.q_stride;
   a.lse_stride = c.tq;
-  a.page_bytes = (int64_t(cache.num_kv_heads) * cache.page_size) * (cache.head_dim * 17 / 32);
+  a.page_bytes = cache.num_kv_heads * cache.page_size * (cache.head_dim * 17 / 32);   // at most 4096 * 256 * 68
   a.num_heads = c.num_heads;
   a.num_kv_heads = cache.num_kv_heads;
   a.group = c.group();
