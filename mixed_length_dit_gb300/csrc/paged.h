@@ -222,6 +222,7 @@ struct AttnQ4Head {
   int32_t num_heads;
   int32_t num_kv_heads;
   int32_t group;                // query heads of a key head
+  int32_t group_inv;            // 65536 / group, rounded up
   int32_t table_cols;
   int32_t num_pages;
   int32_t page_shift;
@@ -231,6 +232,12 @@ struct AttnQ4Head {
   float scale_log2;             // softmax scale * log2(e)
   int32_t n_segs;
   int32_t whole;                // > 0: the launch's units; each has a CTA to itself, and no join follows
+
+#ifdef __CUDACC__
+  // The token of a sequence's row, row / group: exact for rows below 512 and groups
+  // up to 128, because row * (group * group_inv - 65536) < 512 * 128.
+  __device__ __forceinline__ int row_token(int row) const { return (row * group_inv) >> 16; }
+#endif
 };
 
 template <int N>

@@ -61,14 +61,15 @@ template <int HD, int NT>
 struct Cfg {
   static constexpr int G = HD / kQ4Group;
   static constexpr int RT = 8 * NT;            // rows of a unit
-  static constexpr int W = 8;                  // warps of a CTA
+  static constexpr int W = NT == 1 ? 6 : 8;    // warps of a CTA
   static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
-  static constexpr int kStages = NT == 1 ? 2 : 3;
+  static constexpr int kStages = 3;
   static constexpr int kRegion = kTile * kQ4Row<HD>;           // keys, or values, of a stage
   static constexpr int kSteps = kTile * kQ4Codes<HD>;          // its steps, behind the codes
   // -8 sum_j: by a product with a constant, the sums of a tile apart (of few rows,
   // whose products cost little), or by subtraction from the codes
   static constexpr bool kOffsetByProduct = NT == 1;
+  static_assert(W <= 8, "a warp's lanes look at 8 warps");
   static constexpr int kPad = HD + 4;          // floats of a row to be joined (rows 2c of four lanes in different banks)
 };
 
@@ -149,8 +150,8 @@ __device__ __forceinline__ void keys_of(const AttnQ4Head& a, int len, int p, int
 
 __device__ __forceinline__ Tiles tiles_of(const AttnQ4Head& a, int len, int q_len, int r0, int r1) {
   int lo, hi, x;
-  keys_of(a, len, len - q_len + r0 / a.group, &lo, &x);
-  keys_of(a, len, len - q_len + (r1 - 1) / a.group, &x, &hi);
+  keys_of(a, len, len - q_len + a.row_token(r0), &lo, &x);
+  keys_of(a, len, len - q_len + a.row_token(r1 - 1), &x, &hi);
   if (hi <= lo) return {0, 0};
   return {lo / kTile, (hi + kTile - 1) / kTile};
 }
@@ -334,11 +335,10 @@ struct Walk {
 struct Spot {
   Walk walk;
   Item item;
-  // of the copies: the first token's codes in page 0, keys' and values', its steps
-  // behind the first code of the block, and the sequence's row of the table
+  // of the copies: the head's block in page 0, keys' and values', and the
+  // sequence's row of the table
   const uint8_t* kv[2];
   const int32_t* entries;
-  int32_t steps;
 };
 
 template <int HD, int NT>
@@ -346,7 +346,7 @@ struct Smem {
   using C = Cfg<HD, NT>;
   alignas(128) uint8_t stage[C::W][C::kStages][2][C::kRegion];
   alignas(16) float part[C::W][8][C::kPad];    // 8 rows of every warp
-  float m[C::W][C::RT], l[C::W][C::RT];
+  float m[C::W][C::RT], l[C::W][C::RT], lse[C::RT];
   // Of the item's queries: fragments of q^T for a group's two products, and their first
   // sums, -8 sum q of rows 2c, 2c + 1 for keys g and g + 8.
   uint4 q[NT][C::G][32];
@@ -380,9 +380,7 @@ __device__ __forceinline__ int chunk_at(int row, int chunk, bool values) {
 }
 
 // A warp's tiles, one after another: a copy is set off as soon as a stage is free,
-// with the page numbers that were fetched when the one before was.  A unit's tiles
-// of a warp are W tiles (256 keys) apart, the largest page's length, so they begin
-// at the same row of their pages.
+// with the page numbers that were fetched when the one before was.
 template <int HD, int NT, int N>
 struct Loader {
   using C = Cfg<HD, NT>;
@@ -393,7 +391,6 @@ struct Loader {
   int tile, end;                               // of the item; tile >= end: none left
   int page[2];                                 // of its first and its second 16 tokens
   uint32_t stage = 0;
-  static_assert(C::W * kTile == 256, "tiles of a warp begin at the same row of a page");
 
   __device__ __forceinline__ void fetch(const AttnQ4Args<N>& a) {
     const int32_t* e = at->entries + ((tile * kTile) >> a.page_shift);
@@ -409,11 +406,9 @@ struct Loader {
       end = at->item.s1;
     } while (tile >= end);
     if ((threadIdx.x & 31) == 0) {
-      const int ps = 1 << a.page_shift, row = (tile * kTile) & (ps - 1);
-      const int64_t codes = ((static_cast<int64_t>(at->item.hk) * kQ4Row<HD>) << a.page_shift) + row * kQ4Codes<HD>;
-      at->kv[0] = a.k_pages + codes;
-      at->kv[1] = a.v_pages + codes;
-      at->steps = ps * kQ4Codes<HD> + row * (kQ4Steps<HD> - kQ4Codes<HD>);
+      const int64_t block = (static_cast<int64_t>(at->item.hk) * kQ4Row<HD>) << a.page_shift;
+      at->kv[0] = a.k_pages + block;
+      at->kv[1] = a.v_pages + block;
       at->entries = a.page_table + static_cast<int64_t>(a.segs[at->item.seg].seq) * a.table_cols;
     }
     __syncwarp();
@@ -441,8 +436,9 @@ struct Loader {
       const uint32_t to = smem_u32(sm->stage[warp][stage][0]);
       const uint32_t to_k = to + 16 * lane, to_v = to + C::kRegion + chunk_at<HD>(lane / kLanes, lane % kLanes, true);
       constexpr int kHalf = 16 * kQ4Codes<HD>;
-      const uint8_t* k = at->kv[0] + 16 * lane;
-      const uint8_t* v = at->kv[1] + 16 * lane;
+      const int row = (tile * kTile) & ((1 << a.page_shift) - 1);
+      const uint8_t* k = at->kv[0] + (row * kQ4Codes<HD> + 16 * lane);
+      const uint8_t* v = at->kv[1] + (row * kQ4Codes<HD> + 16 * lane);
       const uint8_t* k0 = in_page(k, page[0], a.page_bytes);
       const uint8_t* v0 = in_page(v, page[0], a.page_bytes);
       copy16<0, 0>(to_k, k0);
@@ -473,7 +469,8 @@ struct Loader {
         const bool second = a.page_shift == 4 && of >= kStepLanes / 2;
         if (both || !second)
           copy16<C::kSteps, 0>(to + values * C::kRegion + 16 * of,
-                               in_page(at->kv[values] + (at->steps + 16 * (second ? of - kStepLanes / 2 : of)),
+                               in_page(at->kv[values] + ((kQ4Codes<HD> << a.page_shift) + row * kQ4Steps<HD> +
+                                                         16 * (second ? of - kStepLanes / 2 : of)),
                                        second ? page[1] : page[0], a.page_bytes));
       }
       tile += C::W;
@@ -505,7 +502,7 @@ struct Rows {
 #pragma unroll 1
     for (int i = threadIdx.x >> 5; i < NT * G; i += C::W) {
       const int n = i / G, x = i % G, r = 8 * n + g;
-      const int row = it.rt * C::RT + r, tok = row / a.group;
+      const int row = it.rt * C::RT + r, tok = a.row_token(row);
       const __nv_bfloat16* src = a.q + (a.segs[it.seg].q_row0 + static_cast<int64_t>(tok)) * a.q_stride +
                                  (it.hk * a.group + row - tok * a.group) * HD + 8 * c;
       uint4 u = make_uint4(0, 0, 0, 0);
@@ -603,7 +600,7 @@ struct Rows {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if constexpr (EDGE) {
-          const int tok = min(it.rt * C::RT + 8 * n + 2 * c + e, it.rt * C::RT + it.rows - 1) / a.group;
+          const int tok = a.row_token(min(it.rt * C::RT + 8 * n + 2 * c + e, it.rt * C::RT + it.rows - 1));
           int lo, hi;
           keys_of(a, it.len, it.len - it.q_len + tok, &lo, &hi);
 #pragma unroll
@@ -737,14 +734,14 @@ struct Rows {
   }
 };
 
-// Joins the warps' shares of an item and writes its rows.
+// Joins the warps' shares of an item and writes its rows: every warp weights its
+// sums by what it has of a row, and threads add them up, 8 rows at a time.
 template <int HD, int NT, int N>
 __device__ __forceinline__ void finish(const AttnQ4Args<N>& a, const Item& it, Smem<HD, NT>* sm, Rows<HD, NT>& r) {
   using C = Cfg<HD, NT>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const int n_warps = min(C::W, max(1, it.s1 - it.s0));        // the others had no tile
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float l = r.l[n][e];
@@ -755,50 +752,54 @@ __device__ __forceinline__ void finish(const AttnQ4Args<N>& a, const Item& it, S
         sm->l[warp][8 * n + 2 * c + e] = l * 0x1p-60f;
       }
     }
-  }
+  __syncthreads();
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    if (warp < n_warps) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < 2; ++e) {
+      // lane g looks at warp g; the rows' maximum, sum and this warp's weight
+      const int i = 8 * n + 2 * c + e;
+      const float m = g < C::W ? sm->m[g][i] : -INFINITY;
+      float top = m;
 #pragma unroll
-        for (int x = 0; x < C::G; ++x)
-          *reinterpret_cast<float4*>(&sm->part[warp][2 * c + e][32 * x + 4 * g]) =
-              make_float4(r.o[n][x][0][e] * kOutScale, r.o[n][x][0][2 + e] * (kOutScale / 16), r.o[n][x][1][e] * kOutScale,
-                          r.o[n][x][1][2 + e] * (kOutScale / 16));
+      for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      top = top == -INFINITY ? 0.f : top;
+      float l = g < C::W ? fast_exp2(m - top) * sm->l[g][i] : 0.f;             // 0 of a warp that has seen no key
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      const bool seen = l != 0.f;              // (a NaN is handed on)
+      const float f = seen ? fast_exp2(r.m[n][e] - top) / l * kOutScale : 0.f;
+      if (warp == 0 && g == 0) sm->lse[i] = seen ? (top + log2f(l)) * kLn2 : -INFINITY;
+#pragma unroll
+      for (int x = 0; x < C::G; ++x)
+        *reinterpret_cast<float4*>(&sm->part[warp][2 * c + e][32 * x + 4 * g]) =
+            make_float4(r.o[n][x][0][e] * f, r.o[n][x][0][2 + e] * (f * 0.0625f), r.o[n][x][1][e] * f,
+                        r.o[n][x][1][2 + e] * (f * 0.0625f));
     }
     __syncthreads();
     constexpr int F4 = HD / 4;
     for (int y = threadIdx.x; y < 8 * F4; y += 32 * C::W) {
       const int k = y / F4, col = 4 * (y % F4), i = 8 * n + k;
       if (i >= it.rows) break;                 // rows come in order
-      float top = -INFINITY;
-      for (int w = 0; w < n_warps; ++w) top = fmaxf(top, sm->m[w][i]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < n_warps; ++w) {
-        const float f = fast_exp2(sm->m[w][i] - ref);          // 0 for a warp that has seen no key
+      float4 o = *reinterpret_cast<const float4*>(&sm->part[0][k][col]);
+#pragma unroll
+      for (int w = 1; w < C::W; ++w) {
         const float4 u = *reinterpret_cast<const float4*>(&sm->part[w][k][col]);
-        l = fmaf(f, sm->l[w][i], l);
-        o.x = fmaf(f, u.x, o.x);
-        o.y = fmaf(f, u.y, o.y);
-        o.z = fmaf(f, u.z, o.z);
-        o.w = fmaf(f, u.w, o.w);
+        o.x += u.x;
+        o.y += u.y;
+        o.z += u.z;
+        o.w += u.w;
       }
-      const bool seen = l != 0.f;              // (a NaN is handed on)
-      const float inv = seen ? 1.f / l : 0.f;
-      const float lse = seen ? (ref + log2f(l)) * kLn2 : -INFINITY;
       if (it.slot >= 0) {
         const int64_t at = static_cast<int64_t>(it.slot) * C::RT + i;
-        *reinterpret_cast<float4*>(a.o_part + at * HD + col) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (col == 0) a.lse_part[at] = lse;
+        *reinterpret_cast<float4*>(a.o_part + at * HD + col) = o;
+        if (col == 0) a.lse_part[at] = sm->lse[i];
       } else {
-        const int row = it.rt * C::RT + i, tok = row / a.group, h = it.hk * a.group + row - tok * a.group;
+        const int row = it.rt * C::RT + i, tok = a.row_token(row), h = it.hk * a.group + row - tok * a.group;
         const int64_t q_row = a.segs[it.seg].q_row0 + static_cast<int64_t>(tok);
         *reinterpret_cast<uint2*>(a.o + (q_row * a.num_heads + h) * HD + col) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (col == 0) a.lse[h * a.lse_stride + q_row] = lse;
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        if (col == 0) a.lse[h * a.lse_stride + q_row] = sm->lse[i];
       }
     }
     __syncthreads();
@@ -836,8 +837,8 @@ paged_attn_q4_kernel(const __grid_constant__ AttnQ4Args<N> a) {
     // keys that every row sees
     int lo, hi, x;
     const int last = it.rt * C::RT + it.rows - 1;
-    keys_of(a, it.len, it.len - it.q_len + it.rt * C::RT / a.group, &x, &hi);
-    keys_of(a, it.len, it.len - it.q_len + last / a.group, &lo, &x);
+    keys_of(a, it.len, it.len - it.q_len + a.row_token(it.rt * C::RT), &x, &hi);
+    keys_of(a, it.len, it.len - it.q_len + a.row_token(last), &lo, &x);
 #pragma unroll 1
     for (int t = it.s0 + warp; t < it.s1; t += C::W) {
       copies_wait<C::kStages - 1>();
@@ -880,7 +881,7 @@ template <int HD>
 __device__ __forceinline__ void put_row(const AttnQ4Head& a, const Q4Join& j, int r, const float (&x)[HD / 32], float inv,
                                         float lse) {
   const int lane = threadIdx.x & 31;
-  const int row = j.row0 + r, tok = row / a.group, h = j.hk * a.group + row - tok * a.group;
+  const int row = j.row0 + r, tok = a.row_token(row), h = j.hk * a.group + row - tok * a.group;
   const int64_t q_row = j.q_row0 + static_cast<int64_t>(tok);
   __nv_bfloat16* dst = a.o + (q_row * a.num_heads + h) * HD + lane * (HD / 32);
   if constexpr (HD == 128)

@@ -425,6 +425,7 @@ zl_status launch_attn(const Attend& c, const zl_paged_cache_t& cache, const Chos
 // their queries, and handed to the bf16 attention, a batch at a time: as many as
 // kScratchBytes hold, or one.
 constexpr int64_t kQ4Rows = 64;
+static_assert(kQ4Rows < 512, "row_token");
 constexpr int64_t kScratchBytes = int64_t(1) << 30;
 
 struct Q4Plan {
@@ -533,6 +534,7 @@ zl_status launch_few_q4(const Attend& c, void* workspace) {
   a.num_heads = c.num_heads;
   a.num_kv_heads = cache.num_kv_heads;
   a.group = c.group();
+  a.group_inv = (65536 + a.group - 1) / a.group;
   a.table_cols = cache.table_cols;
   a.num_pages = cache.num_pages;
   a.page_shift = shift_of(cache.page_size);
