@@ -231,7 +231,9 @@ struct AttnQ4Head {
   int32_t window;
   float scale_log2;             // softmax scale * log2(e)
   int32_t n_segs;
-  int32_t whole;                // > 0: the launch's units; each has a CTA to itself, and no join follows
+  int32_t whole;                // > 0: the launch's units; each has `share` CTAs, a cluster, to itself, and no
+                                // join follows
+  int32_t share;                // else 1
 
 #ifdef __CUDACC__
   // The token of a sequence's row, row / group: exact for rows below 512 and groups

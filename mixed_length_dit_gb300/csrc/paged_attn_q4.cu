@@ -32,10 +32,10 @@
 // A unit is (sequence, key head, tile of 8 NT rows: queries times the heads that
 // share the key head).  The tiles of 32 keys of all units stand in one line that
 // is cut into equal pieces, one a CTA, as in the bf16 attention; the warps of a
-// CTA take a unit's tiles in turn, each with copies of its own in flight, and are
-// joined in shared memory; units that a cut goes through are joined by a second
-// launch.  The copies are 16 bytes a lane: bulk copies (TMA), four to a tile, took
-// their warp through a loop over the lanes that issue them.
+// CTA take a unit's tiles in turn and are joined in shared memory; units that a cut
+// goes through are joined by a second launch.  Few short units have a CTA each, or a
+// cluster, whose CTAs share the tiles and join them through distributed shared
+// memory.  One warp of a CTA copies the tiles of all others.
 #include <algorithm>
 #include <atomic>
 
@@ -61,11 +61,11 @@ template <int HD, int NT>
 struct Cfg {
   static constexpr int G = HD / kQ4Group;
   static constexpr int RT = 8 * NT;            // rows of a unit
-  static constexpr int W = NT == 1 ? 6 : 8;    // warps of a CTA
+  static constexpr int W = 7;                  // warps of a CTA that compute; one more copies
+  static constexpr int kThreads = 32 * (W + 1);
   static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = NT == 1 ? 2 : 3;
   static constexpr int kRegion = kTile * kQ4Row<HD>;           // keys, or values, of a stage
-  static constexpr int kSteps = kTile * kQ4Codes<HD>;          // its steps, behind the codes
   // -8 sum_j: by a product with a constant, the sums of a tile apart (of few rows,
   // whose products cost little), or by subtraction from the codes
   static constexpr bool kOffsetByProduct = NT == 1;
@@ -73,17 +73,10 @@ struct Cfg {
   static constexpr int kPad = HD + 4;          // floats of a row to be joined (rows 2c of four lanes in different banks)
 };
 
-template <int TO, int FROM>
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;"
-               :: "r"(dst), "l"(__cvta_generic_to_global(src)), "n"(TO), "n"(FROM) : "memory");
+__device__ __forceinline__ void bulk_load(uint32_t dst, const uint8_t* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ const uint8_t* in_page(const uint8_t* p, int page, int page_bytes) {
-  return p + static_cast<int64_t>(page) * page_bytes;
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 // d = a b + c.
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint2& b, const float (&c)[4]) {
@@ -127,13 +120,13 @@ __device__ __forceinline__ void load_floats(const float* p, float (&w)[G]) {
 
 // A token's steps from its bytes to floats.
 template <int G>
-__device__ __forceinline__ void spread_steps(float* to, const uint8_t* p) {
+__device__ __forceinline__ void spread_steps(float* to, const uint8_t* p, bool there = true) {
   if constexpr (G == 4) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    const uint32_t w = there ? *reinterpret_cast<const uint32_t*>(p) : 0u;
     const float2 a = q4_steps01(w), b = q4_steps23(w);
     *reinterpret_cast<float4*>(to) = make_float4(a.x, a.y, b.x, b.y);
   } else {
-    *reinterpret_cast<float2*>(to) = q4_steps01(*reinterpret_cast<const uint16_t*>(p));
+    *reinterpret_cast<float2*>(to) = q4_steps01(there ? *reinterpret_cast<const uint16_t*>(p) : 0u);
   }
 }
 
@@ -181,8 +174,8 @@ __device__ __forceinline__ int unit_weight(const AttnQ4Head& a, int len, int q_l
 
 // The weight of a segment's row tiles for one key head.
 template <int W, int RT>
-__device__ __forceinline__ int64_t seg_weight(const AttnQ4Head& a, int len, int q_len) {
-  int64_t sum = 0;
+__device__ __forceinline__ int seg_weight(const AttnQ4Head& a, int len, int q_len) {
+  int sum = 0;
   for (int rt = 0; rt < row_tiles<RT>(a, q_len); ++rt) sum += unit_weight<W, RT>(a, len, q_len, rt);
   return sum;
 }
@@ -192,71 +185,78 @@ __device__ __forceinline__ int64_t div_nonneg(int64_t a, int64_t b) {
   return a / b;
 }
 
-__device__ __forceinline__ int64_t warp_sum(int64_t x) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-  return x;
-}
-
-// The CTA's piece of the line, by warp 0 (all of it; the others wait).
+// The CTA's piece of the line, by all threads.  weights: room for every segment's.
 template <int W, int RT, int N>
-__device__ void find_piece(const AttnQ4Args<N>& a, Q4Piece* out) {
+__device__ void find_piece(const AttnQ4Args<N>& a, int32_t* weights, Q4Piece* out) {
   const int lane = threadIdx.x & 31;
-  const int c = blockIdx.x, nk = a.num_kv_heads;
+  const int nk = a.num_kv_heads;
   Q4Piece p = {0, 0, 0, 0, 0, 1};
-  if (a.whole > 0) {                           // few short units: each CTA has one to itself
-    int x = c;
-    for (;; ++p.seg) {
-      const int units = row_tiles<RT>(a, a.segs[p.seg].q_len) * nk;
-      if (x < units) break;
-      x -= units;
+  if (a.whole > 0) {                           // few short units: each CTA, or cluster, has one to itself
+    if (threadIdx.x < 32) {
+      int x = blockIdx.x / a.share;
+      for (;; ++p.seg) {
+        const int units = row_tiles<RT>(a, a.segs[p.seg].q_len) * nk;
+        if (x < units) break;
+        x -= units;
+      }
+      const int rts = row_tiles<RT>(a, a.segs[p.seg].q_len);
+      p.hk = x / rts;
+      p.rt = x - p.hk * rts;
+      p.left = 1;                              // any piece ends within its first unit
+      if (lane == 0) *out = p;
     }
-    const int rts = row_tiles<RT>(a, a.segs[p.seg].q_len);
-    p.hk = x / rts;
-    p.rt = x - p.hk * rts;
-    p.left = 1;                                // any piece ends within its first unit
-    if (lane == 0) *out = p;
+    __syncthreads();
     return;
   }
-  int64_t total = 0;
-  for (int s = lane; s < a.n_segs; s += 32) total += seg_weight<W, RT>(a, length_of(a, s), a.segs[s].q_len);
-  total = warp_sum(total) * nk;
-  p.per = max(int64_t(1 + kUnitCost), div_nonneg(total + gridDim.x - 1, gridDim.x));
-  const int64_t g = c * p.per;
-  p.left = max(int64_t(0), min(total - g, p.per));
-  if (p.left > 0) {
-    int64_t base = 0;
-    for (int chunk = 0;; chunk += 32) {
-      int64_t w = 0;
-      if (chunk + lane < a.n_segs) w = seg_weight<W, RT>(a, length_of(a, chunk + lane), a.segs[chunk + lane].q_len);
-      int64_t incl = w * nk;
+  for (int s = threadIdx.x; s < a.n_segs; s += blockDim.x)
+    weights[s] = seg_weight<W, RT>(a, length_of(a, s), a.segs[s].q_len);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int64_t total = 0;
+    for (int s = lane; s < a.n_segs; s += 32) total += weights[s];
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += y;
-      }
-      incl += base;
-      const uint32_t past = __ballot_sync(0xffffffffu, incl > g);
-      if (past != 0) {
-        const int k = __ffs(past) - 1;
-        const int64_t one = __shfl_sync(0xffffffffu, w, k);
-        int64_t off = g - (__shfl_sync(0xffffffffu, incl, k) - one * nk);
-        p.seg = chunk + k;
-        p.hk = static_cast<int>(div_nonneg(off, one));
-        off -= p.hk * one;
-        const int len = length_of(a, p.seg), q_len = a.segs[p.seg].q_len;
-        for (;; ++p.rt) {
-          const int weight = unit_weight<W, RT>(a, len, q_len, p.rt);
-          if (off < weight) break;
-          off -= weight;
+    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    total *= nk;
+    p.per = max(int64_t(1 + kUnitCost), div_nonneg(total + gridDim.x - 1, gridDim.x));
+    const int64_t g = blockIdx.x * p.per;
+    p.left = max(int64_t(0), min(total - g, p.per));
+    if (p.left > 0) {
+      int64_t base = 0;
+      for (int chunk = 0;; chunk += 32) {
+        const int64_t w = chunk + lane < a.n_segs ? weights[chunk + lane] : 0;
+        int64_t incl = w * nk;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += y;
         }
-        p.off = static_cast<int>(off);
-        break;
+        incl += base;
+        const uint32_t past = __ballot_sync(0xffffffffu, incl > g);
+        if (past != 0) {
+          const int k = __ffs(past) - 1;
+          const int64_t one = __shfl_sync(0xffffffffu, w, k);
+          int64_t off = g - (__shfl_sync(0xffffffffu, incl, k) - one * nk);
+          p.seg = chunk + k;
+          p.hk = static_cast<int>(div_nonneg(off, one));
+          off -= p.hk * one;
+          const int q_len = a.segs[p.seg].q_len;
+          if (row_tiles<RT>(a, q_len) > 1) {
+            const int len = length_of(a, p.seg);
+            for (;; ++p.rt) {
+              const int weight = unit_weight<W, RT>(a, len, q_len, p.rt);
+              if (off < weight) break;
+              off -= weight;
+            }
+          }
+          p.off = static_cast<int>(off);
+          break;
+        }
+        base = __shfl_sync(0xffffffffu, incl, 31);
       }
-      base = __shfl_sync(0xffffffffu, incl, 31);
     }
+    if (lane == 0) *out = p;
   }
-  if (lane == 0) *out = p;
+  __syncthreads();
 }
 
 // One item: the tiles [s0, s1) of a unit that the CTA has.
@@ -330,17 +330,6 @@ struct Walk {
   }
 };
 
-// A warp's place in the CTA's piece, and the item there.  It changes once in many
-// tiles, so it is kept in shared memory.
-struct Spot {
-  Walk walk;
-  Item item;
-  // of the copies: the head's block in page 0, keys' and values', and the
-  // sequence's row of the table
-  const uint8_t* kv[2];
-  const int32_t* entries;
-};
-
 template <int HD, int NT>
 struct Smem {
   using C = Cfg<HD, NT>;
@@ -352,135 +341,112 @@ struct Smem {
   uint4 q[NT][C::G][32];
   float4 q_sum[NT][C::G][4];
   float q_scale[C::RT];                        // a row's scores from its sums: scale and log2 e, its own scale
+  alignas(8) uint64_t full[C::W][C::kStages], empty[C::W][C::kStages];
   Q4Piece piece;
-  Spot spot[2][C::W];                        // of every warp's copies, and of its products
+  Walk walk[C::W];                             // of the warps that compute: it changes once in many tiles
+  Item item[C::W];
+  int abort_flag;
+  int32_t weights[kMaxSegs];
 };
 
-// The next item, by all lanes of the warp; false: none left.
+// The next item of a warp, by all its lanes; false: none left.
 template <int W, int RT, int N>
-__device__ __forceinline__ bool next_item(const AttnQ4Args<N>& a, Spot* at) {
-  Walk walk = at->walk;
+__device__ __forceinline__ bool next_item(const AttnQ4Args<N>& a, Walk* walk, Item* item) {
+  Walk w = *walk;
   Item it;
-  const bool ok = walk.next<W, RT>(a, &it);
+  const bool ok = w.next<W, RT>(a, &it);
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
-    at->walk = walk;
-    at->item = it;
+    *walk = w;
+    *item = it;
   }
   __syncwarp();
   return ok;
 }
 
 // ------------------------------------------------------------------ copies
-// Where 16 bytes (chunk) of a token's codes lie in a region: a value's chunks of
-// the rows that four neighbouring lanes read are in different banks.
+// Where the 16 keys of half a tile lie in a region: pages of 16 tokens are copied
+// with their steps behind their codes, larger pages' codes and steps apart.
+struct Layout {
+  int codes_half, steps, steps_half;
+};
+
 template <int HD>
-__device__ __forceinline__ int chunk_at(int row, int chunk, bool values) {
-  return row * kQ4Codes<HD> + 16 * (HD == 128 && values ? chunk ^ ((row >> 1) & 3) : chunk);
+__device__ __forceinline__ Layout layout_of(const AttnQ4Head& a) {
+  if (a.page_shift == 4) return {16 * kQ4Row<HD>, 16 * kQ4Codes<HD>, 16 * kQ4Row<HD>};
+  return {16 * kQ4Codes<HD>, kTile * kQ4Codes<HD>, 16 * kQ4Steps<HD>};
 }
 
-// A warp's tiles, one after another: a copy is set off as soon as a stage is free,
-// with the page numbers that were fetched when the one before was.
+// The first tile of an item for the CTA's first warp; the others' follow, and a
+// warp's next one is W tiles on, or, of a unit that a cluster of `share` CTAs has, W
+// tiles times that.
+template <int W>
+__device__ __forceinline__ int first_tile(const AttnQ4Head& a, const Item& it) {
+  return it.s0 + (a.share > 1 ? static_cast<int>(blockIdx.x) % a.share * W : 0);
+}
+
+// The warp that copies (TMA bulk): a tile for each warp of the CTA at a time, by four
+// lanes a tile.  They bring keys' codes and steps and values' codes and steps, or of
+// pages of 16 each one's two pages, or of pages of 32 each one's page.
 template <int HD, int NT, int N>
-struct Loader {
+__device__ void produce(const AttnQ4Args<N>& a, Smem<HD, NT>* sm, const Q4Piece& piece) {
   using C = Cfg<HD, NT>;
-  static constexpr int kLanes = kQ4Codes<HD> / 16;             // that copy a token's codes
-  static constexpr int kRows = 32 / kLanes;                    // tokens of a warp's copy
-  static constexpr int kStepLanes = kTile * kQ4Steps<HD> / 16; // that copy a tile's steps
-  Spot* at;
-  int tile, end;                               // of the item; tile >= end: none left
-  int page[2];                                 // of its first and its second 16 tokens
-  uint32_t stage = 0;
-
-  __device__ __forceinline__ void fetch(const AttnQ4Args<N>& a) {
-    const int32_t* e = at->entries + ((tile * kTile) >> a.page_shift);
-    page[0] = __ldg(e);
-    page[1] = a.page_shift > 4 ? page[0] : tile * kTile + 16 < at->item.len ? __ldg(e + 1) : 0;
-  }
-
-  // The next item with a tile for this warp.
-  __device__ __forceinline__ void settle(const AttnQ4Args<N>& a) {
-    do {
-      if (!next_item<C::W, C::RT>(a, at)) return;
-      tile = at->item.s0 + (threadIdx.x >> 5);
-      end = at->item.s1;
-    } while (tile >= end);
-    if ((threadIdx.x & 31) == 0) {
-      const int64_t block = (static_cast<int64_t>(at->item.hk) * kQ4Row<HD>) << a.page_shift;
-      at->kv[0] = a.k_pages + block;
-      at->kv[1] = a.v_pages + block;
-      at->entries = a.page_table + static_cast<int64_t>(a.segs[at->item.seg].seq) * a.table_cols;
-    }
-    __syncwarp();
-    fetch(a);
-  }
-
-  __device__ __forceinline__ void start(const AttnQ4Args<N>& a, Spot* spot) {
-    at = spot;
-    tile = end = 0;
-    settle(a);
-  }
-
-  // One tile's copies, and the next one's page numbers.
-  __device__ __forceinline__ void issue(const AttnQ4Args<N>& a, Smem<HD, NT>* sm) {
-    if (tile < end) {
-      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-      const bool both = a.page_shift > 4 || tile * kTile + 16 < at->item.len;  // else the second page is not there
-      if (static_cast<uint32_t>(page[0]) >= static_cast<uint32_t>(a.num_pages) ||
-          static_cast<uint32_t>(page[1]) >= static_cast<uint32_t>(a.num_pages)) {
-        atomicOr(&g_attn_q4_err, ERR_BAD_PAGE);                // reads page 0 in its place
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (static_cast<uint32_t>(page[i]) >= static_cast<uint32_t>(a.num_pages)) page[i] = 0;
-      }
-      const uint32_t to = smem_u32(sm->stage[warp][stage][0]);
-      const uint32_t to_k = to + 16 * lane, to_v = to + C::kRegion + chunk_at<HD>(lane / kLanes, lane % kLanes, true);
-      constexpr int kHalf = 16 * kQ4Codes<HD>;
-      const int row = (tile * kTile) & ((1 << a.page_shift) - 1);
-      const uint8_t* k = at->kv[0] + (row * kQ4Codes<HD> + 16 * lane);
-      const uint8_t* v = at->kv[1] + (row * kQ4Codes<HD> + 16 * lane);
-      const uint8_t* k0 = in_page(k, page[0], a.page_bytes);
-      const uint8_t* v0 = in_page(v, page[0], a.page_bytes);
-      copy16<0, 0>(to_k, k0);
-      copy16<0, 0>(to_v, v0);
-      if constexpr (kRows < 16) {
-        copy16<512, 512>(to_k, k0);
-        copy16<512, 512>(to_v, v0);
-      }
-      if (a.page_shift > 4) {
-        copy16<kHalf, kHalf>(to_k, k0);
-        copy16<kHalf, kHalf>(to_v, v0);
-        if constexpr (kRows < 16) {
-          copy16<kHalf + 512, kHalf + 512>(to_k, k0);
-          copy16<kHalf + 512, kHalf + 512>(to_v, v0);
+  const int lane = threadIdx.x & 31, w = lane >> 2, part = lane & 1;
+  const int ps = 1 << a.page_shift;
+  const bool small = a.page_shift == 4, values = lane & 2;
+  uint32_t stage = 0, parity = 1;              // of warp w's stages
+  Walk walk;
+  walk.start(a, piece);
+  Item it;
+  while (walk.next<C::W, C::RT>(a, &it)) {
+    const uint8_t* block = (values ? a.v_pages : a.k_pages) + ((static_cast<int64_t>(it.hk) * kQ4Row<HD>) << a.page_shift);
+    const int32_t* entries = a.page_table + static_cast<int64_t>(a.segs[it.seg].seq) * a.table_cols;
+    int tile = first_tile<C::W>(a, it) + w;
+    const auto fetch = [&]() {                 // the page of the lane's copy
+      const int pos = tile * kTile + (small ? 16 * part : 0);
+      return w < C::W && tile < it.s1 && pos < it.len ? __ldg(entries + (pos >> a.page_shift)) : 0;
+    };
+    int page = fetch();
+    while (true) {
+      const bool mine = w < C::W && tile < it.s1;
+      if (!__any_sync(0xffffffffu, mine)) break;
+      const int pos = tile * kTile, row = pos & (ps - 1);
+      const bool both = !small || pos + 16 < it.len;             // else the second page is not there
+      uint32_t bytes = 0, from = 0, to = 0;
+      if (mine) {
+        if (small) {
+          bytes = part == 0 || both ? 16 * kQ4Row<HD> : 0;
+          to = part * 16 * kQ4Row<HD>;
+        } else if (ps == kTile) {
+          bytes = part ? 0 : C::kRegion;
+        } else {
+          bytes = part ? kTile * kQ4Steps<HD> : kTile * kQ4Codes<HD>;
+          from = part ? ps * kQ4Codes<HD> + row * kQ4Steps<HD> : row * kQ4Codes<HD>;
+          to = part ? kTile * kQ4Codes<HD> : 0;
         }
-      } else if (both) {                       // the second 16 tokens are in a page of their own
-        const uint8_t* k1 = in_page(k, page[1], a.page_bytes);
-        const uint8_t* v1 = in_page(v, page[1], a.page_bytes);
-        copy16<kHalf, 0>(to_k, k1);
-        copy16<kHalf, 0>(to_v, v1);
-        if constexpr (kRows < 16) {
-          copy16<kHalf + 512, 512>(to_k, k1);
-          copy16<kHalf + 512, 512>(to_v, v1);
+        if (bytes > 0 && static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) {
+          atomicOr(&g_attn_q4_err, ERR_BAD_PAGE);                // reads page 0 in its place
+          page = 0;
         }
       }
-      if (lane < 2 * kStepLanes) {
-        const int values = lane / kStepLanes, of = lane % kStepLanes;
-        const bool second = a.page_shift == 4 && of >= kStepLanes / 2;
-        if (both || !second)
-          copy16<C::kSteps, 0>(to + values * C::kRegion + 16 * of,
-                               in_page(at->kv[values] + ((kQ4Codes<HD> << a.page_shift) + row * kQ4Steps<HD> +
-                                                         16 * (second ? of - kStepLanes / 2 : of)),
-                                       second ? page[1] : page[0], a.page_bytes));
+      const uint8_t* src = block + static_cast<int64_t>(page) * a.page_bytes + from;
+      tile += C::W * a.share;
+      page = fetch();
+      // (after a wait that ran out nothing is read any more)
+      const bool ok = !mine || mbar_wait(&sm->empty[w][stage], parity, &sm->abort_flag, &g_attn_q4_err, ERR_TIMEOUT_PRODUCER);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      uint64_t* bar = &sm->full[mine ? w : 0][stage];
+      if (mine && (lane & 3) == 0) mbar_arrive_expect_tx(bar, both ? 2 * C::kRegion : C::kRegion);
+      __syncwarp();
+      if (bytes > 0) bulk_load(smem_u32(sm->stage[w][stage][values]) + to, src, bytes, bar);
+      if (mine && ++stage == C::kStages) {
+        stage = 0;
+        parity ^= 1u;
       }
-      tile += C::W;
-      if (tile < end) fetch(a);
-      else settle(a);
+      __syncwarp();
     }
-    copies_commit();
-    if (++stage == C::kStages) stage = 0;
   }
-};
+}
 
 // ------------------------------------------------------------------ products
 // A warp's share of a unit: lane (g, c) = (lane / 4, lane % 4) of the products'
@@ -534,7 +500,7 @@ struct Rows {
       const float s0 = __shfl_sync(0xffffffffu, sum, 8 * c), s1 = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
       if (g == 0) sm->q_sum[n][x][c] = make_float4(s0, s1, s0, s1);
     }
-    __syncthreads();
+    named_bar_sync(1, 32 * C::W);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -552,25 +518,28 @@ struct Rows {
     }
   }
 
-  // A tile of 32 keys from position `pos` on.  EDGE: some row does not see all of
+  // A tile of 32 keys from position `pos` on.  edge: some row does not see all of
   // them.  `steps`: room for 64 tokens' steps.
-  template <bool EDGE>
   __device__ __forceinline__ void tile(const AttnQ4Head& a, const Item& it, const Smem<HD, NT>* sm, const uint8_t* kr,
-                                       const uint8_t* vr, float* steps, int pos) {
+                                       const uint8_t* vr, const Layout& lay, float* steps, int pos, bool edge) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    spread_steps<G>(steps + lane * G, kr + C::kSteps + lane * G);
-    spread_steps<G>(steps + (kTile + lane) * G, vr + C::kSteps + lane * G);
+    // the key of rows g, and 8 on: four lanes' values of a column are in different banks
+    const int key_g = g ^ ((g >> 1) & 1);
+    const int held = lay.steps + (lane >> 4) * lay.steps_half + (lane & 15) * G;
+    spread_steps<G>(steps + lane * G, kr + held);
+    // (past the sequence anything may be held)
+    spread_steps<G>(steps + (kTile + lane) * G, vr + held, pos + lane < it.len);
     __syncwarp();
     float s[2][NT][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {              // 16 keys
       uint32_t wa[G], wb[G];
       float sa[G], sb[G];
-      const uint8_t* codes = kr + (16 * h + g) * kQ4Codes<HD> + c * (4 * G);
+      const uint8_t* codes = kr + h * lay.codes_half + key_g * kQ4Codes<HD> + c * (4 * G);
       load_words<G>(codes, wa);
       load_words<G>(codes + 8 * kQ4Codes<HD>, wb);
-      load_floats<G>(steps + (16 * h + g) * G, sa);
-      load_floats<G>(steps + (16 * h + 8 + g) * G, sb);
+      load_floats<G>(steps + (16 * h + key_g) * G, sa);
+      load_floats<G>(steps + (16 * h + 8 + key_g) * G, sb);
 #pragma unroll
       for (int x = 0; x < G; ++x) {
         const uint32_t w0[4] = {wa[x] & kLow, wb[x] & kLow, wa[x] & kHigh, wb[x] & kHigh};
@@ -594,12 +563,11 @@ struct Rows {
         }
       }
     }
-    bool raise = false;
+    if (edge) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if constexpr (EDGE) {
+        for (int e = 0; e < 2; ++e) {
           const int tok = a.row_token(min(it.rt * C::RT + 8 * n + 2 * c + e, it.rt * C::RT + it.rows - 1));
           int lo, hi;
           keys_of(a, it.len, it.len - it.q_len + tok, &lo, &hi);
@@ -607,15 +575,20 @@ struct Rows {
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const int key = pos + 16 * h + 8 * k + g;
+              const int key = pos + 16 * h + 8 * k + key_g;
               if (key < lo || key >= hi) s[h][n][2 * k + e] = -INFINITY;
             }
         }
+    }
+    bool raise = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
         // (a mask's -inf stays -inf: f is above zero, NaN, or 0 for a row of zeros)
         const float top = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
         raise = raise || top * f[n][e] > m[n][e] + kRescale;
       }
-    }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -656,20 +629,19 @@ struct Rows {
     float2 st[2][2];
 #pragma unroll
     for (int x = 0; x < G; ++x) {
-      // the codes of keys 2c, 2c + 1 and 2c + 8, 2c + 9 of each 16, and the steps of
-      // keys g, g + 8, for two groups: four columns of a group are half a word
+      // the codes of the keys of rows 2c, 2c + 1 and 2c + 8, 2c + 9 of each 16, and the steps
+      // of those of rows g, g + 8, for two groups: four columns of a group are half a word
       if ((x & 1) == 0) {
         asm volatile("" ::: "memory");         // not loaded further ahead: registers
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int row = 16 * h + 2 * c + (k & 1) + 8 * (k >> 1);
-            w[h][k] = *reinterpret_cast<const uint32_t*>(vr + (G == 4 ? chunk_at<HD>(row, g >> 1, true) + 8 * (g & 1) + 2 * x
-                                                                      : row * kQ4Codes<HD> + 4 * g));
+            const int row = ((2 * c + (k & 1)) ^ (c & 1)) + 8 * (k >> 1);
+            w[h][k] = *reinterpret_cast<const uint32_t*>(vr + h * lay.codes_half + row * kQ4Codes<HD> + 2 * G * g + 2 * x);
           }
-          st[h][0] = *reinterpret_cast<const float2*>(steps + (kTile + 16 * h + g) * G + x);
-          st[h][1] = *reinterpret_cast<const float2*>(steps + (kTile + 16 * h + 8 + g) * G + x);
+          st[h][0] = *reinterpret_cast<const float2*>(steps + (kTile + 16 * h + key_g) * G + x);
+          st[h][1] = *reinterpret_cast<const float2*>(steps + (kTile + 16 * h + 8 + key_g) * G + x);
         }
       }
       uint2 b[2][NT];
@@ -682,11 +654,6 @@ struct Rows {
           for (int k = 0; k < 2; ++k) {
             const float step = x & 1 ? st[h][k].y : st[h][k].x;
             f2_unpack(f2_mul(f2_pack(s[h][n][2 * k], s[h][n][2 * k + 1]), f2_pack(step, step)), t[2 * k], t[2 * k + 1]);
-          }
-          if constexpr (EDGE) {                // a key that is not seen may have any step
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (s[h][n][i] == 0.f) t[i] = 0.f;
           }
           b[h][n] = make_uint2(transpose8(pack_bf16x2(t[0], t[1])), transpose8(pack_bf16x2(t[2], t[3])));
         }
@@ -734,6 +701,44 @@ struct Rows {
   }
 };
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// What the cluster's CTA `rank` has at p of its shared memory.
+__device__ __forceinline__ uint32_t in_cluster(const void* p, int rank) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(in_cluster(p, rank)) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 ld_cluster4(const float* p, int rank) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(in_cluster(p, rank)) : "memory");
+  return x;
+}
+
+__device__ __forceinline__ void add4(float4& o, float f, const float4& u) {
+  o.x = fmaf(f, u.x, o.x);
+  o.y = fmaf(f, u.y, o.y);
+  o.z = fmaf(f, u.z, o.z);
+  o.w = fmaf(f, u.w, o.w);
+}
+
+// Four columns of a row of the item's sequence.
+template <int HD, int N>
+__device__ __forceinline__ void put_row(const AttnQ4Args<N>& a, const Item& it, int row, int col, const float4& o, float lse) {
+  const int tok = a.row_token(row), h = it.hk * a.group + row - tok * a.group;
+  const int64_t q_row = a.segs[it.seg].q_row0 + static_cast<int64_t>(tok);
+  *reinterpret_cast<uint2*>(a.o + (q_row * a.num_heads + h) * HD + col) =
+      make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  if (col == 0) a.lse[h * a.lse_stride + q_row] = lse;
+}
+
 // Joins the warps' shares of an item and writes its rows: every warp weights its
 // sums by what it has of a row, and threads add them up, 8 rows at a time.
 template <int HD, int NT, int N>
@@ -752,7 +757,7 @@ __device__ __forceinline__ void finish(const AttnQ4Args<N>& a, const Item& it, S
         sm->l[warp][8 * n + 2 * c + e] = l * 0x1p-60f;
       }
     }
-  __syncthreads();
+  named_bar_sync(1, 32 * C::W);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -776,87 +781,118 @@ __device__ __forceinline__ void finish(const AttnQ4Args<N>& a, const Item& it, S
             make_float4(r.o[n][x][0][e] * f, r.o[n][x][0][2 + e] * (f * 0.0625f), r.o[n][x][1][e] * f,
                         r.o[n][x][1][2 + e] * (f * 0.0625f));
     }
-    __syncthreads();
+    named_bar_sync(1, 32 * C::W);
     constexpr int F4 = HD / 4;
     for (int y = threadIdx.x; y < 8 * F4; y += 32 * C::W) {
       const int k = y / F4, col = 4 * (y % F4), i = 8 * n + k;
       if (i >= it.rows) break;                 // rows come in order
       float4 o = *reinterpret_cast<const float4*>(&sm->part[0][k][col]);
 #pragma unroll
-      for (int w = 1; w < C::W; ++w) {
-        const float4 u = *reinterpret_cast<const float4*>(&sm->part[w][k][col]);
-        o.x += u.x;
-        o.y += u.y;
-        o.z += u.z;
-        o.w += u.w;
-      }
-      if (it.slot >= 0) {
+      for (int w = 1; w < C::W; ++w) add4(o, 1.f, *reinterpret_cast<const float4*>(&sm->part[w][k][col]));
+      if (a.share > 1) {                       // the cluster's CTAs join theirs below
+        *reinterpret_cast<float4*>(&sm->part[0][k][col]) = o;
+      } else if (it.slot >= 0) {
         const int64_t at = static_cast<int64_t>(it.slot) * C::RT + i;
         *reinterpret_cast<float4*>(a.o_part + at * HD + col) = o;
         if (col == 0) a.lse_part[at] = sm->lse[i];
       } else {
-        const int row = it.rt * C::RT + i, tok = a.row_token(row), h = it.hk * a.group + row - tok * a.group;
-        const int64_t q_row = a.segs[it.seg].q_row0 + static_cast<int64_t>(tok);
-        *reinterpret_cast<uint2*>(a.o + (q_row * a.num_heads + h) * HD + col) =
-            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-        if (col == 0) a.lse[h * a.lse_stride + q_row] = sm->lse[i];
+        put_row<HD>(a, it, it.rt * C::RT + i, col, o, sm->lse[i]);
       }
     }
-    __syncthreads();
+    if (a.share > 1) {
+      cluster_sync();
+      const int rank = blockIdx.x % a.share;
+      for (int y = threadIdx.x + 32 * C::W * rank; y < 8 * F4; y += 32 * C::W * a.share) {
+        const int k = y / F4, col = 4 * (y % F4), i = 8 * n + k;
+        if (i >= it.rows) break;
+        float top = -INFINITY;
+        for (int r2 = 0; r2 < a.share; ++r2) top = fmaxf(top, ld_cluster(&sm->lse[i], r2));
+        top = top == -INFINITY ? 0.f : top;
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r2 = 0; r2 < a.share; ++r2) {
+          const float lse = ld_cluster(&sm->lse[i], r2);
+          if (lse == -INFINITY) continue;      // a CTA that has seen no key
+          const float f = expf(lse - top);
+          l += f;
+          add4(o, f, ld_cluster4(&sm->part[0][k][col], r2));
+        }
+        const bool seen = l != 0.f;
+        const float inv = seen ? 1.f / l : 0.f;
+        put_row<HD>(a, it, it.rt * C::RT + i, col, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv),
+                    seen ? top + logf(l) : -INFINITY);
+      }
+      cluster_sync();                          // the others have read
+    }
+    named_bar_sync(1, 32 * C::W);
   }
 }
 
 template <int HD, int NT, int N>
-__global__ void __launch_bounds__(32 * Cfg<HD, NT>::W, Cfg<HD, NT>::kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, Cfg<HD, NT>::kCtasPerSm)
 paged_attn_q4_kernel(const __grid_constant__ AttnQ4Args<N> a) {
   using C = Cfg<HD, NT>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   auto* sm = reinterpret_cast<Smem<HD, NT>*>(smem_raw);
-  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (a.whole == 0 && threadIdx.x == 0) a.joins[blockIdx.x].last = -1;
-  if (warp == 0) find_piece<C::W, C::RT, N>(a, &sm->piece);
+  if (warp < C::W && lane < C::kStages) {
+    mbar_init(&sm->full[warp][lane], 1);
+    mbar_init(&sm->empty[warp][lane], 1);
+  }
+  if (threadIdx.x == 0) sm->abort_flag = 0;
+  fence_mbar_init();
+  find_piece<C::W, C::RT, N>(a, sm->weights, &sm->piece);
   // the join may be set up from here on; it waits for this grid's end itself
   if (a.whole == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __syncthreads();
   const Q4Piece piece = sm->piece;
 
-  if ((threadIdx.x & 31) == 0)
-    for (int i = 0; i < 2; ++i) sm->spot[i][warp].walk.start(a, piece);
-  __syncwarp();
-
-  Loader<HD, NT, N> load;
-  load.start(a, &sm->spot[0][warp]);
+  if (warp == C::W) {
+    produce<HD, NT, N>(a, sm, piece);
+    if (a.share > 1)                           // as often as the other warps, below
+      for (int i = 0; i < 2 * NT; ++i) cluster_sync();
+  } else {
+    Walk* walk = &sm->walk[warp];
+    if (lane == 0) walk->start(a, piece);
+    __syncwarp();
+    Rows<HD, NT> rows;
+    const Item& it = sm->item[warp];
+    const Layout lay = layout_of<HD>(a);
+    uint32_t stage = 0, parity = 0;
+    float* steps = &sm->part[warp][0][0];      // free until the unit's end
+    while (next_item<C::W, C::RT>(a, walk, &sm->item[warp])) {
+      rows.start(a, it, sm);
+      // keys that every row sees
+      int lo, hi, x;
+      const int last = it.rt * C::RT + it.rows - 1;
+      keys_of(a, it.len, it.len - it.q_len + a.row_token(it.rt * C::RT), &x, &hi);
+      keys_of(a, it.len, it.len - it.q_len + a.row_token(last), &lo, &x);
 #pragma unroll 1
-  for (int s = 0; s < C::kStages; ++s) load.issue(a, sm);
-
-  Rows<HD, NT> rows;
-  uint32_t stage = 0;
-  const Item& it = sm->spot[1][warp].item;
-  while (next_item<C::W, C::RT>(a, &sm->spot[1][warp])) {
-    rows.start(a, it, sm);
-    // keys that every row sees
-    int lo, hi, x;
-    const int last = it.rt * C::RT + it.rows - 1;
-    keys_of(a, it.len, it.len - it.q_len + a.row_token(it.rt * C::RT), &x, &hi);
-    keys_of(a, it.len, it.len - it.q_len + a.row_token(last), &lo, &x);
-#pragma unroll 1
-    for (int t = it.s0 + warp; t < it.s1; t += C::W) {
-      copies_wait<C::kStages - 1>();
-      __syncwarp();
-      const uint8_t* kr = sm->stage[warp][stage][0];
-      const uint8_t* vr = sm->stage[warp][stage][1];
-      float* steps = &sm->part[warp][0][0];    // free until the unit's end
-      const int pos = t * kTile;
-      if (pos >= lo && pos + kTile <= hi) rows.template tile<false>(a, it, sm, kr, vr, steps, pos);
-      else rows.template tile<true>(a, it, sm, kr, vr, steps, pos);
-      __syncwarp();                            // the stage has been read
-      load.issue(a, sm);
-      if (++stage == C::kStages) stage = 0;
+      for (int t = first_tile<C::W>(a, it) + warp; t < it.s1; t += C::W * a.share) {
+        // (a wait that runs out is recorded, and the rows' values are wrong)
+        mbar_wait(&sm->full[warp][stage], parity, &sm->abort_flag, &g_attn_q4_err, ERR_TIMEOUT_OTHER);
+        __syncwarp();
+        const int pos = t * kTile;
+        rows.tile(a, it, sm, sm->stage[warp][stage][0], sm->stage[warp][stage][1], lay, steps, pos,
+                  pos < lo || pos + kTile > hi);
+        __syncwarp();                          // the stage has been read
+        if (lane == 0) mbar_arrive(&sm->empty[warp][stage]);
+        if (++stage == C::kStages) {
+          stage = 0;
+          parity ^= 1u;
+        }
+      }
+      finish<HD, NT, N>(a, it, sm, rows);
+      if (it.behind > 0 && threadIdx.x == 0)   // the CTAs behind have a whole piece each
+        a.joins[blockIdx.x] = {a.segs[it.seg].q_row0, it.rt * C::RT, it.rows, it.hk,
+                               static_cast<int32_t>(blockIdx.x + div_nonneg(it.behind + piece.per - 1, piece.per))};
     }
-    finish<HD, NT, N>(a, it, sm, rows);
-    if (it.behind > 0 && threadIdx.x == 0)     // the CTAs behind have a whole piece each
-      a.joins[blockIdx.x] = {a.segs[it.seg].q_row0, it.rt * C::RT, it.rows, it.hk,
-                             static_cast<int32_t>(blockIdx.x + div_nonneg(it.behind + piece.per - 1, piece.per))};
+  }
+  __syncthreads();
+  if (*reinterpret_cast<volatile int*>(&sm->abort_flag)) {       // copies may still be on their way
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 2000000ull) {
+    }
   }
 }
 
@@ -878,7 +914,7 @@ struct Acc {
 };
 
 template <int HD>
-__device__ __forceinline__ void put_row(const AttnQ4Head& a, const Q4Join& j, int r, const float (&x)[HD / 32], float inv,
+__device__ __forceinline__ void put_joined(const AttnQ4Head& a, const Q4Join& j, int r, const float (&x)[HD / 32], float inv,
                                         float lse) {
   const int lane = threadIdx.x & 31;
   const int row = j.row0 + r, tok = a.row_token(row), h = j.hk * a.group + row - tok * a.group;
@@ -963,7 +999,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_q4_kernel(const __grid_cons
       }
     }
     const bool seen = sum != 0.f;              // (a NaN is handed on)
-    put_row<HD>(a, j, r, acc.x, seen ? 1.f / sum : 0.f, seen ? (m == -INFINITY ? 0.f : m) + logf(sum) : -INFINITY);
+    put_joined<HD>(a, j, r, acc.x, seen ? 1.f / sum : 0.f, seen ? (m == -INFINITY ? 0.f : m) + logf(sum) : -INFINITY);
   }
 }
 
@@ -992,8 +1028,18 @@ cudaError_t launch_kind(const AttnQ4Args<N>& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     word.fetch_or(uint64_t(1) << (dev & 63));
   }
-  paged_attn_q4_kernel<HD, NT, N><<<a.whole > 0 ? a.whole : attn_q4_ctas(NT), 32 * C::W, smem, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.whole > 0 ? a.whole * a.share : attn_q4_ctas(NT));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = a.share;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = a.share > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_attn_q4_kernel<HD, NT, N>, a);
 }
 
 template <int HD, int NT>

@@ -471,14 +471,22 @@ size_t few_workspace(int32_t nt, int32_t hd) {
   return up256(ctas * sizeof(zl::Q4Join)) + 2 * ctas * 8 * nt * (hd + 1) * sizeof(float);
 }
 
-// The launch's units if each is left whole, one CTA to a unit (no sums over the
-// lengths, no join); 0 if they are cut into equal shares.
-int32_t whole_q4(const zl::AttnQ4Head& a, const Few& f, int ctas) {
-  const int64_t units = f.row_tiles * a.num_kv_heads;
-  if (units > ctas) return 0;
-  int64_t keys = a.max_kv_len;
-  if (a.window > 0 && a.causal) keys = std::min(keys, int64_t(a.window) + 64);
-  return keys <= 1024 ? static_cast<int32_t>(units) : 0;
+// Whether the launch's units are left whole: each has a CTA, or a cluster of up to 8,
+// to itself (no sums over the lengths, no join).  Sets whole (0: they are cut into
+// equal shares) and share.
+void whole_q4(zl::AttnQ4Head* a, const Few& f, int ctas) {
+  a->whole = 0;
+  a->share = 1;
+  const int64_t units = f.row_tiles * a->num_kv_heads;
+  if (units > ctas) return;
+  int64_t keys = a->max_kv_len;
+  if (a->window > 0 && a->causal) keys = std::min(keys, int64_t(a->window) + 64);
+  const int64_t wave = 224;                        // keys that a CTA's warps have at a time
+  int32_t share = 1;
+  while (share < 8 && units * share * 2 <= ctas && share * wave < keys) share *= 2;
+  if (keys > share * wave * 6) return;
+  a->whole = static_cast<int32_t>(units);
+  a->share = share;
 }
 
 zl_status plan_q4(const int32_t* cu, int32_t num_seqs, int32_t max_kv_len, int32_t nh, int32_t nk, int32_t hd,
@@ -555,7 +563,7 @@ zl_status launch_few_q4(const Attend& c, void* workspace) {
     a.joins = static_cast<zl::Q4Join*>(workspace);
     a.o_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up256(ctas * sizeof(zl::Q4Join)));
     a.lse_part = a.o_part + int64_t(2) * ctas * 8 * f.nt * cache.head_dim;
-    a.whole = whole_q4(a, f, ctas);
+    whole_q4(&a, f, ctas);
     zl_status st = launch_counted("paged_attn_q4", c.stream,
                                   [&] { return zl::launch_attn_q4(cache.head_dim, f.nt, a, c.stream); });
     if (st == ZL_OK && a.whole == 0)
