@@ -288,8 +288,8 @@ cudaError_t launch_paged_join(int head_dim, bool pair, const PagedAttnHead& args
 cudaError_t launch_append_q4(const RopeArgs<kMaxSegs>& args, int num_sms, cudaStream_t stream);
 cudaError_t launch_read_q4(const ReadQ4Args<kMaxSegs>& args, int num_sms, cudaStream_t stream);
 cudaError_t launch_unpack_q4(int head_dim, const UnpackQ4Args<kMaxSegs>& args, cudaStream_t stream);
-// nt: tiles of 8 rows in a unit, 1, 2 or 4; attn_q4_ctas: CTAs of such a launch.
-int attn_q4_ctas(int nt);
+// nt: tiles of 8 rows in a unit, 1 or 2; attn_q4_ctas: CTAs of such a launch.
+int attn_q4_ctas();
 cudaError_t launch_attn_q4(int head_dim, int nt, const AttnQ4Args<kMaxSegs>& args, cudaStream_t stream);
 // Joins the cut units of a launch_attn_q4 with the same arguments.
 cudaError_t launch_join_q4(int head_dim, int nt, const AttnQ4Head& args, cudaStream_t stream);

@@ -7,7 +7,7 @@
 // n = c + 8 are not made into values: the products run over n itself,
 //
 //     S = scale sum_g s_k[g] (sum_(i in g) q_i n_i - 8 sum_(i in g) q_i)
-//     o_i = sum_j (p_j s_v[j, g]) n_ji - 8 sum_j (p_j s_v[j, g])
+//     o_i = sum_j (p_j s_v[j, g]) (n_ji - 8)
 //
 // so that a key's steps multiply four sums instead of 128 codes, and a value's
 // steps the probability before it is rounded to bf16 (the one rounding, as in the
@@ -61,14 +61,11 @@ template <int HD, int NT>
 struct Cfg {
   static constexpr int G = HD / kQ4Group;
   static constexpr int RT = 8 * NT;            // rows of a unit
-  static constexpr int W = 7;                  // warps of a CTA that compute; one more copies
+  static constexpr int W = NT == 1 ? 7 : 5;    // warps of a CTA that compute; one more copies
   static constexpr int kThreads = 32 * (W + 1);
-  static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
+  static constexpr int kCtasPerSm = 2;
   static constexpr int kStages = NT == 1 ? 2 : 3;
   static constexpr int kRegion = kTile * kQ4Row<HD>;           // keys, or values, of a stage
-  // -8 sum_j: by a product with a constant, the sums of a tile apart (of few rows,
-  // whose products cost little), or by subtraction from the codes
-  static constexpr bool kOffsetByProduct = NT == 1;
   static_assert(W <= 8, "a warp's lanes look at 8 warps");
   static constexpr int kPad = HD + 4;          // floats of a row to be joined (rows 2c of four lanes in different banks)
 };
@@ -657,13 +654,6 @@ struct Rows {
           }
           b[h][n] = make_uint2(transpose8(pack_bf16x2(t[0], t[1])), transpose8(pack_bf16x2(t[2], t[3])));
         }
-      float base[4];
-      if constexpr (C::kOffsetByProduct) {
-        const uint32_t minus[4] = {kMinus8, kMinus128, kMinus8, kMinus128};
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        mma(base, minus, b[0][0], zero);
-        mma(base, minus, b[1][0], base);
-      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int byte = 2 * (x & 1) + t;      // of each word: the codes of rows g and (16 times) g + 8 of the tile
@@ -673,28 +663,13 @@ struct Rows {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t u = __byte_perm(w[h][2 * k], w[h][2 * k + 1], byte | (4 + byte) << 8);
-            v[h][2 * k] = u & kLow;
-            v[h][2 * k + 1] = u & kHigh;
-            if constexpr (!C::kOffsetByProduct) {
-              v[h][2 * k] = add_bf16x2(v[h][2 * k], kMinus8);
-              v[h][2 * k + 1] = add_bf16x2(v[h][2 * k + 1], kMinus128);
-            }
+            v[h][2 * k] = add_bf16x2(u & kLow, kMinus8);
+            v[h][2 * k + 1] = add_bf16x2(u & kHigh, kMinus128);
           }
-        if constexpr (C::kOffsetByProduct) {
-          float d[4];
-          mma(d, v[0], b[0][0], base);
-          mma(d, v[1], b[1][0], d);
 #pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            float* to = &o[0][x][t][i];
-            f2_unpack(f2_add(f2_pack(to[0], to[1]), f2_pack(d[i], d[i + 1])), to[0], to[1]);
-          }
-        } else {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma(o[n][x][t], v[0], b[0][n], o[n][x][t]);
-            mma(o[n][x][t], v[1], b[1][n], o[n][x][t]);
-          }
+        for (int n = 0; n < NT; ++n) {
+          mma(o[n][x][t], v[0], b[0][n], o[n][x][t]);
+          mma(o[n][x][t], v[1], b[1][n], o[n][x][t]);
         }
       }
     }
@@ -1029,7 +1004,7 @@ cudaError_t launch_kind(const AttnQ4Args<N>& a, cudaStream_t stream) {
     word.fetch_or(uint64_t(1) << (dev & 63));
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.whole > 0 ? a.whole * a.share : attn_q4_ctas(NT));
+  cfg.gridDim = dim3(a.whole > 0 ? a.whole * a.share : attn_q4_ctas());
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -1050,12 +1025,12 @@ cudaError_t launch_segs(const AttnQ4Args<kMaxSegs>& a, cudaStream_t stream) {
 
 template <int HD>
 cudaError_t launch_tiles(int nt, const AttnQ4Args<kMaxSegs>& a, cudaStream_t stream) {
-  return nt == 1 ? launch_segs<HD, 1>(a, stream) : nt == 2 ? launch_segs<HD, 2>(a, stream) : launch_segs<HD, 4>(a, stream);
+  return nt == 1 ? launch_segs<HD, 1>(a, stream) : launch_segs<HD, 2>(a, stream);
 }
 
 }  // namespace
 
-int attn_q4_ctas(int nt) { return kPagedCtas * (nt == 1 ? Cfg<128, 1>::kCtasPerSm : Cfg<128, 2>::kCtasPerSm); }
+int attn_q4_ctas() { return kPagedCtas * Cfg<128, 1>::kCtasPerSm; }
 
 cudaError_t launch_attn_q4(int head_dim, int nt, const AttnQ4Args<kMaxSegs>& a, cudaStream_t stream) {
   return head_dim == 64 ? launch_tiles<64>(nt, a, stream) : launch_tiles<128>(nt, a, stream);
@@ -1064,7 +1039,7 @@ cudaError_t launch_attn_q4(int head_dim, int nt, const AttnQ4Args<kMaxSegs>& a, 
 // Its launch overlaps the attention's last CTAs (programmatic dependent launch).
 cudaError_t launch_join_q4(int head_dim, int nt, const AttnQ4Head& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(attn_q4_ctas(nt), nt == 1 ? 4 : 8);
+  cfg.gridDim = dim3(attn_q4_ctas(), nt == 1 ? 4 : 8);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};

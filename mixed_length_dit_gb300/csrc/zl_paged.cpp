@@ -458,7 +458,7 @@ Few next_few(const int32_t* cu, int32_t num_seqs, int32_t group, int32_t* i) {
     ++f.segs;
     most = std::max(most, rows);
   }
-  f.nt = most <= 8 ? 1 : most <= 16 ? 2 : 4;
+  f.nt = most <= 8 ? 1 : 2;
   for (int32_t x = first; x < *i; ++x) {
     const int64_t rows = int64_t(cu[x + 1] - cu[x]) * group;
     if (rows <= kQ4Rows) f.row_tiles += (rows + 8 * f.nt - 1) / (8 * f.nt);
@@ -467,7 +467,7 @@ Few next_few(const int32_t* cu, int32_t num_seqs, int32_t group, int32_t* i) {
 }
 
 size_t few_workspace(int32_t nt, int32_t hd) {
-  const size_t ctas = zl::attn_q4_ctas(nt);
+  const size_t ctas = zl::attn_q4_ctas();
   return up256(ctas * sizeof(zl::Q4Join)) + 2 * ctas * 8 * nt * (hd + 1) * sizeof(float);
 }
 
@@ -481,7 +481,7 @@ void whole_q4(zl::AttnQ4Head* a, const Few& f, int ctas) {
   if (units > ctas) return;
   int64_t keys = a->max_kv_len;
   if (a->window > 0 && a->causal) keys = std::min(keys, int64_t(a->window) + 64);
-  const int64_t wave = 224;                        // keys that a CTA's warps have at a time
+  const int64_t wave = f.nt == 1 ? 224 : 160;      // keys that a CTA's warps have at a time
   int32_t share = 1;
   while (share < 8 && units * share * 2 <= ctas && share * wave < keys) share *= 2;
   if (keys > share * wave * 6) return;
@@ -559,7 +559,7 @@ zl_status launch_few_q4(const Attend& c, void* workspace) {
       const int32_t n = c.queries(x);
       if (n > 0 && int64_t(n) * a.group <= kQ4Rows) a.segs[a.n_segs++] = zl::PagedSeg{x, c.cu[x], n};
     }
-    const int ctas = zl::attn_q4_ctas(f.nt);
+    const int ctas = zl::attn_q4_ctas();
     a.joins = static_cast<zl::Q4Join*>(workspace);
     a.o_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up256(ctas * sizeof(zl::Q4Join)));
     a.lse_part = a.o_part + int64_t(2) * ctas * 8 * f.nt * cache.head_dim;
