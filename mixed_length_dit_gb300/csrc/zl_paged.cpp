@@ -473,7 +473,17 @@ size_t few_workspace(int32_t nt, int32_t hd) {
 
 // Whether the launch's units are left whole: each has a CTA, or a cluster of up to 8,
 // to itself (no sums over the lengths, no join).  Sets whole (0: they are cut into
-// equal shares) and share.
+// equal shares) and share.  Measured (us of the GPU, a call repeated; d = 128, pages
+// of 64, every length at its bound): whole with one CTA, whole with clusters, cut
+//   keys                  256              512             1024             2048             4096             8192
+//   8 units     6.0  6.9  9.1    7.4  7.0  9.5   10.5  7.4 10.7   16.9  8.8 10.5   28.7  9.9 11.4   52.8 12.7 12.7
+//   32 units    6.4  7.4  9.9    7.8  7.6 10.0   10.9  8.6 11.0   17.1 10.5 12.6   29.1 12.2 14.4   53.1 16.0 17.1
+//   96 units    6.8  8.4 10.9    8.4  9.6 11.5   11.3 11.9 12.4   17.5 16.1 16.3   29.4 24.4 22.2   56.4 42.7 32.9
+//   288 units   9.3  9.4 10.7   11.3 11.3 12.7   15.2 15.2 16.7   24.7 24.7 26.1   42.6 42.6 45.9   77.3 77.3 78.9
+// A cluster's CTAs need two waves of keys each to gain (eight where they make a second
+// CTA on an SM).  The lengths themselves are on the device; half the bound is taken for
+// their mean, so that equal shares have units * keys / 2 / ctas, and may begin three
+// waves later.
 void whole_q4(zl::AttnQ4Head* a, const Few& f, int ctas) {
   a->whole = 0;
   a->share = 1;
@@ -483,8 +493,8 @@ void whole_q4(zl::AttnQ4Head* a, const Few& f, int ctas) {
   if (a->window > 0 && a->causal) keys = std::min(keys, int64_t(a->window) + 64);
   const int64_t wave = f.nt == 1 ? 224 : 160;      // keys that a CTA's warps have at a time
   int32_t share = 1;
-  while (share < 8 && units * share * 2 <= ctas && share * wave < keys) share *= 2;
-  if (keys > share * wave * 6) return;
+  while (share < 8 && units * share * 2 <= ctas && keys >= (units * share * 2 <= ctas / 2 ? 2 : 8) * share * wave) share *= 2;
+  if (keys / share - units * keys / (2 * ctas) > 3 * wave) return;
   a->whole = static_cast<int32_t>(units);
   a->share = share;
 }
