@@ -45,12 +45,16 @@ __device__ __forceinline__ float2 q4_steps23(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// The largest magnitude among 8 bf16, as two bf16 patterns: patterns of
-// magnitudes order as integers, and what is not finite is above all others.
-__device__ __forceinline__ uint32_t q4_top(const uint4& x) {
-  constexpr uint32_t m = 0x7fff7fffu;
-  return __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m));
+// The larger magnitudes of two pairs of bf16; a NaN is handed on.
+__device__ __forceinline__ uint32_t q4_max2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&m);
 }
+
+// The largest magnitude among 8 bf16, as two of them.  Their patterns order as
+// integers, with what is not finite above all others.
+__device__ __forceinline__ uint32_t q4_top(const uint4& x) { return q4_max2(q4_max2(x.x, x.y), q4_max2(x.z, x.w)); }
 
 // The byte of the step for a group whose largest magnitude is the bf16 `top`:
 // top / 7 with four significant bits, halves up.  top has 8 bits, so a quotient
@@ -74,21 +78,31 @@ __device__ __forceinline__ float q4_inverse(uint32_t byte) {
 // The codes of 8 bf16, c + 8 in four bits each.  A half between two codes is a
 // bf16 itself (two times c + 1/2 and a step of four bits have eight), and its
 // neighbours lie 2^-10 steps away at least: 2^-12 added before cutting puts the
-// halves on the upper side although the inverse and the product are rounded.
-__device__ __forceinline__ uint32_t q4_codes(const uint4& x, float inv) {
+// halves on the upper side although the inverse and the product are rounded.  A
+// step rounded to four bits is at least 16/17 of the seventh, so that x / s stays below
+// 7.5: only steps below 2^-14 and the largest one need clamping.
+template <bool CLAMP>
+__device__ __forceinline__ uint32_t q4_codes_of(const uint4& x, float inv) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t r = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = bf16x2_to_float2(w[i]);
-    const float a = fminf(fmaxf(fmaf(f.x, inv, 8.5f + 0x1p-12f), 0.f), 15.5f);
-    const float b = fminf(fmaxf(fmaf(f.y, inv, 8.5f + 0x1p-12f), 0.f), 15.5f);
+    float a = fmaf(f.x, inv, 8.5f + 0x1p-12f), b = fmaf(f.y, inv, 8.5f + 0x1p-12f);
+    if (CLAMP) {
+      a = fminf(fmaxf(a, 0.f), 15.5f);
+      b = fminf(fmaxf(b, 0.f), 15.5f);
+    }
     // cut to whole numbers in the float's low bits
     r += __float_as_uint(__fadd_rd(a, 8388608.f)) << (8 * i);
     r += __float_as_uint(__fadd_rd(b, 8388608.f)) << (8 * i + 4);
   }
   return r - ((0x4b000000u) + (0x4b000000u << 4));   // the float's upper bits (what was shifted further is gone)
 }
+__device__ __forceinline__ uint32_t q4_codes(const uint4& x, float inv, bool clamp) {
+  return clamp ? q4_codes_of<true>(x, inv) : q4_codes_of<false>(x, inv);
+}
+__device__ __forceinline__ bool q4_clamps(uint32_t byte) { return byte - 8u >= 0xf7u - 8u; }
 
 // A piece's words, one for each group, as they are held, and back.
 template <int G>

@@ -128,16 +128,27 @@ template <int HD>
 __device__ __forceinline__ void keep(const Piece<HD>& p, uint8_t* block, int page_size, int row, int c, bool values,
                                      bool store) {
   constexpr int G = Piece<HD>::G;
-  uint32_t w[G], steps = 0;
+  // The groups' largest magnitudes, two in a word, over the four threads; thread c
+  // then finds the step of group c for all of them.
+  uint32_t t[G / 2];
 #pragma unroll
-  for (int q = 0; q < G; ++q) {
-    uint32_t top = q4_top(p.x[q]);
-    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const uint32_t byte = q4_step_byte(max(top & 0xffffu, top >> 16));
-    w[q] = q4_codes(p.x[q], q4_inverse(byte));
-    steps |= byte << (8 * q);
+  for (int y = 0; y < G / 2; ++y) {
+    const uint32_t u = q4_top(p.x[2 * y]), v = q4_top(p.x[2 * y + 1]);
+    t[y] = q4_max2(__byte_perm(u, v, 0x5410), __byte_perm(u, v, 0x7632));
+    t[y] = q4_max2(t[y], __shfl_xor_sync(0xffffffffu, t[y], 1));
+    t[y] = q4_max2(t[y], __shfl_xor_sync(0xffffffffu, t[y], 2));
   }
+  const int q0 = c & (G - 1);
+  const uint32_t pair = G == 4 && q0 >= 2 ? t[G / 2 - 1] : t[0];
+  const uint32_t byte = q4_step_byte(q0 & 1 ? pair >> 16 : pair & 0xffffu);
+  const float inv = q4_inverse(byte);
+  uint32_t steps = c < G ? byte << (8 * q0) : 0u;
+  steps |= __shfl_xor_sync(0xffffffffu, steps, 1);
+  steps |= __shfl_xor_sync(0xffffffffu, steps, 2);
+  const bool clamp = __any_sync(0xffffffffu, q4_clamps(byte));
+  uint32_t w[G];
+#pragma unroll
+  for (int q = 0; q < G; ++q) w[q] = q4_codes(p.x[q], __shfl_sync(0xffffffffu, inv, q, 4), clamp);
   if (!store) return;
   if (values) q4_order_values(w);
   uint8_t* codes = block + static_cast<int64_t>(row) * kQ4Codes<HD> + c * (4 * G);
@@ -153,8 +164,9 @@ __device__ __forceinline__ void keep(const Piece<HD>& p, uint8_t* block, int pag
 
 // ------------------------------------------------------------------ append
 template <int HD, int SEQS>
-__global__ void __launch_bounds__(kThreads)
-append_q4_kernel(const __grid_constant__ RopeArgs<SEQS> a, int tokens_per_block, int heads_per_block) {
+__global__ void __launch_bounds__(kThreads, 3)
+append_q4_kernel(const __grid_constant__ RopeArgs<SEQS> a, int tokens_per_block, int heads_per_block,
+                 uint32_t heads_inv) {
   __shared__ __align__(16) float2 cs[kTokensMax][HD / 2];
   __shared__ int32_t pos_of[kTokensMax];
   __shared__ int32_t page_of[kTokensMax];      // -1: left out
@@ -186,7 +198,8 @@ append_q4_kernel(const __grid_constant__ RopeArgs<SEQS> a, int tokens_per_block,
   for (int x0 = 0; x0 < nt * per_token; x0 += kHeads) {        // whole warps: heads exchange among four threads
     const int x = x0 + (threadIdx.x >> 2);
     const bool any = x < nt * per_token;
-    const int tl = any ? x / per_token : 0;
+    // x / heads_per_block (a block of fewer heads has one token); exact, as x times the heads is below 2^32
+    const int tl = any && nt > 1 ? static_cast<int>(__umulhi(x, heads_inv)) : 0;
     const int h = any ? h0 + x - tl * per_token : 0;
     const int64_t t = a.token0 + t0 + tl;
     const int kind = h < a.nq ? 0 : h < a.nq + a.nk ? 1 : 2;   // query, key, value
@@ -343,12 +356,13 @@ cudaError_t launch_append_q4(const RopeArgs<kMaxSegs>& a, int num_sms, cudaStrea
   while (hpb > kHeads && blocks * ((heads + hpb - 1) / hpb) < 2 * num_sms) hpb = (hpb + 1) / 2;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + hpb - 1) / hpb));
   const bool few = a.n_seqs <= kFewSegs;
+  const uint32_t inv = static_cast<uint32_t>((uint64_t(1) << 32) / hpb + 1);
   if (a.head_dim == 64) {
-    if (few) append_q4_kernel<64, kFewSegs><<<grid, kThreads, 0, stream>>>(cut_cu<kFewSegs>(a), tpb, hpb);
-    else append_q4_kernel<64, kMaxSegs><<<grid, kThreads, 0, stream>>>(a, tpb, hpb);
+    if (few) append_q4_kernel<64, kFewSegs><<<grid, kThreads, 0, stream>>>(cut_cu<kFewSegs>(a), tpb, hpb, inv);
+    else append_q4_kernel<64, kMaxSegs><<<grid, kThreads, 0, stream>>>(a, tpb, hpb, inv);
   } else {
-    if (few) append_q4_kernel<128, kFewSegs><<<grid, kThreads, 0, stream>>>(cut_cu<kFewSegs>(a), tpb, hpb);
-    else append_q4_kernel<128, kMaxSegs><<<grid, kThreads, 0, stream>>>(a, tpb, hpb);
+    if (few) append_q4_kernel<128, kFewSegs><<<grid, kThreads, 0, stream>>>(cut_cu<kFewSegs>(a), tpb, hpb, inv);
+    else append_q4_kernel<128, kMaxSegs><<<grid, kThreads, 0, stream>>>(a, tpb, hpb, inv);
   }
   return cudaGetLastError();
 }
