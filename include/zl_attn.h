@@ -625,7 +625,18 @@ zl_status zl_paged_attn_q4_workspace_size(const int32_t* cu_seqlens_q, int32_t n
                                           size_t* bytes);
 
 /*
- * zl_paged_attn over a cache held in 4 bits: same arguments and rules.
+ * zl_paged_attn over a cache held in 4 bits: the same arguments, mask and rules, o and
+ * lse as of the values held.  Scores, the running maximum and sum, and the output
+ * accumulate in float32; a probability, or its product with a value's step, is rounded
+ * to bf16 once.  Queries up to 2^114 in magnitude.  As in zl_paged_attn a sequence's
+ * values must be finite; a key of NaN reaches the rows that see it.
+ *
+ * Sequences of at most 64 rows (queries times num_heads / num_kv_heads) run over the
+ * codes; longer ones are unpacked into the workspace first, once for all of their
+ * queries, and run as zl_paged_attn.  One or two launches per 640 sequences of the
+ * first kind, one per batch that the workspace holds of the second and
+ * zl_paged_attn's behind it.  The same batch gives the same bits on every run; where a
+ * sequence's keys are cut follows from the whole batch and from max_kv_len.
  */
 zl_status zl_paged_attn_q4(const zl_paged_cache_t* cache, const void* q, int64_t q_stride, const int32_t* cu_seqlens_q,
                            int32_t num_seqs, int32_t max_kv_len, int32_t num_heads, float softmax_scale,

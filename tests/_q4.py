@@ -31,7 +31,8 @@ class Batch:
     """New tokens and a 4-bit cache in use: pages in any order; pool rows and
     table entries that belong to nobody hold what must not matter."""
 
-    def __init__(self, new, lens, heads, kv_heads, hd, page, seed=0, spare_cols=2, fill=0xff, device="cuda"):
+    def __init__(self, new, lens, heads, kv_heads, hd, page, seed=0, spare_cols=2, fill=0xff, device="cuda",
+                 scales=(1.0, 1.0, 1.0)):
         rng = np.random.default_rng(seed)
         self.new, self.lens, self.hd, self.page, self.kv_heads = list(new), list(lens), hd, page, kv_heads
         self.cu = [0]
@@ -47,7 +48,8 @@ class Batch:
             self.table[s, :n] = numbers[at:at + n]
             self.table[s, n:] = rng.integers(-5, self.num_pages + 5, cols - n)      # past the sequence: anything
             at += n
-        self.k_pages, self.v_pages = (random_pool(rng, self.num_pages, kv_heads, page, hd, k) for k in (True, False))
+        self.k_pages, self.v_pages = (random_pool(rng, self.num_pages, kv_heads, page, hd, k, x)
+                                      for k, x in ((True, scales[1]), (False, scales[2])))
         for pool in (self.k_pages, self.v_pages):
             for s, n in enumerate(lens):
                 if n % page:
@@ -55,7 +57,7 @@ class Batch:
             for p in numbers[at:]:
                 self.fill(pool, int(p), 0, fill)
         self.k_pages, self.v_pages = self.k_pages.to(device), self.v_pages.to(device)
-        self.q = torch.tensor(rng.standard_normal((self.cu[-1], heads, hd)), dtype=BF16, device=device)
+        self.q = torch.tensor(rng.standard_normal((self.cu[-1], heads, hd)) * scales[0], dtype=BF16, device=device)
         self.dtable = torch.tensor(self.table, device=device)
         self.dlens = torch.tensor(self.lens, dtype=torch.int32, device=device)
 

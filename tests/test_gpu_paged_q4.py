@@ -383,6 +383,34 @@ def test_large_scores():
     assert torch.isfinite(o.float()).all()
 
 
+@pytest.mark.parametrize("q_exp,k_exp,v_exp", [(60, 0, 0), (-60, 0, 0), (110, -8, 10), (-120, 12, -12), (0, -12, 13), (0, 13, -13)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_large_and_small_numbers(q_exp, k_exp, v_exp, hd):
+    """Queries, keys and values of other sizes, the scale making the scores what they
+    were: the same tolerances (all but the roundings is a power of two), but for steps
+    below 2^-14, whose units of 2^-17 the oracle has too."""
+    b = Batch([1, 12, 30, 140], [500, 300, 77, 400], 4, 2, hd, 16, seed=39,
+              scales=(2.0 ** q_exp, 2.0 ** k_exp, 2.0 ** v_exp))
+    scale = 2.0 ** -(q_exp + k_exp) * hd ** -0.5
+    o, lse = b.run(softmax_scale=scale)
+    zl.sync_check()
+    check(b, o, lse, scale=scale)
+
+
+def test_steps_of_all_sizes_side_by_side():
+    """Values whose steps differ by 2^30 from token to token: the small ones count
+    where the large ones are not seen."""
+    b = Batch([4, 1], [200, 200], 4, 2, 128, 16, seed=47)
+    for pool, byte in ((b.v_pages, 0xf0), (b.k_pages, 0x08)):
+        page = pool[int(b.table[0, 199 // 16])].view(2, -1)
+        page[:, 16 * 64 + 199 % 16 * 4:16 * 64 + (199 % 16 + 1) * 4] = byte          # the newest token's steps
+        page = pool[int(b.table[1, 3])].view(2, -1)
+        page[:, 16 * 64:16 * 64 + 4 * 5] = 8 if byte == 0xf0 else 0
+    o, lse = b.run()
+    zl.sync_check()
+    check(b, o, lse)
+
+
 @pytest.mark.parametrize("new,lens,heads,kv_heads,hd", [
     ([1, 1], [40, 300], 8, 2, 128), ([12, 3], [200, 90], 10, 2, 64), ([100], [260], 1, 1, 128), ([300, 70], [300, 900], 4, 2, 64),
     ([1], [20000], 6, 2, 128), ([20], [9000], 2, 1, 64), ([5], [333], 8, 2, 128),
