@@ -495,8 +495,9 @@ struct Rows {
       // below 2^-7 and goes up by 2^127.  Codes are n 2^-133.
       const int up_exp = min(374 - static_cast<int>(top >> 7), 254);
       const float up = __uint_as_float(static_cast<uint32_t>(up_exp) << 23);
-      const float down = top >= 0x7f80u ? __uint_as_float(0x7fffffffu)
-                                        : __uint_as_float(static_cast<uint32_t>(min(387 - up_exp, 254)) << 23) * a.scale_log2;
+      // (above zero for a row of NaN or infinities as well, whose products are NaN by
+      // themselves: keys that it does not see stay at -inf)
+      const float down = __uint_as_float(static_cast<uint32_t>(min(387 - up_exp, 254)) << 23) * a.scale_log2;
       if (c == 0 && x == 0) sm->q_scale[r] = down;
       const float2 x0 = bf16x2_to_float2(u.x), x1 = bf16x2_to_float2(u.y), x2 = bf16x2_to_float2(u.z), x3 = bf16x2_to_float2(u.w);
       // columns j and j + 4 beside one another, as a word's codes are taken; the odd ones' codes come 16 times over
@@ -595,7 +596,7 @@ struct Rows {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        // (a mask's -inf stays -inf: f is above zero, NaN, or 0 for a row of zeros)
+        // (a mask's -inf stays -inf: f is above zero)
         const float top = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
         raise = raise || top * f[n][e] > m[n][e] + kRescale;
       }

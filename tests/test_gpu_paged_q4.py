@@ -440,6 +440,26 @@ def test_nan_is_handed_on(new, lens, heads, kv_heads, hd):
     assert torch.equal(o3[~nan], o1[~nan]) and torch.equal(l3.T[~nan], l1.T[~nan])
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("heads,kv_heads,hd", [(4, 2, 64), (4, 4, 128)])
+def test_a_query_that_is_not_finite_and_sees_no_key(heads, kv_heads, hd, value):
+    """Such a row is zero and its lse -inf, as any row that sees nothing; one that
+    sees keys is NaN."""
+    new, lens = [1, 5, 9, 300], [0, 2, 40, 250]          # 3 queries, and 50, come before their cache
+    b = Batch(new, lens, heads, kv_heads, hd, 16, seed=41)
+    o1, l1 = b.run()
+    q = b.q.clone()
+    blind = [0, 1, 3, 15, 64]                            # rows of the packed batch that see nothing
+    q[blind + [4, 10], 0, 5] = value
+    o2, l2 = b.run(q=q)
+    zl.sync_check()
+    assert torch.all(o2[blind] == 0) and torch.isneginf(l2[:, blind]).all()
+    assert o2[[4, 10], 0].isnan().all() and l2[0, [4, 10]].isnan().all()
+    hit = torch.zeros((b.cu[-1], heads), dtype=torch.bool, device="cuda")
+    hit[[4, 10], 0] = True
+    assert torch.equal(o2[~hit], o1[~hit]) and torch.equal(l2.T[~hit], l1.T[~hit])
+
+
 def test_queries_inside_wider_rows_and_given_buffers():
     b = Batch([1, 200, 7], [50, 260, 130], 6, 2, 128, 32, seed=34)
     o1, l1 = b.run()
