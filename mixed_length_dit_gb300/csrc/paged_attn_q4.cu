@@ -25,7 +25,7 @@
 // products take such numbers as they are.  So a code in bits 0 to 3 is n, one in
 // bits 4 to 7 is 16 n, and the other factor brings the size: a row of q is scaled
 // by a power of two so that its largest element lies at 2^120 (columns whose codes
-// come 16 times over by 1/16 of it), P by 2^60.  All of it is exact.
+// come 16 times over by 1/16 of it), a value's step by 2^60.  All of it is exact.
 // A word's codes are four operands after five logical operations; two tokens' codes
 // of a column, as V wants them, take a byte permutation more for each.
 //
@@ -61,7 +61,7 @@ constexpr uint32_t kLow = 0x000f000fu;         // of codes: n, and 16 n
 constexpr uint32_t kHigh = 0x00f000f0u;
 constexpr uint32_t kMinus8 = 0x80088008u;      // -8 n's unit, twice, and 16 times that
 constexpr uint32_t kMinus128 = 0x80808080u;
-constexpr float kPScale = 60.f;                // P comes 2^60 times over
+constexpr float kValueScale = 0x1p60f;         // of values' steps, and so of P
 constexpr float kOutScale = 0x1p73f;           // from sums of codes to the output
 
 template <int HD, int NT>
@@ -126,15 +126,20 @@ __device__ __forceinline__ void load_floats(const float* p, float (&w)[G]) {
   }
 }
 
-// A token's steps from its bytes to floats.
+// A token's steps from its bytes to floats, times `by`.
 template <int G>
-__device__ __forceinline__ void spread_steps(float* to, const uint8_t* p, bool there = true) {
+__device__ __forceinline__ void spread_steps(float* to, const uint8_t* p, float by, bool there = true) {
+  const uint64_t by2 = f2_pack(by, by);
+  const auto scaled = [&](float2 x) {
+    f2_unpack(f2_mul(f2_pack(x.x, x.y), by2), x.x, x.y);
+    return x;
+  };
   if constexpr (G == 4) {
     const uint32_t w = there ? *reinterpret_cast<const uint32_t*>(p) : 0u;
-    const float2 a = q4_steps01(w), b = q4_steps23(w);
+    const float2 a = scaled(q4_steps01(w)), b = scaled(q4_steps23(w));
     *reinterpret_cast<float4*>(to) = make_float4(a.x, a.y, b.x, b.y);
   } else {
-    *reinterpret_cast<float2*>(to) = q4_steps01(there ? *reinterpret_cast<const uint16_t*>(p) : 0u);
+    *reinterpret_cast<float2*>(to) = scaled(q4_steps01(there ? *reinterpret_cast<const uint16_t*>(p) : 0u));
   }
 }
 
@@ -468,7 +473,7 @@ struct Rows {
   using C = Cfg<HD, NT>;
   static constexpr int G = C::G;
   float o[NT][G][2][4];                        // [tile of 16 columns][fragment]
-  float m[NT][2], l[NT][2];                    // of rows 2c, 2c + 1; l: the lane's keys alone, 2^60 times
+  float m[NT][2], l[NT][2];                    // of rows 2c, 2c + 1; l: the lane's keys alone
   float f[NT][2];                              // their q_scale
 
   template <int N>
@@ -537,9 +542,9 @@ struct Rows {
     // the key of rows g, and 8 on: four lanes' values of a column are in different banks
     const int key_g = g ^ ((g >> 1) & 1);
     const int held = lay.steps + (lane >> 4) * lay.steps_half + (lane & 15) * G;
-    spread_steps<G>(steps + lane * G, kr + held);
+    spread_steps<G>(steps + lane * G, kr + held, 1.f);
     // (past the sequence anything may be held)
-    spread_steps<G>(steps + (kTile + lane) * G, vr + held, pos + lane < it.len);
+    spread_steps<G>(steps + (kTile + lane) * G, vr + held, kValueScale, pos + lane < it.len);
     __syncwarp();
     float s[2][NT][4];
 #pragma unroll
@@ -622,20 +627,26 @@ struct Rows {
             }
         }
     }
+    // The scaled score is rounded as the maximum was, so that the largest one's difference
+    // is zero whatever its size: a fused product would leave the maximum's rounding, 2^8
+    // for scores of 2^32, in the exponent.  (The compiler fuses products and sums that
+    // are both packed.)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      const uint64_t neg2 = f2_pack(m[n][0] == -INFINITY ? 0.f : -m[n][0], m[n][1] == -INFINITY ? 0.f : -m[n][1]);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float neg = m[n][e] == -INFINITY ? 0.f : kPScale - m[n][e];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int k = 0; k < 2; ++k) {
+          float* p = &s[h][n][2 * k];
+          f2_unpack(f2_add(f2_pack(__fmul_rn(p[0], f[n][0]), __fmul_rn(p[1], f[n][1])), neg2), p[0], p[1]);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float& p = s[h][n][2 * k + e];
-            p = fast_exp2(fmaf(p, f[n][e], neg));
-            l[n][e] += p;
+          for (int e = 0; e < 2; ++e) {
+            p[e] = fast_exp2(p[e]);
+            l[n][e] += p[e];
           }
-      }
+        }
+    }
     uint32_t w[2][4];
     float2 st[2][2];
 #pragma unroll
@@ -743,7 +754,7 @@ __device__ __forceinline__ void finish(const AttnQ4Args<N>& a, const Item& it, S
       for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
       if (g == 0) {
         sm->m[warp][8 * n + 2 * c + e] = r.m[n][e];
-        sm->l[warp][8 * n + 2 * c + e] = l * 0x1p-60f;
+        sm->l[warp][8 * n + 2 * c + e] = l;
       }
     }
   named_bar_sync(1, 32 * C::W);

@@ -1,0 +1,113 @@
+"""The 4-bit paged cache at the ends of its numbers' range, against float64.
+
+What a score may be off by (derived, for the arithmetic over codes): a group's sum
+over its 32 columns begins at -8 sum q, a float32 sum of 32 numbers (off by 8 * 2^-24
+of 8 sum|q| at most: five sums in a row), and two products of 16 columns add n q with
+n <= 15.  No partial sum passes 23 sum|q|.  A product cuts each of its 17 addends, and
+their sum, at 2^-23 of the largest at worst: 2 * 18 * 2^-23 * 23 sum|q| together.
+Times the step, over the groups, with four roundings more of the row's sum (2^-21 of
+each term), and the scale:
+
+    E = scale sum_g s_g sum|q|_g (2 * 18 * 2^-23 * 23 + 64 * 2^-24 + 2^-21 * 8)
+
+An LSE is off by the largest E of the row's keys and 2^-20 of itself (scale and
+maximum in float32); each probability and their sum by that much of themselves too,
+on top of 2^-8 for P's rounding (half a step, to bf16) and 2^-8 |o| for the output's.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mixed_length_dit_gb300 as zl
+from oracle import paged_f64 as ref
+from oracle import q4_f64 as q4
+from _helpers import f64
+from _q4 import BF16, Batch, pool_values
+
+pytestmark = pytest.mark.gpu
+
+E_SUM = 2 * 18 * 2.0 ** -23 * 23 + 64 * 2.0 ** -24 + 2.0 ** -21 * 8
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def randn(seed, *shape, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(BF16)
+
+
+def rows_of(b, q, scale, causal=True, window=0):
+    """For each (packed row, head): its scores over all keys of its sequence (-inf
+    where hidden), what they may be off by, and the values [keys, d]."""
+    kv, vv = pool_values(b.k_pages, True), pool_values(b.v_pages, False)
+    steps = {}
+    raw = b.k_pages.cpu().numpy()
+    p, hk, page, row = raw.shape
+    _, byte = q4.unpack(raw.reshape(p, hk, page * row), page, b.hd, True)
+    held = q4.STEPS[byte]                                   # [P, Hk, page, d / 32]
+    group = q.shape[1] // hk
+    for s in range(len(b.new)):
+        n, length = b.new[s], b.lens[s]
+        k, v = ref.gather(kv, b.table[s], length), ref.gather(vv, b.table[s], length)
+        st = ref.gather(held, b.table[s], length)
+        j = np.arange(length)
+        for i in range(n):
+            pos = length - n + i
+            seen = (j <= pos) if causal else np.ones(length, dtype=bool)
+            if window:
+                seen = seen & (j > pos - window)
+            for h in range(q.shape[1]):
+                x = q[b.cu[s] + i, h]
+                score = np.where(seen, k[:, h // group] @ x * scale, -np.inf)
+                off = st[:, h // group] @ np.abs(x).reshape(-1, 32).sum(-1) * scale * E_SUM
+                yield b.cu[s] + i, h, score, np.where(seen, off, 0.0), v[:, h // group]
+
+
+# ------------------------------------------------------------------ scores of any size
+@pytest.mark.parametrize("exp", [12, 24, 29, 30, 31, 32, 40, 64, 100])
+@pytest.mark.parametrize("new,lens,heads,kv_heads,hd,most", [
+    ([1, 2], [200, 77], 8, 2, 128, 200),                    # units of 8 rows, whole
+    ([1] * 3, [5000, 90, 1200], 4, 2, 64, 16000),           # cut
+    ([4, 9], [900, 300], 8, 2, 128, 900),                   # units of 16 rows
+    ([1], [3000], 2, 1, 64, 3000),                          # a cluster
+])
+def test_scores_of_any_size(new, lens, heads, kv_heads, hd, most, exp):
+    """Scores of up to 2^100 and more: finite outputs, the lse to the scores' own
+    rounding, and, where the largest score leads by more than the roundings of two
+    scores and 60, the value of its key: a probability of one times a step is a bf16, and
+    so is the value; the other keys together count for less than 2^-60."""
+    b = Batch(new, lens, heads, kv_heads, hd, 16, seed=50, spare_cols=1000, scales=(2.0 ** exp, 1.0, 1.0))
+    scale = hd ** -0.5
+    o, lse = b.run(most=most)
+    zl.sync_check()
+    o, lse = f64(o), f64(lse)
+    assert np.isfinite(o).all() and np.isfinite(lse).all()
+    clear = 0
+    for row, h, score, off, v in rows_of(b, f64(b.q), scale):
+        top = int(score.argmax())
+        m = score[top]
+        want = m + np.log(np.exp(score - m).sum())
+        assert abs(lse[h, row] - want) <= off.max() + 2.0 ** -20 * abs(want)
+        second = np.partition(score, -2)[-2] if len(score) > 1 else -np.inf
+        if m - second > 2 * (off.max() + 2.0 ** -22 * abs(m)) + 60:
+            clear += 1
+            assert np.abs(o[row, h] - v[top]).max() <= 2.0 ** -60, (row, h)
+    assert exp < 24 or clear >= 0.8 * o.shape[0] * o.shape[1]
+
+
+def test_scores_of_a_chunk_up_to_their_bound():
+    """Chunks run over the bf16 kernel, whose probabilities keep the rounding of the scaled
+    maximum, below 2^7 in the exponent for scores below 2^30: finite, and the lse to the
+    scores' rounding (twice the bound above: eight products of 16 columns, partial sums
+    below 7 sum_g s_g sum|q|_g, 8 * 18 * 2^-23 * 7)."""
+    b = Batch([100, 70], [300, 90], 2, 2, 128, 16, seed=49, scales=(2.0 ** 27, 1.0, 1.0))
+    o, lse = b.run()
+    zl.sync_check()
+    o, lse = f64(o), f64(lse)
+    assert np.isfinite(o).all() and np.isfinite(lse).all()
+    for row, h, score, off, v in rows_of(b, f64(b.q), 128 ** -0.5):
+        assert score.max() < 2.0 ** 30
+        want = score.max() + np.log(np.exp(score - score.max()).sum())
+        assert abs(lse[h, row] - want) <= 2 * off.max() + 2.0 ** -20 * abs(want)
