@@ -628,10 +628,10 @@ zl_status zl_paged_attn_q4_workspace_size(const int32_t* cu_seqlens_q, int32_t n
  * zl_paged_attn over a cache held in 4 bits: the same arguments, mask and rules, o and
  * lse as of the values held.  Scores, the running maximum and sum, and the output
  * accumulate in float32; a probability, or its product with a value's step, is rounded
- * to bf16 once.  Queries up to 2^114 in magnitude.  Scores may have any size that float32
- * holds; those of sequences that run as zl_paged_attn (below) stay below 2^30 in
- * magnitude.  As in zl_paged_attn a sequence's values must be finite; a key of NaN reaches
- * the rows that see it.
+ * to bf16 once.  Queries may have any size, and scores any that float32 holds; of
+ * sequences that run as zl_paged_attn (below) scores stay below 2^30 in magnitude, and
+ * within float32 without the softmax scale.  As in zl_paged_attn a sequence's values must
+ * be finite; a key of NaN reaches the rows that see it.
  *
  * Sequences of at most 64 rows (queries times num_heads / num_kv_heads) run over the
  * codes; longer ones are unpacked into the workspace first, once for all of their

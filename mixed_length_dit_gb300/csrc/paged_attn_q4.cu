@@ -25,7 +25,8 @@
 // products take such numbers as they are.  So a code in bits 0 to 3 is n, one in
 // bits 4 to 7 is 16 n, and the other factor brings the size: a row of q is scaled
 // by a power of two so that its largest element lies at 2^120 (columns whose codes
-// come 16 times over by 1/16 of it), a value's step by 2^60.  All of it is exact.
+// come 16 times over by 1/16 of it), a key's step by 2^40 and a value's by 2^60.  All of
+// it is exact.
 // A word's codes are four operands after five logical operations; two tokens' codes
 // of a column, as V wants them, take a byte permutation more for each.
 //
@@ -45,6 +46,7 @@
 // their offset taken off took 179 us, masks alone 141.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 
 #include "paged.h"
 #include "paged_q4.cuh"
@@ -61,6 +63,8 @@ constexpr uint32_t kLow = 0x000f000fu;         // of codes: n, and 16 n
 constexpr uint32_t kHigh = 0x00f000f0u;
 constexpr uint32_t kMinus8 = 0x80088008u;      // -8 n's unit, twice, and 16 times that
 constexpr uint32_t kMinus128 = 0x80808080u;
+constexpr int kKeyExp = 40;                    // keys' steps, and so scores before the row's scale, come 2^40 times over
+constexpr float kKeyScale = 0x1p40f;
 constexpr float kValueScale = 0x1p60f;         // of values' steps, and so of P
 constexpr float kOutScale = 0x1p73f;           // from sums of codes to the output
 
@@ -500,19 +504,22 @@ struct Rows {
       // below 2^-7 and goes up by 2^127.  Codes are n 2^-133.
       const int up_exp = min(374 - static_cast<int>(top >> 7), 254);
       const float up = __uint_as_float(static_cast<uint32_t>(up_exp) << 23);
-      // (above zero for a row of NaN or infinities as well, whose products are NaN by
-      // themselves: keys that it does not see stay at -inf)
-      const float down = __uint_as_float(static_cast<uint32_t>(min(387 - up_exp, 254)) << 23) * a.scale_log2;
-      if (c == 0 && x == 0) sm->q_scale[r] = down;
+      // 2^133 of the codes and 2^-40 of the keys' steps, back by the row's scale: 2^-34 to
+      // 2^101, for the largest queries too.  Finite and above zero whatever the softmax
+      // scale, and for a row of NaN or infinities as well, whose products are NaN by
+      // themselves: sums of zero stay zero, and keys that are not seen at -inf.
+      const float down = __uint_as_float(static_cast<uint32_t>(387 - kKeyExp - up_exp) << 23) * a.scale_log2;
+      if (c == 0 && x == 0) sm->q_scale[r] = fminf(fmaxf(down, FLT_MIN), FLT_MAX);
       const float2 x0 = bf16x2_to_float2(u.x), x1 = bf16x2_to_float2(u.y), x2 = bf16x2_to_float2(u.z), x3 = bf16x2_to_float2(u.w);
       // columns j and j + 4 beside one another, as a word's codes are taken; the odd ones' codes come 16 times over
       const float odd = up * 0.0625f;
       sm->q[n][x][lane] = make_uint4(pack_bf16x2(x0.x * up, x2.x * up), pack_bf16x2(x0.y * odd, x2.y * odd),
                                      pack_bf16x2(x1.x * up, x3.x * up), pack_bf16x2(x1.y * odd, x3.y * odd));
-      float sum = ((x0.x + x0.y) + (x1.x + x1.y)) + ((x2.x + x2.y) + (x3.x + x3.y));
+      // of scaled elements: 32 of the largest bf16 do not fit a float
+      float sum = ((x0.x * up + x0.y * up) + (x1.x * up + x1.y * up)) + ((x2.x * up + x2.y * up) + (x3.x * up + x3.y * up));
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      sum = sum * up * (-8.f * 0x1p-66f) * 0x1p-67f;
+      sum = sum * (-8.f * 0x1p-66f) * 0x1p-67f;
       const float s0 = __shfl_sync(0xffffffffu, sum, 8 * c), s1 = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
       if (g == 0) sm->q_sum[n][x][c] = make_float4(s0, s1, s0, s1);
     }
@@ -542,7 +549,7 @@ struct Rows {
     // the key of rows g, and 8 on: four lanes' values of a column are in different banks
     const int key_g = g ^ ((g >> 1) & 1);
     const int held = lay.steps + (lane >> 4) * lay.steps_half + (lane & 15) * G;
-    spread_steps<G>(steps + lane * G, kr + held, 1.f);
+    spread_steps<G>(steps + lane * G, kr + held, kKeyScale);
     // (past the sequence anything may be held)
     spread_steps<G>(steps + (kTile + lane) * G, vr + held, kValueScale, pos + lane < it.len);
     __syncwarp();

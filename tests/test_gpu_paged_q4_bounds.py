@@ -111,3 +111,53 @@ def test_scores_of_a_chunk_up_to_their_bound():
         assert score.max() < 2.0 ** 30
         want = score.max() + np.log(np.exp(score - score.max()).sum())
         assert abs(lse[h, row] - want) <= 2 * off.max() + 2.0 ** -20 * abs(want)
+
+
+# ------------------------------------------------------------------ queries of any size
+@pytest.mark.parametrize("exp", [100, 113, 115, 120, 125])
+@pytest.mark.parametrize("new,lens,heads,kv_heads,hd,most", [
+    ([1, 2], [200, 77], 8, 2, 128, 200), ([1] * 3, [5000, 90, 1200], 4, 2, 64, 16000), ([4, 9], [900, 300], 8, 2, 128, 900),
+])
+def test_queries_up_to_the_largest(new, lens, heads, kv_heads, hd, most, exp):
+    """Queries near the end of bf16's range, two rows at the largest number itself (its
+    columns' sum does not fit a float32), and a scale that makes the scores ordinary."""
+    b = Batch(new, lens, heads, kv_heads, hd, 16, seed=51, spare_cols=1000, scales=(2.0 ** exp, 2.0 ** -10, 1.0))
+    largest = float(torch.finfo(BF16).max)
+    if exp == 125:
+        b.q[0, 0] = largest
+        b.q[-1, -1] = -largest
+    scale = 2.0 ** (10 - exp) * hd ** -0.5
+    o, lse = b.run(most=most, softmax_scale=scale)
+    zl.sync_check()
+    o, lse = f64(o), f64(lse)
+    for row, h, score, off, v in rows_of(b, f64(b.q), scale):
+        m = score.max()
+        p = np.exp(score - m)
+        want = m + np.log(p.sum())
+        assert abs(lse[h, row] - want) <= off.max() + 2.0 ** -20 * max(abs(want), 1), (row, h, lse[h, row], want)
+        p /= p.sum()
+        reach, out = p @ np.abs(v), p @ v
+        assert np.all(np.abs(o[row, h] - out) <= (2.0 ** -8 + 2 * off.max() + 2.0 ** -19) * reach + 2.0 ** -8 * np.abs(out))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_large_queries_at_a_scale_of_one(hd):
+    """A scale that is not small, and keys of which some read as zero: no infinity
+    times zero comes in, and a row whose keys are all zero is their mean."""
+    b = Batch([2, 3], [90, 40], 4, 2, hd, 16, seed=52, scales=(2.0 ** 122, 2.0 ** -12, 1.0))
+    page = b.k_pages.shape[2]
+    for s in (0, 1):                                        # the first sequence's first page, all of the second
+        for p in b.table[s, :1 if s == 0 else 3]:
+            b.k_pages[int(p)].view(2, -1)[:, page * hd // 2:] = 0
+    o, lse = b.run(softmax_scale=1.0)
+    zl.sync_check()
+    o, lse = f64(o), f64(lse)
+    assert np.isfinite(o).all() and np.isfinite(lse).all()
+    for row, h, score, off, v in rows_of(b, f64(b.q), 1.0):
+        if row >= b.cu[1]:
+            n = int(np.isfinite(score).sum())
+            assert abs(lse[h, row] - np.log(n)) <= 2.0 ** -20 * np.log(n)
+            reach = np.abs(v[:n]).mean(0)
+            assert np.all(np.abs(o[row, h] - v[:n].mean(0)) <= 2.0 ** -8 * np.abs(v[:n].mean(0)) + 2.0 ** -19 * reach)
+        else:
+            assert abs(lse[h, row] - score.max()) <= off.max() + 2.0 ** -20 * abs(score.max()) + np.log(90)
