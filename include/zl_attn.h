@@ -578,7 +578,7 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
  *
  * so that groups below 2^-18 * 7 in magnitude read as zero and those above
  * 7 * 61,440 are clamped.  A group with an element that is not finite has the
- * byte 255 and reads as NaN.
+ * byte 255, codes of zero, and reads as NaN.
  *
  * k_pages and v_pages are [num_pages][Hk] blocks of page_size * (d/2 + d/32)
  * bytes: the codes of the page's tokens, d/2 bytes each, and behind them their

@@ -83,6 +83,7 @@ __device__ __forceinline__ float q4_inverse(uint32_t byte) {
 // 7.5: only steps below 2^-14 and the largest one need clamping.
 template <bool CLAMP>
 __device__ __forceinline__ uint32_t q4_codes_of(const uint4& x, float inv) {
+  if (CLAMP && inv == 0.f) return 0x88888888u;   // zero, or not finite
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t r = 0;
 #pragma unroll

@@ -161,3 +161,37 @@ def test_large_queries_at_a_scale_of_one(hd):
             assert np.all(np.abs(o[row, h] - v[:n].mean(0)) <= 2.0 ** -8 * np.abs(v[:n].mean(0)) + 2.0 ** -19 * reach)
         else:
             assert abs(lse[h, row] - score.max()) <= off.max() + 2.0 ** -20 * abs(score.max()) + np.log(90)
+
+
+# ------------------------------------------------------------------ what the pages hold
+def pool_bytes(pool, b, rows, keys):
+    """A pool's bytes once rows [T, Hk, d] are the sequences' last tokens."""
+    raw = pool.cpu().numpy().copy()
+    p, hk, page, row = raw.shape
+    d = row * 32 // 17
+    flat = raw.reshape(p, hk, page * row)
+    codes, byte = q4.quantise(rows)
+    for s in range(len(b.new)):
+        for i in range(b.new[s]):
+            pos = b.lens[s] - b.new[s] + i
+            to, at = flat[b.table[s][pos // page]], pos % page
+            block = q4.pack(codes[b.cu[s] + i][:, None], byte[b.cu[s] + i][:, None], keys)
+            to[:, at * d // 2:(at + 1) * d // 2] = block[:, :d // 2]
+            to[:, page * d // 2 + at * d // 32:page * d // 2 + (at + 1) * d // 32] = block[:, d // 2:]
+    return raw
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("-nan"), float("inf"), float("-inf")])
+def test_the_bytes_of_groups_that_are_not_finite(value, hd):
+    """Their step is 255 and their codes are all zero (8 in the nibbles), whatever
+    else they hold."""
+    k = randn(53, 6, 2, hd)
+    k[0, 0, 3], k[1, 1, 40], k[2, 0, hd - 1] = value, value, value
+    k[3, 0, :32], k[4, 1, 32:64], k[5] = value, value, value
+    k[4, 0, 7], k[4, 0, 9] = value, -value
+    b = Batch([6], [20], 2, 2, hd, 16, seed=54)
+    want = pool_bytes(b.k_pages, b, f64(k), True), pool_bytes(b.v_pages, b, f64(k), False)
+    zl.paged_append_q4(k, k, *b.cache, b.cu)
+    zl.sync_check()
+    assert np.array_equal(b.k_pages.cpu().numpy(), want[0]) and np.array_equal(b.v_pages.cpu().numpy(), want[1])
