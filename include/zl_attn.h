@@ -592,9 +592,9 @@ zl_status zl_paged_attn(const zl_paged_cache_t* cache, const void* q, int64_t q_
  */
 
 /*
- * zl_paged_append_ex into a cache held in 4 bits: same arguments.  Turned keys
- * are rounded to bf16 and then quantised, values and keys that are not turned
- * as they are given.
+ * zl_paged_append_ex into a cache held in 4 bits: same arguments.  What is held
+ * is what that entry writes, quantised: turned keys are rounded to bf16 first, and
+ * they and the turned queries are the same bits as its own.
  */
 zl_status zl_paged_append_q4(const zl_paged_cache_t* cache, const void* k, int64_t k_stride, const void* v,
                              int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs, const zl_rope_t* plan,

@@ -59,16 +59,17 @@ __device__ __forceinline__ void turn_halves(uint4& a, uint4& b, const float2* cs
   for (int i = 0; i < 8; i += 2) {
     const float4 w = *reinterpret_cast<const float4*>(cs + i);
     const float a0 = u[i], b0 = v[i], a1 = u[i + 1], b1 = v[i + 1];
-    u[i] = a0 * w.x - b0 * w.y;
-    v[i] = a0 * w.y + b0 * w.x;
-    u[i + 1] = a1 * w.z - b1 * w.w;
-    v[i + 1] = a1 * w.w + b1 * w.z;
+    u[i] = rope_first(a0, b0, w.x, w.y);
+    v[i] = rope_second<false>(a0, b0, w.x, w.y);
+    u[i + 1] = rope_first(a1, b1, w.z, w.w);
+    v[i + 1] = rope_second<false>(a1, b1, w.z, w.w);
   }
   a = pack8(u);
   b = pack8(v);
 }
 
 // Four neighbouring pairs, those with an element at or behind `pairs` kept.
+template <bool ALONE>
 __device__ __forceinline__ void turn_neighbours(uint4& x, const float2* cs, int pairs) {
   float u[8];
   unpack8(x, u);
@@ -77,8 +78,8 @@ __device__ __forceinline__ void turn_neighbours(uint4& x, const float2* cs, int 
     if (i < pairs) {
       const float2 w = cs[i];
       const float a = u[2 * i], b = u[2 * i + 1];
-      u[2 * i] = a * w.x - b * w.y;
-      u[2 * i + 1] = a * w.y + b * w.x;
+      u[2 * i] = rope_first(a, b, w.x, w.y);
+      u[2 * i + 1] = rope_second<ALONE>(a, b, w.x, w.y);
     }
   x = pack8(u);
 }
@@ -90,11 +91,14 @@ __device__ __forceinline__ void turn(Piece<HD>& p, const zl_rope_t& r, const flo
                                      int c) {
   constexpr int G = Piece<HD>::G;
   const int half = r.rot_dim / 2;
+  const bool alone = rope_alone(r, 2);
   if (r.interleaved) {
 #pragma unroll
     for (int q = 0; q < G; ++q) {
       const int first = 16 * q + 4 * c;        // pair
-      if (first < half) turn_neighbours(p.x[q], cs + first, half - first);
+      if (first >= half) continue;
+      if (alone) turn_neighbours<true>(p.x[q], cs + first, half - first);
+      else turn_neighbours<false>(p.x[q], cs + first, half - first);
     }
   } else if (half == 32) {                     // groups q and q + 1
     turn_halves(p.x[0], p.x[1], cs + 8 * c);
@@ -115,7 +119,9 @@ __device__ __forceinline__ void turn(Piece<HD>& p, const zl_rope_t& r, const flo
         const bool is_first = j < half;
         const float2 w = cs[is_first ? j : j - half];
         const float other = __bfloat162float(src[is_first ? j + half : j - half]);
-        u[i] = is_first ? u[i] * w.x - other * w.y : other * w.y + u[i] * w.x;
+        u[i] = is_first ? rope_first(u[i], other, w.x, w.y)
+               : alone  ? rope_second<true>(other, u[i], w.x, w.y)
+                        : rope_second<false>(other, u[i], w.x, w.y);
       }
       p.x[q] = pack8(u);
     }

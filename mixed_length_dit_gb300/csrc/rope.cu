@@ -120,16 +120,16 @@ struct Unit {
             // pairs i, i+1 of the unit: columns 2i .. 2i+3 of the 2N loaded ones
             float* z = 2 * i < N ? u + 2 * i : v + 2 * i - N;
             const float z0 = z[0], z1 = z[1], z2 = z[2], z3 = z[3];
-            z[0] = z0 * w.x - z1 * w.y;
-            z[1] = z0 * w.y + z1 * w.x;
-            z[2] = z2 * w.z - z3 * w.w;
-            z[3] = z2 * w.w + z3 * w.z;
+            z[0] = rope_first(z0, z1, w.x, w.y);
+            z[1] = rope_second<!VECTOR>(z0, z1, w.x, w.y);
+            z[2] = rope_first(z2, z3, w.z, w.w);
+            z[3] = rope_second<!VECTOR>(z2, z3, w.z, w.w);
           } else {
             const float a0 = u[i], b0 = v[i], a1 = u[i + 1], b1 = v[i + 1];
-            u[i] = a0 * w.x - b0 * w.y;
-            v[i] = a0 * w.y + b0 * w.x;
-            u[i + 1] = a1 * w.z - b1 * w.w;
-            v[i + 1] = a1 * w.w + b1 * w.z;
+            u[i] = rope_first(a0, b0, w.x, w.y);
+            v[i] = rope_second<!VECTOR>(a0, b0, w.x, w.y);
+            u[i + 1] = rope_first(a1, b1, w.z, w.w);
+            v[i + 1] = rope_second<!VECTOR>(a1, b1, w.z, w.w);
           }
         }
         x = Vec16<T>::pack(u);
@@ -139,8 +139,8 @@ struct Unit {
       *reinterpret_cast<uint4*>(dst + second()) = y;
     } else {
       const float2 w = kept() ? make_float2(1.f, 0.f) : cs[unit];
-      put(dst + first(), kept() ? a : a * w.x - b * w.y);
-      put(dst + second(), kept() ? b : a * w.y + b * w.x);
+      put(dst + first(), kept() ? a : rope_first(a, b, w.x, w.y));
+      put(dst + second(), kept() ? b : rope_second<!VECTOR>(a, b, w.x, w.y));
     }
   }
 };
@@ -275,7 +275,7 @@ cudaError_t launch_rope(const RopeArgs<kMaxSegs>& a, int num_sms, cudaStream_t s
   const int heads = a.nq + (a.append ? 2 : 1) * a.nk;
   if (a.tokens == 0 || heads == 0) return cudaSuccess;
   const int per_unit = a.elem_bytes == 2 ? 8 : 4;
-  const bool vec = (a.rope.rot_dim / 2) % per_unit == 0;
+  const bool vec = !rope_alone(a.rope, a.elem_bytes);
   const int units = a.head_dim / (vec ? 2 * per_unit : 2);
   // Few tokens: one a block, and its heads dealt out to more blocks (each
   // block makes the token's cosines again) until the SMs have a block or two.

@@ -27,6 +27,22 @@ __device__ __forceinline__ float2 rope_turn(const zl_rope_t& r, int64_t p, int i
   return make_float2(c * r.magnitude, (inverse ? -s : s) * r.magnitude);
 }
 
+// Whether a plan's pairs do not fill 16-byte pieces of elements of that size.
+__host__ __device__ __forceinline__ bool rope_alone(const zl_rope_t& r, int elem_bytes) {
+  return (r.rot_dim / 2) % (16 / elem_bytes) != 0;
+}
+
+// A pair by its cosine and sine.  The roundings are spelled out, so that every kernel
+// gives the same bits: ALONE for plans whose pairs do not fill 16-byte pieces
+// (rope_alone), where the fused product of the second element is the other one.
+__device__ __forceinline__ float rope_first(float a, float b, float c, float s) {
+  return __fmaf_rn(a, c, -__fmul_rn(b, s));
+}
+template <bool ALONE>
+__device__ __forceinline__ float rope_second(float a, float b, float c, float s) {
+  return ALONE ? __fmaf_rn(b, c, __fmul_rn(a, s)) : __fmaf_rn(a, s, __fmul_rn(b, c));
+}
+
 // Where a batch's packed token t lies in the cache: its position in the sequence
 // (below zero where the length does not count it) and its page, or -1.  A holds
 // the batch's sequences and the tables: RopeArgs, ReadQ4Args.

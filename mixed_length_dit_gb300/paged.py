@@ -321,10 +321,12 @@ def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None
 
 def paged_append_q4(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None, q_out=None, rope=None,
                     positions=None, stream=None, status=None):
-    """paged_append into a cache held in 4 bits.  Keys that are turned are rounded
-    to bf16 first; what is held is a group's values to the nearest of 16 steps,
-    the step its largest one's seventh (paged_read_q4 gives the values).  A group
-    of 32 columns with an element that is not finite reads as NaN."""
+    """paged_append into a cache held in 4 bits: what that would write, quantised
+    (turned keys are rounded to bf16 first, to the same bits).  A group's 32 values
+    are held to the nearest whole number of steps, -7 to 7 of them, the step its
+    largest one's seventh to four bits (paged_read_q4 gives the values; the header
+    has the ends of the range).  A group with an element that is not finite reads
+    as NaN."""
     return _append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q, q_out, rope, positions, stream, status,
                    True)
 

@@ -195,3 +195,31 @@ def test_the_bytes_of_groups_that_are_not_finite(value, hd):
     zl.paged_append_q4(k, k, *b.cache, b.cu)
     zl.sync_check()
     assert np.array_equal(b.k_pages.cpu().numpy(), want[0]) and np.array_equal(b.v_pages.cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("hd,heads,kv_heads,page,kw", [
+    (64, 4, 2, 16, {}), (128, 10, 2, 64, {"interleaved": True}), (128, 3, 3, 256, {"axes": (64,)}),
+    (64, 2, 1, 32, {"axes": (6,), "interleaved": True}), (128, 2, 1, 16, {"axes": (96,)}), (64, 3, 1, 16, {"axes": (6,)}),
+    (128, 1, 1, 16, {"axes": (128,), "magnitude": 1.25}), (128, 2, 2, 16, {"axes": (70,), "interleaved": True}),
+    (64, 1, 1, 16, {"axes": (62,)}), (128, 6, 2, 16, {"axes": (44, 42, 42)}), (64, 2, 2, 16, {"axes": (32,), "interleaved": True}),
+    (128, 2, 2, 16, {"axes": (40, 24, 32), "interleaved": True, "magnitude": 0.75}), (64, 4, 4, 16, {"axes": (32, 16, 16)}),
+])
+def test_turned_keys_are_those_of_the_bf16_cache(hd, heads, kv_heads, page, kw):
+    """The same bits: queries as paged_append and rope_fwd turn them, and the pages'
+    bytes those of the keys that they turn."""
+    b = Batch([1, 40, 0, 130, 300], [90, 40, 5, 333, 559], heads, kv_heads, hd, page, seed=55)
+    c = Batch([1, 40, 0, 130, 300], [90, 40, 5, 333, 559], heads, kv_heads, hd, page, seed=55)
+    k, v = randn(56, b.cu[-1], kv_heads, hd), randn(57, b.cu[-1], kv_heads, hd)
+    plan, axes = zl.RopePlan(hd, **kw), len(kw.get("axes", (hd,)))
+    pos = np.concatenate([np.arange(n - m, n) for m, n in zip(b.new, b.lens)]).astype(np.int32)
+    pos = i32(pos) if axes == 1 else i32(np.stack([pos * (a + 3) % 777 for a in range(axes)]))
+    given = {} if axes == 1 else {"positions": pos}
+    q = zl.paged_append_q4(k, v, *b.cache, b.cu, q=b.q, rope=plan, **given)
+    qt, kt = zl.rope_fwd(b.q, k, pos, plan)
+    zl.paged_append_q4(kt, v, *c.cache, c.cu)
+    pools = [torch.zeros((b.num_pages, kv_heads, page, hd), dtype=BF16, device="cuda") for _ in range(2)]
+    qb = zl.paged_append(k, v, *pools, *b.cache[2:], b.cu, q=b.q, rope=plan, **given)
+    zl.sync_check()
+    assert torch.equal(qt, qb)
+    assert torch.equal(q, qt), float((q != qt).float().mean())
+    assert torch.equal(b.k_pages, c.k_pages) and torch.equal(b.v_pages, c.v_pages)
