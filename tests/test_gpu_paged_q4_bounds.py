@@ -223,3 +223,99 @@ def test_turned_keys_are_those_of_the_bf16_cache(hd, heads, kv_heads, page, kw):
     assert torch.equal(qt, qb)
     assert torch.equal(q, qt), float((q != qt).float().mean())
     assert torch.equal(b.k_pages, c.k_pages) and torch.equal(b.v_pages, c.v_pages)
+
+
+# ------------------------------------------------------------------ each key once
+@pytest.mark.parametrize("new,lens,heads,kv_heads,hd,page,most", [
+    ([1, 3, 1], [20011, 513, 6000], 8, 2, 128, 64, None), ([1, 3, 1], [20011, 513, 6000], 8, 2, 128, 16, 100000),
+    ([1], [9001], 4, 1, 64, 32, None), ([1], [131], 40, 8, 128, 16, None), ([1] * 3, [3000, 1, 700], 3, 1, 128, 128, None),
+    ([5, 2, 7], [4000, 333, 7011], 8, 4, 64, 16, None), ([9] * 4, [6001, 40, 2500, 8000], 4, 1, 128, 32, None),
+    ([1] * 40, [100 + 53 * i for i in range(40)], 8, 8, 64, 16, 30000), ([3, 16, 1], [5000, 5000, 5000], 4, 4, 128, 256, None),
+    ([33, 150], [3000, 2500], 2, 2, 128, 16, None),
+])
+def test_every_key_counts_once(new, lens, heads, kv_heads, hd, page, most):
+    """Queries of zero: every key that is seen has the same probability, the lse is the
+    logarithm of their number n (to 2^-17: logarithms below 16 in float32 are off by 2^-21,
+    a part's, its weight's and the sum's add up to a few of them; a key more or less is
+    1 / n), and as 32 keys have their values in one column and the next 32 in another, an
+    output's columns say how many of their keys were counted (a probability of one times a
+    step and the sums of sevens are exact: off by the last rounding, 2^-8, and 2^-17)."""
+    b = Batch(new, lens, heads, kv_heads, hd, page, seed=58, spare_cols=3)
+    if most is not None:
+        b.dtable = torch.nn.functional.pad(b.dtable, (0, -(-most // page))).contiguous()
+    b.q.zero_()
+    rows = torch.zeros((sum(lens), kv_heads, hd), dtype=BF16)
+    j = np.concatenate([np.arange(n) for n in lens])
+    rows[torch.arange(len(j)), :, torch.tensor(j // 32 % hd)] = 7
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    zl.paged_append_q4(randn(60, *rows.shape), rows.cuda(), *b.cache, cu)
+    for kw in ({}, {"window": 700}, {"causal": False}, {"window": 2049, "causal": False}):
+        o, lse = b.run(most=most, **kw)
+        zl.sync_check()
+        o, lse = f64(o), f64(lse)
+        for s, n in enumerate(new):
+            for i in range(n):
+                pos = lens[s] - n + i
+                hi = pos + 1 if kw.get("causal", True) else lens[s]
+                lo = max(0, pos - kw["window"] + 1) if "window" in kw else 0
+                want = np.bincount(np.arange(lo, hi) // 32 % hd, minlength=hd) * 7 / (hi - lo)
+                row = b.cu[s] + i
+                assert np.abs(lse[:, row] - np.log(hi - lo)).max() <= 2.0 ** -17, (s, i, kw)
+                assert np.all(np.abs(o[row] - want) <= (2.0 ** -8 + 2.0 ** -17) * want), (s, i, kw)
+
+
+# ------------------------------------------------------------------ chunks in several batches
+@pytest.mark.parametrize("heads,kv_heads,most,batches", [(16, 8, 131072, 4), (4, 2, 1100000, 7)])
+def test_chunks_unpacked_batch_after_batch(heads, kv_heads, most, batches):
+    """Seven chunks whose bound of the lengths lets the workspace hold two at a time,
+    or one (a sequence of more than its 1 GiB), with single tokens and empty sequences
+    between them.  (Scores of the bf16 products: eight of 16 columns, whose partial
+    sums stay below 7 sum_g s_g sum|q|_g: 8 * 18 * 2^-23 * 7, below twice the bound above.)"""
+    new = [1, 70, 0, 129, 2, 90, 200, 0, 65, 1, 100, 300, 1]
+    lens = [300, 70, 9, 140, 600, 350, 201, 0, 500, 1, 90, 310, 77]
+    b = Batch(new, lens, heads, kv_heads, 128, 256, seed=59)
+    b.dtable = torch.nn.functional.pad(b.dtable, (0, most // 256 + 1 - b.dtable.shape[1]), value=-1).contiguous()
+    for kw in ({}, {"causal": False}):
+        zl.profile_begin()
+        o, lse = b.run(most=most, **kw)
+        names = zl.profile_end()
+        zl.sync_check()
+        assert names["paged_unpack_q4"][0] == batches, names
+        o, lse = f64(o), f64(lse)
+        for row, h, score, off, v in rows_of(b, f64(b.q), 128 ** -0.5, **kw):
+            if not np.isfinite(score).any():
+                assert np.isneginf(lse[h, row]) and np.all(o[row, h] == 0)
+                continue
+            off = 2 * off
+            m = score.max()
+            p = np.exp(score - m)
+            want = m + np.log(p.sum())
+            assert abs(lse[h, row] - want) <= off.max() + 2.0 ** -20 * max(abs(want), 1)
+            p /= p.sum()
+            reach, out = p @ np.abs(v), p @ v
+            assert np.all(np.abs(o[row, h] - out) <= (2.0 ** -8 + 2 * off.max() + 2.0 ** -19) * reach + 2.0 ** -8 * np.abs(out))
+
+
+# ------------------------------------------------------------------ ordinary scores
+@pytest.mark.parametrize("new,lens,heads,kv_heads,hd,page,kw", [
+    ([1, 3, 1], [20011, 513, 6000], 8, 2, 128, 64, {}), ([1, 3, 1], [20011, 513, 6000], 8, 2, 128, 16, {"window": 4097}),
+    ([1] * 4, [1001, 33, 1, 700], 10, 2, 64, 16, {}), ([12, 40], [3000, 60], 4, 4, 128, 32, {"causal": False}),
+    ([7, 3], [4100, 9000], 32, 8, 128, 32, {"window": 4096}),
+])
+def test_outputs_to_the_bound_of_their_arithmetic(new, lens, heads, kv_heads, hd, page, kw):
+    """The bounds above for queries over codes, with steps as they come (some 20 times
+    below what products of codes with 128 added would be allowed)."""
+    b = Batch(new, lens, heads, kv_heads, hd, page, seed=61)
+    o, lse = b.run(**kw)
+    zl.sync_check()
+    o, lse = f64(o), f64(lse)
+    for row, h, score, off, v in rows_of(b, f64(b.q), hd ** -0.5, **kw):
+        m = score.max()
+        p = np.exp(score - m)
+        want = m + np.log(p.sum())
+        p /= p.sum()
+        err = p @ off
+        assert abs(lse[h, row] - want) <= err + 2.0 ** -20 * max(abs(want), 8), (row, h)
+        reach, out = p @ np.abs(v), p @ v
+        tol = (2.0 ** -8 + 2 * off.max() + 2.0 ** -19) * reach + 2.0 ** -8 * np.abs(out)
+        assert np.all(np.abs(o[row, h] - out) <= tol), (row, h)
