@@ -13,12 +13,15 @@
 // steps the probability before it is rounded to bf16 (the one rounding, as in the
 // bf16 attention: the tensor cores take P in V's type).
 //
-// Bound by HBM at best, by instructions otherwise: an SM's share of HBM is 43
-// codes a clock.  So K and V are the A operands of warp-level products (16 keys,
-// or 16 columns, by the 8 rows of a query tile), unpacked in registers where they
-// are used.  The 5th-generation tensor cores take B from shared memory only, and A
-// from there or from TMEM: unpacked codes would cross shared memory twice, 170
-// bytes a clock of its 128.
+// Bound by HBM at best, by the way from codes to operands otherwise: an SM's share
+// of HBM is 43 codes a clock.  So K and V are the A operands of warp-level products
+// (16 keys, or 16 columns, by the 8 rows of a query tile), unpacked in registers
+// where they are used.  The 5th-generation tensor cores take B from shared memory
+// only, and A from there or from TMEM: at HBM's rate unpacked codes would cross
+// shared memory twice, 170 bytes a clock of its 128, so three quarters of that rate
+// at best.  For few rows that is little more than what follows reaches; for 32 rows
+// and more, whose codes are unpacked here again for every 16, it would be several
+// times faster, and is not built.
 //
 // The codes become operands by masks alone.  A 16-bit pattern below 256 is, as a
 // bf16, its number times 2^-133 (subnormal, or with the lowest exponent), and the
@@ -38,12 +41,14 @@
 // cluster, whose CTAs share the tiles and join them through distributed shared
 // memory.  One warp of a CTA copies the tiles of all others.
 //
-// Measured: 48 tokens over caches to 16,384 keys (40 / 8 heads, pages of 16) in 118 us,
-// 483 MB at 4.1 TB/s; the same cache in bf16 takes 290.  Copies alone take 84 us there,
-// everything but the copies 103: half of the issue slots, the logical unit 55% busy,
-// shared memory 60%, HBM 54%.  8-bit products (e4m3 codes, q in two parts) are made of
-// two 16-bit ones and conversions on this GPU and gained nothing; codes as 128 + n with
-// their offset taken off took 179 us, masks alone 141.
+// Measured: 48 tokens over caches to 16,384 keys (40 / 8 heads, pages of 16) in 120 us,
+// 483 MB at 4.0 TB/s; the same cache in bf16 takes 290.  Copies alone took 84 us there,
+// everything but the copies 103.  Nothing is saturated: issue slots 52%, logical unit
+// 50%, shared memory's data path 46%, tensor pipe 22%, HBM 55%; a tile is one chain of
+// products, exponentials and products, and an SM has 14 warps to overlap them.  8-bit
+// products (e4m3 codes, q in two parts) are made of two 16-bit ones and conversions on
+// this GPU and gained nothing; codes as 128 + n with their offset taken off took 179 us,
+// masks alone 141.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>

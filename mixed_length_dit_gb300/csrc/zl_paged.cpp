@@ -421,7 +421,8 @@ zl_status launch_attn(const Attend& c, const zl_paged_cache_t& cache, const Chos
 
 // ------------------------------------------------------------------ attention over 4 bits
 // Sequences of at most kQ4Rows rows (queries times the heads of a key head) run
-// over the codes as they are.  Longer ones are unpacked to bf16, once for all of
+// over the codes as they are, a single token of more than 64 heads to a key head not
+// among them.  Longer ones are unpacked to bf16, once for all of
 // their queries, and handed to the bf16 attention, a batch at a time: as many as
 // kScratchBytes hold, or one.
 constexpr int64_t kQ4Rows = 64;
@@ -441,7 +442,9 @@ struct Q4Plan {
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// The next launch over codes: sequences from *i on, units of nt tiles of 8 rows.
+// The next launch over codes: sequences from *i on, units of nt tiles of 8 rows.  The
+// longest sequence decides for all: 47 single tokens and one draft of 15 rows over long
+// caches take 169 us, 48 single tokens 117.
 struct Few {
   int32_t segs = 0;
   int32_t nt = 1;
@@ -483,7 +486,13 @@ size_t few_workspace(int32_t nt, int32_t hd) {
 // A cluster's CTAs need two waves of keys each to gain (eight where they make a second
 // CTA on an SM).  The lengths themselves are on the device; half the bound is taken for
 // their mean, so that equal shares have units * keys / 2 / ctas, and may begin three
-// waves later.
+// waves later.  Of the table the rule takes the slower way at 32 units of 4,096 keys
+// (cut 14.4, clusters 12.2), at 96 of 1,024 (cut 12.4, whole 11.3) and 2,048 (16.3,
+// 16.1), and at 288 of 2,048 and more (cut, 2 to 8% slower); with lengths spread from an
+// eighth of the bound to it, cut against whole:  32 units of 4,096 14.8 12.7,  96 of
+// 1,024 12.7 10.7,  288 of 2,048 23.0 21.7, but 288 of 4,096 32.8 37.8 and of 8,192 50.6
+// 68.4, which is what the cut is for.  It was measured for 8 rows, d = 128 and pages of
+// 64 alone; other units go by the same constants.
 void whole_q4(zl::AttnQ4Head* a, const Few& f, int ctas) {
   a->whole = 0;
   a->share = 1;
